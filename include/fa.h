@@ -55,7 +55,9 @@ typedef enum {
   FA_ERR_LAUNCH = -4,      /* CUDA launch or runtime error (see cudaGetLastError) */
   FA_ERR_TIMEOUT = -5,     /* a device pipeline wait exceeded its limit; outputs undefined */
   FA_ERR_WORKSPACE = -6,   /* workspace pointer null or smaller than fa_bwd_workspace_bytes() */
-  FA_ERR_DEVICE = -7       /* current device is not an sm_103 GPU (this library is sm_103a only) */
+  FA_ERR_DEVICE = -7,      /* current device is not an sm_103 GPU (this library is sm_103a only) */
+  FA_ERR_INDEX = -8        /* a length, page number or plan in device memory is out of range
+                              (reported by fa_check; nothing out of range is read or written) */
 } fa_status;
 
 /*
@@ -262,8 +264,115 @@ int fa_naive_fwd(const void *q, const void *k, const void *v, void *o, float *ls
 int fa_softmax_rows(const float *x, float *p, float *lse, long long rows, int n, fa_stream_t stream);
 
 /*
+ * Rotary positions. Pair i < rot/2 of a head is turned by the angle
+ *     phi = position[axis(i)] * inv_freq[i]:  (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi),
+ * the pair being dims (i, i + rot/2), or (2i, 2i + 1) when `interleaved`; dims from rot on pass
+ * through. One axis is text; several (time, height, width) are images and video. The angle is exact to
+ * about 2^-32 of a turn for every 32-bit position (whole turns are dropped in integers), the products
+ * are fp32, and each output is rounded to bf16 once.
+ */
+typedef struct {
+  const float *inv_freq;      /* device, [rot/2], finite: radians per position */
+  const unsigned char *axes;  /* HOST, [rot/2]: the axis of each pair; NULL: all axis 0 */
+  int naxes;                  /* 1..4 */
+  int rot;                    /* dims that are turned: a multiple of 16, at most d */
+  int interleaved;
+} fa_rotary;
+
+/*
+ * Rotates q and k, and with fa_rope_bwd the gradients of the rotated q and k back (the transposed
+ * rotation, so the gradient of inv_freq or of the positions is not formed).
+ *   q, q_out : [B][Hq ][N][d] bf16 with any strides; d contiguous.
+ *   k, k_out : [B][Hkv][N][d] bf16; both NULL (and Hkv 0): q alone.
+ *   strides  : HOST, 12 values in elements, multiples of 8: (batch, head, token) of q, q_out, k, k_out.
+ *              So q and k may be views of a fused projection's output while q_out and k_out are the
+ *              dense tensors that fa_fwd takes, and the other way round for their gradients.
+ *   positions: device int32; axis a of token n of batch element b is at a * pos_axis + b * pos_batch + n.
+ * An output may be its own input (same pointer and strides); it must not overlap anything else.
+ */
+int fa_rope(const void *q, void *q_out, const void *k, void *k_out, const long long *strides, const int *positions,
+            long long pos_axis, long long pos_batch, const fa_rotary *rotary, int B, int Hq, int Hkv, int N, int d,
+            fa_stream_t stream);
+int fa_rope_bwd(const void *dq_out, void *dq, const void *dk_out, void *dk, const long long *strides,
+                const int *positions, long long pos_axis, long long pos_batch, const fa_rotary *rotary, int B, int Hq,
+                int Hkv, int N, int d, fa_stream_t stream);
+
+/*
+ * A ragged batch over a paged cache, as one serving step has it. Sequence s brings q_len new tokens,
+ * tokens cu_q[s] .. cu_q[s + 1] - 1 of the step's T, and has kv_len[s] tokens in the cache once they
+ * are appended: new token j stands at position kv_len - q_len + j, and position x lives in page
+ * block_table[s][x / page_size], slot x % page_size. Sequences may share pages (a common prefix).
+ * Tokens outside every sequence (padding) are neither read nor written.
+ */
+typedef struct {
+  const int *block_table;  /* device int32 [S][max_pages]; read only where a visible key or a new token lives */
+  long long table_stride;  /* elements from row to row */
+  void *plan;              /* device, >= fa_paged_plan_bytes(S) bytes, 16-byte aligned; see fa_paged_plan */
+  size_t plan_bytes;
+  int S, T;                /* sequences, and rows of the step's token tensors (>= cu_q[S]); both may be 0 */
+  int max_q;               /* no sequence has more new tokens than this */
+  int max_pages;           /* columns of the table; max_pages * page_size must fit an int */
+  int page_size;           /* 16, 32, 64, 128 or 256 */
+  int Hq, Hkv, d;          /* Hq % Hkv == 0; d 64 or 128 */
+  int causal;              /* a query sees keys up to its own position (else all of its sequence's) */
+  int window;              /* > 0: and only after its position - window (implies causal); 0: no window */
+} fa_paged_batch;
+
+/* Keys and values, bf16: element (page, head, slot, dim) at page * strides[0] + head * strides[1] +
+ * slot * strides[2] + dim, strides multiples of 8. [page][head][slot][d] is the natural order;
+ * [page][slot][head][d], or both halves of one tensor, work as well. */
+typedef struct {
+  void *k, *v;              /* device, 16-byte aligned */
+  long long k_strides[3], v_strides[3];
+  int num_pages;            /* page numbers outside [0, num_pages) are reported, not followed */
+} fa_paged_cache;
+
+/*
+ * Lays a batch out for the calls below: checks the lengths and divides the work among the SMs by key
+ * blocks, on the device (no length is read back, so the call can be captured and follows new lengths
+ * at each replay). Once per step; all layers' calls with the same batch use the same plan, in order.
+ * Calls of fa_fwd_paged that overlap on the GPU need a plan and a workspace each.
+ *   cu_q: device int32 [S + 1]; kv_len: device int32 [S].
+ * Lengths out of range (cu_q falling or beyond T, more than max_q new tokens, kv_len beyond the table)
+ * are reported by fa_check as FA_ERR_INDEX, and that sequence is left out.
+ */
+size_t fa_paged_plan_bytes(int S);
+int fa_paged_plan(const int *cu_q, const int *kv_len, const fa_paged_batch *batch, fa_stream_t stream);
+
+/*
+ * Brings a step's new keys and values into the cache, rotating keys (and the queries, into q_out) by
+ * each token's position on the way.
+ *   q, q_out : [T][Hq][d] bf16, or both NULL; k, v: [T][Hkv][d] bf16.
+ *   strides  : HOST, 8 values in elements, multiples of 8: (token, head) of q, q_out, k, v.
+ *   rotary   : NULL: no rotation (q must then be NULL).
+ *   positions: device int32, axis a of token t at a * pos_axis + t; NULL (one axis only): the token's
+ *              position in its sequence.
+ * q_out may be q. Two tokens with the same page and slot leave either one's values there.
+ */
+int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, const long long *strides,
+                    const fa_paged_cache *cache, const fa_paged_batch *batch, const fa_rotary *rotary,
+                    const int *positions, long long pos_axis, fa_stream_t stream);
+
+/*
+ * Attention of a step's new tokens over the cache (their own keys and values included, so after
+ * fa_paged_append): one token per sequence, chunks, or both in one batch. Same mathematics as fa_fwd
+ * (and fa_fwd_window, with the window).
+ *   q : [T][Hq][d] bf16; q_strides: HOST, (token, head) in elements, multiples of 8.
+ *   o : [T][Hq][d] bf16 and lse: [T][Hq] fp32 (natural log), contiguous. A query that sees no key gets
+ *       o = 0 and lse = -inf.
+ *   workspace: >= fa_fwd_paged_workspace_bytes(d) bytes, 16-byte aligned; contents on entry do not
+ *       matter.
+ * Cache slots that no query of the sequence sees, and table entries for them, may hold anything. The
+ * result does not depend on scheduling: the same call gives the same bits.
+ */
+size_t fa_fwd_paged_workspace_bytes(int d);
+int fa_fwd_paged(const void *q, const long long *q_strides, const fa_paged_cache *cache, const fa_paged_batch *batch,
+                 void *o, float *lse, float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status word:
- * FA_OK, FA_ERR_TIMEOUT (a kernel gave up waiting) or FA_ERR_LAUNCH (the stream reported
+ * FA_OK, FA_ERR_TIMEOUT (a kernel gave up waiting), FA_ERR_INDEX (a length, page number or plan in
+ * device memory was out of range) or FA_ERR_LAUNCH (the stream reported
  * a CUDA error).
  */
 int fa_check(fa_stream_t stream);

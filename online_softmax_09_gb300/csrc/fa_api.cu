@@ -111,6 +111,8 @@ unsigned long long fa::current_context_id() {
 
 int fa::check_current_device() { return current_device(nullptr); }
 
+int fa::device_state(uint32_t** status, int* num_sms) { return current_device(status, num_sms); }
+
 namespace {
 
 bool load_encoder() {
@@ -531,7 +533,8 @@ int fa_check(fa_stream_t stream) {
   if (h != 0) {
     const uint32_t zero = 0;
     if (cudaMemcpy(status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return FA_ERR_LAUNCH;
-    return h == 1 ? FA_ERR_TIMEOUT : FA_ERR_LAUNCH;  // 2: a kernel found its shared memory misaligned
+    // 2: a kernel found its shared memory misaligned
+    return h == fa::kStatusTimeout ? FA_ERR_TIMEOUT : (h == fa::kStatusIndex ? FA_ERR_INDEX : FA_ERR_LAUNCH);
   }
   return FA_OK;
 }
@@ -540,16 +543,17 @@ const char* fa_strerror(int status) {
   switch (status) {
     case FA_OK: return "ok";
     case FA_ERR_INVALID: return "invalid argument (null pointer, size < 1, Hq % Hkv != 0 or size overflow)";
-    case FA_ERR_UNSUPPORTED: return "unsupported head dimension (d must be 64 or 128)";
+    case FA_ERR_UNSUPPORTED: return "unsupported head dimension (d must be 64 or 128) or page size (16, 32, 64, 128 or 256)";
     case FA_ERR_ALIGN: return "pointer not 16-byte aligned";
     case FA_ERR_LAUNCH: return "CUDA launch or runtime error";
     case FA_ERR_TIMEOUT: return "a device pipeline wait exceeded its time limit; outputs are undefined";
-    case FA_ERR_WORKSPACE: return "backward workspace missing or smaller than fa_bwd_workspace_bytes()";
+    case FA_ERR_WORKSPACE: return "workspace or plan missing or smaller than its size function says";
+    case FA_ERR_INDEX: return "a length, page number or plan in device memory is out of range; outputs are undefined";
     case FA_ERR_DEVICE: return "current device is not an sm_103 (GB300) GPU";
     default: return "unknown status";
   }
 }
 
-int fa_version(void) { return (1 << 16) | 0; }
+int fa_version(void) { return (1 << 16) | 1; }
 
 }  // extern "C"

@@ -89,6 +89,9 @@ unsigned long long current_context_id();
 // FA_OK if the current device is an sm_103 GPU; FA_ERR_DEVICE (or FA_ERR_LAUNCH) otherwise.
 int check_current_device();
 
+// The same, with the device's status word and its number of SMs (each may be NULL).
+int device_state(uint32_t** status, int* num_sms);
+
 // The argument checks of fa_bwd that need no CUDA call (sizes, pointers): FA_OK or the status
 // fa_bwd would return for them.
 int check_bwd_args(const void* q, const void* k, const void* v, const void* o, const void* dout, const void* lse,

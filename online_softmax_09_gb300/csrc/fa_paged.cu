@@ -1,0 +1,483 @@
+// fa_paged.cu -- attention of the newest tokens of a ragged batch over a paged key/value cache.
+//
+// For sequence s with q_len new tokens of kv_len, token j at position p = kv_len - q_len + j, and kv
+// head h, with keys and values read through the sequence's page table:
+//     x_t = scale * q_j . k_t  for t < kv_len, t <= p (causal), t > p - window (window > 0)
+//     o_j = sum_t exp(x_t - lse_j) v_t,  lse_j = log sum_t exp(x_t);  nothing visible: o = 0, lse = -inf.
+//
+// fa_paged_plan_kernel lays the batch out (fa_paged.cuh); fa_paged_rows_kernel attends.
+#include <math.h>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+// ------------------------------------------------------------------------------------------ plan
+// One CTA: checks every sequence's place and lengths, counts its work in both kinds of unit and
+// forms the running sums. A sequence out of range gets no tokens (nothing of it is read or written)
+// and raises the status word.
+__global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restrict__ cu_q,
+                                                             const int* __restrict__ kv_len, PagedBatch b, int d,
+                                                             int max_q, int pair_rows) {
+  __shared__ long long sums[2][32];
+  __shared__ long long carry[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 2) carry[tid] = 0;
+  bool bad = false;
+  for (int i = tid; i < 2 * kPlanCtas; i += 1024) b.plan.counters[0][i] = 0;
+  for (int s0 = 0; s0 < b.S; s0 += 1024) {
+    const int s = s0 + tid;
+    PlanSeq ps = {0, 0, 0, 0};
+    long long w[2] = {0, 0};
+    if (s < b.S) {
+      const int a = cu_q[s], e = cu_q[s + 1], n = kv_len[s];
+      const bool ok = a >= 0 && e >= a && e <= b.T && e - a <= max_q && n >= 0 &&
+                      (long long)n <= (long long)b.max_pages * b.page_size;
+      if (ok) ps = {a, e - a, n, 0};
+      bad |= !ok;
+      b.plan.seq[s] = ps;
+    }
+    const bool pairs = (long long)ps.ql * b.G > pair_rows;
+    if (!pairs) {
+      const int nt = tile_count<false>(ps.ql, b.G, b.pair_tokens);
+      for (int i = 0; i < nt; ++i) {
+        int t0, t1, b0, nb;
+        tile_tokens<false>(i, ps.ql, b.G, b.pair_tokens, t0, t1);
+        tile_blocks<false>(t0, t1, ps.ql, ps.kvl, b.causal, b.window, b0, nb);
+        w[0] += nb;
+      }
+    }
+    // Long chunks: the warp counts each one's tiles together.
+    for (uint32_t todo = __ballot_sync(0xffffffffu, pairs); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int ql = __shfl_sync(0xffffffffu, ps.ql, src), kvl = __shfl_sync(0xffffffffu, ps.kvl, src);
+      const int nt = tile_count<true>(ql, b.G, b.pair_tokens);
+      long long sum = 0;
+      for (int i = lane; i < nt; i += 32) {
+        int t0, t1, b0, nb;
+        tile_tokens<true>(i, ql, b.G, b.pair_tokens, t0, t1);
+        tile_blocks<true>(t0, t1, ql, kvl, b.causal, b.window, b0, nb);
+        sum += nb;
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane == src) w[1] = sum;
+    }
+    __syncthreads();  // carry of the previous round is set
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      w[k] *= b.Hkv;
+      long long x = w[k];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += v;
+      }
+      if (lane == 31) sums[k][warp] = x;
+      w[k] = x - w[k];  // before this sequence, within the warp
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      long long before = carry[k];
+      for (int i = 0; i < warp; ++i) before += sums[k][i];
+      if (s < b.S) b.plan.units[k][s] = before + w[k];
+    }
+    __syncthreads();
+    if (tid < 2)
+      for (int i = 0; i < 32; ++i) carry[tid] += sums[tid][i];
+  }
+  __syncthreads();
+  if (tid < 2) b.plan.units[tid][b.S] = carry[tid];
+  if (bad) record_index_error(b.status);
+  if (tid == 0) {
+    PlanHeader h = {};
+    h.magic = kPlanMagic;
+    h.S = b.S;
+    h.T = b.T;
+    h.Hq = b.Hq;
+    h.Hkv = b.Hkv;
+    h.d = d;
+    h.page_size = b.page_size;
+    h.max_pages = b.max_pages;
+    h.causal = b.causal;
+    h.window = b.window;
+    *b.plan.head = h;
+  }
+}
+
+cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int d, int max_q, int pair_rows,
+                              cudaStream_t st) {
+  fa_paged_plan_kernel<<<1, 1024, 0, st>>>(cu_q, kv_len, b, d, max_q, pair_rows);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------- 16-row tiles
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+  const int n = full ? 16 : 0;  // 0: the 16 bytes are zero-filled and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+
+constexpr int kRowWarps = 4, kRowThreads = 32 * kRowWarps;
+constexpr int kGran = kRowBlk / kRowWarps;  // keys that one warp takes at a time: 16, within one page
+
+template <int D>
+struct RowSmem {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kTile = kGran * D * 2;       // K or V of one granule
+  static constexpr int kWarp = kStages * 2 * kTile;  // ring of one warp
+  static constexpr int kStat = kRowWarps * kWarp;    // m, l, rounded l of each warp's 16 rows
+  static constexpr int kFlag = kStat + kRowWarps * 3 * kRowTile * 4;
+  static constexpr int kBytes = kFlag + 16;
+};
+
+// A partial result of one CTA: o [16][D], then m, l, rounded l of the 16 rows.
+template <int D>
+constexpr int kRowPart = kRowTile * (D + 3);
+
+// fa_paged_rows_kernel: tiles of 16 rows. Four warps per CTA, two CTAs per SM; each warp takes every
+// fourth granule of 16 keys with a ring of its own, so no barrier stands in the loop: it waits for its
+// own cp.async copies, forms the 16 x 16 scores (m16n8k16), carries its own running max and sums, and
+// adds P V. The four warps' results are joined once per stretch, and the stretches of a tile that
+// several CTAs share by the CTA that finishes last, in the order of the keys.
+//
+// Weights are rounded to bf16 for the product with V; o is divided by the sum of the rounded weights,
+// so a row that one key dominates is not off by that rounding, and lse holds the unrounded sum.
+template <int D>
+__global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const PagedFwd p) {
+  using L = RowSmem<D>;
+  constexpr int kChunks = D / 8;        // 16-byte chunks of a row
+  constexpr int kRowsPer = 32 / kChunks;  // rows that one copy instruction of a warp covers
+  constexpr int kNT = D / 8;            // 8-column tiles of o
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = sbase + warp * L::kWarp;
+  float* stat = reinterpret_cast<float*>(smem + L::kStat);
+  int* flag = reinterpret_cast<int*>(smem + L::kFlag);
+  const PagedBatch& b = p.b;
+  if (!plan_matches(b, D)) {
+    if (threadIdx.x == 0) record_index_error(b.status);
+    return;
+  }
+  // Copies: this lane's row and chunk within a group of rows, and its swizzled place.
+  const int crow = lane / kChunks, cchunk = lane % kChunks;
+  // ldmatrix rows of this lane.
+  const int krow = (lane & 7) + ((lane >> 4) << 3), kchk = (lane >> 3) & 1;  // K: keys 0-7 | 8-15, chunk 0 | 1
+  const int vrow = lane & 15, vchk = lane >> 4;                              // V: keys 0-15, chunk 0 | 1
+  const int g = lane >> 2, c2 = (lane & 3) * 2;                              // rows g, g + 8; columns c2, c2 + 1
+
+  SegIter<false> it(b);
+  Seg s;
+  while (it.next(s)) {
+    const int G = b.G;
+    const long long R = (long long)s.ql * G, r0 = (long long)s.tile * kRowTile;
+    const int rows = (int)min((long long)kRowTile, R - r0);
+    int lo, hi;
+    key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
+    const int* tab = b.table + (long long)s.seq * b.table_stride;
+    const int key0 = s.blk * kRowBlk + warp * kGran;  // first key of this warp's granule 0
+    int pages = 0;                                    // lane i: the page of granule (i0 & ~31) + i
+    const __nv_bfloat16* kh = p.c.k + s.head * p.c.k_head + cchunk * 8;
+    const __nv_bfloat16* vh = p.c.v + s.head * p.c.v_head + cchunk * 8;
+
+    auto issue = [&](int i) {
+      if ((i & 31) == 0) {
+        const int key = key0 + (i + lane) * kRowBlk;
+        const bool in = i + lane < s.n && key < hi && key + kGran > lo;
+        pages = in ? tab[key >> b.page_shift] : -1;
+        if (in && (unsigned)pages >= (unsigned)b.num_pages) {
+          record_index_error(b.status);
+          pages = -1;
+        }
+      }
+      if (i < s.n) {
+        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+        const int key = key0 + i * kRowBlk;
+        const int slot = key & (b.page_size - 1);
+        const uint32_t st = ring + (i % L::kStages) * 2 * L::kTile;
+        const long long pg = page < 0 ? 0 : page;
+#pragma unroll
+        for (int r = 0; r < kGran; r += kRowsPer) {
+          const int row = r + crow;
+          const bool in = page >= 0 && key + row >= lo && key + row < hi;
+          const uint32_t dst = st + row * (D * 2) + ((cchunk ^ (row & 7)) << 4);
+          cp_async16(dst, kh + pg * p.c.k_page + (in ? (slot + row) * p.c.k_tok : 0), in);
+        }
+#pragma unroll
+        for (int r = 0; r < kGran; r += kRowsPer) {
+          const int row = r + crow;
+          const bool in = page >= 0 && key + row >= lo && key + row < hi;
+          const uint32_t dst = st + L::kTile + row * (D * 2) + ((cchunk ^ (row & 7)) << 4);
+          cp_async16(dst, vh + pg * p.c.v_page + (in ? (slot + row) * p.c.v_tok : 0), in);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < L::kStages - 1; ++i) issue(i);
+
+    // Queries as A operands, zero rows past the tile; visible keys [klo, klim] of the lane's two rows.
+    uint32_t qa[D / 16][4];
+    int klo[2], klim[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h;
+      const bool ok = r < rows;
+      const long long rr = r0 + (ok ? r : 0);
+      const int tok = (int)(rr / G), hd = (int)(rr - (long long)tok * G);
+      const __nv_bfloat16* qp = p.q + (long long)(s.q0 + tok) * p.q_tok + (long long)(s.head * G + hd) * p.q_head;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qa[kk][h] = ok ? *reinterpret_cast<const uint32_t*>(qp + kk * 16 + c2) : 0;
+        qa[kk][2 + h] = ok ? *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 8 + c2) : 0;
+      }
+      const int pos = s.kvl - s.ql + tok;
+      klim[h] = b.causal ? pos : s.kvl - 1;
+      klo[h] = b.window > 0 ? pos - b.window + 1 : 0;
+    }
+    // Granules inside every row's range need no mask.
+    const int all_lo = __reduce_max_sync(0xffffffffu, max(klo[0], klo[1]));
+    const int all_lim = __reduce_min_sync(0xffffffffu, min(klim[0], klim[1]));
+
+    float o[kNT][4];
+#pragma unroll
+    for (int j = 0; j < kNT; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
+
+    for (int i = 0; i < s.n; ++i) {
+      issue(i + L::kStages - 1);
+      cp_async_wait<L::kStages - 1>();
+      __syncwarp();
+      const uint32_t sk = ring + (i % L::kStages) * 2 * L::kTile, sv = sk + L::kTile;
+      const int key = key0 + i * kRowBlk;
+      float x[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[t][k] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t kb[4];
+        ldsm4(sk + krow * (D * 2) + (((2 * kk + kchk) ^ (krow & 7)) << 4), kb);
+        mma16816(x[0], qa[kk], kb[0], kb[1]);
+        mma16816(x[1], qa[kk], kb[2], kb[3]);
+      }
+      if (key < all_lo || key + kGran - 1 > all_lim) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int kx = key + 8 * t + c2 + (k & 1);
+            if (kx > klim[k >> 1] || kx < klo[k >> 1]) x[t][k] = -INFINITY;
+          }
+      }
+      float mt[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        mt[h] = v * p.scale_log2;
+      }
+      // The reference max moves only when a row has outgrown it by 2^8 (any reference gives the same
+      // softmax, and weights up to 2^8 lose nothing in fp32 or bf16).
+      if (__any_sync(0xffffffffu, mt[0] > m[0] + 8.f || mt[1] > m[1] + 8.f)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mn = fmaxf(m[h], mt[h]);
+          const float corr = mn > m[h] ? ex2(m[h] - mn) : 1.f;
+          m[h] = mn;
+          l[h] *= corr;
+          lr[h] *= corr;
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) {
+            o[j][2 * h] *= corr;
+            o[j][2 * h + 1] *= corr;
+          }
+        }
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float mu = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float a = ex2(fmaf(x[t][2 * h], p.scale_log2, -mu)), c = ex2(fmaf(x[t][2 * h + 1], p.scale_log2, -mu));
+          const uint32_t pk = pack_bf16(a, c);
+          pa[2 * t + h] = pk;
+          l[h] += a + c;
+          lr[h] += __uint_as_float(pk << 16) + __uint_as_float(pk & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kNT; j += 2) {
+        uint32_t vb[4];
+        ldsm4t(sv + vrow * (D * 2) + (((j + vchk) ^ (vrow & 7)) << 4), vb);
+        mma16816(o[j], pa, vb[0], vb[1]);
+        mma16816(o[j + 1], pa, vb[2], vb[3]);
+      }
+      __syncwarp();  // the stage is read: the next copies may overwrite it
+    }
+
+    // ---- join the four warps: each leaves o in its own ring (drained), m and the sums in `stat`
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], 1);
+      lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], 2);
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    float* mine = reinterpret_cast<float*>(smem + warp * L::kWarp);
+#pragma unroll
+    for (int j = 0; j < kNT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(mine + (g + 8 * h) * D + j * 8 + c2) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+    if ((lane & 3) == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        stat[(warp * 3 + 0) * kRowTile + g + 8 * h] = m[h];
+        stat[(warp * 3 + 1) * kRowTile + g + 8 * h] = l[h];
+        stat[(warp * 3 + 2) * kRowTile + g + 8 * h] = lr[h];
+      }
+    }
+    __syncthreads();
+    // Eight threads per row, D / 8 columns each.
+    constexpr int kCols = D / 8;
+    const int row = threadIdx.x >> 3, col0 = (threadIdx.x & 7) * 4;  // columns col0 + 32 * i .. + 3
+    float M = -INFINITY, Ls = 0.f, Lr = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, stat[(w * 3) * kRowTile + row]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+    float acc[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+      const float f = ex2(stat[(w * 3) * kRowTile + row] - Mu);
+      Ls += f * stat[(w * 3 + 1) * kRowTile + row];
+      Lr += f * stat[(w * 3 + 2) * kRowTile + row];
+      const float* src = reinterpret_cast<const float*>(smem + w * L::kWarp) + row * D + col0;
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(src + 32 * i);
+        acc[4 * i] += f * v.x;
+        acc[4 * i + 1] += f * v.y;
+        acc[4 * i + 2] += f * v.z;
+        acc[4 * i + 3] += f * v.w;
+      }
+    }
+    bool write = true;
+    if (!(s.first && s.last)) {
+      // A tile that other CTAs share: leave the partial result; the last of them to arrive joins all.
+      const int c0 = it.owner(s.u0), c1 = it.owner(s.u1 - 1);
+      float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * kRowPart<D>;
+      if (row < rows) {
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i)
+          *reinterpret_cast<float4*>(slot + row * D + col0 + 32 * i) =
+              make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        if ((threadIdx.x & 7) == 0) {
+          slot[kRowTile * D + row] = M;
+          slot[kRowTile * (D + 1) + row] = Ls;
+          slot[kRowTile * (D + 2) + row] = Lr;
+        }
+      }
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const bool last = atomicAdd(&b.plan.counters[0][c0], 1u) == (uint32_t)(c1 - c0);
+        if (last) b.plan.counters[0][c0] = 0;
+        __threadfence();
+        *flag = last;
+      }
+      __syncthreads();
+      write = *flag != 0;
+      if (write && row < rows) {
+        M = -INFINITY;
+        Ls = Lr = 0.f;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+          const float* src = p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kRowPart<D>;
+          const float mi = __ldcg(src + kRowTile * D + row);
+          const float mn = fmaxf(M, mi), mu = mn == -INFINITY ? 0.f : mn;
+          const float fa = ex2(M - mu), fb = ex2(mi - mu);
+          M = mn;
+          Ls = Ls * fa + fb * __ldcg(src + kRowTile * (D + 1) + row);
+          Lr = Lr * fa + fb * __ldcg(src + kRowTile * (D + 2) + row);
+#pragma unroll
+          for (int i = 0; i < kCols / 4; ++i) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D + col0 + 32 * i));
+            acc[4 * i] = acc[4 * i] * fa + fb * v.x;
+            acc[4 * i + 1] = acc[4 * i + 1] * fa + fb * v.y;
+            acc[4 * i + 2] = acc[4 * i + 2] * fa + fb * v.z;
+            acc[4 * i + 3] = acc[4 * i + 3] * fa + fb * v.w;
+          }
+        }
+      }
+    }
+    if (write && row < rows) {
+      const long long rr = r0 + row;
+      const int tok = (int)(rr / G), hd = (int)(rr - (long long)tok * G);
+      const long long out = (long long)(s.q0 + tok) * b.Hq + s.head * G + hd;
+      const float inv = Lr > 0.f || Lr != Lr ? 1.f / Lr : 0.f;  // a row that sees nothing: o = 0
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) {
+        uint2 w;
+        w.x = pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv);
+        w.y = pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
+        *reinterpret_cast<uint2*>(p.o + out * D + col0 + 32 * i) = w;
+      }
+      if ((threadIdx.x & 7) == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
+    }
+    __syncthreads();  // the rings and `stat` are free for the next stretch
+  }
+}
+
+template <int D>
+static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) {
+  constexpr int smem = RowSmem<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(fa_paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  fa_paged_rows_kernel<D><<<2 * num_sms, kRowThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+size_t paged_workspace_bytes(int d) { return plan_up((size_t)4 * kPagedSms * kRowTile * (d + 3) * 4); }
+
+cudaError_t launch_paged_fwd(const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
+  num_sms = num_sms < kPagedSms ? num_sms : kPagedSms;
+  return d == 128 ? launch_rows<128>(p, num_sms, st) : launch_rows<64>(p, num_sms, st);
+}
+
+}  // namespace fa

@@ -1,0 +1,295 @@
+// fa_paged.cuh -- the plan of a ragged batch over a paged cache, and how a kernel's CTAs walk it.
+//
+// The plan is built on the device from the batch's lengths (fa_paged.cu), so no length is read back
+// by the host and a captured graph follows new lengths. It holds each sequence's place, and per
+// sequence the running sum of its work in units; CTA c of P takes the units [c * per, (c + 1) * per),
+// per = ceil(W / P), whatever sequences and heads they belong to. So every CTA has the same number of
+// key blocks however ragged the batch is, and only the first and the last item of a CTA can be part
+// of a row tile that another CTA shares: at most two partial results per CTA, whatever the batch.
+#pragma once
+
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+constexpr uint32_t kPlanMagic = 0x70a6ed01u;
+constexpr int kPlanCtas = 512;  // most CTAs that a kernel over a plan may have (its merge counters)
+constexpr int kPagedSms = 160;  // most SMs that are used: bounds the partial results without asking the device
+
+// Row tiles of two kinds: 16 rows against 64-key blocks, and pairs of 128 rows against 128-key
+// blocks. A row is one query head of one new token: row r of a (sequence, kv head) is token r / G,
+// head r % G, so the heads that share keys share a tile.
+constexpr int kRowTile = 16, kRowBlk = 64;
+constexpr int kPairBlk = 128;
+
+struct PlanHeader {  // 64 words; what the plan was built for, checked by every kernel that reads it
+  uint32_t magic;
+  int S, T, Hq, Hkv, d, page_size, max_pages, causal, window;
+  int pad[54];
+};
+
+struct PlanSeq {
+  int q0, ql, kvl, pad;  // first token, new tokens, cached tokens with them
+};
+
+struct PlanView {
+  PlanHeader* head;
+  PlanSeq* seq;               // [S]
+  long long* units[2];        // [S + 1] running sums: 16-row tiles, 256-row pairs
+  uint32_t* counters[2];      // [kPlanCtas] arrivals at tiles shared by several CTAs; zero between calls
+};
+
+__host__ __device__ inline size_t plan_up(size_t x) { return (x + 255) / 256 * 256; }
+
+__host__ __device__ inline size_t plan_layout(void* base, int S, PlanView* v) {
+  char* b = static_cast<char*>(base);
+  size_t at = sizeof(PlanHeader);
+  size_t off[5];
+  off[0] = at;
+  at += plan_up((size_t)S * sizeof(PlanSeq));
+  for (int i = 0; i < 2; ++i) {
+    off[1 + i] = at;
+    at += plan_up(((size_t)S + 1) * 8);
+  }
+  for (int i = 0; i < 2; ++i) {
+    off[3 + i] = at;
+    at += kPlanCtas * 4;
+  }
+  if (v != nullptr) {
+    v->head = reinterpret_cast<PlanHeader*>(b);
+    v->seq = reinterpret_cast<PlanSeq*>(b + off[0]);
+    for (int i = 0; i < 2; ++i) {
+      v->units[i] = reinterpret_cast<long long*>(b + off[1 + i]);
+      v->counters[i] = reinterpret_cast<uint32_t*>(b + off[3 + i]);
+    }
+  }
+  return at;
+}
+
+// What a kernel needs of the batch (by value).
+struct PagedBatch {
+  PlanView plan;
+  const int* table;  // [S][table_stride]
+  long long table_stride;
+  int S, T, Hq, Hkv, G, page_size, page_shift, max_pages, num_pages, causal, window;
+  int pair_tokens;  // tokens of a pair of 128-row tiles: 2 * (128 / G)
+  uint32_t* status;
+};
+
+__device__ __forceinline__ void record_index_error(uint32_t* status) { atomicCAS(status, kStatusOk, kStatusIndex); }
+
+// The plan was built for this batch (a stale or unset buffer would send indexes out of range).
+__device__ __forceinline__ bool plan_matches(const PagedBatch& b, int d) {
+  const PlanHeader* h = b.plan.head;
+  return h->magic == kPlanMagic && h->S == b.S && h->T == b.T && h->Hq == b.Hq && h->Hkv == b.Hkv && h->d == d &&
+         h->page_size == b.page_size && h->max_pages == b.max_pages && h->causal == b.causal && h->window == b.window;
+}
+
+// Keys [lo, hi) that some query of tokens [t0, t1] sees: token j stands at position kvl - ql + j and
+// sees keys up to its own (causal) and after position - window (window > 0).
+__host__ __device__ __forceinline__ void key_range(int t0, int t1, int ql, int kvl, int causal, int window, int& lo,
+                                                   int& hi) {
+  const int p0 = kvl - ql + t0, p1 = kvl - ql + t1;
+  hi = causal ? (p1 + 1 < 0 ? 0 : p1 + 1) : kvl;
+  lo = (window > 0 && p0 - window + 1 > 0) ? p0 - window + 1 : 0;
+  if (lo > hi) lo = hi;
+}
+
+// Row tile `i` of a sequence: its tokens [t0, t1], and how many tiles there are.
+template <bool kPairs>
+__host__ __device__ __forceinline__ int tile_count(int ql, int G, int pair_tokens) {
+  return kPairs ? (ql + pair_tokens - 1) / pair_tokens : (int)(((long long)ql * G + kRowTile - 1) / kRowTile);
+}
+template <bool kPairs>
+__host__ __device__ __forceinline__ void tile_tokens(int i, int ql, int G, int pair_tokens, int& t0, int& t1) {
+  if (kPairs) {
+    t0 = i * pair_tokens;
+    t1 = (t0 + pair_tokens < ql ? t0 + pair_tokens : ql) - 1;
+  } else {
+    const long long r0 = (long long)i * kRowTile, R = (long long)ql * G;
+    const long long r1 = (r0 + kRowTile < R ? r0 + kRowTile : R) - 1;
+    t0 = (int)(r0 / G);
+    t1 = (int)(r1 / G);
+  }
+}
+// Key blocks [b0, b0 + n) of tokens [t0, t1]; one block at least, so that rows that see nothing are
+// still written.
+template <bool kPairs>
+__host__ __device__ __forceinline__ void tile_blocks(int t0, int t1, int ql, int kvl, int causal, int window, int& b0,
+                                                     int& n) {
+  constexpr int kBlk = kPairs ? kPairBlk : kRowBlk;
+  int lo, hi;
+  key_range(t0, t1, ql, kvl, causal, window, lo, hi);
+  b0 = lo / kBlk;
+  n = (int)(((long long)hi + kBlk - 1) / kBlk) - b0;
+  if (n < 1) n = 1;
+}
+
+// One stretch of key blocks of one row tile, as a CTA works it off.
+struct Seg {
+  int seq, head, tile;
+  int q0, ql, kvl;
+  int t0, t1;      // tokens of the tile
+  int blk, n;      // key blocks [blk, blk + n) of this stretch
+  bool first, last;  // holds the tile's first / last block (both: no other CTA shares the tile)
+  long long u0, u1;  // the tile's units [u0, u1)
+};
+
+// Walk of one CTA's units. Every call is made by whole warps (the searches are warp-wide), and all
+// warps of a CTA that walk get the same stretches.
+template <bool kPairs>
+struct SegIter {
+  const PagedBatch& b;
+  const long long* U;
+  long long u, u_end, per, tile_u0;
+  int seq, head, tile, ntiles, t0, t1, b0, nb;
+  PlanSeq ps;
+
+  __device__ __forceinline__ SegIter(const PagedBatch& batch) : b(batch), U(batch.plan.units[kPairs ? 1 : 0]) {
+    const long long W = U[b.S];
+    per = (W + gridDim.x - 1) / gridDim.x;
+    u = min(W, per * blockIdx.x);
+    u_end = min(W, u + per);
+    seq = -1;
+  }
+  __device__ __forceinline__ int owner(long long unit) const { return (int)(unit / per); }
+
+  __device__ __forceinline__ void find_seq() {
+    const int lane = threadIdx.x & 31;
+    // The last s with U[s] <= u: the next 32 entries first (the walk moves forward), then a 32-way search.
+    int lo = seq + 1, hi = b.S;  // U[lo] <= u < U[hi]
+    if (seq >= 0) {
+      const int idx = min(lo + 1 + lane, b.S);
+      const int c = __popc(__ballot_sync(0xffffffffu, U[idx] <= u));
+      if (c < 32) {
+        lo += c;
+        hi = lo + 1;
+      } else {
+        lo += 32;
+      }
+    }
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const long long idx = (long long)lo + (long long)(lane + 1) * step;
+      const bool le = idx < hi && U[idx] <= u;
+      const int c = __popc(__ballot_sync(0xffffffffu, le));
+      lo += c * step;
+      hi = (int)min((long long)hi, (long long)lo + step);
+    }
+    seq = lo;
+    ps = b.plan.seq[seq];
+    ntiles = tile_count<kPairs>(ps.ql, b.G, b.pair_tokens);
+    const long long base = U[seq], per_head = (U[seq + 1] - base) / b.Hkv;
+    const long long rem = u - base;
+    head = (int)(rem / per_head);
+    // The tile that holds unit u of this head: running sums over 32 tiles at a time.
+    long long at = base + head * per_head;
+    for (int i0 = 0;; i0 += 32) {
+      int x0 = 0, x1 = 0, y0 = 0, yn = 0;
+      if (i0 + lane < ntiles) {
+        tile_tokens<kPairs>(i0 + lane, ps.ql, b.G, b.pair_tokens, x0, x1);
+        tile_blocks<kPairs>(x0, x1, ps.ql, ps.kvl, b.causal, b.window, y0, yn);
+      }
+      long long sum = yn;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += v;
+      }
+      const int c = __popc(__ballot_sync(0xffffffffu, at + sum <= u));
+      if (c < 32 || i0 + 32 >= ntiles) {
+        const int src = min(c, 31);
+        tile = i0 + src;
+        t0 = __shfl_sync(0xffffffffu, x0, src);
+        t1 = __shfl_sync(0xffffffffu, x1, src);
+        b0 = __shfl_sync(0xffffffffu, y0, src);
+        nb = __shfl_sync(0xffffffffu, yn, src);
+        tile_u0 = at + __shfl_sync(0xffffffffu, sum, src) - nb;
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (u >= u_end) return false;
+    if (seq < 0 || head == b.Hkv) find_seq();
+    s.seq = seq;
+    s.head = head;
+    s.tile = tile;
+    s.q0 = ps.q0;
+    s.ql = ps.ql;
+    s.kvl = ps.kvl;
+    s.t0 = t0;
+    s.t1 = t1;
+    s.u0 = tile_u0;
+    s.u1 = tile_u0 + nb;
+    const int off = (int)(u - tile_u0);
+    s.blk = b0 + off;
+    s.n = (int)min((long long)(nb - off), u_end - u);
+    s.first = off == 0;
+    s.last = off + s.n == nb;
+    u += s.n;
+    if (s.last) {  // on to the next tile, head or (at the next call) sequence
+      tile_u0 += nb;
+      if (ntiles > 1 || head + 1 == b.Hkv) {
+        if (++tile == ntiles) {
+          tile = 0;
+          ++head;
+        }
+        if (head < b.Hkv) {
+          tile_tokens<kPairs>(tile, ps.ql, b.G, b.pair_tokens, t0, t1);
+          tile_blocks<kPairs>(t0, t1, ps.ql, ps.kvl, b.causal, b.window, b0, nb);
+        }
+      } else {
+        ++head;  // one tile per head: the same blocks again
+      }
+    }
+    return true;
+  }
+};
+
+struct PagedCache {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long k_page, k_head, k_tok;  // strides in elements
+  long long v_page, v_head, v_tok;
+};
+
+struct PagedFwd {
+  PagedBatch b;
+  PagedCache c;
+  const __nv_bfloat16* q;
+  long long q_tok, q_head;
+  __nv_bfloat16* o;  // [T][Hq][d]
+  float* lse;        // [T][Hq]
+  float* part;       // partial results: 2 slots per CTA
+  float scale_log2;
+};
+
+// Rotation of q and k (and a copy of v), dense or into a paged cache.
+struct RopeStrides {
+  long long batch, head, tok;  // in elements; of a cache: page, head, slot
+};
+struct RopeLaunch {
+  const __nv_bfloat16* src[3];  // q, k, v
+  __nv_bfloat16* dst[3];
+  RopeStrides in[3], out[3];
+  const int* positions;  // [axes][batch][token], or NULL: the place in the sequence (paged batch)
+  long long pos_axis, pos_batch;
+  const float* inv_freq;  // [rot / 2]
+  uint64_t axes[2];       // two bits per pair
+  long long tokens;       // B * N, or T
+  int N, Hq, Hk, Hv, rot, interleaved, inverse;
+  int tile;  // tokens per CTA
+  PagedBatch b;
+};
+
+cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int d, int max_q, int pair_rows,
+                              cudaStream_t st);
+size_t paged_workspace_bytes(int d);
+cudaError_t launch_paged_fwd(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
+cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, cudaStream_t st);
+
+}  // namespace fa

@@ -14,7 +14,7 @@ namespace fa {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 // Status codes written to the device status word (first failure wins).
-enum : uint32_t { kStatusOk = 0, kStatusTimeout = 1, kStatusSmemAlign = 2 };
+enum : uint32_t { kStatusOk = 0, kStatusTimeout = 1, kStatusSmemAlign = 2, kStatusIndex = 3 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

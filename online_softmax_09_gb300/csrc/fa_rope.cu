@@ -1,0 +1,186 @@
+// fa_rope.cu -- rotary positions: q and k of a dense batch (forward and gradient), and the newest
+// tokens of a ragged batch on their way into a paged cache.
+//
+// Pair i of a head's first `rot` dims, (x_i, x_{i + rot/2}) or (x_{2i}, x_{2i+1}), is turned by
+//     phi = pos[axis(i)] * inv_freq[i]:   (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi);
+// the gradient is the same with -phi. The other dims pass through.
+//
+// Angles. inv_freq / 2 pi is kept as a fraction of a turn in 64-bit fixed point, w = inv_freq / 2 pi * 2^64,
+// so pos * w in 64-bit integers drops whole turns exactly, for any 32-bit position: what is lost is
+// pos * 2^-53 of the angle per position (the double that w comes from), 2^-32 of a turn when the top
+// half is taken, and 2^-24 of the remainder as a float. cos and sin follow from cospi and sinpi.
+//
+// Memory-bound: 2 bytes in and 2 out per element. A thread takes 8 pairs of one head (two 16-byte
+// chunks in, two out); the cos and sin of a CTA's tokens are made once, in shared memory, for all heads.
+#include "fa_paged.cuh"
+
+namespace fa {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;  // most tokens per CTA
+
+template <int D>
+__device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float2* cs, int j, bool interleaved) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&va);
+  uint32_t* c = reinterpret_cast<uint32_t*>(&vb);
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+  const float4* t = reinterpret_cast<const float4*>(cs + 8 * j);  // cos, sin of pairs 8j .. 8j + 7
+  if (!interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = t[i];
+      const float x0 = lo(a[i]), x1 = hi(a[i]), y0 = lo(c[i]), y1 = hi(c[i]);
+      a[i] = pack_bf16(x0 * f.x - y0 * f.y, x1 * f.z - y1 * f.w);
+      c[i] = pack_bf16(y0 * f.x + x0 * f.y, y1 * f.z + x1 * f.w);
+    }
+  } else {  // words a[0..3], c[0..3] hold pairs 8j .. 8j + 7
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = t[i];
+      uint32_t& w0 = i < 2 ? a[2 * i] : c[2 * i - 4];
+      uint32_t& w1 = i < 2 ? a[2 * i + 1] : c[2 * i - 3];
+      const float x0 = lo(w0), y0 = hi(w0), x1 = lo(w1), y1 = hi(w1);
+      w0 = pack_bf16(x0 * f.x - y0 * f.y, y0 * f.x + x0 * f.y);
+      w1 = pack_bf16(x1 * f.z - y1 * f.w, y1 * f.z + x1 * f.w);
+    }
+  }
+}
+
+struct RopeToken {
+  long long in[3];   // element offset of the token in q, k, v
+  long long out[3];  // and in their outputs; v and k of a paged batch: in the cache
+  int pos;           // paged batch without given positions
+  int state;         // bit 0: a token of the batch, bit 1: its cache slot exists
+};
+
+// Token t of the grid's dense batch, or of the plan's ragged one.
+template <bool kPaged>
+__device__ __forceinline__ RopeToken rope_token(const RopeLaunch& p, long long t) {
+  RopeToken k = {};
+  if (t >= p.tokens) return k;
+  if constexpr (!kPaged) {
+    const long long bi = t / p.N, n = t - bi * p.N;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k.in[i] = bi * p.in[i].batch + n * p.in[i].tok;
+      k.out[i] = bi * p.out[i].batch + n * p.out[i].tok;
+    }
+    k.state = 3;
+  } else {
+    const PagedBatch& b = p.b;
+    // The last sequence that starts at or before the token; sequences without tokens share a start.
+    int lo = 0, hi = b.S;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (b.plan.seq[mid].q0 <= t) lo = mid;
+      else hi = mid;
+    }
+    const PlanSeq s = b.plan.seq[lo];
+    const long long j = t - s.q0;
+    if (j < 0 || j >= s.ql) return k;
+    k.state = 1;
+    k.pos = s.kvl - s.ql + (int)j;
+    k.in[0] = t * p.in[0].tok;
+    k.out[0] = t * p.out[0].tok;
+    k.in[1] = t * p.in[1].tok;
+    k.in[2] = t * p.in[2].tok;
+    if (k.pos >= 0) {
+      const int page = b.table[(long long)lo * b.table_stride + (k.pos >> b.page_shift)];
+      if ((unsigned)page < (unsigned)b.num_pages) {
+        const int slot = k.pos & (b.page_size - 1);
+        k.out[1] = page * p.out[1].batch + slot * p.out[1].tok;
+        k.out[2] = page * p.out[2].batch + slot * p.out[2].tok;
+        k.state = 3;
+      } else {
+        record_index_error(b.status);
+      }
+    } else {
+      record_index_error(b.status);  // more new tokens than the sequence has
+    }
+  }
+  return k;
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeLaunch p) {
+  constexpr int kGroups = D / 16;  // threads per head
+  constexpr int kSlots = kRopeThreads / kGroups;
+  __shared__ __align__(16) float2 cs[kRopeTokens][D / 2];
+  __shared__ RopeToken tok[kRopeTokens];
+  const int tid = threadIdx.x;
+  if (kPaged && !plan_matches(p.b, D)) {
+    if (tid == 0) record_index_error(p.b.status);
+    return;
+  }
+  const long long t0 = (long long)blockIdx.x * p.tile;
+  if (tid < p.tile) tok[tid] = rope_token<kPaged>(p, t0 + tid);
+  const int np = p.rot >> 1;
+  if (kPaged) __syncthreads();
+  if (np > 0) {
+    const int per = kRopeThreads / np;  // tokens at a time
+    const int i = tid % np, first = tid / np;
+    if (first < per && first < p.tile) {
+      const double turns = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+      const uint64_t w = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+      const int axis = (int)(p.axes[i >> 5] >> ((i & 31) * 2)) & 3;
+      for (int t = first; t < p.tile; t += per) {
+        long long pos = 0;
+        if (t0 + t < p.tokens) {
+          if (p.positions == nullptr) {
+            pos = tok[t].pos;
+          } else {
+            const long long bi = kPaged ? 0 : (t0 + t) / p.N;
+            pos = p.positions[axis * p.pos_axis + bi * p.pos_batch + (t0 + t - bi * p.N)];
+          }
+        }
+        const int phase = (int)(uint32_t)(((uint64_t)pos * w) >> 32);  // 2^-32 turns, signed
+        float s, c;
+        sincospif((float)phase * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+        cs[t][i] = make_float2(c, p.inverse ? -s : s);
+      }
+    }
+  }
+  __syncthreads();
+  const int g = tid % kGroups, slot = tid / kGroups;
+  const bool turned = g < p.rot / 16;
+  const int ea = turned && !p.interleaved ? 8 * g : 16 * g;
+  const int eb = turned && !p.interleaved ? np + 8 * g : ea + 8;
+  const int heads = p.Hq + p.Hk + p.Hv;
+  const int total = p.tile * heads;
+  int t = slot / heads, h = slot - t * heads;
+  for (int x = slot; x < total; x += kSlots) {
+    const int part = h < p.Hq ? 0 : (h < p.Hq + p.Hk ? 1 : 2);
+    const int hh = h - (part == 0 ? 0 : (part == 1 ? p.Hq : p.Hq + p.Hk));
+    const RopeToken& k = tok[t];
+    if (k.state == 3 || (k.state == 1 && part == 0)) {
+      const __nv_bfloat16* src = p.src[part] + k.in[part] + hh * p.in[part].head;
+      __nv_bfloat16* dst = p.dst[part] + k.out[part] + hh * p.out[part].head;
+      uint4 a = *reinterpret_cast<const uint4*>(src + ea), c = *reinterpret_cast<const uint4*>(src + eb);
+      if (turned && part < 2) turn8<D>(a, c, cs[t], g, p.interleaved);
+      *reinterpret_cast<uint4*>(dst + ea) = a;
+      *reinterpret_cast<uint4*>(dst + eb) = c;
+    }
+    h += kSlots;
+    while (h >= heads) {
+      h -= heads;
+      ++t;
+    }
+  }
+}
+
+cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, cudaStream_t st) {
+  p.tile = kRopeTokens;
+  const long long grid = (p.tokens + p.tile - 1) / p.tile;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (d == 128) {
+    if (paged) fa_rope_kernel<128, true><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
+    else fa_rope_kernel<128, false><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
+  } else {
+    if (paged) fa_rope_kernel<64, true><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
+    else fa_rope_kernel<64, false><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -25,6 +25,21 @@ _i = ctypes.c_int
 _f = ctypes.c_float
 
 
+class _Rotary(ctypes.Structure):  # fa_rotary
+    _fields_ = [("inv_freq", _vp), ("axes", ctypes.c_char_p), ("naxes", _i), ("rot", _i), ("interleaved", _i)]
+
+
+class _Batch(ctypes.Structure):  # fa_paged_batch
+    _fields_ = [("block_table", _vp), ("table_stride", ctypes.c_longlong), ("plan", _vp),
+                ("plan_bytes", ctypes.c_size_t)] + [(n, _i) for n in (
+                    "S", "T", "max_q", "max_pages", "page_size", "Hq", "Hkv", "d", "causal", "window")]
+
+
+class _Cache(ctypes.Structure):  # fa_paged_cache
+    _fields_ = [("k", _vp), ("v", _vp), ("k_strides", ctypes.c_longlong * 3), ("v_strides", ctypes.c_longlong * 3),
+                ("num_pages", _i)]
+
+
 class FAError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: status {status} ({strerror(status)})")
@@ -77,6 +92,20 @@ def lib() -> ctypes.CDLL:
         L.fa_selftest_wait_timeout.restype = _i
         L.fa_softmax_rows.argtypes = [_vp, _vp, _vp, ctypes.c_longlong, _i, _vp]
         L.fa_softmax_rows.restype = _i
+        ll = ctypes.c_longlong
+        for fn in (L.fa_rope, L.fa_rope_bwd):
+            fn.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, ll, ll, _vp, _i, _i, _i, _i, _i, _vp]
+            fn.restype = _i
+        L.fa_paged_plan_bytes.argtypes = [_i]
+        L.fa_paged_plan_bytes.restype = ctypes.c_size_t
+        L.fa_paged_plan.argtypes = [_vp, _vp, _vp, _vp]
+        L.fa_paged_plan.restype = _i
+        L.fa_paged_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ll, _vp]
+        L.fa_paged_append.restype = _i
+        L.fa_fwd_paged_workspace_bytes.argtypes = [_i]
+        L.fa_fwd_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.fa_fwd_paged.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, ctypes.c_size_t, _vp]
+        L.fa_fwd_paged.restype = _i
         L.fa_check.argtypes = [_vp]
         L.fa_check.restype = _i
         L.fa_strerror.argtypes = [_i]
@@ -353,6 +382,234 @@ def softmax_rows(x, out=None, lse=None, with_lse: bool = True, stream=None):
     if r != FA_OK:
         raise FAError(r, "fa_softmax_rows")
     return p, l
+
+
+class Rotary:
+    """Frequencies of a rotary position embedding (fa_rotary): ``inv_freq`` fp32 CUDA [rot / 2] in radians per
+    position; dims from rot on pass through. ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + rot / 2).
+    ``axes``: the axis of each pair, for positions with several axes (e.g. time, height, width)."""
+
+    def __init__(self, inv_freq, interleaved: bool = False, axes=None):
+        if not inv_freq.is_cuda or inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 \
+                or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous 1-D float32 CUDA tensor [rot / 2]")
+        self.inv_freq = inv_freq
+        self.rot = 2 * inv_freq.numel()
+        self.interleaved = bool(interleaved)
+        ids = None if axes is None else [int(a) for a in axes]
+        if ids is not None and (len(ids) != inv_freq.numel() or any(not 0 <= a < 4 for a in ids)):
+            raise ValueError("axes must name an axis 0..3 for each of the rot / 2 pairs")
+        self.naxes = 1 if ids is None else max(ids) + 1
+        self._c = _Rotary(inv_freq.data_ptr(), None if ids is None else bytes(ids) + b"\0", self.naxes, self.rot,
+                          int(self.interleaved))
+        self._ref = ctypes.addressof(self._c)
+
+
+def _dev_index(t):
+    i = t.device.index
+    if i != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{i}, which is not the current device (use torch.cuda.device)")
+    return i
+
+
+def _stream_of(stream, index):
+    return int(stream.cuda_stream) if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor that belongs to ``stream`` (the caller's, or the current one)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _bf16(name, t, shape, device=None):
+    """``t`` is a bf16 CUDA tensor of ``shape`` with contiguous last dim (its other strides are free)."""
+    if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.stride(-1) != 1 \
+            or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor {list(shape)} with contiguous last dim, on one device")
+    return t
+
+
+def _strides(*tensors):
+    """(strides but the last) of each tensor, in elements; a dim of size one counts as dense (its stride means
+    nothing), and a missing tensor as zeros."""
+    out = []
+    for t, n in tensors:
+        if t is None:
+            out += [0] * n
+        else:
+            out += [s if e > 1 else 8 for s, e in zip(t.stride()[:-1], t.shape[:-1])]
+    return (ctypes.c_longlong * len(out))(*out)
+
+
+def _rope(name, fn, q, k, positions, rotary, q_out, k_out, stream):
+    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
+        raise ValueError("q must be [B, Hq, N, d] and k [B, Hkv, N, d] with the same B, N, d")
+    B, Hq, N, d = q.shape
+    Hkv = k.shape[1] if k is not None else 0
+    _bf16("q", q, q.shape)
+    i = _dev_index(q)
+    if k is not None:
+        _bf16("k", k, k.shape, q.device)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    A = rotary.naxes
+    want = {1: [(N,), (B, N), (1, N), (1, B, N)]}.get(A, [(A, N), (A, B, N)])
+    if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous() \
+            or tuple(positions.shape) not in want or positions.device != q.device \
+            or rotary.inv_freq.device != q.device:
+        raise ValueError(f"positions must be a contiguous int32 CUDA tensor of shape {want[0]} or {want[1]}")
+    per_batch = B > 1 and positions.numel() == A * B * N
+    pos_axis = positions.numel() // A
+    q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else _bf16("q_out", q_out, q.shape, q.device)
+    if k is not None:
+        k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else _bf16("k_out", k_out, k.shape,
+                                                                                      q.device)
+    if N == 0 or B == 0:
+        return q_out, k_out
+    r = fn(q.data_ptr(), q_out.data_ptr(), k.data_ptr() if k is not None else None,
+           k_out.data_ptr() if k is not None else None, _strides((q, 3), (q_out, 3), (k, 3), (k_out, 3)),
+           positions.data_ptr(), pos_axis, N if per_batch else 0, rotary._ref, B, Hq, Hkv, N, d, _stream_of(stream, i))
+    if r != FA_OK:
+        raise FAError(r, name)
+    return q_out, k_out
+
+
+def rope(q, k, positions, rotary, q_out=None, k_out=None, stream=None):
+    """Rotated (q, k) (fa_rope). q [B,Hq,N,d], k [B,Hkv,N,d] or None: bf16 CUDA, any strides with contiguous
+    last dim (e.g. views of a fused projection); outputs are contiguous unless given. positions: int32 CUDA
+    [N] or [B,N]; with several axes [A,N] or [A,B,N]. An output may be its input."""
+    return _rope("fa_rope", lib().fa_rope, q, k, positions, rotary, q_out, k_out, stream)
+
+
+def rope_backward(dq, dk, positions, rotary, q_out=None, k_out=None, stream=None):
+    """Gradients of rope's q and k from those of its outputs (fa_rope_bwd); arguments as for rope."""
+    return _rope("fa_rope_bwd", lib().fa_rope_bwd, dq, dk, positions, rotary, q_out, k_out, stream)
+
+
+class PagedPlan:
+    """The layout of one serving step over a paged cache (fa_paged_batch, its plan and a workspace); made by
+    paged_plan and taken by paged_append and forward_paged of every layer of the step."""
+
+    def __init__(self, S, T, max_q, max_pages, page_size, Hq, Hkv, d, causal, window, device, stream):
+        L = lib()
+        if S < 0:
+            raise ValueError("cu_q must hold S + 1 values")
+        self.key = (S, T, max_q, max_pages, page_size, Hq, Hkv, d, causal, window, device)
+        self.T, self.Hq, self.Hkv, self.d, self.page_size, self.device = T, Hq, Hkv, d, page_size, device
+        self.buffer = _empty(int(L.fa_paged_plan_bytes(S)), torch.uint8, device, stream)
+        self.ws_bytes = int(L.fa_fwd_paged_workspace_bytes(d))
+        self.workspace = _empty(max(self.ws_bytes, 16), torch.uint8, device, stream)
+        self.home = _stream_of(stream, device.index)
+        self._c = _Batch(None, 0, self.buffer.data_ptr(), self.buffer.numel(), S, T, max_q, max_pages, page_size, Hq,
+                         Hkv, d, causal, window)
+        self._ref = ctypes.addressof(self._c)
+
+    def _use(self, stream, index):
+        """The raw stream of a call; the buffers outlive their use on a stream that they were not made on."""
+        raw = _stream_of(stream, index)
+        if raw != self.home and not torch.cuda.is_current_stream_capturing():
+            s = stream if stream is not None else torch.cuda.current_stream(index)
+            for t in (self.buffer, self.workspace, self.table):
+                t.record_stream(s)
+        return raw
+
+    def _cache(self, k_cache, v_cache):
+        shape = (k_cache.shape[0], self.Hkv, self.page_size, self.d)
+        _bf16("k_cache", k_cache, shape, self.device)
+        _bf16("v_cache", v_cache, shape, self.device)
+        ks, vs = ([s if e > 1 else 8 for s, e in zip(t.stride()[:3], shape)] for t in (k_cache, v_cache))
+        return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), (ctypes.c_longlong * 3)(*ks),
+                      (ctypes.c_longlong * 3)(*vs), shape[0])
+
+
+def paged_plan(cu_q, kv_lens, block_table, num_tokens: int, max_q: int, page_size: int, Hq: int, Hkv: int, d: int,
+               causal: bool = True, window: int = 0, plan=None, stream=None):
+    """Lay out one step's ragged batch over a paged cache (fa_paged_plan). cu_q int32 CUDA [S+1]: the new tokens of
+    sequence s are rows cu_q[s] .. cu_q[s+1]-1 of the step's num_tokens; kv_lens int32 CUDA [S]: its cached tokens,
+    the new ones included; block_table int32 CUDA [S, max_pages]; max_q bounds the new tokens of a sequence.
+    ``plan``: an earlier plan of the same sizes, laid out anew in place (as a captured graph needs). Lengths stay on
+    the device; out of range, they are reported by check()."""
+    for name, t in (("cu_q", cu_q), ("kv_lens", kv_lens)):
+        if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
+    S = cu_q.numel() - 1
+    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 \
+            or block_table.shape[0] != S or kv_lens.numel() != S or block_table.shape[1] < 1 \
+            or block_table.stride(1) != 1 or not cu_q.device == kv_lens.device == block_table.device:
+        raise ValueError("block_table must be an int32 CUDA tensor [S, max_pages], cu_q [S + 1] and kv_lens [S], "
+                         "on one device")
+    i = _dev_index(cu_q)
+    key = (S, int(num_tokens), int(max_q), block_table.shape[1], int(page_size), int(Hq), int(Hkv), int(d),
+           int(bool(causal)), int(window), cu_q.device)
+    if plan is None:
+        plan = PagedPlan(*key, stream)
+    elif plan.key != key:
+        raise ValueError("plan was made for other sizes")
+    plan.table = block_table
+    plan._c.block_table = block_table.data_ptr()
+    plan._c.table_stride = block_table.stride(0)
+    r = lib().fa_paged_plan(cu_q.data_ptr(), kv_lens.data_ptr(), plan._ref, plan._use(stream, i))
+    if r != FA_OK:
+        raise FAError(r, "fa_paged_plan")
+    return plan
+
+
+def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q_out=None, stream=None):
+    """Put a step's k and v [T,Hkv,d] into the cache, k rotated by ``rotary`` (None: as it is), and return q
+    [T,Hq,d] rotated (q None: nothing) (fa_paged_append). k_cache, v_cache: bf16 CUDA [pages, Hkv, page_size, d],
+    any strides with contiguous last dim. positions: int32 CUDA [T], or [A,T] for several axes; None: each token's
+    position in its sequence."""
+    T, d = plan.T, plan.d
+    _bf16("k", k, (T, plan.Hkv, d), plan.device)
+    _bf16("v", v, (T, plan.Hkv, d), plan.device)
+    if q is not None:
+        if rotary is None:
+            raise ValueError("q is only rotated: it needs a rotary")
+        _bf16("q", q, (T, plan.Hq, d), plan.device)
+        q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else _bf16("q_out", q_out, q.shape,
+                                                                                      plan.device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if positions is not None:
+        A = rotary.naxes if rotary is not None else 0
+        if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous() \
+                or tuple(positions.shape) not in ([(T,), (1, T)] if A == 1 else [(A, T)]) \
+                or positions.device != plan.device:
+            raise ValueError("positions must be a contiguous int32 CUDA tensor [T], or [A, T] for several axes")
+    if rotary is not None and rotary.inv_freq.device != plan.device:
+        raise ValueError("rotary is on another device")
+    i = _dev_index(k)
+    r = lib().fa_paged_append(q.data_ptr() if q is not None else None, q_out.data_ptr() if q is not None else None,
+                              k.data_ptr(), v.data_ptr(), _strides((q, 2), (q_out, 2), (k, 2), (v, 2)),
+                              ctypes.byref(plan._cache(k_cache, v_cache)), plan._ref, rotary._ref if rotary is not None else None,
+                              positions.data_ptr() if positions is not None else None, T, plan._use(stream, i))
+    if r != FA_OK:
+        raise FAError(r, "fa_paged_append")
+    return q_out
+
+
+def forward_paged(q, k_cache, v_cache, plan, scale: float | None = None, out=None, lse=None, stream=None):
+    """O [T,Hq,d], LSE [T,Hq]: attention of a step's new tokens over the paged cache (fa_fwd_paged). q [T,Hq,d] bf16
+    CUDA, any strides with contiguous last dim. Rows that belong to no sequence are left as they were."""
+    T, Hq, d = plan.T, plan.Hq, plan.d
+    _bf16("q", q, (T, Hq, d), plan.device)
+    i = _dev_index(q)
+    o = out if out is not None else _empty((T, Hq, d), torch.bfloat16, q.device, stream)
+    l = lse if lse is not None else _empty((T, Hq), torch.float32, q.device, stream)
+    if out is not None and not _bf16("out", out, (T, Hq, d), plan.device).is_contiguous():
+        raise ValueError("out must be contiguous")
+    if lse is not None and (not l.is_cuda or l.dtype != torch.float32 or tuple(l.shape) != (T, Hq)
+                            or not l.is_contiguous() or l.device != plan.device):
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
+    r = lib().fa_fwd_paged(q.data_ptr(), _strides((q, 2)), ctypes.byref(plan._cache(k_cache, v_cache)), plan._ref,
+                           o.data_ptr(), l.data_ptr(), 0.0 if scale is None else float(scale), plan.workspace.data_ptr(),
+                           plan.ws_bytes, plan._use(stream, i))
+    if r != FA_OK:
+        raise FAError(r, "fa_fwd_paged")
+    return o, l
 
 
 def check(stream=None, device=None) -> None:
