@@ -360,12 +360,12 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, co
  *   q : [T][Hq][d] bf16; q_strides: HOST, (token, head) in elements, multiples of 8.
  *   o : [T][Hq][d] bf16 and lse: [T][Hq] fp32 (natural log), contiguous. A query that sees no key gets
  *       o = 0 and lse = -inf.
- *   workspace: >= fa_fwd_paged_workspace_bytes(d) bytes, 16-byte aligned; contents on entry do not
- *       matter.
+ *   workspace: >= fa_fwd_paged_workspace_bytes(batch) bytes (of Hq, Hkv, d and max_q alone), 16-byte
+ *       aligned; contents on entry do not matter.
  * Cache slots that no query of the sequence sees, and table entries for them, may hold anything. The
  * result does not depend on scheduling: the same call gives the same bits.
  */
-size_t fa_fwd_paged_workspace_bytes(int d);
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_batch *batch);
 int fa_fwd_paged(const void *q, const long long *q_strides, const fa_paged_cache *cache, const fa_paged_batch *batch,
                  void *o, float *lse, float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
 

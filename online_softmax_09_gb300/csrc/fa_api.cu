@@ -127,6 +127,12 @@ bool load_encoder() {
   return g_encode != nullptr;
 }
 
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 fa::tensor_map_encoder() { return load_encoder() ? g_encode : nullptr; }
+
+namespace {
+
 // 3-D map over a [planes][N][d] bf16 tensor; box = 64 columns (128 B, one swizzle span) x
 // box_rows rows (128 unless given) x 1 plane, 128-byte swizzle. Rows past N read as zero (loads)
 // or are not written (stores).

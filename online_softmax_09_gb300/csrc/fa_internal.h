@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
@@ -91,6 +92,9 @@ int check_current_device();
 
 // The same, with the device's status word and its number of SMs (each may be NULL).
 int device_state(uint32_t** status, int* num_sms);
+
+// cuTensorMapEncodeTiled, or NULL if the driver has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // The argument checks of fa_bwd that need no CUDA call (sizes, pointers): FA_OK or the status
 // fa_bwd would return for them.

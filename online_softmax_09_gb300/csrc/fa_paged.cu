@@ -473,9 +473,9 @@ static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) 
   return cudaGetLastError();
 }
 
-size_t paged_workspace_bytes(int d) { return plan_up((size_t)4 * kPagedSms * kRowTile * (d + 3) * 4); }
+size_t paged_rows_workspace_bytes(int d) { return plan_up((size_t)4 * kPagedSms * kRowTile * (d + 3) * 4); }
 
-cudaError_t launch_paged_fwd(const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
+cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
   num_sms = num_sms < kPagedSms ? num_sms : kPagedSms;
   return d == 128 ? launch_rows<128>(p, num_sms, st) : launch_rows<64>(p, num_sms, st);
 }

@@ -288,8 +288,20 @@ struct RopeLaunch {
 
 cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int d, int max_q, int pair_rows,
                               cudaStream_t st);
-size_t paged_workspace_bytes(int d);
-cudaError_t launch_paged_fwd(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
+size_t paged_rows_workspace_bytes(int d);
+cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
+
+struct TileMaps {
+  CUtensorMap q;     // [T][Hq][d], box 64 dims x G heads x 128 / G tokens
+  CUtensorMap k, v;  // [pages][Hkv][page_size][d], box 64 dims x min(page_size, 128) slots
+};
+size_t paged_tiles_workspace_bytes(int d);
+cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st);
+
+// Sequences with more rows (new tokens times heads per kv head) than this are worked off in pairs of
+// 128-row tiles; up to 16 rows they are one 16-row tile.
+constexpr int kPairRows = 16;
+inline int pair_rows_of(int G) { return G <= kTile ? kPairRows : 0x7fffffff; }
 cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, cudaStream_t st);
 
 }  // namespace fa

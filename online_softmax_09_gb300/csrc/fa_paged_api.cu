@@ -1,5 +1,7 @@
 // fa_paged_api.cu -- the C ABI of rotary positions, the paged cache and attention over it (include/fa.h):
 // argument checks and launches. Every check comes before any CUDA call.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <cstdint>
 
@@ -21,10 +23,11 @@ int check_ptr(const void* p, uintptr_t align) {
   return (reinterpret_cast<uintptr_t>(p) & (align - 1)) ? FA_ERR_ALIGN : FA_OK;
 }
 
-// Element strides of a 16-byte-chunked tensor; `written`: places of different indices must differ.
-int check_strides(const long long* s, const long long* extent, int n, bool written) {
+// Element strides of a 16-byte-chunked tensor; `distinct`: no stride may be 0 (a tensor that is written, or
+// that a tensor map describes).
+int check_strides(const long long* s, const long long* extent, int n, bool distinct) {
   for (int i = 0; i < n; ++i) {
-    if (s[i] < 0 || s[i] > (1LL << 46) || (written && extent[i] > 1 && s[i] == 0)) return FA_ERR_INVALID;
+    if (s[i] < 0 || s[i] > (1LL << 46) || (distinct && extent[i] > 1 && s[i] == 0)) return FA_ERR_INVALID;
     if (s[i] & 7) return FA_ERR_ALIGN;
   }
   return FA_OK;
@@ -102,13 +105,13 @@ int check_table(const fa_paged_batch* b) {
   return b->table_stride < 0 ? FA_ERR_INVALID : FA_OK;
 }
 
-int check_cache(const fa_paged_cache* c, const fa_paged_batch* b, bool written) {
+int check_cache(const fa_paged_cache* c, const fa_paged_batch* b) {
   if (c == nullptr || c->num_pages < 1) return FA_ERR_INVALID;
   FA_TRY(check_ptr(c->k, 16));
   FA_TRY(check_ptr(c->v, 16));
   const long long extent[3] = {c->num_pages, b->Hkv, b->page_size};
-  FA_TRY(check_strides(c->k_strides, extent, 3, written));
-  return check_strides(c->v_strides, extent, 3, written);
+  FA_TRY(check_strides(c->k_strides, extent, 3, true));
+  return check_strides(c->v_strides, extent, 3, true);
 }
 
 fa::PagedBatch device_batch(const fa_paged_batch* b, int num_pages, uint32_t* status) {
@@ -130,6 +133,37 @@ fa::PagedBatch device_batch(const fa_paged_batch* b, int num_pages, uint32_t* st
   x.pair_tokens = x.G <= 128 ? 2 * (128 / x.G) : 1;
   x.status = status;
   return x;
+}
+
+// Some sequence may have more rows than a 16-row tile: pairs of 128-row tiles are launched as well.
+bool with_pairs(const fa_paged_batch* b) {
+  const int G = b->Hq / b->Hkv;
+  return (long long)b->max_q * G > fa::pair_rows_of(G);
+}
+
+// Workspace: the partial results of the two kernels.
+size_t workspace_bytes(const fa_paged_batch* b) {
+  return fa::paged_rows_workspace_bytes(b->d) + (with_pairs(b) ? fa::paged_tiles_workspace_bytes(b->d) : 0);
+}
+
+// Tensor map of bf16 data with 128-byte swizzled boxes of 64 elements; `strides` in elements.
+int make_map(CUtensorMap* m, const void* base, int rank, const long long* dims, const long long* strides,
+             const int* box) {
+  const auto encode = fa::tensor_map_encoder();
+  if (encode == nullptr) return FA_ERR_LAUNCH;
+  cuuint64_t d[4], s[3];
+  cuuint32_t x[4], e[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    x[i] = (cuuint32_t)box[i];
+    e[i] = 1;
+    if (i > 0) s[i - 1] = (cuuint64_t)(strides[i - 1] > 0 ? strides[i - 1] : 8) * 2;  // 0: extent 1
+  }
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, x, e,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FA_OK
+             : FA_ERR_INVALID;
 }
 
 }  // namespace
@@ -160,8 +194,8 @@ int fa_paged_plan(const int* cu_q, const int* kv_len, const fa_paged_batch* batc
   if (batch->S > 0) FA_TRY(check_ptr(kv_len, 4));
   uint32_t* status = nullptr;
   FA_TRY(fa::device_state(&status, nullptr));
-  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status), batch->d, batch->max_q, 0x7fffffff,
-                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status), batch->d, batch->max_q,
+                               fa::pair_rows_of(batch->Hq / batch->Hkv), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_LAUNCH;
 }
@@ -180,7 +214,7 @@ int fa_paged_append(const void* q, void* q_out, const void* k, const void* v, co
   } else if (with_q || positions != nullptr) {
     return FA_ERR_INVALID;
   }
-  FA_TRY(check_cache(cache, batch, true));
+  FA_TRY(check_cache(cache, batch));
   if (batch->S == 0 || batch->T == 0) return FA_OK;
   FA_TRY(check_table(batch));
   const void* ptr[4] = {q, q_out, k, v};
@@ -215,15 +249,20 @@ int fa_paged_append(const void* q, void* q_out, const void* k, const void* v, co
                                                                                                   : FA_ERR_LAUNCH;
 }
 
-size_t fa_fwd_paged_workspace_bytes(int d) { return check_d(d) == FA_OK ? fa::paged_workspace_bytes(d) : 0; }
+size_t fa_fwd_paged_workspace_bytes(const fa_paged_batch* batch) {
+  if (batch == nullptr || batch->Hq < 1 || batch->Hkv < 1 || batch->Hq % batch->Hkv != 0 || batch->max_q < 0 ||
+      check_d(batch->d) != FA_OK)
+    return 0;
+  return workspace_bytes(batch);
+}
 
 int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache* cache, const fa_paged_batch* batch,
                  void* o, float* lse, float scale, void* workspace, size_t workspace_bytes, fa_stream_t stream) {
   fa::TraceRange trace("fa_fwd_paged");
   FA_TRY(check_batch(batch));
   if (q_strides == nullptr) return FA_ERR_INVALID;
-  FA_TRY(check_cache(cache, batch, false));
-  if (workspace == nullptr || workspace_bytes < fa::paged_workspace_bytes(batch->d)) return FA_ERR_WORKSPACE;
+  FA_TRY(check_cache(cache, batch));
+  if (workspace == nullptr || workspace_bytes < ::workspace_bytes(batch)) return FA_ERR_WORKSPACE;
   FA_TRY(check_ptr(workspace, 16));
   if (batch->S == 0 || batch->T == 0) return FA_OK;
   FA_TRY(check_table(batch));
@@ -231,7 +270,7 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   FA_TRY(check_ptr(o, 16));
   FA_TRY(check_ptr(lse, 4));
   const long long extent[2] = {batch->T, batch->Hq};
-  FA_TRY(check_strides(q_strides, extent, 2, false));
+  FA_TRY(check_strides(q_strides, extent, 2, true));
   uint32_t* status = nullptr;
   int num_sms = 0;
   FA_TRY(fa::device_state(&status, &num_sms));
@@ -253,9 +292,23 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   p.part = static_cast<float*>(workspace);
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt((float)batch->d);
   p.scale_log2 = s * 1.4426950408889634f;
-  return fa::launch_paged_fwd(p, batch->d, num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FA_OK
-             : FA_ERR_LAUNCH;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (with_pairs(batch)) {
+    fa::TileMaps m;
+    const int d = batch->d;
+    const long long qd[3] = {d, batch->Hq, batch->T}, qs[2] = {q_strides[1], q_strides[0]};
+    const int qb[3] = {64, p.b.G, p.b.pair_tokens / 2};
+    FA_TRY(make_map(&m.q, q, 3, qd, qs, qb));
+    const long long cd[4] = {d, batch->page_size, batch->Hkv, cache->num_pages};
+    const long long ks[3] = {p.c.k_tok, p.c.k_head, p.c.k_page}, vs[3] = {p.c.v_tok, p.c.v_head, p.c.v_page};
+    const int cb[4] = {64, batch->page_size < 128 ? batch->page_size : 128, 1, 1};
+    FA_TRY(make_map(&m.k, cache->k, 4, cd, ks, cb));
+    FA_TRY(make_map(&m.v, cache->v, 4, cd, vs, cb));
+    fa::PagedFwd pt = p;
+    pt.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + fa::paged_rows_workspace_bytes(d));
+    if (fa::launch_paged_tiles(m, pt, d, num_sms, st) != cudaSuccess) return FA_ERR_LAUNCH;
+  }
+  return fa::launch_paged_rows(p, batch->d, num_sms, st) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

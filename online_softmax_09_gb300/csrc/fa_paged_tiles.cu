@@ -1,0 +1,617 @@
+// fa_paged_tiles.cu -- attention of chunks of new tokens over a paged cache, on the tensor cores' own
+// memory: pairs of 128-row tiles against 128-key blocks with tcgen05 (the mathematics, the plan and the
+// division among CTAs are in fa_paged.cu and fa_paged.cuh).
+//
+// A row is one query head of one new token; a tile's rows are 128 / G tokens times the G heads that
+// share a kv head, so short chunks fill a tile and each key block is loaded once for all of them. One
+// CTA per SM works off its stretch of the plan's units:
+//   warp 8     TMA producer: the pair's queries, then per block the keys and values, one box per page
+//              (lane i brings page i of the block; the table entries of the next block are read ahead).
+//              Boxes of pages that no row sees are zero-filled without looking at the table.
+//   warp 9     MMA issue: S_t = Q_t K^T, O_t += P_t V, the two tiles taking turns.
+//   warps 0-7  softmax, one row per thread, four warps per tile: running max and sum in base 2, the
+//              reference max moved only when a row outgrows it by 2^8, P as bf16 over the scores'
+//              columns, and the rounding of each tile's largest weight carried along as in the dense
+//              forward, so that o is not off where one key dominates.
+// Slots of the last page past the sequence hold anything, NaN too, and 0 * NaN is NaN: the rows of V
+// past the last key are set to zero in shared memory before the product.
+// A pair that several CTAs share leaves unnormalised sums in the workspace, columns first so that the
+// threads of a warp write neighbours; the tile's last CTA joins them in the order of the keys.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "fa_paged.cuh"
+
+namespace fa {
+
+constexpr int kTileThreads = 320;
+constexpr uint32_t kTileTmemCols = 512;
+constexpr float kTileRescale = 8.f;
+
+template <int D>
+struct TileSmem {
+  static constexpr int NK = D == 128 ? 2 : 4, NV = NK;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTileBytes;
+  static constexpr int kV = kK + NK * kTileBytes;
+  static constexpr int kOStage = kV + NV * kTileBytes;  // 4 KB per softmax warp: 32 rows x 64 columns
+  static constexpr int kBar = kOStage + 8 * 4096;
+  static constexpr int bQ = 0;
+  static constexpr int bKFull = bQ + 2;
+  static constexpr int bKEmpty = bKFull + NK;
+  static constexpr int bVFull = bKEmpty + NK;
+  static constexpr int bVEmpty = bVFull + NV;
+  static constexpr int bSFull = bVEmpty + NV;
+  static constexpr int bPFull = bSFull + 2;
+  static constexpr int bOFull = bPFull + 2;
+  static constexpr int bQEmpty = bOFull + 2;
+  static constexpr int bOFree = bQEmpty + 2;
+  static constexpr int bDrain = bOFree + 2;
+  static constexpr int kNumBars = bDrain + 1;
+  static constexpr int kTmemSlot = kBar + kNumBars * 8;
+  static constexpr int kAbort = kTmemSlot + 4;
+  static constexpr int kFlag = kAbort + 4;  // one word per tile: this CTA joins the tile
+  static constexpr int kBytes = kFlag + 8;
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+// One partial result of a CTA: per tile of the pair, o [D][128] and m, l, e [128].
+constexpr int tile_part(int D) { return 2 * kTile * (D + 3); }
+
+// The blocks that each tile of a stretch's pair has work in, relative to block j0.
+struct TileItem {
+  int j0, n_max;
+  int a[2], b[2];
+  bool exists[2];
+};
+
+__device__ __forceinline__ TileItem tile_item(const Seg& s, const PagedBatch& p) {
+  TileItem it;
+  const int tpt = p.pair_tokens >> 1;
+  int lo[2], hi[2];
+  bool any = false;
+  it.j0 = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int t0 = s.t0 + t * tpt;
+    it.exists[t] = t0 < s.ql;
+    lo[t] = hi[t] = 0;
+    if (!it.exists[t]) continue;
+    int k0, k1;
+    key_range(t0, min(t0 + tpt, s.ql) - 1, s.ql, s.kvl, p.causal, p.window, k0, k1);
+    lo[t] = max(k0 / kPairBlk, s.blk);
+    hi[t] = min((k1 + kPairBlk - 1) / kPairBlk, s.blk + s.n);
+    if (k1 <= k0 || hi[t] < lo[t]) hi[t] = lo[t];
+    if (hi[t] > lo[t]) {
+      it.j0 = any ? min(it.j0, lo[t]) : lo[t];
+      any = true;
+    }
+  }
+  it.n_max = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.a[t] = hi[t] > lo[t] ? lo[t] - it.j0 : 0;
+    it.b[t] = hi[t] > lo[t] ? hi[t] - it.j0 : 0;
+    it.n_max = max(it.n_max, it.b[t]);
+  }
+  return it;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+__device__ __forceinline__ void group_sync(int id) {  // the 128 threads of one tile
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+
+__device__ __forceinline__ float max64f(const uint32_t (&a)[32], const uint32_t (&b)[32], float init) {
+  float m[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    m[k] = max3f(__uint_as_float(a[k]), __uint_as_float(a[k + 8]), __uint_as_float(a[k + 16]));
+    m[k] = max3f(m[k], __uint_as_float(a[k + 24]), __uint_as_float(b[k]));
+    m[k] = max3f(m[k], __uint_as_float(b[k + 8]), __uint_as_float(b[k + 16]));
+    m[k] = fmaxf(m[k], __uint_as_float(b[k + 24]));
+  }
+  return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), max3f(m[6], m[7], init));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const PagedFwd p) {
+  using L = TileSmem<D>;
+  constexpr int NK = L::NK, NV = L::NV;
+  const PagedBatch& b = p.b;
+  if (!plan_matches(b, D)) {
+    if (threadIdx.x == 0) record_index_error(b.status);
+    return;
+  }
+  {
+    const long long W = b.plan.units[1][b.S];
+    if ((W + gridDim.x - 1) / gridDim.x * blockIdx.x >= W) return;  // no work for this CTA
+  }
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
+  volatile int* join_flag = reinterpret_cast<volatile int*>(smem + L::kFlag);
+  const Ctl ctl{abort_flag, b.status};
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tpt = b.pair_tokens >> 1;  // tokens per tile; rows tpt * G .. 127 are unused
+  const int used = tpt * b.G;
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(L::bQ + t), 1);
+      mbar_init(bar(L::bSFull + t), 1);
+      mbar_init(bar(L::bPFull + t), 128);
+      mbar_init(bar(L::bOFull + t), 1);
+      mbar_init(bar(L::bQEmpty + t), 1);
+      mbar_init(bar(L::bOFree + t), 128);
+    }
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(bar(L::bKFull + s), 1);
+      mbar_init(bar(L::bKEmpty + s), 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(bar(L::bVFull + s), 1);
+      mbar_init(bar(L::bVEmpty + s), 1);
+    }
+    mbar_init(bar(L::bDrain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // Rows that no load fills are zero, so that their scores are.
+  for (int i = threadIdx.x; i < 2 * (D / 64) * (kTile - used) * 8; i += kTileThreads) {
+    const int part = i / ((kTile - used) * 8), at = i - part * ((kTile - used) * 8);
+    st_shared_v4(sQ + part * 16384 + used * 128 + at * 16, 0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), kTileTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  SegIter<true> walk(b);
+  Seg s;
+  if (warp == 8) {
+    // ------------------------------------------------------------------ TMA producer
+    const int box = b.page_size < kPairBlk ? b.page_size : kPairBlk;  // keys of one box
+    const int nbox = kPairBlk / box;
+    const uint32_t q_bytes = (uint32_t)used * D * 2;
+    uint32_t gk = 0, gv = 0, qn[2] = {0, 0};
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const TileItem it = tile_item(s, b);
+      if (it.n_max == 0) continue;
+      int lo, hi;
+      key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
+      const int* tab = b.table + (long long)s.seq * b.table_stride;
+      // The page of this lane's box of block j, num_pages (beyond the map: zeros) where nothing is seen.
+      auto page_of = [&](int j) -> int {
+        const int key = (it.j0 + j) * kPairBlk + lane * box;
+        if (lane >= nbox || key >= hi || key + box <= lo) return b.num_pages;
+        const int pg = tab[key >> b.page_shift];
+        if ((unsigned)pg < (unsigned)b.num_pages) return pg;
+        record_index_error(b.status);
+        return b.num_pages;
+      };
+      int page = page_of(0);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || it.b[t] == it.a[t]) continue;
+        if (!(ok = mbar_wait_warp(bar(L::bQEmpty + t), (qn[t] & 1) ^ 1, ctl))) continue;
+        if (lane == 0) {
+          mbar_expect_tx(bar(L::bQ + t), q_bytes);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sQ + t * L::kTileBytes + c * 16384, &tm_q, bar(L::bQ + t), c * 64, s.head * b.G,
+                        s.q0 + s.t0 + t * tpt);
+        }
+        ++qn[t];
+      }
+      for (int j = 0; ok && j < it.n_max; ++j) {
+        const int slot = ((it.j0 + j) * kPairBlk + lane * box) & (b.page_size - 1);
+        const int pg = page;
+        if (j + 1 < it.n_max) page = page_of(j + 1);
+        const uint32_t sk = gk % NK, sv = gv % NV;
+        if (!(ok = mbar_wait_warp(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
+        if (lane == 0) mbar_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
+        __syncwarp();
+        if (lane < nbox) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sK + sk * L::kTileBytes + c * 16384 + lane * box * 128, &tm_k, bar(L::bKFull + sk), c * 64, slot,
+                        s.head, pg);
+        }
+        ++gk;
+        if (!(ok = mbar_wait_warp(bar(L::bVEmpty + sv), ((gv / NV) & 1) ^ 1, ctl))) break;
+        if (lane == 0) mbar_expect_tx(bar(L::bVFull + sv), L::kTileBytes);
+        __syncwarp();
+        if (lane < nbox) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sV + sv * L::kTileBytes + c * 16384 + lane * box * 128, &tm_v, bar(L::bVFull + sv), c * 64, slot,
+                        s.head, pg);
+        }
+        ++gv;
+      }
+    }
+    if (*abort_flag && lane == 0) {  // every copy in flight lands before shared memory is freed
+      for (int t = 0; t < 2; ++t)
+        if (qn[t] > 0) drain_wait(bar(L::bQ + t), (qn[t] - 1) & 1);
+      for (uint32_t g = gk > NK ? gk - NK : 0; g < gk; ++g) drain_wait(bar(L::bKFull + g % NK), (g / NK) & 1);
+      for (uint32_t g = gv > NV ? gv - NV : 0; g < gv; ++g) drain_wait(bar(L::bVFull + g % NV), (g / NV) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ MMA issue
+    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
+    const uint64_t dQ = sdesc_sw128(sQ, 16, 1024);
+    const uint64_t dK = sdesc_sw128(sK, 16, 1024);
+    const uint64_t dV = sdesc_sw128(sV, 16384, 1024);
+    uint32_t gk = 0, gv = 0, qn[2] = {0, 0}, pc[2] = {0, 0};
+    auto commit = [&](uint32_t x) {
+      if (elect_one()) mma_commit(x);
+      __syncwarp();
+    };
+    auto issue_s = [&](int t, uint32_t g, bool ready) -> bool {
+      const uint32_t sk = g % NK;
+      if (!ready && !mbar_wait_warp(bar(L::bKFull + sk), (g / NK) & 1, ctl)) return false;
+      tc_fence_after();
+      const uint64_t a = dQ + (uint32_t)(t * (L::kTileBytes >> 4));
+      const uint64_t bk = dK + sk * (uint32_t)(L::kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + 128 * t, a + off, bk + off, idS, kk > 0);
+        }
+        mma_commit(bar(L::bSFull + t));
+      }
+      __syncwarp();
+      return true;
+    };
+    auto issue_pv = [&](int t, uint32_t g, bool first, bool last, bool ready) -> bool {
+      const uint32_t sv = g % NV;
+      if (!mbar_wait_warp(bar(L::bPFull + t), pc[t] & 1, ctl)) return false;
+      if (!ready && !mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
+      if (first && qn[t] > 1 && !mbar_wait_warp(bar(L::bOFree + t), (qn[t] - 2) & 1, ctl)) return false;
+      tc_fence_after();
+      const uint64_t bv = dV + sv * (uint32_t)(L::kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + kk * 8, bv + (uint32_t)(kk * (2048 >> 4)), idO,
+                 (!first || kk > 0));
+        if (last) mma_commit(bar(L::bOFull + t));
+      }
+      __syncwarp();
+      ++pc[t];
+      return true;
+    };
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const TileItem it = tile_item(s, b);
+      if (it.n_max == 0) continue;
+      bool k_ready = false;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || it.b[t] == it.a[t]) continue;
+        if (!(ok = mbar_wait_warp(bar(L::bQ + t), qn[t] & 1, ctl))) continue;
+        ++qn[t];
+        tc_fence_after();
+        if (it.a[t] == 0) {
+          if (!(ok = issue_s(t, gk, k_ready))) continue;
+          k_ready = true;
+          if (it.b[t] == 1) commit(bar(L::bQEmpty + t));
+        }
+      }
+      if (!ok) break;
+      commit(bar(L::bKEmpty + gk % NK));
+      for (int j = 0; ok && j < it.n_max; ++j) {
+        bool v_ready = false, k_next_ready = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (ok && it.a[t] <= j && j < it.b[t]) {
+            if (!(ok = issue_pv(t, gv + j, j == it.a[t], j + 1 == it.b[t], v_ready))) continue;
+            v_ready = true;
+          }
+          if (ok && it.a[t] <= j + 1 && j + 1 < it.b[t]) {
+            if (!(ok = issue_s(t, gk + j + 1, k_next_ready))) continue;
+            k_next_ready = true;
+            if (j + 2 == it.b[t]) commit(bar(L::bQEmpty + t));
+          }
+        }
+        if (!ok) break;
+        commit(bar(L::bVEmpty + (gv + j) % NV));
+        if (j + 1 < it.n_max) commit(bar(L::bKEmpty + (gk + j + 1) % NK));
+      }
+      gk += it.n_max;
+      gv += it.n_max;
+    }
+    if (*abort_flag) {
+      if (elect_one()) {
+        mma_commit(bar(L::bDrain));
+        drain_wait(bar(L::bDrain), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;  // row within the tile
+    const int r_tok = r / b.G, r_head = r - r_tok * b.G;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + 128 * t + lane_off;
+    const uint32_t tO = tmem + 256 + 128 * t + lane_off;
+    const float sl2 = p.scale_log2;
+    const uint32_t o_stage = sbase + L::kOStage + (uint32_t)warp * 4096;
+    uint32_t sc = 0, on = 0, gv = 0;
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const TileItem it = tile_item(s, b);
+      const uint32_t gv0 = gv;
+      gv += it.n_max;
+      if (!(t ? it.exists[1] : it.exists[0])) continue;
+      const int a_t = t ? it.a[1] : it.a[0];
+      const int n_kv = (t ? it.b[1] : it.b[0]) - a_t;
+      const int tok0 = s.t0 + t * tpt;
+      const int tok = tok0 + r_tok;
+      const bool valid = r < used && tok < s.ql;
+      const int pos = s.kvl - s.ql + tok;
+      const int klim = min(s.kvl - 1, b.causal ? pos : s.kvl - 1);
+      const int klo = b.window > 0 ? pos - b.window + 1 : 0;
+      const int pos0 = s.kvl - s.ql + tok0, pos1 = pos0 + tpt - 1;
+      float m_run = -INFINITY, m_hi = -INFINITY, l_run = 0.f, e_run = 0.f;
+      for (int j = 0; j < n_kv; ++j) {
+        if (!mbar_wait_warp(bar(L::bSFull + t), (sc + j) & 1, ctl)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int kv0 = (it.j0 + a_t + j) * kPairBlk;
+        const bool tail = kv0 + kPairBlk > s.kvl;
+        const bool need_mask = tail || (b.causal && kv0 + kPairBlk - 1 > pos0) ||
+                               (b.window > 0 && kv0 < pos1 - b.window + 1);
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c]);
+        if (need_mask) {
+          const int lim = klim - kv0, lo = klo - kv0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i > lim || c * 32 + i < lo) sr[c][i] = 0xff800000u;
+        }
+        const float mx = max64f(sr[2], sr[3], max64f(sr[0], sr[1], -INFINITY));
+        const float mt = mx * sl2;
+        m_hi = fmaxf(m_hi, mt);
+        const bool resc = __any_sync(0xffffffffu, m_hi > m_run + kTileRescale);
+        const float m_new = resc ? m_hi : m_run;
+        const float corr = (m_new > m_run) ? ex2(m_run - m_new) : 1.f;
+        m_run = m_new;
+        const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
+        {
+          const float pmx = ex2(fmaf(mx, sl2, -m_use));
+          e_run = e_run * corr + (__uint_as_float(pack_bf16(pmx, 0.f) << 16) - pmx);
+        }
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sl2x2 = make_float2(sl2, sl2), negm = make_float2(-m_use, -m_use);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 x = fma2(make_float2(__uint_as_float(sr[c][i]), __uint_as_float(sr[c][i + 1])), sl2x2, negm);
+            const float2 pp = make_float2(ex2(x.x), ex2(x.y));
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], pp);
+            pk[i >> 1] = pack_bf16(pp.x, pp.y);
+          }
+          tmem_st16(tS + c * 16, pk);
+        }
+        if (j > 0 && resc) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                    make_float2(corr, corr));
+              o[i] = __float_as_uint(v.x);
+              o[i + 1] = __float_as_uint(v.y);
+            }
+            tmem_st32(tO + c * 32, o);
+          }
+        }
+        l_run = l_run * corr + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
+        if (tail) {
+          // Rows of V past the last key (both tiles may write the same zeros): after the copy has
+          // landed, before the product that the arrival below lets start.
+          const uint32_t g = gv0 + a_t + j, sv = g % NV;
+          if (!mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) {
+            ok = false;
+            break;
+          }
+          for (int row = s.kvl - kv0 + (r >> 3); row < kPairBlk; row += 16)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              st_shared_v4(sV + sv * L::kTileBytes + c * 16384 + row * 128 + (r & 7) * 16, 0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(L::bPFull + t));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------------- epilogue
+      if (n_kv > 0) {
+        if (!(ok = mbar_wait_warp(bar(L::bOFull + t), on & 1, ctl))) break;
+        ++on;
+        sc += n_kv;
+        tc_fence_after();
+      }
+      float inv = 0.f;
+      bool write = true;
+      uint4 w[D / 32][4];
+      auto pack = [&](int c, const float* f, float x) {
+        uint32_t* wp = reinterpret_cast<uint32_t*>(w[c]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) wp[i] = pack_bf16(f[2 * i] * x, f[2 * i + 1] * x);
+      };
+      if (s.first && s.last) {
+        const float z = l_run + e_run;
+        inv = (l_run > 0.f || l_run != l_run) ? 1.f / z : 0.f;  // a row that sees nothing: o = 0
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (n_kv > 0) {
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+          pack(c, reinterpret_cast<const float*>(o), inv);
+        }
+        if (n_kv > 0) {
+          tc_fence_before();
+          mbar_arrive(bar(L::bOFree + t));
+        }
+      } else {
+        const int c0 = walk.owner(s.u0), c1 = walk.owner(s.u1 - 1);
+        float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3) + r;
+        if (n_kv > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) slot[(c * 32 + i) * kTile] = __uint_as_float(o[i]);
+          }
+          tc_fence_before();
+          mbar_arrive(bar(L::bOFree + t));
+        }
+        slot[D * kTile] = m_run;  // -inf: nothing seen here, and o is not there
+        slot[(D + 1) * kTile] = l_run;
+        slot[(D + 2) * kTile] = e_run;
+        __threadfence();
+        group_sync(1 + t);
+        if (r == 0) {
+          uint32_t* cnt = &b.plan.counters[1][2 * c0 + t];
+          const bool last = atomicAdd(cnt, 1u) == (uint32_t)(c1 - c0);
+          if (last) *cnt = 0;
+          __threadfence();
+          join_flag[t] = last;
+        }
+        group_sync(1 + t);
+        write = join_flag[t] != 0;
+        if (write) {
+          auto part = [&](int c) {
+            return p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3) + r;
+          };
+          m_run = -INFINITY;
+          for (int c = c0; c <= c1; ++c) m_run = fmaxf(m_run, __ldcg(part(c) + D * kTile));
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+          l_run = e_run = 0.f;
+          for (int c = c0; c <= c1; ++c) {
+            const float f = ex2(__ldcg(part(c) + D * kTile) - mu);
+            l_run += f * __ldcg(part(c) + (D + 1) * kTile);
+            e_run += f * __ldcg(part(c) + (D + 2) * kTile);
+          }
+          inv = (l_run > 0.f || l_run != l_run) ? 1.f / (l_run + e_run) : 0.f;
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            float acc[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+            for (int c = c0; c <= c1; ++c) {
+              const float mi = __ldcg(part(c) + D * kTile);
+              if (mi == -INFINITY) continue;
+              const float f = ex2(mi - mu);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) acc[i] = fmaf(f, __ldcg(part(c) + (k * 32 + i) * kTile), acc[i]);
+            }
+            pack(k, acc, inv);
+          }
+        }
+      }
+      if (write) {
+        // Through this warp's buffer, so that eight lanes write 128 neighbouring bytes of a row.
+        const long long out = valid ? (long long)(s.q0 + tok) * b.Hq + s.head * b.G + r_head : -1;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const uint4 v4 = w[2 * c + (g >> 2)][g & 3];
+            st_shared_v4(o_stage + (uint32_t)lane * 128 + ((g ^ (lane & 7)) << 4), v4.x, v4.y, v4.z, v4.w);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3), g = lane & 7;
+            const long long ro = __shfl_sync(0xffffffffu, out, row);
+            const uint4 v4 = *reinterpret_cast<const uint4*>(smem + L::kOStage + warp * 4096 + row * 128 +
+                                                             ((g ^ (row & 7)) << 4));
+            if (ro >= 0) *reinterpret_cast<uint4*>(p.o + ro * D + c * 64 + g * 8) = v4;
+          }
+        }
+        if (valid) p.lse[out] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTileTmemCols);
+  }
+}
+
+template <int D>
+static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, int num_sms, cudaStream_t st) {
+  constexpr int smem = TileSmem<D>::kAlloc;
+  static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-CTA limit");
+  cudaError_t e = cudaFuncSetAttribute(fa_paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  fa_paged_tiles_kernel<D><<<num_sms, kTileThreads, smem, st>>>(m.q, m.k, m.v, p);
+  return cudaGetLastError();
+}
+
+size_t paged_tiles_workspace_bytes(int d) { return plan_up((size_t)2 * kPagedSms * tile_part(d) * 4); }
+
+cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
+  num_sms = num_sms < kPagedSms ? num_sms : kPagedSms;
+  return d == 128 ? launch_tiles<128>(m, p, num_sms, st) : launch_tiles<64>(m, p, num_sms, st);
+}
+
+}  // namespace fa

@@ -102,7 +102,7 @@ def lib() -> ctypes.CDLL:
         L.fa_paged_plan.restype = _i
         L.fa_paged_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ll, _vp]
         L.fa_paged_append.restype = _i
-        L.fa_fwd_paged_workspace_bytes.argtypes = [_i]
+        L.fa_fwd_paged_workspace_bytes.argtypes = [_vp]
         L.fa_fwd_paged_workspace_bytes.restype = ctypes.c_size_t
         L.fa_fwd_paged.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, ctypes.c_size_t, _vp]
         L.fa_fwd_paged.restype = _i
@@ -500,12 +500,12 @@ class PagedPlan:
         self.key = (S, T, max_q, max_pages, page_size, Hq, Hkv, d, causal, window, device)
         self.T, self.Hq, self.Hkv, self.d, self.page_size, self.device = T, Hq, Hkv, d, page_size, device
         self.buffer = _empty(int(L.fa_paged_plan_bytes(S)), torch.uint8, device, stream)
-        self.ws_bytes = int(L.fa_fwd_paged_workspace_bytes(d))
-        self.workspace = _empty(max(self.ws_bytes, 16), torch.uint8, device, stream)
         self.home = _stream_of(stream, device.index)
         self._c = _Batch(None, 0, self.buffer.data_ptr(), self.buffer.numel(), S, T, max_q, max_pages, page_size, Hq,
                          Hkv, d, causal, window)
         self._ref = ctypes.addressof(self._c)
+        self.ws_bytes = int(L.fa_fwd_paged_workspace_bytes(self._ref))
+        self.workspace = _empty(max(self.ws_bytes, 16), torch.uint8, device, stream)
 
     def _use(self, stream, index):
         """The raw stream of a call; the buffers outlive their use on a stream that they were not made on."""

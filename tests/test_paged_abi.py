@@ -91,8 +91,10 @@ def test_plan_refusals_and_sizes(fa):
     assert L.fa_paged_plan_bytes(1000) > L.fa_paged_plan_bytes(10)
     short = _batch(fa, S=1000, plan_bytes=L.fa_paged_plan_bytes(1000) - 1)
     assert L.fa_paged_plan(P, P, ctypes.byref(short), None) == -6
-    assert L.fa_fwd_paged_workspace_bytes(96) == 0
-    assert L.fa_fwd_paged_workspace_bytes(128) > L.fa_fwd_paged_workspace_bytes(64) > 0
+    ws = lambda **kw: L.fa_fwd_paged_workspace_bytes(ctypes.byref(_batch(fa, **kw)))
+    assert ws(d=96) == 0 and ws(Hq=3) == 0 and ws(max_q=-1) == 0 and L.fa_fwd_paged_workspace_bytes(None) == 0
+    assert ws(d=128) > ws(d=64) > 0
+    assert ws(max_q=100) > ws(max_q=1)  # chunks need room for larger partial results
 
 
 BAD_CACHE = [({"k": None}, -1), ({"v": None}, -1), ({"k": P + 8}, -3), ({"v": P + 2}, -3), ({"pages": 0}, -1),
@@ -132,7 +134,7 @@ def test_append_refusals(fa):
 
 def test_attention_refusals(fa):
     L, b, c = fa.lib(), _batch(fa), _cache(fa)
-    need = L.fa_fwd_paged_workspace_bytes(128)
+    need = L.fa_fwd_paged_workspace_bytes(ctypes.byref(b))
 
     def call(q=P, st=(512, 128), cache=c, batch=b, o=P, lse=P, ws=P, n=need):
         return L.fa_fwd_paged(q, _ll(*st) if st else None, ctypes.byref(cache), ctypes.byref(batch), o, lse, 0.0, ws, n,
