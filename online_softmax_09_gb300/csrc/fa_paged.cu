@@ -159,6 +159,71 @@ struct RowSmem {
 template <int D>
 constexpr int kRowPart = kRowTile * (D + 3);
 
+// The pairs of 128-row tiles that several CTAs of the kernel before shared: their partial results joined
+// in the order of the keys, 16 rows at a time, all of this grid's CTAs together. (Joined by the last CTA
+// to finish each tile, on 64 of 152 SMs, this took 18 us at 512 tokens over 32768 keys; here 6.)
+template <int D>
+__device__ __forceinline__ void join_pairs(const PagedFwd& p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before is complete
+  const PagedBatch& b = p.b;
+  const int tpt = b.pair_tokens >> 1, used = tpt * b.G;
+  const int units = p.tile_ctas * 2 * (kTile / 16);
+  for (int x = blockIdx.x; x < units; x += gridDim.x) {
+    const int c0 = x >> 4, t = (x >> 3) & 1;
+    const TileShare s = p.share[2 * c0 + t];
+    const int r = (x & 7) * 16 + (threadIdx.x & 15);
+    const int tok = s.tok0 + r / b.G;
+    if (s.c1 < 0 || r >= used || tok >= s.ql) continue;
+    auto part = [&](int c) {
+      return p.tile_part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
+    };
+    const int g0 = threadIdx.x >> 4;  // columns 4 * (g0 + 8 i) ..
+    float M = -INFINITY, Ls = 0.f, Es = 0.f, acc[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) acc[i] = 0.f;
+    for (int c = c0; c <= s.c1; c += 2) {
+      float4 v[2][D / 32];
+      float mi[2], li[2], ei[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {  // two results' loads together
+        const float* src = part(min(c + y, s.c1));
+        mi[y] = src[D * kTile + r];
+        li[y] = src[(D + 1) * kTile + r];
+        ei[y] = src[(D + 2) * kTile + r];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          v[y][i] = *reinterpret_cast<const float4*>(src + ((g0 + 8 * i) * kTile + r) * 4);
+      }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if (c + y > s.c1 || mi[y] == -INFINITY) continue;  // nothing seen there: o was not written
+        const float mn = fmaxf(M, mi[y]);
+        const float fa = ex2(M - mn), fb = ex2(mi[y] - mn);
+        M = mn;
+        Ls = Ls * fa + fb * li[y];
+        Es = Es * fa + fb * ei[y];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          acc[4 * i] = acc[4 * i] * fa + fb * v[y][i].x;
+          acc[4 * i + 1] = acc[4 * i + 1] * fa + fb * v[y][i].y;
+          acc[4 * i + 2] = acc[4 * i + 2] * fa + fb * v[y][i].z;
+          acc[4 * i + 3] = acc[4 * i + 3] * fa + fb * v[y][i].w;
+        }
+      }
+    }
+    const float inv = (Ls > 0.f || Ls != Ls) ? 1.f / (Ls + Es) : 0.f;
+    const long long out = (long long)(s.q0 + tok) * b.Hq + s.head * b.G + r % b.G;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint2 w;
+      w.x = pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv);
+      w.y = pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
+      *reinterpret_cast<uint2*>(p.o + out * D + (g0 + 8 * i) * 4) = w;
+    }
+    if (g0 == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
+  }
+}
+
 // fa_paged_rows_kernel: tiles of 16 rows. Four warps per CTA, two CTAs per SM; each warp takes every
 // fourth granule of 16 keys with a ring of its own, so no barrier stands in the loop: it waits for its
 // own cp.async copies, forms the 16 x 16 scores (m16n8k16), carries its own running max and sums, and
@@ -180,8 +245,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
   float* stat = reinterpret_cast<float*>(smem + L::kStat);
   int* flag = reinterpret_cast<int*>(smem + L::kFlag);
   const PagedBatch& b = p.b;
+  SegIter<false> it(b);  // (its loads and the plan's check go out together)
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
+    if (p.tile_ctas > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   // Copies: this lane's row and chunk within a group of rows, and its swizzled place.
@@ -191,7 +258,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
   const int vrow = lane & 15, vchk = lane >> 4;                              // V: keys 0-15, chunk 0 | 1
   const int g = lane >> 2, c2 = (lane & 3) * 2;                              // rows g, g + 8; columns c2, c2 + 1
 
-  SegIter<false> it(b);
   Seg s;
   while (it.next(s)) {
     const int G = b.G;
@@ -399,7 +465,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
     bool write = true;
     if (!(s.first && s.last)) {
       // A tile that other CTAs share: leave the partial result; the last of them to arrive joins all.
-      const int c0 = it.owner(s.u0), c1 = it.owner(s.u1 - 1);
+      const int c0 = s.c0, c1 = s.c1;
       float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * kRowPart<D>;
       if (row < rows) {
 #pragma unroll
@@ -462,6 +528,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
     }
     __syncthreads();  // the rings and `stat` are free for the next stretch
   }
+  if (p.tile_ctas > 0) join_pairs<D>(p);
 }
 
 template <int D>
@@ -469,14 +536,23 @@ static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) 
   constexpr int smem = RowSmem<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(fa_paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  fa_paged_rows_kernel<D><<<2 * num_sms, kRowThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * num_sms);
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  // After the pairs' kernel: start on the SMs that it leaves free (what is read of it comes after a wait).
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = p.tile_ctas > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fa_paged_rows_kernel<D>, p);
 }
 
 size_t paged_rows_workspace_bytes(int d) { return plan_up((size_t)4 * kPagedSms * kRowTile * (d + 3) * 4); }
 
 cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
-  num_sms = num_sms < kPagedSms ? num_sms : kPagedSms;
   return d == 128 ? launch_rows<128>(p, num_sms, st) : launch_rows<64>(p, num_sms, st);
 }
 

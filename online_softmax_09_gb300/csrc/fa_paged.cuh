@@ -133,56 +133,69 @@ struct Seg {
   int t0, t1;      // tokens of the tile
   int blk, n;      // key blocks [blk, blk + n) of this stretch
   bool first, last;  // holds the tile's first / last block (both: no other CTA shares the tile)
-  long long u0, u1;  // the tile's units [u0, u1)
+  int c0, c1;        // the first and last CTA with a stretch of the tile
 };
 
-// Walk of one CTA's units. Every call is made by whole warps (the searches are warp-wide), and all
-// warps of a CTA that walk get the same stretches.
+// Walk of one CTA's units, made by whole warps (the searches are warp-wide). The entries of 32
+// sequences are held across the lanes, read together when the walk starts, so that finding the first
+// stretch and moving on to the next sequence cost no chain of loads.
 template <bool kPairs>
 struct SegIter {
   const PagedBatch& b;
   const long long* U;
   long long u, u_end, per, tile_u0;
-  int seq, head, tile, ntiles, t0, t1, b0, nb;
+  long long wU;  // lane i: U[w0 + i], past the end the largest value
+  PlanSeq wS;    // lane i: sequence w0 + i
+  int w0, seq, head, tile, ntiles, t0, t1, b0, nb;
   PlanSeq ps;
 
+  __device__ __forceinline__ void load_window(int at) {
+    const int i = at + (threadIdx.x & 31);
+    w0 = at;
+    wU = i <= b.S ? U[i] : 0x7fffffffffffffffLL;
+    wS = i < b.S ? b.plan.seq[i] : PlanSeq{0, 0, 0, 0};
+  }
   __device__ __forceinline__ SegIter(const PagedBatch& batch) : b(batch), U(batch.plan.units[kPairs ? 1 : 0]) {
+    load_window(0);
     const long long W = U[b.S];
     per = (W + gridDim.x - 1) / gridDim.x;
     u = min(W, per * blockIdx.x);
     u_end = min(W, u + per);
-    seq = -1;
+    head = b.Hkv;  // no sequence yet
   }
   __device__ __forceinline__ int owner(long long unit) const { return (int)(unit / per); }
 
   __device__ __forceinline__ void find_seq() {
     const int lane = threadIdx.x & 31;
-    // The last s with U[s] <= u: the next 32 entries first (the walk moves forward), then a 32-way search.
-    int lo = seq + 1, hi = b.S;  // U[lo] <= u < U[hi]
-    if (seq >= 0) {
-      const int idx = min(lo + 1 + lane, b.S);
-      const int c = __popc(__ballot_sync(0xffffffffu, U[idx] <= u));
-      if (c < 32) {
-        lo += c;
-        hi = lo + 1;
-      } else {
-        lo += 32;
+    // The last s with U[s] <= u. The walk moves forward, so U[w0] <= u.
+    int c = __popc(__ballot_sync(0xffffffffu, wU <= u));
+    if (c == 32) {
+      int lo = w0 + 31, hi = b.S;  // U[lo] <= u < U[hi]; a 32-way search down to one window
+      while (hi - lo > 31) {
+        const int step = (hi - lo + 31) / 32;
+        const long long idx = (long long)lo + (long long)(lane + 1) * step;
+        const int k = __popc(__ballot_sync(0xffffffffu, idx < hi && U[idx] <= u));
+        lo += k * step;
+        hi = (int)min((long long)hi, (long long)lo + step);
       }
+      load_window(lo);
+      c = __popc(__ballot_sync(0xffffffffu, wU <= u));
     }
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const long long idx = (long long)lo + (long long)(lane + 1) * step;
-      const bool le = idx < hi && U[idx] <= u;
-      const int c = __popc(__ballot_sync(0xffffffffu, le));
-      lo += c * step;
-      hi = (int)min((long long)hi, (long long)lo + step);
-    }
-    seq = lo;
-    ps = b.plan.seq[seq];
+    const int src = c - 1;  // at most 30: U[w0 + 31] > u
+    seq = w0 + src;
+    const long long base = __shfl_sync(0xffffffffu, wU, src), units = __shfl_sync(0xffffffffu, wU, c) - base;
+    ps.q0 = __shfl_sync(0xffffffffu, wS.q0, src);
+    ps.ql = __shfl_sync(0xffffffffu, wS.ql, src);
+    ps.kvl = __shfl_sync(0xffffffffu, wS.kvl, src);
     ntiles = tile_count<kPairs>(ps.ql, b.G, b.pair_tokens);
-    const long long base = U[seq], per_head = (U[seq + 1] - base) / b.Hkv;
-    const long long rem = u - base;
-    head = (int)(rem / per_head);
+    long long per_head;
+    if (units <= 0x7fffffffLL) {  // the usual case, without 64-bit divisions
+      per_head = (int)units / b.Hkv;
+      head = (int)(u - base) / (int)per_head;
+    } else {
+      per_head = units / b.Hkv;
+      head = (int)((u - base) / per_head);
+    }
     // The tile that holds unit u of this head: running sums over 32 tiles at a time.
     long long at = base + head * per_head;
     for (int i0 = 0;; i0 += 32) {
@@ -192,20 +205,21 @@ struct SegIter {
         tile_blocks<kPairs>(x0, x1, ps.ql, ps.kvl, b.causal, b.window, y0, yn);
       }
       long long sum = yn;
+      if (ntiles > 1) {
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += v;
+        for (int off = 1; off < 32; off <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, sum, off);
+          if (lane >= off) sum += v;
+        }
       }
-      const int c = __popc(__ballot_sync(0xffffffffu, at + sum <= u));
-      if (c < 32 || i0 + 32 >= ntiles) {
-        const int src = min(c, 31);
-        tile = i0 + src;
-        t0 = __shfl_sync(0xffffffffu, x0, src);
-        t1 = __shfl_sync(0xffffffffu, x1, src);
-        b0 = __shfl_sync(0xffffffffu, y0, src);
-        nb = __shfl_sync(0xffffffffu, yn, src);
-        tile_u0 = at + __shfl_sync(0xffffffffu, sum, src) - nb;
+      const int k = ntiles > 1 ? __popc(__ballot_sync(0xffffffffu, at + sum <= u)) : 0;
+      if (k < 32) {
+        tile = i0 + k;
+        t0 = __shfl_sync(0xffffffffu, x0, k);
+        t1 = __shfl_sync(0xffffffffu, x1, k);
+        b0 = __shfl_sync(0xffffffffu, y0, k);
+        nb = __shfl_sync(0xffffffffu, yn, k);
+        tile_u0 = at + __shfl_sync(0xffffffffu, sum, k) - nb;
         break;
       }
       at += __shfl_sync(0xffffffffu, sum, 31);
@@ -214,7 +228,7 @@ struct SegIter {
 
   __device__ __forceinline__ bool next(Seg& s) {
     if (u >= u_end) return false;
-    if (seq < 0 || head == b.Hkv) find_seq();
+    if (head == b.Hkv) find_seq();
     s.seq = seq;
     s.head = head;
     s.tile = tile;
@@ -223,17 +237,18 @@ struct SegIter {
     s.kvl = ps.kvl;
     s.t0 = t0;
     s.t1 = t1;
-    s.u0 = tile_u0;
-    s.u1 = tile_u0 + nb;
     const int off = (int)(u - tile_u0);
     s.blk = b0 + off;
     s.n = (int)min((long long)(nb - off), u_end - u);
     s.first = off == 0;
     s.last = off + s.n == nb;
+    // A tile that is not this CTA's alone is shared by the CTAs that own its first to its last unit.
+    s.c0 = s.first ? (int)blockIdx.x : owner(tile_u0);
+    s.c1 = s.last ? (int)blockIdx.x : owner(tile_u0 + nb - 1);
     u += s.n;
     if (s.last) {  // on to the next tile, head or (at the next call) sequence
       tile_u0 += nb;
-      if (ntiles > 1 || head + 1 == b.Hkv) {
+      if (ntiles > 1) {
         if (++tile == ntiles) {
           tile = 0;
           ++head;
@@ -257,6 +272,12 @@ struct PagedCache {
   long long v_page, v_head, v_tok;
 };
 
+// A tile of 128 rows that CTA c (the index in PagedFwd::share) began and CTAs up to c1 went on with.
+struct TileShare {
+  int c1;  // -1: none
+  int q0, ql, tok0, head;
+};
+
 struct PagedFwd {
   PagedBatch b;
   PagedCache c;
@@ -264,9 +285,15 @@ struct PagedFwd {
   long long q_tok, q_head;
   __nv_bfloat16* o;  // [T][Hq][d]
   float* lse;        // [T][Hq]
-  float* part;       // partial results: 2 slots per CTA
+  float* part;       // partial results of the 16-row tiles: 2 slots per CTA
+  float* tile_part;  // and of the pairs, with what each CTA shares with those after it
+  TileShare* share;  // [tile_ctas][2 tiles]
+  int tile_ctas;     // CTAs of the pairs' kernel (0: it does not run)
   float scale_log2;
 };
+
+// One partial result of a pair: per tile o [D / 4][128][4], unnormalised, and m, l, e [128].
+__host__ __device__ constexpr int tile_part(int D) { return 2 * kTile * (D + 3); }
 
 // Rotation of q and k (and a copy of v), dense or into a paged cache.
 struct RopeStrides {

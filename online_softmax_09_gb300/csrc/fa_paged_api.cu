@@ -293,6 +293,7 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt((float)batch->d);
   p.scale_log2 = s * 1.4426950408889634f;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  num_sms = num_sms < fa::kPagedSms ? num_sms : fa::kPagedSms;
   if (with_pairs(batch)) {
     fa::TileMaps m;
     const int d = batch->d;
@@ -304,9 +305,11 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
     const int cb[4] = {64, batch->page_size < 128 ? batch->page_size : 128, 1, 1};
     FA_TRY(make_map(&m.k, cache->k, 4, cd, ks, cb));
     FA_TRY(make_map(&m.v, cache->v, 4, cd, vs, cb));
-    fa::PagedFwd pt = p;
-    pt.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + fa::paged_rows_workspace_bytes(d));
-    if (fa::launch_paged_tiles(m, pt, d, num_sms, st) != cudaSuccess) return FA_ERR_LAUNCH;
+    char* ws = static_cast<char*>(workspace) + fa::paged_rows_workspace_bytes(d);
+    p.tile_part = reinterpret_cast<float*>(ws);
+    p.share = reinterpret_cast<fa::TileShare*>(ws + fa::plan_up((size_t)2 * fa::kPagedSms * fa::tile_part(d) * 4));
+    p.tile_ctas = num_sms;
+    if (fa::launch_paged_tiles(m, p, d, num_sms, st) != cudaSuccess) return FA_ERR_LAUNCH;
   }
   return fa::launch_paged_rows(p, batch->d, num_sms, st) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }

@@ -15,8 +15,8 @@
 //              forward, so that o is not off where one key dominates.
 // Slots of the last page past the sequence hold anything, NaN too, and 0 * NaN is NaN: the rows of V
 // past the last key are set to zero in shared memory before the product.
-// A pair that several CTAs share leaves unnormalised sums in the workspace, columns first so that the
-// threads of a warp write neighbours; the tile's last CTA joins them in the order of the keys.
+// A pair that several CTAs share leaves unnormalised sums in the workspace, the rows of a warp side by
+// side; the kernel that follows joins them in the order of the keys (fa_paged.cu).
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -27,6 +27,17 @@ namespace fa {
 constexpr int kTileThreads = 320;
 constexpr uint32_t kTileTmemCols = 512;
 constexpr float kTileRescale = 8.f;
+
+constexpr int kSegSlots = 4;
+
+// A stretch as the producer hands it to the other warps: the blocks that each tile of its pair has work
+// in, [a, b) relative to block j0 (none: a == b).
+struct TileSeg {
+  int n_max;  // blocks that some tile has work in; -1: the end of the CTA's stretches
+  int j0, a[2], b[2], exists[2];
+  int head, q0, ql, kvl, t0;
+  int first, last, c0, c1;
+};
 
 template <int D>
 struct TileSmem {
@@ -47,27 +58,19 @@ struct TileSmem {
   static constexpr int bOFull = bPFull + 2;
   static constexpr int bQEmpty = bOFull + 2;
   static constexpr int bOFree = bQEmpty + 2;
-  static constexpr int bDrain = bOFree + 2;
+  static constexpr int bSegFull = bOFree + 2;
+  static constexpr int bSegEmpty = bSegFull + kSegSlots;
+  static constexpr int bDrain = bSegEmpty + kSegSlots;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
-  static constexpr int kFlag = kAbort + 4;  // one word per tile: this CTA joins the tile
-  static constexpr int kBytes = kFlag + 8;
+  static constexpr int kSeg = kAbort + 4;  // ring of stretches
+  static constexpr int kBytes = kSeg + kSegSlots * sizeof(TileSeg);
   static constexpr int kAlloc = kBytes + 1024;
 };
 
-// One partial result of a CTA: per tile of the pair, o [D][128] and m, l, e [128].
-constexpr int tile_part(int D) { return 2 * kTile * (D + 3); }
-
-// The blocks that each tile of a stretch's pair has work in, relative to block j0.
-struct TileItem {
-  int j0, n_max;
-  int a[2], b[2];
-  bool exists[2];
-};
-
-__device__ __forceinline__ TileItem tile_item(const Seg& s, const PagedBatch& p) {
-  TileItem it;
+__device__ __forceinline__ TileSeg tile_seg(const Seg& s, const PagedBatch& p) {
+  TileSeg it;
   const int tpt = p.pair_tokens >> 1;
   int lo[2], hi[2];
   bool any = false;
@@ -95,6 +98,15 @@ __device__ __forceinline__ TileItem tile_item(const Seg& s, const PagedBatch& p)
     it.b[t] = hi[t] > lo[t] ? hi[t] - it.j0 : 0;
     it.n_max = max(it.n_max, it.b[t]);
   }
+  it.head = s.head;
+  it.q0 = s.q0;
+  it.ql = s.ql;
+  it.kvl = s.kvl;
+  it.t0 = s.t0;
+  it.first = s.first;
+  it.last = s.last;
+  it.c0 = s.c0;
+  it.c1 = s.c1;
   return it;
 }
 
@@ -105,10 +117,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
-}
-
-__device__ __forceinline__ void group_sync(int id) {  // the 128 threads of one tile
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
 
 __device__ __forceinline__ float max64f(const uint32_t (&a)[32], const uint32_t (&b)[32], float init) {
@@ -130,14 +138,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   using L = TileSmem<D>;
   constexpr int NK = L::NK, NV = L::NV;
   const PagedBatch& b = p.b;
+  SegIter<true> walk(b);  // (its loads and the plan's check go out together)
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
     return;
   }
-  {
-    const long long W = b.plan.units[1][b.S];
-    if ((W + gridDim.x - 1) / gridDim.x * blockIdx.x >= W) return;  // no work for this CTA
-  }
+  if (threadIdx.x < 2) p.share[2 * blockIdx.x + threadIdx.x].c1 = -1;
+  if (walk.u >= walk.u_end) return;  // no work for this CTA
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -145,7 +152,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t sQ = sbase + L::kQ, sK = sbase + L::kK, sV = sbase + L::kV;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
-  volatile int* join_flag = reinterpret_cast<volatile int*>(smem + L::kFlag);
+  TileSeg* segs = reinterpret_cast<TileSeg*>(smem + L::kSeg);
   const Ctl ctl{abort_flag, b.status};
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -169,9 +176,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(bar(L::bVFull + s), 1);
       mbar_init(bar(L::bVEmpty + s), 1);
     }
+    for (int s = 0; s < kSegSlots; ++s) {
+      mbar_init(bar(L::bSegFull + s), 1);
+      mbar_init(bar(L::bSegEmpty + s), 9);  // the MMA warp and the eight softmax warps
+    }
     mbar_init(bar(L::bDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
   // Rows that no load fills are zero, so that their scores are.
   for (int i = threadIdx.x; i < 2 * (D / 64) * (kTile - used) * 8; i += kTileThreads) {
@@ -183,18 +199,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), kTileTmemCols);
     tmem_relinquish();
   }
-  if (warp == 8 && lane == 0) {
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel may start on SMs left free
 
-  SegIter<true> walk(b);
-  Seg s;
+  // Stretch i of the CTA, once the producer has handed it out; and its slot given back.
+  auto take = [&](uint32_t i) -> const TileSeg* {
+    return mbar_wait_warp(bar(L::bSegFull + i % kSegSlots), (i / kSegSlots) & 1, ctl) ? segs + i % kSegSlots : nullptr;
+  };
+  auto give_back = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(L::bSegEmpty + i % kSegSlots));
+  };
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA producer
     const int box = b.page_size < kPairBlk ? b.page_size : kPairBlk;  // keys of one box
@@ -202,8 +220,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t q_bytes = (uint32_t)used * D * 2;
     uint32_t gk = 0, gv = 0, qn[2] = {0, 0};
     bool ok = true;
-    while (ok && walk.next(s)) {
-      const TileItem it = tile_item(s, b);
+    Seg s;
+    for (uint32_t i = 0; ok; ++i) {
+      const bool more = walk.next(s);
+      TileSeg it;
+      it.n_max = -1;
+      if (more) it = tile_seg(s, b);
+      if (!(ok = mbar_wait_warp(bar(L::bSegEmpty + i % kSegSlots), ((i / kSegSlots) & 1) ^ 1, ctl))) break;
+      if (lane == 0) {
+        segs[i % kSegSlots] = it;
+        mbar_arrive(bar(L::bSegFull + i % kSegSlots));
+      }
+      if (!more) break;
       if (it.n_max == 0) continue;
       int lo, hi;
       key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
@@ -313,8 +341,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       return true;
     };
     bool ok = true;
-    while (ok && walk.next(s)) {
-      const TileItem it = tile_item(s, b);
+    for (uint32_t i = 0; ok; ++i) {
+      const TileSeg* sp = take(i);
+      if (sp == nullptr) break;
+      const TileSeg it = *sp;
+      give_back(i);
+      if (it.n_max < 0) break;
       if (it.n_max == 0) continue;
       bool k_ready = false;
 #pragma unroll
@@ -371,20 +403,57 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t o_stage = sbase + L::kOStage + (uint32_t)warp * 4096;
     uint32_t sc = 0, on = 0, gv = 0;
     bool ok = true;
-    while (ok && walk.next(s)) {
-      const TileItem it = tile_item(s, b);
+    // 64 columns of this warp's rows of o, through its buffer, so that eight lanes write 128 neighbouring
+    // bytes of a row; `out`: this thread's row (-1: none).
+    auto store_cols = [&](const uint4 (&w)[2][4], int c, long long out) {
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const uint4 v4 = w[g >> 2][g & 3];
+        st_shared_v4(o_stage + (uint32_t)lane * 128 + ((g ^ (lane & 7)) << 4), v4.x, v4.y, v4.z, v4.w);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + (lane >> 3), g = lane & 7;
+        const long long ro = __shfl_sync(0xffffffffu, out, row);
+        const uint4 v4 = *reinterpret_cast<const uint4*>(smem + L::kOStage + warp * 4096 + row * 128 +
+                                                         ((g ^ (row & 7)) << 4));
+        if (ro >= 0) *reinterpret_cast<uint4*>(p.o + ro * D + c * 64 + g * 8) = v4;
+      }
+    };
+    auto pack = [](uint4 (&w)[4], const float* f, float x) {
+      uint32_t* wp = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) wp[i] = pack_bf16(f[2 * i] * x, f[2 * i + 1] * x);
+    };
+    auto row_out = [&](int q0, int tok, int ql, int head) -> long long {
+      return r < used && tok < ql ? (long long)(q0 + tok) * b.Hq + head * b.G + r_head : -1;
+    };
+    for (uint32_t i = 0; ok; ++i) {
+      const TileSeg* sp = take(i);
+      if (sp == nullptr) {
+        ok = false;
+        break;
+      }
+      const TileSeg& s = *sp;  // given back at the end of the stretch
+      const int n_max = s.n_max;
+      if (n_max < 0) break;
       const uint32_t gv0 = gv;
-      gv += it.n_max;
-      if (!(t ? it.exists[1] : it.exists[0])) continue;
-      const int a_t = t ? it.a[1] : it.a[0];
-      const int n_kv = (t ? it.b[1] : it.b[0]) - a_t;
+      gv += n_max;
+      if (!s.exists[t]) {
+        give_back(i);
+        continue;
+      }
+      const int a_t = s.a[t];
+      const int n_kv = s.b[t] - a_t;
+      const int kv_first = (s.j0 + a_t) * kPairBlk, kvl = s.kvl;
       const int tok0 = s.t0 + t * tpt;
       const int tok = tok0 + r_tok;
-      const bool valid = r < used && tok < s.ql;
-      const int pos = s.kvl - s.ql + tok;
-      const int klim = min(s.kvl - 1, b.causal ? pos : s.kvl - 1);
+      const int pos = kvl - s.ql + tok;
+      const int klim = min(kvl - 1, b.causal ? pos : kvl - 1);
       const int klo = b.window > 0 ? pos - b.window + 1 : 0;
-      const int pos0 = s.kvl - s.ql + tok0, pos1 = pos0 + tpt - 1;
+      const int pos0 = kvl - s.ql + tok0, pos1 = pos0 + tpt - 1;
       float m_run = -INFINITY, m_hi = -INFINITY, l_run = 0.f, e_run = 0.f;
       for (int j = 0; j < n_kv; ++j) {
         if (!mbar_wait_warp(bar(L::bSFull + t), (sc + j) & 1, ctl)) {
@@ -392,8 +461,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           break;
         }
         tc_fence_after();
-        const int kv0 = (it.j0 + a_t + j) * kPairBlk;
-        const bool tail = kv0 + kPairBlk > s.kvl;
+        const int kv0 = kv_first + j * kPairBlk;
+        const bool tail = kv0 + kPairBlk > kvl;
         const bool need_mask = tail || (b.causal && kv0 + kPairBlk - 1 > pos0) ||
                                (b.window > 0 && kv0 < pos1 - b.window + 1);
         uint32_t sr[4][32];
@@ -460,7 +529,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             ok = false;
             break;
           }
-          for (int row = s.kvl - kv0 + (r >> 3); row < kPairBlk; row += 16)
+          for (int row = kvl - kv0 + (r >> 3); row < kPairBlk; row += 16)
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
               st_shared_v4(sV + sv * L::kTileBytes + c * 16384 + row * 128 + (r & 7) * 16, 0, 0, 0, 0);
@@ -478,17 +547,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         sc += n_kv;
         tc_fence_after();
       }
-      float inv = 0.f;
-      bool write = true;
-      uint4 w[D / 32][4];
-      auto pack = [&](int c, const float* f, float x) {
-        uint32_t* wp = reinterpret_cast<uint32_t*>(w[c]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) wp[i] = pack_bf16(f[2 * i] * x, f[2 * i + 1] * x);
-      };
       if (s.first && s.last) {
-        const float z = l_run + e_run;
-        inv = (l_run > 0.f || l_run != l_run) ? 1.f / z : 0.f;  // a row that sees nothing: o = 0
+        const float inv = (l_run > 0.f || l_run != l_run) ? 1.f / (l_run + e_run) : 0.f;  // nothing seen: o = 0
+        uint4 w[D / 64][2][4];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -497,17 +558,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_ld_wait(o);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
+            for (int k = 0; k < 32; ++k) o[k] = 0;
           }
-          pack(c, reinterpret_cast<const float*>(o), inv);
+          pack(w[c >> 1][c & 1], reinterpret_cast<const float*>(o), inv);
         }
         if (n_kv > 0) {
           tc_fence_before();
           mbar_arrive(bar(L::bOFree + t));
         }
+        const long long out = row_out(s.q0, tok, s.ql, s.head);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) store_cols(w[c], c, out);
+        if (out >= 0) p.lse[out] = (m_run + log2f(l_run)) * 0.6931471805599453f;
       } else {
-        const int c0 = walk.owner(s.u0), c1 = walk.owner(s.u1 - 1);
-        float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3) + r;
+        float* slot = p.tile_part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
         if (n_kv > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -515,78 +579,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tmem_ld32(tO + c * 32, o);
             tmem_ld_wait(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) slot[(c * 32 + i) * kTile] = __uint_as_float(o[i]);
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(slot + ((c * 8 + k) * kTile + r) * 4) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
           tc_fence_before();
           mbar_arrive(bar(L::bOFree + t));
         }
-        slot[D * kTile] = m_run;  // -inf: nothing seen here, and o is not there
-        slot[(D + 1) * kTile] = l_run;
-        slot[(D + 2) * kTile] = e_run;
-        __threadfence();
-        group_sync(1 + t);
-        if (r == 0) {
-          uint32_t* cnt = &b.plan.counters[1][2 * c0 + t];
-          const bool last = atomicAdd(cnt, 1u) == (uint32_t)(c1 - c0);
-          if (last) *cnt = 0;
-          __threadfence();
-          join_flag[t] = last;
-        }
-        group_sync(1 + t);
-        write = join_flag[t] != 0;
-        if (write) {
-          auto part = [&](int c) {
-            return p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3) + r;
-          };
-          m_run = -INFINITY;
-          for (int c = c0; c <= c1; ++c) m_run = fmaxf(m_run, __ldcg(part(c) + D * kTile));
-          const float mu = m_run == -INFINITY ? 0.f : m_run;
-          l_run = e_run = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float f = ex2(__ldcg(part(c) + D * kTile) - mu);
-            l_run += f * __ldcg(part(c) + (D + 1) * kTile);
-            e_run += f * __ldcg(part(c) + (D + 2) * kTile);
-          }
-          inv = (l_run > 0.f || l_run != l_run) ? 1.f / (l_run + e_run) : 0.f;
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            float acc[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-              const float mi = __ldcg(part(c) + D * kTile);
-              if (mi == -INFINITY) continue;
-              const float f = ex2(mi - mu);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = fmaf(f, __ldcg(part(c) + (k * 32 + i) * kTile), acc[i]);
-            }
-            pack(k, acc, inv);
-          }
-        }
+        slot[D * kTile + r] = m_run;  // -inf: nothing seen here, and o is not there
+        slot[(D + 1) * kTile + r] = l_run;
+        slot[(D + 2) * kTile + r] = e_run;
+        if (s.first && r == 0) p.share[2 * blockIdx.x + t] = TileShare{s.c1, s.q0, s.ql, tok0, s.head};
       }
-      if (write) {
-        // Through this warp's buffer, so that eight lanes write 128 neighbouring bytes of a row.
-        const long long out = valid ? (long long)(s.q0 + tok) * b.Hq + s.head * b.G + r_head : -1;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          __syncwarp();
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const uint4 v4 = w[2 * c + (g >> 2)][g & 3];
-            st_shared_v4(o_stage + (uint32_t)lane * 128 + ((g ^ (lane & 7)) << 4), v4.x, v4.y, v4.z, v4.w);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 4 * i + (lane >> 3), g = lane & 7;
-            const long long ro = __shfl_sync(0xffffffffu, out, row);
-            const uint4 v4 = *reinterpret_cast<const uint4*>(smem + L::kOStage + warp * 4096 + row * 128 +
-                                                             ((g ^ (row & 7)) << 4));
-            if (ro >= 0) *reinterpret_cast<uint4*>(p.o + ro * D + c * 64 + g * 8) = v4;
-          }
-        }
-        if (valid) p.lse[out] = (m_run + log2f(l_run)) * 0.6931471805599453f;
-      }
+      give_back(i);
     }
   }
   tc_fence_before();
@@ -607,10 +612,11 @@ static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, int num_sm
   return cudaGetLastError();
 }
 
-size_t paged_tiles_workspace_bytes(int d) { return plan_up((size_t)2 * kPagedSms * tile_part(d) * 4); }
+size_t paged_tiles_workspace_bytes(int d) {
+  return plan_up((size_t)2 * kPagedSms * tile_part(d) * 4) + plan_up((size_t)2 * kPagedSms * sizeof(TileShare));
+}
 
 cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
-  num_sms = num_sms < kPagedSms ? num_sms : kPagedSms;
   return d == 128 ? launch_tiles<128>(m, p, num_sms, st) : launch_tiles<64>(m, p, num_sms, st);
 }
 
