@@ -167,13 +167,36 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before is complete
   const PagedBatch& b = p.b;
   const int tpt = b.pair_tokens >> 1, used = tpt * b.G;
-  const int units = p.tile_ctas * 2 * (kTile / 16);
+  // The shared tiles, listed by every CTA for itself (one read of all the descriptors).
+  extern __shared__ __align__(1024) uint8_t smem[];
+  short* list = reinterpret_cast<short*>(smem);
+  int* count = reinterpret_cast<int*>(smem + 2 * kPagedSms * sizeof(short));
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int n = 0;
+    constexpr int kRounds = 2 * kPagedSms / 32;
+    int c1[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int x = i * 32 + threadIdx.x;
+      c1[i] = x < 2 * p.tile_ctas ? p.share[x].c1 : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const uint32_t some = __ballot_sync(0xffffffffu, c1[i] >= 0);
+      if (c1[i] >= 0) list[n + __popc(some & ((1u << threadIdx.x) - 1))] = (short)(i * 32 + threadIdx.x);
+      n += __popc(some);
+    }
+    if (threadIdx.x == 0) *count = n;
+  }
+  __syncthreads();
+  const int units = *count * (kTile / 16);
   for (int x = blockIdx.x; x < units; x += gridDim.x) {
-    const int c0 = x >> 4, t = (x >> 3) & 1;
+    const int c0 = list[x >> 3] >> 1, t = list[x >> 3] & 1;
     const TileShare s = p.share[2 * c0 + t];
     const int r = (x & 7) * 16 + (threadIdx.x & 15);
     const int tok = s.tok0 + r / b.G;
-    if (s.c1 < 0 || r >= used || tok >= s.ql) continue;
+    if (r >= used || tok >= s.ql) continue;
     auto part = [&](int c) {
       return p.tile_part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
     };
@@ -181,11 +204,12 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
     float M = -INFINITY, Ls = 0.f, Es = 0.f, acc[D / 8];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) acc[i] = 0.f;
-    for (int c = c0; c <= s.c1; c += 2) {
-      float4 v[2][D / 32];
-      float mi[2], li[2], ei[2];
+    constexpr int kAtOnce = 4;
+    for (int c = c0; c <= s.c1; c += kAtOnce) {
+      float4 v[kAtOnce][D / 32];
+      float mi[kAtOnce], li[kAtOnce], ei[kAtOnce];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {  // two results' loads together
+      for (int y = 0; y < kAtOnce; ++y) {  // the loads of several results together
         const float* src = part(min(c + y, s.c1));
         mi[y] = src[D * kTile + r];
         li[y] = src[(D + 1) * kTile + r];
@@ -195,7 +219,7 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
           v[y][i] = *reinterpret_cast<const float4*>(src + ((g0 + 8 * i) * kTile + r) * 4);
       }
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
+      for (int y = 0; y < kAtOnce; ++y) {
         if (c + y > s.c1 || mi[y] == -INFINITY) continue;  // nothing seen there: o was not written
         const float mn = fmaxf(M, mi[y]);
         const float fa = ex2(M - mn), fb = ex2(mi[y] - mn);
