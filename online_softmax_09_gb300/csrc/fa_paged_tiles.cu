@@ -199,6 +199,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), kTileTmemCols);
     tmem_relinquish();
   }
+  // The producer's stretch: its place in the batch, the blocks of its tiles, and the table entry of this
+  // lane's box of the next block to load. Found here for the first time, beside the setup.
+  Seg s;
+  TileSeg it;
+    struct Look {
+    const int* tab;
+    int lo, hi;
+  } cur = {nullptr, 0, 0};
+  int entry = 0;
+  bool seen = false;  // a row sees a key of the box (else its entry is not read)
+  const int box = b.page_size < kPairBlk ? b.page_size : kPairBlk;  // keys of one box
+  const int nbox = kPairBlk / box;
+  auto read_entry = [&](int blk) {
+    const int key = blk * kPairBlk + lane * box;
+    seen = lane < nbox && key < cur.hi && key + box > cur.lo;
+    if (seen) entry = cur.tab[key >> b.page_shift];
+  };
+  auto page_at = [&]() -> int {  // num_pages lies beyond the map: zeros
+    if (seen && (unsigned)entry < (unsigned)b.num_pages) return entry;
+    if (seen) record_index_error(b.status);
+    return b.num_pages;
+  };
+  auto look = [&]() {
+    it.n_max = -1;
+    if (!walk.next(s)) return;
+    it = tile_seg(s, b);
+    key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, cur.lo, cur.hi);
+    cur.tab = b.table + (long long)s.seq * b.table_stride;
+    if (it.n_max > 0) read_entry(it.j0);
+  };
+  if (warp == 8) look();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -215,54 +246,46 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA producer
-    const int box = b.page_size < kPairBlk ? b.page_size : kPairBlk;  // keys of one box
-    const int nbox = kPairBlk / box;
     const uint32_t q_bytes = (uint32_t)used * D * 2;
     uint32_t gk = 0, gv = 0, qn[2] = {0, 0};
-    bool ok = true;
-    Seg s;
-    for (uint32_t i = 0; ok; ++i) {
-      const bool more = walk.next(s);
-      TileSeg it;
-      it.n_max = -1;
-      if (more) it = tile_seg(s, b);
-      if (!(ok = mbar_wait_warp(bar(L::bSegEmpty + i % kSegSlots), ((i / kSegSlots) & 1) ^ 1, ctl))) break;
+    uint32_t handed = 0;
+    bool ok = true, next_seen = false;
+    int next_entry = 0;
+    Look keep, nxt = cur;
+    auto hand_out = [&]() -> bool {
+      if (!mbar_wait_warp(bar(L::bSegEmpty + handed % kSegSlots), ((handed / kSegSlots) & 1) ^ 1, ctl)) return false;
       if (lane == 0) {
-        segs[i % kSegSlots] = it;
-        mbar_arrive(bar(L::bSegFull + i % kSegSlots));
+        segs[handed % kSegSlots] = it;
+        mbar_arrive(bar(L::bSegFull + handed % kSegSlots));
       }
-      if (!more) break;
-      if (it.n_max == 0) continue;
-      int lo, hi;
-      key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
-      const int* tab = b.table + (long long)s.seq * b.table_stride;
-      // The page of this lane's box of block j, num_pages (beyond the map: zeros) where nothing is seen.
-      auto page_of = [&](int j) -> int {
-        const int key = (it.j0 + j) * kPairBlk + lane * box;
-        if (lane >= nbox || key >= hi || key + box <= lo) return b.num_pages;
-        const int pg = tab[key >> b.page_shift];
-        if ((unsigned)pg < (unsigned)b.num_pages) return pg;
-        record_index_error(b.status);
-        return b.num_pages;
-      };
-      int page = page_of(0);
+      ++handed;
+      return true;
+    };
+    ok = hand_out();
+    while (ok && it.n_max >= 0) {
+      const int head = s.head, tok = s.q0 + s.t0, j0 = it.j0, n_max = it.n_max;
+      const bool with[2] = {it.b[0] > it.a[0], it.b[1] > it.a[1]};
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!ok || it.b[t] == it.a[t]) continue;
+        if (!ok || !with[t]) continue;
         if (!(ok = mbar_wait_warp(bar(L::bQEmpty + t), (qn[t] & 1) ^ 1, ctl))) continue;
         if (lane == 0) {
           mbar_expect_tx(bar(L::bQ + t), q_bytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sQ + t * L::kTileBytes + c * 16384, &tm_q, bar(L::bQ + t), c * 64, s.head * b.G,
-                        s.q0 + s.t0 + t * tpt);
+            tma_load_3d(sQ + t * L::kTileBytes + c * 16384, &tm_q, bar(L::bQ + t), c * 64, head * b.G, tok + t * tpt);
         }
         ++qn[t];
       }
-      for (int j = 0; ok && j < it.n_max; ++j) {
-        const int slot = ((it.j0 + j) * kPairBlk + lane * box) & (b.page_size - 1);
-        const int pg = page;
-        if (j + 1 < it.n_max) page = page_of(j + 1);
+      if (n_max == 0) {  // no tile sees a key: nothing to load
+        look();
+        if (ok) ok = hand_out();
+        continue;
+      }
+      for (int j = 0; ok && j < n_max; ++j) {
+        const int slot = ((j0 + j) * kPairBlk + lane * box) & (b.page_size - 1);
+        const int pg = page_at();
+        if (j + 1 < n_max) read_entry(j0 + j + 1);
         const uint32_t sk = gk % NK, sv = gv % NV;
         if (!(ok = mbar_wait_warp(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
         if (lane == 0) mbar_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
@@ -271,7 +294,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(sK + sk * L::kTileBytes + c * 16384 + lane * box * 128, &tm_k, bar(L::bKFull + sk), c * 64, slot,
-                        s.head, pg);
+                        head, pg);
         }
         ++gk;
         if (!(ok = mbar_wait_warp(bar(L::bVEmpty + sv), ((gv / NV) & 1) ^ 1, ctl))) break;
@@ -281,10 +304,28 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(sV + sv * L::kTileBytes + c * 16384 + lane * box * 128, &tm_v, bar(L::bVFull + sv), c * 64, slot,
-                        s.head, pg);
+                        head, pg);
         }
         ++gv;
+        if (j == 0) {
+          // The next stretch is looked up and handed out early, so that at the end of this one its
+          // queries load as soon as their buffers are free. (This one's next table entry is in hand.)
+          const int e = entry;
+          const bool sn = seen;
+          keep = cur;
+          look();
+          next_entry = entry;
+          next_seen = seen;
+          entry = e;
+          seen = sn;
+          nxt = cur;
+          cur = keep;
+          if (!(ok = hand_out())) break;
+        }
       }
+      cur = nxt;
+      entry = next_entry;
+      seen = next_seen;
     }
     if (*abort_flag && lane == 0) {  // every copy in flight lands before shared memory is freed
       for (int t = 0; t < 2; ++t)
@@ -436,7 +477,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = false;
         break;
       }
-      const TileSeg& s = *sp;  // given back at the end of the stretch
+      const TileSeg& s = *sp;
       const int n_max = s.n_max;
       if (n_max < 0) break;
       const uint32_t gv0 = gv;
@@ -547,7 +588,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         sc += n_kv;
         tc_fence_after();
       }
-      if (s.first && s.last) {
+      const TileSeg e = s;
+      give_back(i);  // before the stores: an arrival after them would wait for them
+      if (e.first && e.last) {
         const float inv = (l_run > 0.f || l_run != l_run) ? 1.f / (l_run + e_run) : 0.f;  // nothing seen: o = 0
         uint4 w[D / 64][2][4];
 #pragma unroll
@@ -566,12 +609,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           tc_fence_before();
           mbar_arrive(bar(L::bOFree + t));
         }
-        const long long out = row_out(s.q0, tok, s.ql, s.head);
+        const long long out = row_out(e.q0, tok, e.ql, e.head);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) store_cols(w[c], c, out);
         if (out >= 0) p.lse[out] = (m_run + log2f(l_run)) * 0.6931471805599453f;
       } else {
-        float* slot = p.tile_part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
+        float* slot = p.tile_part + (size_t)(2 * blockIdx.x + (e.first ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
         if (n_kv > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -589,9 +632,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         slot[D * kTile + r] = m_run;  // -inf: nothing seen here, and o is not there
         slot[(D + 1) * kTile + r] = l_run;
         slot[(D + 2) * kTile + r] = e_run;
-        if (s.first && r == 0) p.share[2 * blockIdx.x + t] = TileShare{s.c1, s.q0, s.ql, tok0, s.head};
+        if (e.first && r == 0) p.share[2 * blockIdx.x + t] = TileShare{e.c1, e.q0, e.ql, tok0, e.head};
       }
-      give_back(i);
     }
   }
   tc_fence_before();
