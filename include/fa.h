@@ -310,7 +310,7 @@ typedef struct {
   void *plan;              /* device, >= fa_paged_plan_bytes(S) bytes, 16-byte aligned; see fa_paged_plan */
   size_t plan_bytes;
   int S, T;                /* sequences, and rows of the step's token tensors (>= cu_q[S]); both may be 0 */
-  int max_q;               /* no sequence has more new tokens than this */
+  int max_q;               /* no sequence has more new tokens than this; max_q * Hq / Hkv must fit an int */
   int max_pages;           /* columns of the table; max_pages * page_size must fit an int */
   int page_size;           /* 16, 32, 64, 128 or 256 */
   int Hq, Hkv, d;          /* Hq % Hkv == 0; d 64 or 128 */

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < 2) carry[tid] = 0;
   bool bad = false;
-  for (int i = tid; i < 2 * kPlanCtas; i += 1024) b.plan.counters[0][i] = 0;
+  for (int i = tid; i < kPlanCtas; i += 1024) b.plan.counters[i] = 0;
   for (int s0 = 0; s0 < b.S; s0 += 1024) {
     const int s = s0 + tid;
     PlanSeq ps = {0, 0, 0, 0};
@@ -284,9 +284,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
 
   Seg s;
   while (it.next(s)) {
-    const int G = b.G;
-    const long long R = (long long)s.ql * G, r0 = (long long)s.tile * kRowTile;
-    const int rows = (int)min((long long)kRowTile, R - r0);
+    const unsigned G = b.G, r0 = (unsigned)s.tile * kRowTile;
+    const int rows = (int)min((unsigned)kRowTile, (unsigned)s.ql * G - r0);
     int lo, hi;
     key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
     const int* tab = b.table + (long long)s.seq * b.table_stride;
@@ -338,8 +337,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
     for (int h = 0; h < 2; ++h) {
       const int r = g + 8 * h;
       const bool ok = r < rows;
-      const long long rr = r0 + (ok ? r : 0);
-      const int tok = (int)(rr / G), hd = (int)(rr - (long long)tok * G);
+      const unsigned rr = r0 + (ok ? r : 0);
+      const int tok = (int)(rr / G), hd = (int)(rr - tok * G);
       const __nv_bfloat16* qp = p.q + (long long)(s.q0 + tok) * p.q_tok + (long long)(s.head * G + hd) * p.q_head;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -486,8 +485,26 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
         acc[4 * i + 3] += f * v.w;
       }
     }
-    bool write = true;
-    if (!(s.first && s.last)) {
+    auto put = [&](int row, int col, float4 v, float sum) {  // four columns of a row of o
+      const unsigned rr = r0 + row;
+      const int tok = (int)(rr / G), hd = (int)(rr - tok * G);
+      const long long out = (long long)(s.q0 + tok) * b.Hq + s.head * (int)G + hd;
+      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees nothing: o = 0
+      uint2 w;
+      w.x = pack_bf16(v.x * inv, v.y * inv);
+      w.y = pack_bf16(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(p.o + out * D + col) = w;
+      return out;
+    };
+    if (s.first && s.last) {
+      if (row < rows) {
+        long long out = 0;
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i)
+          out = put(row, col0 + 32 * i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]), Lr);
+        if ((threadIdx.x & 7) == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
+      }
+    } else {
       // A tile that other CTAs share: leave the partial result; the last of them to arrive joins all.
       const int c0 = s.c0, c1 = s.c1;
       float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * kRowPart<D>;
@@ -502,53 +519,61 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
           slot[kRowTile * (D + 2) + row] = Lr;
         }
       }
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
-        const bool last = atomicAdd(&b.plan.counters[0][c0], 1u) == (uint32_t)(c1 - c0);
-        if (last) b.plan.counters[0][c0] = 0;
-        __threadfence();
+        // The barrier orders the CTA's stores before this thread's release, which covers them all.
+        uint32_t before;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(&b.plan.counters[c0])
+                     : "memory");
+        const bool last = before == (uint32_t)(c1 - c0);
+        if (last) b.plan.counters[c0] = 0;
         *flag = last;
       }
       __syncthreads();
-      write = *flag != 0;
-      if (write && row < rows) {
-        M = -INFINITY;
-        Ls = Lr = 0.f;
+      if (*flag != 0) {
+        // Four columns of a row per thread, eight results' loads at a time.
+        for (int x = threadIdx.x; x < rows * (D / 4); x += kRowThreads) {
+          const int rw = x / (D / 4), col = (x - rw * (D / 4)) * 4;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          float m0 = -INFINITY, ls = 0.f, lsr = 0.f;
+          constexpr int kAtOnce = 8;
+          for (int c = c0; c <= c1; c += kAtOnce) {
+            float4 v[kAtOnce];
+            float mi[kAtOnce], li[kAtOnce], ri[kAtOnce], mx = m0;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-          const float* src = p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * kRowPart<D>;
-          const float mi = __ldcg(src + kRowTile * D + row);
-          const float mn = fmaxf(M, mi), mu = mn == -INFINITY ? 0.f : mn;
-          const float fa = ex2(M - mu), fb = ex2(mi - mu);
-          M = mn;
-          Ls = Ls * fa + fb * __ldcg(src + kRowTile * (D + 1) + row);
-          Lr = Lr * fa + fb * __ldcg(src + kRowTile * (D + 2) + row);
+            for (int y = 0; y < kAtOnce; ++y) {
+              const int cc = min(c + y, c1);
+              const float* src = p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * kRowPart<D>;
+              v[y] = __ldcg(reinterpret_cast<const float4*>(src + rw * D + col));
+              mi[y] = c + y <= c1 ? __ldcg(src + kRowTile * D + rw) : -INFINITY;
+              li[y] = __ldcg(src + kRowTile * (D + 1) + rw);
+              ri[y] = __ldcg(src + kRowTile * (D + 2) + rw);
+            }
 #pragma unroll
-          for (int i = 0; i < kCols / 4; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D + col0 + 32 * i));
-            acc[4 * i] = acc[4 * i] * fa + fb * v.x;
-            acc[4 * i + 1] = acc[4 * i + 1] * fa + fb * v.y;
-            acc[4 * i + 2] = acc[4 * i + 2] * fa + fb * v.z;
-            acc[4 * i + 3] = acc[4 * i + 3] * fa + fb * v.w;
+            for (int y = 0; y < kAtOnce; ++y) mx = fmaxf(mx, mi[y]);
+            const float mu = mx == -INFINITY ? 0.f : mx, f0 = ex2(m0 - mu);
+            m0 = mx;
+            a = make_float4(a.x * f0, a.y * f0, a.z * f0, a.w * f0);
+            ls *= f0;
+            lsr *= f0;
+#pragma unroll
+            for (int y = 0; y < kAtOnce; ++y) {
+              if (c + y > c1) continue;
+              const float f = ex2(mi[y] - mu);
+              a.x = fmaf(f, v[y].x, a.x);
+              a.y = fmaf(f, v[y].y, a.y);
+              a.z = fmaf(f, v[y].z, a.z);
+              a.w = fmaf(f, v[y].w, a.w);
+              ls = fmaf(f, li[y], ls);
+              lsr = fmaf(f, ri[y], lsr);
+            }
           }
+          const long long out = put(rw, col, a, lsr);
+          if (col == 0) p.lse[out] = (m0 + log2f(ls)) * 0.6931471805599453f;
         }
       }
-    }
-    if (write && row < rows) {
-      const long long rr = r0 + row;
-      const int tok = (int)(rr / G), hd = (int)(rr - (long long)tok * G);
-      const long long out = (long long)(s.q0 + tok) * b.Hq + s.head * G + hd;
-      const float inv = Lr > 0.f || Lr != Lr ? 1.f / Lr : 0.f;  // a row that sees nothing: o = 0
-#pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) {
-        uint2 w;
-        w.x = pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv);
-        w.y = pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
-        *reinterpret_cast<uint2*>(p.o + out * D + col0 + 32 * i) = w;
-      }
-      if ((threadIdx.x & 7) == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
     }
     __syncthreads();  // the rings and `stat` are free for the next stretch
   }

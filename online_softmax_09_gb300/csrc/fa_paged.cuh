@@ -37,7 +37,7 @@ struct PlanView {
   PlanHeader* head;
   PlanSeq* seq;               // [S]
   long long* units[2];        // [S + 1] running sums: 16-row tiles, 256-row pairs
-  uint32_t* counters[2];      // [kPlanCtas] arrivals at tiles shared by several CTAs; zero between calls
+  uint32_t* counters;         // [kPlanCtas] arrivals at 16-row tiles that several CTAs share; zero between calls
 };
 
 __host__ __device__ inline size_t plan_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -45,24 +45,20 @@ __host__ __device__ inline size_t plan_up(size_t x) { return (x + 255) / 256 * 2
 __host__ __device__ inline size_t plan_layout(void* base, int S, PlanView* v) {
   char* b = static_cast<char*>(base);
   size_t at = sizeof(PlanHeader);
-  size_t off[5];
+  size_t off[4];
   off[0] = at;
   at += plan_up((size_t)S * sizeof(PlanSeq));
   for (int i = 0; i < 2; ++i) {
     off[1 + i] = at;
     at += plan_up(((size_t)S + 1) * 8);
   }
-  for (int i = 0; i < 2; ++i) {
-    off[3 + i] = at;
-    at += kPlanCtas * 4;
-  }
+  off[3] = at;
+  at += kPlanCtas * 4;
   if (v != nullptr) {
     v->head = reinterpret_cast<PlanHeader*>(b);
     v->seq = reinterpret_cast<PlanSeq*>(b + off[0]);
-    for (int i = 0; i < 2; ++i) {
-      v->units[i] = reinterpret_cast<long long*>(b + off[1 + i]);
-      v->counters[i] = reinterpret_cast<uint32_t*>(b + off[3 + i]);
-    }
+    for (int i = 0; i < 2; ++i) v->units[i] = reinterpret_cast<long long*>(b + off[1 + i]);
+    v->counters = reinterpret_cast<uint32_t*>(b + off[3]);
   }
   return at;
 }
@@ -96,10 +92,11 @@ __host__ __device__ __forceinline__ void key_range(int t0, int t1, int ql, int k
   if (lo > hi) lo = hi;
 }
 
-// Row tile `i` of a sequence: its tokens [t0, t1], and how many tiles there are.
+// Row tile `i` of a sequence: its tokens [t0, t1], and how many tiles there are. (ql * G fits an int:
+// max_q * G is checked on the host.)
 template <bool kPairs>
 __host__ __device__ __forceinline__ int tile_count(int ql, int G, int pair_tokens) {
-  return kPairs ? (ql + pair_tokens - 1) / pair_tokens : (int)(((long long)ql * G + kRowTile - 1) / kRowTile);
+  return kPairs ? (ql + pair_tokens - 1) / pair_tokens : (int)(((unsigned)ql * G + kRowTile - 1) / kRowTile);
 }
 template <bool kPairs>
 __host__ __device__ __forceinline__ void tile_tokens(int i, int ql, int G, int pair_tokens, int& t0, int& t1) {
@@ -107,8 +104,13 @@ __host__ __device__ __forceinline__ void tile_tokens(int i, int ql, int G, int p
     t0 = i * pair_tokens;
     t1 = (t0 + pair_tokens < ql ? t0 + pair_tokens : ql) - 1;
   } else {
-    const long long r0 = (long long)i * kRowTile, R = (long long)ql * G;
-    const long long r1 = (r0 + kRowTile < R ? r0 + kRowTile : R) - 1;
+    const unsigned r0 = (unsigned)i * kRowTile, R = (unsigned)ql * G;
+    if (R <= kRowTile) {  // one tile: no divisions
+      t0 = 0;
+      t1 = ql - 1;
+      return;
+    }
+    const unsigned r1 = (r0 + kRowTile < R ? r0 + kRowTile : R) - 1;
     t0 = (int)(r0 / G);
     t1 = (int)(r1 / G);
   }
@@ -158,12 +160,14 @@ struct SegIter {
   __device__ __forceinline__ SegIter(const PagedBatch& batch) : b(batch), U(batch.plan.units[kPairs ? 1 : 0]) {
     load_window(0);
     const long long W = U[b.S];
-    per = (W + gridDim.x - 1) / gridDim.x;
+    per = W <= 0x7fffffffLL ? (long long)(((unsigned)W + gridDim.x - 1) / gridDim.x) : (W + gridDim.x - 1) / gridDim.x;
     u = min(W, per * blockIdx.x);
     u_end = min(W, u + per);
     head = b.Hkv;  // no sequence yet
   }
-  __device__ __forceinline__ int owner(long long unit) const { return (int)(unit / per); }
+  __device__ __forceinline__ int owner(long long unit) const {
+    return unit <= 0x7fffffffLL ? (int)((unsigned)unit / (unsigned)per) : (int)(unit / per);
+  }
 
   __device__ __forceinline__ void find_seq() {
     const int lane = threadIdx.x & 31;
@@ -190,8 +194,8 @@ struct SegIter {
     ntiles = tile_count<kPairs>(ps.ql, b.G, b.pair_tokens);
     long long per_head;
     if (units <= 0x7fffffffLL) {  // the usual case, without 64-bit divisions
-      per_head = (int)units / b.Hkv;
-      head = (int)(u - base) / (int)per_head;
+      per_head = (unsigned)units / (unsigned)b.Hkv;
+      head = (int)((unsigned)(u - base) / (unsigned)per_head);
     } else {
       per_head = units / b.Hkv;
       head = (int)((u - base) / per_head);

@@ -92,6 +92,7 @@ int check_batch(const fa_paged_batch* b) {
   if (b == nullptr) return FA_ERR_INVALID;
   if (b->S < 0 || b->T < 0 || b->max_q < 0 || b->max_pages < 1 || b->window < 0) return FA_ERR_INVALID;
   if (b->Hq < 1 || b->Hkv < 1 || b->Hq % b->Hkv != 0 || b->Hq > kMaxHeads) return FA_ERR_INVALID;
+  if ((long long)b->max_q * (b->Hq / b->Hkv) > 0x7fffffffLL - fa::kRowTile) return FA_ERR_INVALID;
   FA_TRY(check_d(b->d));
   if (b->page_size < 16 || b->page_size > 256 || (b->page_size & (b->page_size - 1))) return FA_ERR_UNSUPPORTED;
   if ((long long)b->max_pages * b->page_size > 0x7fffffffLL - 1024) return FA_ERR_INVALID;
