@@ -284,7 +284,8 @@ typedef struct {
  * rotation, so the gradient of inv_freq or of the positions is not formed).
  *   q, q_out : [B][Hq ][N][d] bf16 with any strides; d contiguous.
  *   k, k_out : [B][Hkv][N][d] bf16; both NULL (and Hkv 0): q alone.
- *   strides  : HOST, 12 values in elements, multiples of 8: (batch, head, token) of q, q_out, k, k_out.
+ *   strides  : HOST, 12 values in elements, multiples of 8: (batch, head, token) of q, q_out, k, k_out
+ *              (here and below the stride of an extent of 1 is not looked at).
  *              So q and k may be views of a fused projection's output while q_out and k_out are the
  *              dense tensors that fa_fwd takes, and the other way round for their gradients.
  *   positions: device int32; axis a of token n of batch element b is at a * pos_axis + b * pos_batch + n.

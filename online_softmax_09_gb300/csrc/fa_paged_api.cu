@@ -24,10 +24,11 @@ int check_ptr(const void* p, uintptr_t align) {
 }
 
 // Element strides of a 16-byte-chunked tensor; `distinct`: no stride may be 0 (a tensor that is written, or
-// that a tensor map describes).
+// that a tensor map describes). The stride of an extent of 1 means nothing and is not looked at.
 int check_strides(const long long* s, const long long* extent, int n, bool distinct) {
   for (int i = 0; i < n; ++i) {
-    if (s[i] < 0 || s[i] > (1LL << 46) || (distinct && extent[i] > 1 && s[i] == 0)) return FA_ERR_INVALID;
+    if (extent[i] <= 1) continue;
+    if (s[i] < 0 || s[i] > (1LL << 46) || (distinct && s[i] == 0)) return FA_ERR_INVALID;
     if (s[i] & 7) return FA_ERR_ALIGN;
   }
   return FA_OK;
@@ -158,7 +159,7 @@ int make_map(CUtensorMap* m, const void* base, int rank, const long long* dims, 
     d[i] = (cuuint64_t)dims[i];
     x[i] = (cuuint32_t)box[i];
     e[i] = 1;
-    if (i > 0) s[i - 1] = (cuuint64_t)(strides[i - 1] > 0 ? strides[i - 1] : 8) * 2;  // 0: extent 1
+    if (i > 0) s[i - 1] = (cuuint64_t)(dims[i] > 1 ? strides[i - 1] : 8) * 2;
   }
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, x, e,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -36,8 +36,11 @@ class _Batch(ctypes.Structure):  # fa_paged_batch
 
 
 class _Cache(ctypes.Structure):  # fa_paged_cache
-    _fields_ = [("k", _vp), ("v", _vp), ("k_strides", ctypes.c_longlong * 3), ("v_strides", ctypes.c_longlong * 3),
-                ("num_pages", _i)]
+    _fields_ = [("k", _vp), ("v", _vp)] + [(f"{x}_stride{i}", ctypes.c_longlong) for x in "kv" for i in range(3)] + [
+        ("num_pages", _i)]
+
+
+_ll = [ctypes.c_longlong * n for n in range(13)]  # (array types, made once)
 
 
 class FAError(RuntimeError):
@@ -394,6 +397,7 @@ class Rotary:
                 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous 1-D float32 CUDA tensor [rot / 2]")
         self.inv_freq = inv_freq
+        self.index = inv_freq.get_device()
         self.rot = 2 * inv_freq.numel()
         self.interleaved = bool(interleaved)
         ids = None if axes is None else [int(a) for a in axes]
@@ -406,14 +410,14 @@ class Rotary:
 
 
 def _dev_index(t):
-    i = t.device.index
-    if i != torch.cuda.current_device():
+    i = t.get_device()
+    if i != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on cuda:{i}, which is not the current device (use torch.cuda.device)")
     return i
 
 
 def _stream_of(stream, index):
-    return int(stream.cuda_stream) if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(shape, dtype, device, stream):
@@ -424,54 +428,49 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _bf16(name, t, shape, device=None):
-    """``t`` is a bf16 CUDA tensor of ``shape`` with contiguous last dim (its other strides are free)."""
-    if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.stride(-1) != 1 \
-            or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor {list(shape)} with contiguous last dim, on one device")
-    return t
-
-
-def _strides(*tensors):
-    """(strides but the last) of each tensor, in elements; a dim of size one counts as dense (its stride means
-    nothing), and a missing tensor as zeros."""
-    out = []
-    for t, n in tensors:
-        if t is None:
-            out += [0] * n
-        else:
-            out += [s if e > 1 else 8 for s, e in zip(t.stride()[:-1], t.shape[:-1])]
-    return (ctypes.c_longlong * len(out))(*out)
+def _strides_of(name, t, shape, index):
+    """The strides of ``t``, a bf16 tensor of ``shape`` on GPU ``index`` whose last dim is contiguous."""
+    s = t.stride()
+    if t.dtype != torch.bfloat16 or t.get_device() != index or t.shape != shape or s[-1] != 1:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor {list(shape)} with contiguous last dim, on the "
+                         "device of the others")
+    return s
 
 
 def _rope(name, fn, q, k, positions, rotary, q_out, k_out, stream):
-    if q.dim() != 4 or (k is not None and (k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[2:] != q.shape[2:])):
-        raise ValueError("q must be [B, Hq, N, d] and k [B, Hkv, N, d] with the same B, N, d")
-    B, Hq, N, d = q.shape
-    Hkv = k.shape[1] if k is not None else 0
-    _bf16("q", q, q.shape)
+    shape = q.shape
+    if len(shape) != 4 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [B, Hq, N, d]")
+    B, Hq, N, d = shape
     i = _dev_index(q)
+    qs = _strides_of("q", q, shape, i)
     if k is not None:
-        _bf16("k", k, k.shape, q.device)
+        kshape = k.shape
+        if len(kshape) != 4 or kshape[0] != B or kshape[2:] != shape[2:]:
+            raise ValueError("k must be [B, Hkv, N, d] with the same B, N, d as q")
+        ks = _strides_of("k", k, kshape, i)
     elif k_out is not None:
         raise ValueError("k_out without k")
     A = rotary.naxes
-    want = {1: [(N,), (B, N), (1, N), (1, B, N)]}.get(A, [(A, N), (A, B, N)])
-    if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous() \
-            or tuple(positions.shape) not in want or positions.device != q.device \
-            or rotary.inv_freq.device != q.device:
+    n = positions.numel()
+    want = ((A, N), (A, B, N)) if A > 1 else ((N,), (B, N), (1, N), (1, B, N))
+    if positions.dtype != torch.int32 or positions.get_device() != i or not positions.is_contiguous() \
+            or positions.shape not in want or rotary.index != i:
         raise ValueError(f"positions must be a contiguous int32 CUDA tensor of shape {want[0]} or {want[1]}")
-    per_batch = B > 1 and positions.numel() == A * B * N
-    pos_axis = positions.numel() // A
-    q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else _bf16("q_out", q_out, q.shape, q.device)
+    if q_out is None:
+        q_out = _empty(shape, torch.bfloat16, q.device, stream)
+    st = qs[:3] + _strides_of("q_out", q_out, shape, i)[:3]
+    kp = kop = None
     if k is not None:
-        k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else _bf16("k_out", k_out, k.shape,
-                                                                                      q.device)
+        if k_out is None:
+            k_out = _empty(kshape, torch.bfloat16, q.device, stream)
+        st += ks[:3] + _strides_of("k_out", k_out, kshape, i)[:3]
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     if N == 0 or B == 0:
         return q_out, k_out
-    r = fn(q.data_ptr(), q_out.data_ptr(), k.data_ptr() if k is not None else None,
-           k_out.data_ptr() if k is not None else None, _strides((q, 3), (q_out, 3), (k, 3), (k_out, 3)),
-           positions.data_ptr(), pos_axis, N if per_batch else 0, rotary._ref, B, Hq, Hkv, N, d, _stream_of(stream, i))
+    r = fn(q.data_ptr(), q_out.data_ptr(), kp, kop, _ll[12](*st), positions.data_ptr(), n // A,
+           N if B > 1 and n == A * B * N else 0, rotary._ref, B, Hq, kshape[1] if k is not None else 0, N, d,
+           _stream_of(stream, i))
     if r != FA_OK:
         raise FAError(r, name)
     return q_out, k_out
@@ -498,7 +497,8 @@ class PagedPlan:
         if S < 0:
             raise ValueError("cu_q must hold S + 1 values")
         self.key = (S, T, max_q, max_pages, page_size, Hq, Hkv, d, causal, window, device)
-        self.T, self.Hq, self.Hkv, self.d, self.page_size, self.device = T, Hq, Hkv, d, page_size, device
+        self.device, self.index = device, device.index
+        self.q_shape, self.kv_shape, self.lse_shape, self.page_shape = (T, Hq, d), (T, Hkv, d), (T, Hq), (Hkv, page_size, d)
         self.buffer = _empty(int(L.fa_paged_plan_bytes(S)), torch.uint8, device, stream)
         self.home = _stream_of(stream, device.index)
         self._c = _Batch(None, 0, self.buffer.data_ptr(), self.buffer.numel(), S, T, max_q, max_pages, page_size, Hq,
@@ -517,12 +517,10 @@ class PagedPlan:
         return raw
 
     def _cache(self, k_cache, v_cache):
-        shape = (k_cache.shape[0], self.Hkv, self.page_size, self.d)
-        _bf16("k_cache", k_cache, shape, self.device)
-        _bf16("v_cache", v_cache, shape, self.device)
-        ks, vs = ([s if e > 1 else 8 for s, e in zip(t.stride()[:3], shape)] for t in (k_cache, v_cache))
-        return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), (ctypes.c_longlong * 3)(*ks),
-                      (ctypes.c_longlong * 3)(*vs), shape[0])
+        shape = (k_cache.shape[0],) + self.page_shape
+        ks = _strides_of("k_cache", k_cache, shape, self.index)
+        vs = _strides_of("v_cache", v_cache, shape, self.index)
+        return ctypes.byref(_Cache(k_cache.data_ptr(), v_cache.data_ptr(), *ks[:3], *vs[:3], shape[0]))
 
 
 def paged_plan(cu_q, kv_lens, block_table, num_tokens: int, max_q: int, page_size: int, Hq: int, Hkv: int, d: int,
@@ -562,30 +560,37 @@ def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q
     [T,Hq,d] rotated (q None: nothing) (fa_paged_append). k_cache, v_cache: bf16 CUDA [pages, Hkv, page_size, d],
     any strides with contiguous last dim. positions: int32 CUDA [T], or [A,T] for several axes; None: each token's
     position in its sequence."""
-    T, d = plan.T, plan.d
-    _bf16("k", k, (T, plan.Hkv, d), plan.device)
-    _bf16("v", v, (T, plan.Hkv, d), plan.device)
+    i = plan.index
+    if not k.is_cuda or _dev_index(k) != i:
+        raise ValueError("k is not on the plan's device")
+    qp = qop = None
     if q is not None:
         if rotary is None:
             raise ValueError("q is only rotated: it needs a rotary")
-        _bf16("q", q, (T, plan.Hq, d), plan.device)
-        q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else _bf16("q_out", q_out, q.shape,
-                                                                                      plan.device)
+        shape = plan.q_shape
+        qs = _strides_of("q", q, shape, i)
+        if q_out is None:
+            q_out = _empty(shape, torch.bfloat16, q.device, stream)
+        st = qs[:2] + _strides_of("q_out", q_out, shape, i)[:2]
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
+    else:
+        st = (0, 0, 0, 0)
+    shape = plan.kv_shape
+    T = shape[0]
+    st += _strides_of("k", k, shape, i)[:2] + _strides_of("v", v, shape, i)[:2]
+    pp = None
     if positions is not None:
         A = rotary.naxes if rotary is not None else 0
-        if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous() \
-                or tuple(positions.shape) not in ([(T,), (1, T)] if A == 1 else [(A, T)]) \
-                or positions.device != plan.device:
+        if positions.dtype != torch.int32 or positions.get_device() != i or not positions.is_contiguous() \
+                or positions.shape not in (((T,), (1, T)) if A == 1 else ((A, T),)):
             raise ValueError("positions must be a contiguous int32 CUDA tensor [T], or [A, T] for several axes")
-    if rotary is not None and rotary.inv_freq.device != plan.device:
+        pp = positions.data_ptr()
+    if rotary is not None and rotary.index != i:
         raise ValueError("rotary is on another device")
-    i = _dev_index(k)
-    r = lib().fa_paged_append(q.data_ptr() if q is not None else None, q_out.data_ptr() if q is not None else None,
-                              k.data_ptr(), v.data_ptr(), _strides((q, 2), (q_out, 2), (k, 2), (v, 2)),
-                              ctypes.byref(plan._cache(k_cache, v_cache)), plan._ref, rotary._ref if rotary is not None else None,
-                              positions.data_ptr() if positions is not None else None, T, plan._use(stream, i))
+    r = lib().fa_paged_append(qp, qop, k.data_ptr(), v.data_ptr(), _ll[8](*st), plan._cache(k_cache, v_cache),
+                              plan._ref, rotary._ref if rotary is not None else None, pp, T, plan._use(stream, i))
     if r != FA_OK:
         raise FAError(r, "fa_paged_append")
     return q_out
@@ -594,22 +599,24 @@ def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q
 def forward_paged(q, k_cache, v_cache, plan, scale: float | None = None, out=None, lse=None, stream=None):
     """O [T,Hq,d], LSE [T,Hq]: attention of a step's new tokens over the paged cache (fa_fwd_paged). q [T,Hq,d] bf16
     CUDA, any strides with contiguous last dim. Rows that belong to no sequence are left as they were."""
-    T, Hq, d = plan.T, plan.Hq, plan.d
-    _bf16("q", q, (T, Hq, d), plan.device)
-    i = _dev_index(q)
-    o = out if out is not None else _empty((T, Hq, d), torch.bfloat16, q.device, stream)
-    l = lse if lse is not None else _empty((T, Hq), torch.float32, q.device, stream)
-    if out is not None and not _bf16("out", out, (T, Hq, d), plan.device).is_contiguous():
+    shape, i = plan.q_shape, plan.index
+    if not q.is_cuda or _dev_index(q) != i:
+        raise ValueError("q is not on the plan's device")
+    st = _strides_of("q", q, shape, i)[:2]
+    if out is None:
+        out = _empty(shape, torch.bfloat16, q.device, stream)
+    elif _strides_of("out", out, shape, i) and not out.is_contiguous():
         raise ValueError("out must be contiguous")
-    if lse is not None and (not l.is_cuda or l.dtype != torch.float32 or tuple(l.shape) != (T, Hq)
-                            or not l.is_contiguous() or l.device != plan.device):
+    if lse is None:
+        lse = _empty(plan.lse_shape, torch.float32, q.device, stream)
+    elif lse.dtype != torch.float32 or lse.get_device() != i or lse.shape != plan.lse_shape or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
-    r = lib().fa_fwd_paged(q.data_ptr(), _strides((q, 2)), ctypes.byref(plan._cache(k_cache, v_cache)), plan._ref,
-                           o.data_ptr(), l.data_ptr(), 0.0 if scale is None else float(scale), plan.workspace.data_ptr(),
+    r = lib().fa_fwd_paged(q.data_ptr(), _ll[2](*st), plan._cache(k_cache, v_cache), plan._ref, out.data_ptr(),
+                           lse.data_ptr(), 0.0 if scale is None else float(scale), plan.workspace.data_ptr(),
                            plan.ws_bytes, plan._use(stream, i))
     if r != FA_OK:
         raise FAError(r, "fa_fwd_paged")
-    return o, l
+    return out, lse
 
 
 def check(stream=None, device=None) -> None:

@@ -44,7 +44,8 @@ def test_rope_refusals(fa):
     assert _rope(fa, d=96) == -2 and _rope(fa, d=256) == -2
     assert _rope(fa, strides=_ll(*([1024, 512, 128] * 3 + [1024, 512, 4]))) == -3
     assert _rope(fa, strides=_ll(*([1024, 512, 128] * 3 + [1024, 512, 0]))) == -1  # an output broadcast over tokens
-    assert _rope(fa, strides=_ll(*([-1024, 512, 128] + [1024, 512, 128] * 3))) == -1
+    assert _rope(fa, B=2, strides=_ll(*([-1024, 512, 128] + [1024, 512, 128] * 3))) == -1
+    assert _rope(fa, strides=_ll(*([1024, -512, 128] + [1024, 512, 128] * 3))) == -1
     assert _rope(fa, pa=-1) == -1 and _rope(fa, pb=-1) == -1
     for bad in (_rot(fa, rot=0), _rot(fa, rot=8), _rot(fa, rot=40), _rot(fa, rot=256), _rot(fa, naxes=0),
                 _rot(fa, naxes=5), _rot(fa, inv=None), _rot(fa, axes=bytes([1] * 64), naxes=1),
@@ -62,7 +63,7 @@ def _batch(fa, **kw):
 
 
 def _cache(fa, k=P, v=P, ks=(4096, 2048, 128), vs=(4096, 2048, 128), pages=10):
-    return fa._Cache(k, v, _ll(*ks), _ll(*vs), pages)
+    return fa._Cache(k, v, *ks, *vs, pages)
 
 
 BAD_BATCH = [({"S": -1}, -1), ({"T": -1}, -1), ({"max_q": -1}, -1), ({"max_pages": 0}, -1), ({"window": -1}, -1),
