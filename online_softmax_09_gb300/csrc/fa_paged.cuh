@@ -333,6 +333,6 @@ cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int 
 // 128-row tiles; up to 16 rows they are one 16-row tile.
 constexpr int kPairRows = 16;
 inline int pair_rows_of(int G) { return G <= kTile ? kPairRows : 0x7fffffff; }
-cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, cudaStream_t st);
+cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, int num_sms, cudaStream_t st);
 
 }  // namespace fa

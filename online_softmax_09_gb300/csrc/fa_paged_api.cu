@@ -69,7 +69,8 @@ int rope_impl(const void* q, void* q_out, const void* k, void* k_out, const long
     FA_TRY(check_ptr(ptr[i], 16));
     FA_TRY(check_strides(strides + 3 * i, extent, 3, i & 1));
   }
-  FA_TRY(fa::check_current_device());
+  int num_sms = 0;
+  FA_TRY(fa::device_state(nullptr, &num_sms));
   fa::RopeLaunch p = {};
   for (int i = 0; i < (with_k ? 2 : 1); ++i) {
     p.src[i] = static_cast<const __nv_bfloat16*>(ptr[2 * i]);
@@ -86,7 +87,8 @@ int rope_impl(const void* q, void* q_out, const void* k, void* k_out, const long
   p.Hq = Hq;
   p.Hk = with_k ? Hkv : 0;
   p.inverse = inverse;
-  return fa::launch_rope(p, d, false, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return fa::launch_rope(p, d, false, num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
+                                                                                               : FA_ERR_LAUNCH;
 }
 
 int check_batch(const fa_paged_batch* b) {
@@ -226,7 +228,8 @@ int fa_paged_append(const void* q, void* q_out, const void* k, const void* v, co
     FA_TRY(check_strides(strides + 2 * i, extent, 2, i == 1));
   }
   uint32_t* status = nullptr;
-  FA_TRY(fa::device_state(&status, nullptr));
+  int num_sms = 0;
+  FA_TRY(fa::device_state(&status, &num_sms));
   fa::RopeLaunch p = {};
   const int in[3] = {0, 2, 3};
   for (int i = 0; i < 3; ++i) {
@@ -247,8 +250,9 @@ int fa_paged_append(const void* q, void* q_out, const void* k, const void* v, co
   p.Hq = with_q ? batch->Hq : 0;
   p.Hk = p.Hv = batch->Hkv;
   p.b = device_batch(batch, cache->num_pages, status);
-  return fa::launch_rope(p, batch->d, true, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK
-                                                                                                  : FA_ERR_LAUNCH;
+  return fa::launch_rope(p, batch->d, true, num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_LAUNCH;
 }
 
 size_t fa_fwd_paged_workspace_bytes(const fa_paged_batch* batch) {

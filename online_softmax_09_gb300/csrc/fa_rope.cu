@@ -16,20 +16,20 @@
 
 namespace fa {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;  // most tokens per CTA
+constexpr int kRopeThreads = 256;  // most threads per CTA
+constexpr int kRopeTokens = 2;     // most tokens per CTA
 
 template <int D>
-__device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float2* cs, int j, bool interleaved) {
+__device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float4* t, bool interleaved) {
+  constexpr int kStep = D / 16;  // t[kStep * i]: cos, sin of this thread's pairs 2i, 2i + 1
   uint32_t* a = reinterpret_cast<uint32_t*>(&va);
   uint32_t* c = reinterpret_cast<uint32_t*>(&vb);
   auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
   auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-  const float4* t = reinterpret_cast<const float4*>(cs + 8 * j);  // cos, sin of pairs 8j .. 8j + 7
   if (!interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 f = t[i];
+      const float4 f = t[kStep * i];
       const float x0 = lo(a[i]), x1 = hi(a[i]), y0 = lo(c[i]), y1 = hi(c[i]);
       a[i] = pack_bf16(x0 * f.x - y0 * f.y, x1 * f.z - y1 * f.w);
       c[i] = pack_bf16(y0 * f.x + x0 * f.y, y1 * f.z + x1 * f.w);
@@ -37,7 +37,7 @@ __device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float2* cs, in
   } else {  // words a[0..3], c[0..3] hold pairs 8j .. 8j + 7
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 f = t[i];
+      const float4 f = t[kStep * i];
       uint32_t& w0 = i < 2 ? a[2 * i] : c[2 * i - 4];
       uint32_t& w1 = i < 2 ? a[2 * i + 1] : c[2 * i - 3];
       const float x0 = lo(w0), y0 = hi(w0), x1 = lo(w1), y1 = hi(w1);
@@ -105,8 +105,10 @@ __device__ __forceinline__ RopeToken rope_token(const RopeLaunch& p, long long t
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeLaunch p) {
   constexpr int kGroups = D / 16;  // threads per head
-  constexpr int kSlots = kRopeThreads / kGroups;
-  __shared__ __align__(16) float2 cs[kRopeTokens][D / 2];
+  const int slots = blockDim.x / kGroups;
+  // cos, sin of pair 8 g + 2 i + e of each token at [i][g][e]: the eight (or four) threads of a head read
+  // neighbouring 16 bytes (in the pairs' own order they met in two banks, and this bound the kernel).
+  __shared__ __align__(16) float2 cs[kRopeTokens][4][kGroups][2];
   __shared__ RopeToken tok[kRopeTokens];
   const int tid = threadIdx.x;
   if (kPaged && !plan_matches(p.b, D)) {
@@ -115,33 +117,9 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeLaunch 
   }
   const long long t0 = (long long)blockIdx.x * p.tile;
   if (tid < p.tile) tok[tid] = rope_token<kPaged>(p, t0 + tid);
-  const int np = p.rot >> 1;
-  if (kPaged) __syncthreads();
-  if (np > 0) {
-    const int per = kRopeThreads / np;  // tokens at a time
-    const int i = tid % np, first = tid / np;
-    if (first < per && first < p.tile) {
-      const double turns = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-      const uint64_t w = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-      const int axis = (int)(p.axes[i >> 5] >> ((i & 31) * 2)) & 3;
-      for (int t = first; t < p.tile; t += per) {
-        long long pos = 0;
-        if (t0 + t < p.tokens) {
-          if (p.positions == nullptr) {
-            pos = tok[t].pos;
-          } else {
-            const long long bi = kPaged ? 0 : (t0 + t) / p.N;
-            pos = p.positions[axis * p.pos_axis + bi * p.pos_batch + (t0 + t - bi * p.N)];
-          }
-        }
-        const int phase = (int)(uint32_t)(((uint64_t)pos * w) >> 32);  // 2^-32 turns, signed
-        float s, c;
-        sincospif((float)phase * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-        cs[t][i] = make_float2(c, p.inverse ? -s : s);
-      }
-    }
-  }
   __syncthreads();
+
+  const int np = p.rot >> 1;
   const int g = tid % kGroups, slot = tid / kGroups;
   const bool turned = g < p.rot / 16;
   const int ea = turned && !p.interleaved ? 8 * g : 16 * g;
@@ -149,36 +127,80 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeLaunch 
   const int heads = p.Hq + p.Hk + p.Hv;
   const int total = p.tile * heads;
   int t = slot / heads, h = slot - t * heads;
-  for (int x = slot; x < total; x += kSlots) {
+  uint4 va, vb;
+  __nv_bfloat16* dst;
+  const float4* angles;
+  auto load = [&]() {  // this thread's chunks of head h of token t, then on to its next head
+    dst = nullptr;
+    angles = nullptr;
     const int part = h < p.Hq ? 0 : (h < p.Hq + p.Hk ? 1 : 2);
     const int hh = h - (part == 0 ? 0 : (part == 1 ? p.Hq : p.Hq + p.Hk));
     const RopeToken& k = tok[t];
     if (k.state == 3 || (k.state == 1 && part == 0)) {
       const __nv_bfloat16* src = p.src[part] + k.in[part] + hh * p.in[part].head;
-      __nv_bfloat16* dst = p.dst[part] + k.out[part] + hh * p.out[part].head;
-      uint4 a = *reinterpret_cast<const uint4*>(src + ea), c = *reinterpret_cast<const uint4*>(src + eb);
-      if (turned && part < 2) turn8<D>(a, c, cs[t], g, p.interleaved);
-      *reinterpret_cast<uint4*>(dst + ea) = a;
-      *reinterpret_cast<uint4*>(dst + eb) = c;
+      dst = p.dst[part] + k.out[part] + hh * p.out[part].head;
+      if (turned && part < 2) angles = reinterpret_cast<const float4*>(cs[t][0][g]);
+      va = *reinterpret_cast<const uint4*>(src + ea);
+      vb = *reinterpret_cast<const uint4*>(src + eb);
     }
-    h += kSlots;
+    h += slots;
     while (h >= heads) {
       h -= heads;
       ++t;
     }
+  };
+  if (slot < total) load();  // on its way while the angles are formed
+  if (np > 0) {
+    const int per = blockDim.x / np;  // tokens at a time
+    const int i = tid % np, first = tid / np;
+    if (first < per && first < p.tile) {
+      const double turns = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+      const uint64_t w = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+      const int axis = (int)(p.axes[i >> 5] >> ((i & 31) * 2)) & 3;
+      for (int k = first; k < p.tile; k += per) {
+        long long pos = 0;
+        if (t0 + k < p.tokens) {
+          if (p.positions == nullptr) {
+            pos = tok[k].pos;
+          } else {
+            const long long bi = kPaged ? 0 : (t0 + k) / p.N;
+            pos = p.positions[axis * p.pos_axis + bi * p.pos_batch + (t0 + k - bi * p.N)];
+          }
+        }
+        const int phase = (int)(uint32_t)(((uint64_t)pos * w) >> 32);  // 2^-32 turns, signed
+        float s, c;
+        sincospif((float)phase * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+        cs[k][(i >> 1) & 3][i >> 3][i & 1] = make_float2(c, p.inverse ? -s : s);
+      }
+    }
+  }
+  __syncthreads();
+  for (int x = slot; x < total; x += slots) {
+    if (x != slot) load();
+    if (dst == nullptr) continue;
+    if (angles != nullptr) turn8<D>(va, vb, angles, p.interleaved);
+    *reinterpret_cast<uint4*>(dst + ea) = va;
+    *reinterpret_cast<uint4*>(dst + eb) = vb;
   }
 }
 
-cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, cudaStream_t st) {
-  p.tile = kRopeTokens;
+// Threads and tokens per CTA. While the tokens fit one wave of CTAs (six per SM), one token each with all
+// 256 threads: latency counts (17 tokens: 3.2 us a call against 4.1 with two tokens and 128 threads).
+// Beyond that 128 threads, and two tokens in a dense batch: sharing the setup pays (4 x 4096 tokens of 40
+// heads: 109.6 us for both directions, one token 113.8, 256 threads with four 112.8). A paged batch keeps one:
+// its CTA starts with a chain of look-ups, and more CTAs hide more of it (8500 tokens: 34.7 us, two 36.7).
+cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, int num_sms, cudaStream_t st) {
+  const bool one_wave = p.tokens <= 6LL * num_sms;
+  const int threads = one_wave ? kRopeThreads : 128;
+  p.tile = one_wave || paged ? 1 : kRopeTokens;
   const long long grid = (p.tokens + p.tile - 1) / p.tile;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (d == 128) {
-    if (paged) fa_rope_kernel<128, true><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
-    else fa_rope_kernel<128, false><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
+    if (paged) fa_rope_kernel<128, true><<<(unsigned)grid, threads, 0, st>>>(p);
+    else fa_rope_kernel<128, false><<<(unsigned)grid, threads, 0, st>>>(p);
   } else {
-    if (paged) fa_rope_kernel<64, true><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
-    else fa_rope_kernel<64, false><<<(unsigned)grid, kRopeThreads, 0, st>>>(p);
+    if (paged) fa_rope_kernel<64, true><<<(unsigned)grid, threads, 0, st>>>(p);
+    else fa_rope_kernel<64, false><<<(unsigned)grid, threads, 0, st>>>(p);
   }
   return cudaGetLastError();
 }
