@@ -17,7 +17,7 @@ namespace fa {
 // forms the running sums. A sequence out of range gets no tokens (nothing of it is read or written)
 // and raises the status word.
 __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restrict__ cu_q,
-                                                             const int* __restrict__ kv_len, PagedBatch b, int d,
+                                                             const int* __restrict__ kv_len, PagedBatch b,
                                                              int max_q, int pair_rows) {
   __shared__ long long sums[2][32];
   __shared__ long long carry[2];
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
         int t0, t1, b0, nb;
         tile_tokens<true>(i, ql, b.G, b.pair_tokens, t0, t1);
         tile_blocks<true>(t0, t1, ql, kvl, b.causal, b.window, b0, nb);
-        sum += nb;
+        sum += tile_units<true>(t0, t1, b, nb);
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
     h.T = b.T;
     h.Hq = b.Hq;
     h.Hkv = b.Hkv;
-    h.d = d;
+    h.d = b.d;
     h.page_size = b.page_size;
     h.max_pages = b.max_pages;
     h.causal = b.causal;
@@ -106,9 +106,9 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
   }
 }
 
-cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int d, int max_q, int pair_rows,
+cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int max_q, int pair_rows,
                               cudaStream_t st) {
-  fa_paged_plan_kernel<<<1, 1024, 0, st>>>(cu_q, kv_len, b, d, max_q, pair_rows);
+  fa_paged_plan_kernel<<<1, 1024, 0, st>>>(cu_q, kv_len, b, max_q, pair_rows);
   return cudaGetLastError();
 }
 

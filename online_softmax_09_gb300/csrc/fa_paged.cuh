@@ -68,7 +68,7 @@ struct PagedBatch {
   PlanView plan;
   const int* table;  // [S][table_stride]
   long long table_stride;
-  int S, T, Hq, Hkv, G, page_size, page_shift, max_pages, num_pages, causal, window;
+  int S, T, Hq, Hkv, G, d, page_size, page_shift, max_pages, num_pages, causal, window;
   int pair_tokens;  // tokens of a pair of 128-row tiles: 2 * (128 / G)
   uint32_t* status;
 };
@@ -128,6 +128,20 @@ __host__ __device__ __forceinline__ void tile_blocks(int t0, int t1, int ql, int
   if (n < 1) n = 1;
 }
 
+// At d = 64 a pair with tokens for one tile only is worked off as two halves of its keys
+// (fa_paged_tiles.cu), in half a pair's time per block. Pairs are counted in half blocks there, and such a
+// pair's count is rounded up to even, so that every pair starts at an even unit, and so does every CTA
+// (SegIter::per). (At d = 128 two blocks of keys and values are all that fit beside the queries, too few
+// on their way for a CTA that reads twice as fast: halves took 76 us against 63 at 20 rows over 60000 keys.)
+__host__ __device__ __forceinline__ bool halves(int t0, int t1, const PagedBatch& b) {
+  return b.d == 64 && t1 - t0 + 1 <= b.pair_tokens / 2;
+}
+template <bool kPairs>
+__host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBatch& b, int n) {
+  if (!kPairs || b.d != 64) return n;
+  return halves(t0, t1, b) ? (n + 1) & ~1 : 2 * n;
+}
+
 // One stretch of key blocks of one row tile, as a CTA works it off.
 struct Seg {
   int seq, head, tile;
@@ -148,7 +162,8 @@ struct SegIter {
   long long u, u_end, per, tile_u0;
   long long wU;  // lane i: U[w0 + i], past the end the largest value
   PlanSeq wS;    // lane i: sequence w0 + i
-  int w0, seq, head, tile, ntiles, t0, t1, b0, nb;
+  int w0, seq, head, tile, ntiles, t0, t1;
+  int b0, nblk, nb;  // the tile's first key block, its blocks and its units
   PlanSeq ps;
 
   __device__ __forceinline__ void load_window(int at) {
@@ -161,12 +176,18 @@ struct SegIter {
     load_window(0);
     const long long W = U[b.S];
     per = W <= 0x7fffffffLL ? (long long)(((unsigned)W + gridDim.x - 1) / gridDim.x) : (W + gridDim.x - 1) / gridDim.x;
+    if (kPairs && b.d == 64) per = (per + 1) & ~1LL;
     u = min(W, per * blockIdx.x);
     u_end = min(W, u + per);
     head = b.Hkv;  // no sequence yet
   }
   __device__ __forceinline__ int owner(long long unit) const {
     return unit <= 0x7fffffffLL ? (int)((unsigned)unit / (unsigned)per) : (int)(unit / per);
+  }
+
+  __device__ __forceinline__ void measure() {  // the blocks and units of tile [t0, t1]
+    tile_blocks<kPairs>(t0, t1, ps.ql, ps.kvl, b.causal, b.window, b0, nblk);
+    nb = tile_units<kPairs>(t0, t1, b, nblk);
   }
 
   __device__ __forceinline__ void find_seq() {
@@ -207,6 +228,7 @@ struct SegIter {
       if (i0 + lane < ntiles) {
         tile_tokens<kPairs>(i0 + lane, ps.ql, b.G, b.pair_tokens, x0, x1);
         tile_blocks<kPairs>(x0, x1, ps.ql, ps.kvl, b.causal, b.window, y0, yn);
+        yn = tile_units<kPairs>(x0, x1, b, yn);
       }
       long long sum = yn;
       if (ntiles > 1) {
@@ -221,8 +243,7 @@ struct SegIter {
         tile = i0 + k;
         t0 = __shfl_sync(0xffffffffu, x0, k);
         t1 = __shfl_sync(0xffffffffu, x1, k);
-        b0 = __shfl_sync(0xffffffffu, y0, k);
-        nb = __shfl_sync(0xffffffffu, yn, k);
+        measure();
         tile_u0 = at + __shfl_sync(0xffffffffu, sum, k) - nb;
         break;
       }
@@ -242,14 +263,20 @@ struct SegIter {
     s.t0 = t0;
     s.t1 = t1;
     const int off = (int)(u - tile_u0);
-    s.blk = b0 + off;
-    s.n = (int)min((long long)(nb - off), u_end - u);
+    const int take = (int)min((long long)(nb - off), u_end - u);  // units of this stretch
+    if (kPairs && b.d == 64 && !halves(t0, t1, b)) {
+      s.blk = b0 + off / 2;
+      s.n = take / 2;
+    } else {
+      s.blk = b0 + off;
+      s.n = min(take, nblk - off);
+    }
     s.first = off == 0;
-    s.last = off + s.n == nb;
+    s.last = off + take == nb;
     // A tile that is not this CTA's alone is shared by the CTAs that own its first to its last unit.
     s.c0 = s.first ? (int)blockIdx.x : owner(tile_u0);
     s.c1 = s.last ? (int)blockIdx.x : owner(tile_u0 + nb - 1);
-    u += s.n;
+    u += take;
     if (s.last) {  // on to the next tile, head or (at the next call) sequence
       tile_u0 += nb;
       if (ntiles > 1) {
@@ -259,7 +286,7 @@ struct SegIter {
         }
         if (head < b.Hkv) {
           tile_tokens<kPairs>(tile, ps.ql, b.G, b.pair_tokens, t0, t1);
-          tile_blocks<kPairs>(t0, t1, ps.ql, ps.kvl, b.causal, b.window, b0, nb);
+          measure();
         }
       } else {
         ++head;  // one tile per head: the same blocks again
@@ -317,7 +344,7 @@ struct RopeLaunch {
   PagedBatch b;
 };
 
-cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int d, int max_q, int pair_rows,
+cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int max_q, int pair_rows,
                               cudaStream_t st);
 size_t paged_rows_workspace_bytes(int d);
 cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
@@ -329,10 +356,11 @@ struct TileMaps {
 size_t paged_tiles_workspace_bytes(int d);
 cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st);
 
-// Sequences with more rows (new tokens times heads per kv head) than this are worked off in pairs of
-// 128-row tiles; up to 16 rows they are one 16-row tile.
-constexpr int kPairRows = 16;
-inline int pair_rows_of(int G) { return G <= kTile ? kPairRows : 0x7fffffff; }
+// Sequences of more rows (new tokens times heads per kv head) than this are worked off in pairs of 128-row
+// tiles, the others in 16-row tiles (with more than 128 heads per kv head, all of them).
+// At d = 64 two 16-row tiles, which read the keys twice, still beat a 128-row one: 41 us against 49 at 32
+// rows over 60000 keys of 8 kv heads, 53 against 50 at 48 rows; at d = 128 they do not: 85 against 64.
+inline int pair_rows_of(int G, int d) { return G > kTile ? 0x7fffffff : (d == 64 ? 32 : 16); }
 cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, int num_sms, cudaStream_t st);
 
 }  // namespace fa

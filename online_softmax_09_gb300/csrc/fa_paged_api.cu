@@ -128,6 +128,7 @@ fa::PagedBatch device_batch(const fa_paged_batch* b, int num_pages, uint32_t* st
   x.Hq = b->Hq;
   x.Hkv = b->Hkv;
   x.G = b->Hq / b->Hkv;
+  x.d = b->d;
   x.page_size = b->page_size;
   while ((1 << x.page_shift) < b->page_size) ++x.page_shift;
   x.max_pages = b->max_pages;
@@ -142,7 +143,7 @@ fa::PagedBatch device_batch(const fa_paged_batch* b, int num_pages, uint32_t* st
 // Some sequence may have more rows than a 16-row tile: pairs of 128-row tiles are launched as well.
 bool with_pairs(const fa_paged_batch* b) {
   const int G = b->Hq / b->Hkv;
-  return (long long)b->max_q * G > fa::pair_rows_of(G);
+  return (long long)b->max_q * G > fa::pair_rows_of(G, b->d);
 }
 
 // Workspace: the partial results of the two kernels.
@@ -198,8 +199,8 @@ int fa_paged_plan(const int* cu_q, const int* kv_len, const fa_paged_batch* batc
   if (batch->S > 0) FA_TRY(check_ptr(kv_len, 4));
   uint32_t* status = nullptr;
   FA_TRY(fa::device_state(&status, nullptr));
-  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status), batch->d, batch->max_q,
-                               fa::pair_rows_of(batch->Hq / batch->Hkv), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status), batch->max_q,
+                               fa::pair_rows_of(batch->Hq / batch->Hkv, batch->d), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_LAUNCH;
 }

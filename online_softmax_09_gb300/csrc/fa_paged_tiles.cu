@@ -8,7 +8,9 @@
 //   warp 8     TMA producer: the pair's queries, then per block the keys and values, one box per page
 //              (lane i brings page i of the block; the table entries of the next block are read ahead).
 //              Boxes of pages that no row sees are zero-filled without looking at the table.
-//   warp 9     MMA issue: S_t = Q_t K^T, O_t += P_t V, the two tiles taking turns.
+//   warp 9     MMA issue: S_t = Q_t K^T, O_t += P_t V, the two tiles taking turns. Where a sequence has
+//              rows for one tile only, both tiles work on it, each on every other key block, so that one
+//              half's products still run beside the other's softmax; the halves are joined at the end.
 //   warps 0-7  softmax, one row per thread, four warps per tile: running max and sum in base 2, the
 //              reference max moved only when a row outgrows it by 2^8, P as bf16 over the scores'
 //              columns, and the rounding of each tile's largest weight carried along as in the dense
@@ -31,10 +33,10 @@ constexpr float kTileRescale = 8.f;
 constexpr int kSegSlots = 4;
 
 // A stretch as the producer hands it to the other warps: the blocks that each tile of its pair has work
-// in, [a, b) relative to block j0 (none: a == b).
+// in, cnt of them from block j0 + a on, `step` apart.
 struct TileSeg {
   int n_max;  // blocks that some tile has work in; -1: the end of the CTA's stretches
-  int j0, a[2], b[2], exists[2];
+  int j0, a[2], cnt[2], step, exists[2];
   int head, q0, ql, kvl, t0;
   int first, last, c0, c1;
 };
@@ -60,7 +62,9 @@ struct TileSmem {
   static constexpr int bOFree = bQEmpty + 2;
   static constexpr int bSegFull = bOFree + 2;
   static constexpr int bSegEmpty = bSegFull + kSegSlots;
-  static constexpr int bDrain = bSegEmpty + kSegSlots;
+  static constexpr int bTwin = bSegEmpty + kSegSlots;  // tile 1's half is done, and has been taken over
+  static constexpr int bTwinFree = bTwin + 1;
+  static constexpr int bDrain = bTwinFree + 1;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kTmemSlot = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemSlot + 4;
@@ -95,8 +99,16 @@ __device__ __forceinline__ TileSeg tile_seg(const Seg& s, const PagedBatch& p) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     it.a[t] = hi[t] > lo[t] ? lo[t] - it.j0 : 0;
-    it.b[t] = hi[t] > lo[t] ? hi[t] - it.j0 : 0;
-    it.n_max = max(it.n_max, it.b[t]);
+    it.cnt[t] = hi[t] - lo[t];
+    it.n_max = max(it.n_max, it.a[t] + it.cnt[t]);
+  }
+  it.step = 1;
+  if (halves(s.t0, s.t1, p) && it.n_max >= 2) {  // one tile of rows: both work on it, each on every other block
+    it.step = 2;
+    it.a[1] = 1;
+    it.cnt[0] = (it.n_max + 1) / 2;
+    it.cnt[1] = it.n_max / 2;
+    it.exists[1] = 1;
   }
   it.head = s.head;
   it.q0 = s.q0;
@@ -136,6 +148,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const PagedFwd p) {
   using L = TileSmem<D>;
+  constexpr bool kHalves = D == 64;  // see halves() in fa_paged.cuh
   constexpr int NK = L::NK, NV = L::NV;
   const PagedBatch& b = p.b;
   SegIter<true> walk(b);  // (its loads and the plan's check go out together)
@@ -180,6 +193,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(bar(L::bSegFull + s), 1);
       mbar_init(bar(L::bSegEmpty + s), 9);  // the MMA warp and the eight softmax warps
     }
+    mbar_init(bar(L::bTwin), 128);
+    mbar_init(bar(L::bTwinFree), 128);
     mbar_init(bar(L::bDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -264,7 +279,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     ok = hand_out();
     while (ok && it.n_max >= 0) {
       const int head = s.head, tok = s.q0 + s.t0, j0 = it.j0, n_max = it.n_max;
-      const bool with[2] = {it.b[0] > it.a[0], it.b[1] > it.a[1]};
+      const bool with[2] = {it.cnt[0] > 0, it.cnt[1] > 0};
+      const int tile_tok = it.step == 1 ? tpt : 0;  // from tile 0's tokens to tile 1's
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || !with[t]) continue;
@@ -273,7 +289,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           mbar_expect_tx(bar(L::bQ + t), q_bytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sQ + t * L::kTileBytes + c * 16384, &tm_q, bar(L::bQ + t), c * 64, head * b.G, tok + t * tpt);
+            tma_load_3d(sQ + t * L::kTileBytes + c * 16384, &tm_q, bar(L::bQ + t), c * 64, head * b.G,
+                        tok + t * tile_tok);
         }
         ++qn[t];
       }
@@ -389,38 +406,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       give_back(i);
       if (it.n_max < 0) break;
       if (it.n_max == 0) continue;
+      const int step = kHalves ? it.step : 1;
+      const int end[2] = {it.a[0] + (it.cnt[0] - 1) * step, it.a[1] + (it.cnt[1] - 1) * step};  // last blocks
+      auto has = [&](int t, int j) { return it.cnt[t] > 0 && it.a[t] <= j && j <= end[t] && !((j - it.a[t]) & (step - 1)); };
       bool k_ready = false;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!ok || it.b[t] == it.a[t]) continue;
+        if (!ok || it.cnt[t] == 0) continue;
         if (!(ok = mbar_wait_warp(bar(L::bQ + t), qn[t] & 1, ctl))) continue;
         ++qn[t];
         tc_fence_after();
-        if (it.a[t] == 0) {
-          if (!(ok = issue_s(t, gk, k_ready))) continue;
+        if (it.a[t] < step) {
+          if (!(ok = issue_s(t, gk + it.a[t], k_ready && step == 1))) continue;
           k_ready = true;
-          if (it.b[t] == 1) commit(bar(L::bQEmpty + t));
+          if (it.cnt[t] == 1) commit(bar(L::bQEmpty + t));
         }
       }
       if (!ok) break;
       commit(bar(L::bKEmpty + gk % NK));
+      if (step == 2) commit(bar(L::bKEmpty + (gk + 1) % NK));
       for (int j = 0; ok && j < it.n_max; ++j) {
         bool v_ready = false, k_next_ready = false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (ok && it.a[t] <= j && j < it.b[t]) {
-            if (!(ok = issue_pv(t, gv + j, j == it.a[t], j + 1 == it.b[t], v_ready))) continue;
+          if (ok && has(t, j)) {
+            if (!(ok = issue_pv(t, gv + j, j == it.a[t], j == end[t], v_ready))) continue;
             v_ready = true;
           }
-          if (ok && it.a[t] <= j + 1 && j + 1 < it.b[t]) {
-            if (!(ok = issue_s(t, gk + j + 1, k_next_ready))) continue;
+          if (ok && has(t, j + step)) {
+            if (!(ok = issue_s(t, gk + j + step, k_next_ready))) continue;
             k_next_ready = true;
-            if (j + 2 == it.b[t]) commit(bar(L::bQEmpty + t));
+            if (j + step == end[t]) commit(bar(L::bQEmpty + t));
           }
         }
         if (!ok) break;
         commit(bar(L::bVEmpty + (gv + j) % NV));
-        if (j + 1 < it.n_max) commit(bar(L::bKEmpty + (gk + j + 1) % NK));
+        if (j + step < it.n_max) commit(bar(L::bKEmpty + (gk + j + step) % NK));
       }
       gk += it.n_max;
       gv += it.n_max;
@@ -443,6 +464,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const float sl2 = p.scale_log2;
     const uint32_t o_stage = sbase + L::kOStage + (uint32_t)warp * 4096;
     uint32_t sc = 0, on = 0, gv = 0;
+    uint32_t twins = 0;  // stretches so far whose two halves were joined here
+    bool owed = false;   // (tile 1) its half of the last one has not been taken over yet
     bool ok = true;
     // 64 columns of this warp's rows of o, through its buffer, so that eight lanes write 128 neighbouring
     // bytes of a row; `out`: this thread's row (-1: none).
@@ -486,15 +509,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         give_back(i);
         continue;
       }
-      const int a_t = s.a[t];
-      const int n_kv = s.b[t] - a_t;
+      const int a_t = s.a[t], n_kv = s.cnt[t], step = kHalves ? s.step : 1;
+      const bool twin = kHalves && step == 2;
       const int kv_first = (s.j0 + a_t) * kPairBlk, kvl = s.kvl;
-      const int tok0 = s.t0 + t * tpt;
+      const int tok0 = s.t0 + (twin ? 0 : t * tpt);
       const int tok = tok0 + r_tok;
       const int pos = kvl - s.ql + tok;
       const int klim = min(kvl - 1, b.causal ? pos : kvl - 1);
       const int klo = b.window > 0 ? pos - b.window + 1 : 0;
       const int pos0 = kvl - s.ql + tok0, pos1 = pos0 + tpt - 1;
+      // A warp whose rows all lie past the tile's tokens only keeps the barriers going. (At d = 128 such a
+      // CTA waits for memory, and the test cost long chunks 2 %.)
+      const bool idle = kHalves && (warp & 3) * 32 >= min(used, (s.ql - tok0) * b.G);
+      // Rows of V past the last key (both tiles may write the same zeros): after the copy has landed,
+      // before the product that the arrival at bPFull lets start.
+      auto clear_tail = [&](int j, int kv0) -> bool {
+        const uint32_t g = gv0 + a_t + j * step, sv = g % NV;
+        if (!mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
+        for (int row = kvl - kv0 + (r >> 3); row < kPairBlk; row += 16)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            st_shared_v4(sV + sv * L::kTileBytes + c * 16384 + row * 128 + (r & 7) * 16, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        return true;
+      };
       float m_run = -INFINITY, m_hi = -INFINITY, l_run = 0.f, e_run = 0.f;
       for (int j = 0; j < n_kv; ++j) {
         if (!mbar_wait_warp(bar(L::bSFull + t), (sc + j) & 1, ctl)) {
@@ -502,8 +540,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           break;
         }
         tc_fence_after();
-        const int kv0 = kv_first + j * kPairBlk;
+        const int kv0 = kv_first + j * step * kPairBlk;
         const bool tail = kv0 + kPairBlk > kvl;
+        if (idle) {
+          if (tail && !(ok = clear_tail(j, kv0))) break;
+          mbar_arrive(bar(L::bPFull + t));
+          continue;
+        }
         const bool need_mask = tail || (b.causal && kv0 + kPairBlk - 1 > pos0) ||
                                (b.window > 0 && kv0 < pos1 - b.window + 1);
         uint32_t sr[4][32];
@@ -562,20 +605,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         l_run = l_run * corr + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
-        if (tail) {
-          // Rows of V past the last key (both tiles may write the same zeros): after the copy has
-          // landed, before the product that the arrival below lets start.
-          const uint32_t g = gv0 + a_t + j, sv = g % NV;
-          if (!mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) {
-            ok = false;
-            break;
-          }
-          for (int row = kvl - kv0 + (r >> 3); row < kPairBlk; row += 16)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              st_shared_v4(sV + sv * L::kTileBytes + c * 16384 + row * 128 + (r & 7) * 16, 0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
+        if (tail && !(ok = clear_tail(j, kv0))) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar(L::bPFull + t));
@@ -590,25 +620,73 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       const TileSeg e = s;
       give_back(i);  // before the stores: an arrival after them would wait for them
-      if (e.first && e.last) {
+      if (kHalves && owed) {  // this warp's buffer still holds its half of an earlier stretch
+        if (!(ok = mbar_wait_warp(bar(L::bTwinFree), (twins - 1) & 1, ctl))) break;
+        owed = false;
+      }
+      float4* half = reinterpret_cast<float4*>(smem + L::kOStage + (4 + (warp & 3)) * 4096) + lane;
+      if (twin && t == 1) {  // over to tile 0: o stays in tensor memory
+        *half = make_float4(m_run, l_run, e_run, 0.f);
+        tc_fence_before();
+        mbar_arrive(bar(L::bTwin));
+        ++twins;
+        owed = true;
+        continue;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      if (twin) {
+        if (!(ok = mbar_wait_warp(bar(L::bTwin), twins & 1, ctl))) break;
+        ++twins;
+        tc_fence_after();
+        const float4 h = *half;
+        const float mn = fmaxf(m_run, h.x), mu = mn == -INFINITY ? 0.f : mn;
+        f0 = ex2(m_run - mu);
+        f1 = ex2(h.x - mu);
+        m_run = mn;
+        l_run = l_run * f0 + h.y * f1;
+        e_run = e_run * f0 + h.z * f1;
+      }
+      auto read_o = [&](int c, float (&f)[32]) {  // 32 columns of the row's sums
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        if (twin) {
+          uint32_t o1[32];
+          tmem_ld32(tO + 128 + c * 32, o1);
+          tmem_ld_wait(o1);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1;
+        } else {
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(o[k]);
+        }
+      };
+      auto o_read = [&]() {  // the accumulators may be overwritten
+        tc_fence_before();
+        if (n_kv > 0) mbar_arrive(bar(L::bOFree + t));
+        if (twin) {
+          mbar_arrive(bar(L::bOFree + 1));
+          mbar_arrive(bar(L::bTwinFree));
+        }
+      };
+      if (idle) {
+        o_read();
+      } else if (e.first && e.last) {
         const float inv = (l_run > 0.f || l_run != l_run) ? 1.f / (l_run + e_run) : 0.f;  // nothing seen: o = 0
         uint4 w[D / 64][2][4];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
+          float f[32];
           if (n_kv > 0) {
-            tmem_ld32(tO + c * 32, o);
-            tmem_ld_wait(o);
+            read_o(c, f);
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0;
+            for (int k = 0; k < 32; ++k) f[k] = 0.f;
           }
-          pack(w[c >> 1][c & 1], reinterpret_cast<const float*>(o), inv);
+          pack(w[c >> 1][c & 1], f, inv);
         }
-        if (n_kv > 0) {
-          tc_fence_before();
-          mbar_arrive(bar(L::bOFree + t));
-        }
+        o_read();
         const long long out = row_out(e.q0, tok, e.ql, e.head);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) store_cols(w[c], c, out);
@@ -618,17 +696,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (n_kv > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + c * 32, o);
-            tmem_ld_wait(o);
+            float f[32];
+            read_o(c, f);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(slot + ((c * 8 + k) * kTile + r) * 4) =
-                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              *reinterpret_cast<float4*>(slot + ((c * 8 + k) * kTile + r) * 4) =
+                  make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
           }
-          tc_fence_before();
-          mbar_arrive(bar(L::bOFree + t));
         }
+        o_read();
         slot[D * kTile + r] = m_run;  // -inf: nothing seen here, and o is not there
         slot[(D + 1) * kTile + r] = l_run;
         slot[(D + 2) * kTile + r] = e_run;

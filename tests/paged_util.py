@@ -10,7 +10,8 @@ attention: a score is off by e_s = 2 d 2^-24 scale sum|q k| (fp32 accumulation i
   weight therefore by 2 e_s + 2^-20 (exp2 and the reference's rescales), and by 2^-8 once rounded for the product
   with V. o is the weighted mean under the rounded weights, so with eps = 2^-8 + 2 e_s + 2^-20 and weights p:
   |o - ref| <= 1.02 eps sum_j p_j |v_j - ref| + 2^-8 |ref| + 2^-20 max|v|  (fp32 sums of the products: the last).
-  So it is in the 16-row tiles, whose rounded weights are summed. The pairs of 128-row tiles (more than 16 rows) divide
+  So it is in the 16-row tiles, whose rounded weights are summed. The pairs of 128-row tiles (sequences of more
+  than 16 rows, new tokens times heads per kv head, or 32 at d = 64) divide
   by the sum of the weights before rounding, plus the rounding of each block's largest one: with p'_j = p_j (1 + d_j),
   |d_j| <= 2^-8, and M the blocks' largest,
       o' - ref = sum_j p_j d_j v_j - ref sum_{j in M} p_j d_j  (to first order),
@@ -71,6 +72,7 @@ def attention_ref(q, K, V, n, causal, window, scale):
     """One sequence: q [ql, Hq, d], K, V [n, Hkv, d] fp64 -> o, lse and their tolerances."""
     ql, Hq, d = q.shape
     G = Hq // K.shape[1] if n else 1
+    pairs = G <= 128 and ql * G > (32 if d == 64 else 16)
     o = np.zeros((ql, Hq, d))
     lse = np.full((ql, Hq), -np.inf)
     to, tl = np.zeros((ql, Hq, d)), np.zeros((ql, Hq))
@@ -91,7 +93,7 @@ def attention_ref(q, K, V, n, causal, window, scale):
             o[j, h] = w @ v
             lse[j, h] = m + math.log(s)
             spread = w @ np.abs(v - o[j, h])
-            rounding = w @ np.abs(v) + np.abs(o[j, h]) if ql * G > 16 and G <= 128 else spread
+            rounding = w @ np.abs(v) + np.abs(o[j, h]) if pairs else spread
             to[j, h] = 1.02 * (BF * rounding + (2 * es + 2.0 ** -20) * spread) + BF * np.abs(o[j, h])
             to[j, h] += 2.0 ** -20 * np.abs(v).max()
             tl[j, h] = es + 2.0 ** -20 + ((hi - lo) / 64 + 16) * 2.0 ** -24 + 2.0 ** -22 * abs(lse[j, h])

@@ -62,6 +62,27 @@ def test_long_chunks(lens, heads):
     _run(Batch(lens, *heads, 64, 16, seed=lens[0][0]), window=200)
 
 
+@pytest.mark.parametrize("keys", [1, 128, 129, 256, 257, 384, 700, 1500])
+@pytest.mark.parametrize("new", [9, 20, 32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_of_one_tile(keys, new, d):
+    # At most 128 rows: both halves of the pairs' kernel take every other key block; one block, odd and even counts.
+    _run(Batch([(min(new, keys), keys)], 8, 2, d, 16, seed=keys + new))
+    _run(Batch([(min(new, keys), keys), (1, 300), (min(new, keys), 2 * keys)], 4, 1, d, 64, seed=keys), window=150)
+
+
+@pytest.mark.parametrize("heads", [(4, 1), (8, 8), (6, 2)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_and_two_tiles_and_single_tokens_in_one_batch(heads, d):
+    r = np.random.default_rng(heads[0] + d)
+    lens = [(1, int(r.integers(1, 900))) for _ in range(20)] + [(150, 400), (1, 0), (0, 70), (40, 1000), (300, 333),
+                                                               (2, 5), (33, 33)]
+    b = Batch([lens[i] for i in r.permutation(len(lens))], *heads, d, 32, seed=6, pad=2)
+    o, lse = _run(b)
+    o2, lse2 = _run(b)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("layout", ["pshd", "both"])
 @pytest.mark.parametrize("lens", [[(1, 100), (1, 333)], [(90, 300), (1, 77)]])
 def test_cache_layouts_and_strided_queries(layout, lens):
