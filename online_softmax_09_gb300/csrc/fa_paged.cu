@@ -159,92 +159,143 @@ struct RowSmem {
 template <int D>
 constexpr int kRowPart = kRowTile * (D + 3);
 
-// The pairs of 128-row tiles that several CTAs of the kernel before shared: their partial results joined
-// in the order of the keys, 16 rows at a time, all of this grid's CTAs together. (Joined by the last CTA
-// to finish each tile, on 64 of 152 SMs, this took 18 us at 512 tokens over 32768 keys; here 6.)
+// The tiles of 128 rows that several CTAs of the kernel before shared: their partial results joined in the
+// order of the keys, 16 rows at a time, all of this grid's CTAs together, two such pieces per CTA under way
+// at once. (512 tokens over 32768 keys: about 9 us; joined by the last CTA to finish each tile, on 64 of 152
+// SMs, 18 us.)
+template <int D>
+struct JoinPiece {
+  static constexpr int kAtOnce = 4;  // partial results whose loads go out together
+  TileShare s;
+  int c0, t, r, tok;
+  bool on;
+  float4 v[kAtOnce][D / 32];
+  float mi[kAtOnce], li[kAtOnce], ei[kAtOnce];
+  float M, Ls, Es, acc[D / 8];
+  __device__ __forceinline__ const float* part(const PagedFwd& p, int c) const {
+    return p.tile_part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
+  }
+  __device__ __forceinline__ void load(const PagedFwd& p, int c) {
+    if (!on) return;
+    const int g0 = threadIdx.x >> 4;  // columns 4 * (g0 + 8 i) ..
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      const float* src = part(p, min(c + y, s.c1));
+      mi[y] = src[D * kTile + r];
+      li[y] = src[(D + 1) * kTile + r];
+      ei[y] = src[(D + 2) * kTile + r];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) v[y][i] = *reinterpret_cast<const float4*>(src + ((g0 + 8 * i) * kTile + r) * 4);
+    }
+  }
+  __device__ __forceinline__ void add(int c) {
+    if (!on) return;
+#pragma unroll
+    for (int y = 0; y < kAtOnce; ++y) {
+      if (c + y > s.c1 || mi[y] == -INFINITY) continue;  // nothing seen there: o was not written
+      const float mn = fmaxf(M, mi[y]);
+      const float fa = ex2(M - mn), fb = ex2(mi[y] - mn);
+      M = mn;
+      Ls = Ls * fa + fb * li[y];
+      Es = Es * fa + fb * ei[y];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        acc[4 * i] = acc[4 * i] * fa + fb * v[y][i].x;
+        acc[4 * i + 1] = acc[4 * i + 1] * fa + fb * v[y][i].y;
+        acc[4 * i + 2] = acc[4 * i + 2] * fa + fb * v[y][i].z;
+        acc[4 * i + 3] = acc[4 * i + 3] * fa + fb * v[y][i].w;
+      }
+    }
+  }
+};
+
 template <int D>
 __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before is complete
   const PagedBatch& b = p.b;
   const int tpt = b.pair_tokens >> 1, used = tpt * b.G;
-  // The shared tiles, listed by every CTA for itself (one read of all the descriptors).
+  // The shared tiles, listed by every CTA for itself: all descriptors are read at once.
   extern __shared__ __align__(1024) uint8_t smem[];
-  short* list = reinterpret_cast<short*>(smem);
-  int* count = reinterpret_cast<int*>(smem + 2 * kPagedSms * sizeof(short));
+  struct Entry {
+    TileShare s;
+    int x;  // 2 * first CTA + tile
+  };
+  Entry* list = reinterpret_cast<Entry*>(smem);
+  int* counts = reinterpret_cast<int*>(smem + 2 * kPagedSms * sizeof(Entry));  // of each warp
+  constexpr int kEach = (2 * kPagedSms + kRowThreads - 1) / kRowThreads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  TileShare mine[kEach];
+  uint32_t some[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int x = i * kRowThreads + threadIdx.x;
+    mine[i].c1 = -1;
+    if (x < 2 * p.tile_ctas) mine[i] = p.share[x];
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    some[i] = __ballot_sync(0xffffffffu, mine[i].c1 >= 0);
+    n += __popc(some[i]);
+  }
+  __syncthreads();  // the rows' use of this memory is over
+  if (lane == 0) counts[warp] = n;
   __syncthreads();
-  if (threadIdx.x < 32) {
-    int n = 0;
-    constexpr int kRounds = 2 * kPagedSms / 32;
-    int c1[kRounds];
+  int at = 0, total = 0;
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int x = i * 32 + threadIdx.x;
-      c1[i] = x < 2 * p.tile_ctas ? p.share[x].c1 : -1;
-    }
+  for (int w = 0; w < kRowWarps; ++w) {
+    at += w < warp ? counts[w] : 0;
+    total += counts[w];
+  }
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const uint32_t some = __ballot_sync(0xffffffffu, c1[i] >= 0);
-      if (c1[i] >= 0) list[n + __popc(some & ((1u << threadIdx.x) - 1))] = (short)(i * 32 + threadIdx.x);
-      n += __popc(some);
-    }
-    if (threadIdx.x == 0) *count = n;
+  for (int i = 0; i < kEach; ++i) {
+    if (mine[i].c1 >= 0) list[at + __popc(some[i] & ((1u << lane) - 1))] = Entry{mine[i], i * kRowThreads + (int)threadIdx.x};
+    at += __popc(some[i]);
   }
   __syncthreads();
-  const int units = *count * (kTile / 16);
-  for (int x = blockIdx.x; x < units; x += gridDim.x) {
-    const int c0 = list[x >> 3] >> 1, t = list[x >> 3] & 1;
-    const TileShare s = p.share[2 * c0 + t];
-    const int r = (x & 7) * 16 + (threadIdx.x & 15);
-    const int tok = s.tok0 + r / b.G;
-    if (r >= used || tok >= s.ql) continue;
-    auto part = [&](int c) {
-      return p.tile_part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
-    };
-    const int g0 = threadIdx.x >> 4;  // columns 4 * (g0 + 8 i) ..
-    float M = -INFINITY, Ls = 0.f, Es = 0.f, acc[D / 8];
+  const int units = total * (kTile / 16);
+  const int g0 = threadIdx.x >> 4;
+  for (int x = blockIdx.x; x < units; x += 2 * gridDim.x) {
+    JoinPiece<D> j[2];
+    int longest = 0;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[i] = 0.f;
-    constexpr int kAtOnce = 4;
-    for (int c = c0; c <= s.c1; c += kAtOnce) {
-      float4 v[kAtOnce][D / 32];
-      float mi[kAtOnce], li[kAtOnce], ei[kAtOnce];
+    for (int k = 0; k < 2; ++k) {
+      const int u = x + k * gridDim.x;
+      j[k].on = u < units;
+      if (!j[k].on) continue;
+      const Entry& e = list[u >> 3];
+      j[k].s = e.s;
+      j[k].c0 = e.x >> 1;
+      j[k].t = e.x & 1;
+      j[k].r = (u & 7) * 16 + (threadIdx.x & 15);
+      j[k].tok = e.s.tok0 + j[k].r / b.G;
+      j[k].on = j[k].r < used && j[k].tok < e.s.ql;
+      j[k].M = -INFINITY;
+      j[k].Ls = j[k].Es = 0.f;
 #pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) {  // the loads of several results together
-        const float* src = part(min(c + y, s.c1));
-        mi[y] = src[D * kTile + r];
-        li[y] = src[(D + 1) * kTile + r];
-        ei[y] = src[(D + 2) * kTile + r];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          v[y][i] = *reinterpret_cast<const float4*>(src + ((g0 + 8 * i) * kTile + r) * 4);
-      }
-#pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) {
-        if (c + y > s.c1 || mi[y] == -INFINITY) continue;  // nothing seen there: o was not written
-        const float mn = fmaxf(M, mi[y]);
-        const float fa = ex2(M - mn), fb = ex2(mi[y] - mn);
-        M = mn;
-        Ls = Ls * fa + fb * li[y];
-        Es = Es * fa + fb * ei[y];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          acc[4 * i] = acc[4 * i] * fa + fb * v[y][i].x;
-          acc[4 * i + 1] = acc[4 * i + 1] * fa + fb * v[y][i].y;
-          acc[4 * i + 2] = acc[4 * i + 2] * fa + fb * v[y][i].z;
-          acc[4 * i + 3] = acc[4 * i + 3] * fa + fb * v[y][i].w;
-        }
-      }
+      for (int i = 0; i < D / 8; ++i) j[k].acc[i] = 0.f;
+      longest = max(longest, e.s.c1 - j[k].c0 + 1);
     }
-    const float inv = (Ls > 0.f || Ls != Ls) ? 1.f / (Ls + Es) : 0.f;
-    const long long out = (long long)(s.q0 + tok) * b.Hq + s.head * b.G + r % b.G;
+    for (int c = 0; c < longest; c += JoinPiece<D>::kAtOnce) {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint2 w;
-      w.x = pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv);
-      w.y = pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
-      *reinterpret_cast<uint2*>(p.o + out * D + (g0 + 8 * i) * 4) = w;
+      for (int k = 0; k < 2; ++k) j[k].load(p, j[k].c0 + c);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) j[k].add(j[k].c0 + c);
     }
-    if (g0 == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!j[k].on) continue;
+      const float inv = (j[k].Ls > 0.f || j[k].Ls != j[k].Ls) ? 1.f / (j[k].Ls + j[k].Es) : 0.f;
+      const long long out = (long long)(j[k].s.q0 + j[k].tok) * b.Hq + j[k].s.head * b.G + j[k].r % b.G;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint2 w;
+        w.x = pack_bf16(j[k].acc[4 * i] * inv, j[k].acc[4 * i + 1] * inv);
+        w.y = pack_bf16(j[k].acc[4 * i + 2] * inv, j[k].acc[4 * i + 3] * inv);
+        *reinterpret_cast<uint2*>(p.o + out * D + (g0 + 8 * i) * 4) = w;
+      }
+      if (g0 == 0) p.lse[out] = (j[k].M + log2f(j[k].Ls)) * 0.6931471805599453f;
+    }
   }
 }
 
