@@ -37,7 +37,7 @@ namespace {
 // Per-device status word written by kernels whose pipeline waits time out.
 __device__ uint32_t g_fa_status;
 
-constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = fa::kMaxGpus;
 struct DeviceState {
   bool init = false;
   bool supported = false;
@@ -110,6 +110,19 @@ unsigned long long fa::current_context_id() {
 }
 
 int fa::check_current_device() { return current_device(nullptr); }
+
+cudaError_t fa::allow_smem(const void* kernel, int smem, unsigned long long* known) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  const unsigned long long ctx = fa::current_context_id();
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (ctx != 0 && known[dev] == ctx) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) known[dev] = ctx;
+  return e;
+}
 
 int fa::device_state(uint32_t** status, int* num_sms) { return current_device(status, num_sms); }
 

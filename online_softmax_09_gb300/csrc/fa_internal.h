@@ -93,6 +93,12 @@ int check_current_device();
 // The same, with the device's status word and its number of SMs (each may be NULL).
 int device_state(uint32_t** status, int* num_sms);
 
+constexpr int kMaxGpus = 64;  // devices that a process may use
+
+// Allows `smem` bytes of dynamic shared memory to a kernel, once per device and context: *known (one per
+// kernel and device) remembers the context it was done in.
+cudaError_t allow_smem(const void* kernel, int smem, unsigned long long* known);
+
 // cuTensorMapEncodeTiled, or NULL if the driver has none.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 

@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
 template <int D>
 static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) {
   constexpr int smem = RowSmem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(fa_paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static unsigned long long known[kMaxGpus];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_rows_kernel<D>), smem, known);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * num_sms);

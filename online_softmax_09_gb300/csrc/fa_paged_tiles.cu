@@ -724,7 +724,8 @@ template <int D>
 static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, int num_sms, cudaStream_t st) {
   constexpr int smem = TileSmem<D>::kAlloc;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-CTA limit");
-  cudaError_t e = cudaFuncSetAttribute(fa_paged_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static unsigned long long known[kMaxGpus];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_tiles_kernel<D>), smem, known);
   if (e != cudaSuccess) return e;
   fa_paged_tiles_kernel<D><<<num_sms, kTileThreads, smem, st>>>(m.q, m.k, m.v, p);
   return cudaGetLastError();

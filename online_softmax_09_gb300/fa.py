@@ -40,7 +40,7 @@ class _Cache(ctypes.Structure):  # fa_paged_cache
         ("num_pages", _i)]
 
 
-_ll = [ctypes.c_longlong * n for n in range(13)]  # (array types, made once)
+_ll2, _ll8, _ll12 = (ctypes.c_longlong * n for n in (2, 8, 12))  # (array types, made once)
 
 
 class FAError(RuntimeError):
@@ -468,7 +468,7 @@ def _rope(name, fn, q, k, positions, rotary, q_out, k_out, stream):
         kp, kop = k.data_ptr(), k_out.data_ptr()
     if N == 0 or B == 0:
         return q_out, k_out
-    r = fn(q.data_ptr(), q_out.data_ptr(), kp, kop, _ll[12](*st), positions.data_ptr(), n // A,
+    r = fn(q.data_ptr(), q_out.data_ptr(), kp, kop, _ll12(*st), positions.data_ptr(), n // A,
            N if B > 1 and n == A * B * N else 0, rotary._ref, B, Hq, kshape[1] if k is not None else 0, N, d,
            _stream_of(stream, i))
     if r != FA_OK:
@@ -517,10 +517,15 @@ class PagedPlan:
         return raw
 
     def _cache(self, k_cache, v_cache):
-        shape = (k_cache.shape[0],) + self.page_shape
-        ks = _strides_of("k_cache", k_cache, shape, self.index)
-        vs = _strides_of("v_cache", v_cache, shape, self.index)
-        return ctypes.byref(_Cache(k_cache.data_ptr(), v_cache.data_ptr(), *ks[:3], *vs[:3], shape[0]))
+        shape, i = k_cache.shape, self.index
+        ka, kb, kc, kd = k_cache.stride()
+        va, vb, vc, vd = v_cache.stride()
+        if shape[1:] != self.page_shape or v_cache.shape != shape or k_cache.dtype != torch.bfloat16 \
+                or v_cache.dtype != torch.bfloat16 or kd != 1 or vd != 1 or k_cache.get_device() != i \
+                or v_cache.get_device() != i:
+            raise ValueError("k_cache and v_cache must be bfloat16 CUDA tensors [pages, Hkv, page_size, d] "
+                             f"(here [pages, {', '.join(map(str, self.page_shape))}]) with contiguous last dim")
+        return ctypes.byref(_Cache(k_cache.data_ptr(), v_cache.data_ptr(), ka, kb, kc, va, vb, vc, shape[0]))
 
 
 def paged_plan(cu_q, kv_lens, block_table, num_tokens: int, max_q: int, page_size: int, Hq: int, Hkv: int, d: int,
@@ -561,8 +566,8 @@ def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q
     any strides with contiguous last dim. positions: int32 CUDA [T], or [A,T] for several axes; None: each token's
     position in its sequence."""
     i = plan.index
-    if not k.is_cuda or _dev_index(k) != i:
-        raise ValueError("k is not on the plan's device")
+    if i != torch._C._cuda_getDevice():
+        _dev_index(k)
     qp = qop = None
     if q is not None:
         if rotary is None:
@@ -589,7 +594,7 @@ def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q
         pp = positions.data_ptr()
     if rotary is not None and rotary.index != i:
         raise ValueError("rotary is on another device")
-    r = lib().fa_paged_append(qp, qop, k.data_ptr(), v.data_ptr(), _ll[8](*st), plan._cache(k_cache, v_cache),
+    r = (_lib or lib()).fa_paged_append(qp, qop, k.data_ptr(), v.data_ptr(), _ll8(*st), plan._cache(k_cache, v_cache),
                               plan._ref, rotary._ref if rotary is not None else None, pp, T, plan._use(stream, i))
     if r != FA_OK:
         raise FAError(r, "fa_paged_append")
@@ -600,20 +605,23 @@ def forward_paged(q, k_cache, v_cache, plan, scale: float | None = None, out=Non
     """O [T,Hq,d], LSE [T,Hq]: attention of a step's new tokens over the paged cache (fa_fwd_paged). q [T,Hq,d] bf16
     CUDA, any strides with contiguous last dim. Rows that belong to no sequence are left as they were."""
     shape, i = plan.q_shape, plan.index
-    if not q.is_cuda or _dev_index(q) != i:
-        raise ValueError("q is not on the plan's device")
-    st = _strides_of("q", q, shape, i)[:2]
+    st = _strides_of("q", q, shape, i)
+    if i != torch._C._cuda_getDevice():
+        _dev_index(q)
+    if out is not None and not (_strides_of("out", out, shape, i) and out.is_contiguous()):
+        raise ValueError("out must be contiguous")
+    if lse is not None and (lse.dtype != torch.float32 or lse.get_device() != i or lse.shape != plan.lse_shape
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
+    cache = plan._cache(k_cache, v_cache)
+    raw = plan._use(stream, i)
     if out is None:
         out = _empty(shape, torch.bfloat16, q.device, stream)
-    elif _strides_of("out", out, shape, i) and not out.is_contiguous():
-        raise ValueError("out must be contiguous")
     if lse is None:
         lse = _empty(plan.lse_shape, torch.float32, q.device, stream)
-    elif lse.dtype != torch.float32 or lse.get_device() != i or lse.shape != plan.lse_shape or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
-    r = lib().fa_fwd_paged(q.data_ptr(), _ll[2](*st), plan._cache(k_cache, v_cache), plan._ref, out.data_ptr(),
-                           lse.data_ptr(), 0.0 if scale is None else float(scale), plan.workspace.data_ptr(),
-                           plan.ws_bytes, plan._use(stream, i))
+    r = (_lib or lib()).fa_fwd_paged(q.data_ptr(), _ll2(st[0], st[1]), cache, plan._ref, out.data_ptr(),
+                                     lse.data_ptr(), 0.0 if scale is None else float(scale),
+                                     plan.workspace.data_ptr(), plan.ws_bytes, raw)
     if r != FA_OK:
         raise FAError(r, "fa_fwd_paged")
     return out, lse
