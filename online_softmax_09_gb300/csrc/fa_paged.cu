@@ -145,14 +145,20 @@ __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(_
 constexpr int kRowWarps = 4, kRowThreads = 32 * kRowWarps;
 constexpr int kGran = kRowBlk / kRowWarps;  // keys that one warp takes at a time: 16, within one page
 
+constexpr int kHalfRows = kRowTile / 2;  // rows that the warps join at a time
+
 template <int D>
 struct RowSmem {
   static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kTile = kGran * D * 2;       // K or V of one granule
+  static constexpr int kSlots = D == 128 ? 4 : 8;   // stretches in the queue: the one before, the present one, those ahead
+  static constexpr int kTile = kGran * D * 2;        // K or V of one granule
   static constexpr int kWarp = kStages * 2 * kTile;  // ring of one warp
-  static constexpr int kStat = kRowWarps * kWarp;    // m, l, rounded l of each warp's 16 rows
-  static constexpr int kFlag = kStat + kRowWarps * 3 * kRowTile * 4;
-  static constexpr int kBytes = kFlag + 16;
+  static constexpr int kMerge = kRowWarps * kWarp;   // 8 rows of o of each warp
+  static constexpr int kStat = kMerge + kRowWarps * kHalfRows * D * 4;  // m, l, rounded l of each warp's 16 rows
+  static constexpr int kQueue = kStat + kRowWarps * 3 * kRowTile * 4;
+  static constexpr int kFlag = kQueue + kSlots * (int)sizeof(Seg);
+  static constexpr int kBytes = (kFlag + 4 + 15) / 16 * 16;
+  static_assert(kBytes <= 115712, "two CTAs must fit an SM");
 };
 
 // A partial result of one CTA: o [16][D], then m, l, rounded l of the 16 rows.
@@ -302,8 +308,11 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
 // fa_paged_rows_kernel: tiles of 16 rows. Four warps per CTA, two CTAs per SM; each warp takes every
 // fourth granule of 16 keys with a ring of its own, so no barrier stands in the loop: it waits for its
 // own cp.async copies, forms the 16 x 16 scores (m16n8k16), carries its own running max and sums, and
-// adds P V. The four warps' results are joined once per stretch, and the stretches of a tile that
-// several CTAs share by the CTA that finishes last, in the order of the keys.
+// adds P V. The ring runs on across the CTA's stretches: the copies of the next ones are under way while
+// one is finished (a stretch of a short sequence is a few granules, and its chain of table, keys, join and
+// store would stand in the open each time). The four warps' results are joined once per stretch, eight rows
+// at a time, and the stretches of a tile that several CTAs share by the CTA that finishes last, in the order
+// of the keys.
 //
 // Weights are rounded to bf16 for the product with V; o is divided by the sum of the rounded weights,
 // so a row that one key dominates is not off by that rounding, and lse holds the unrounded sum.
@@ -317,7 +326,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t ring = sbase + warp * L::kWarp;
+  float* merge = reinterpret_cast<float*>(smem + L::kMerge);
   float* stat = reinterpret_cast<float*>(smem + L::kStat);
+  Seg* queue = reinterpret_cast<Seg*>(smem + L::kQueue);
   int* flag = reinterpret_cast<int*>(smem + L::kFlag);
   const PagedBatch& b = p.b;
   SegIter<false> it(b);  // (its loads and the plan's check go out together)
@@ -332,58 +343,77 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
   const int krow = (lane & 7) + ((lane >> 4) << 3), kchk = (lane >> 3) & 1;  // K: keys 0-7 | 8-15, chunk 0 | 1
   const int vrow = lane & 15, vchk = lane >> 4;                              // V: keys 0-15, chunk 0 | 1
   const int g = lane >> 2, c2 = (lane & 3) * 2;                              // rows g, g + 8; columns c2, c2 + 1
+  const unsigned G = b.G;
 
-  Seg s;
-  while (it.next(s)) {
-    const unsigned G = b.G, r0 = (unsigned)s.tile * kRowTile;
+  // The copying side: the stretch it is at, taken from the walk and put in the queue. (All warps put the
+  // same stretches in the same slots. A warp is at most kStages - 1 granules, so that many stretches, ahead
+  // of its own computing, and computing warps are never a stretch apart.)
+  uint32_t fetched = 0;     // stretches put in the queue
+  uint32_t copied = 0;      // granules copied, of all stretches
+  int ln = 0, li = 0;       // granules of the stretch, and the next one
+  int lkey = 0, llo = 0, lhi = 0, lhead = 0;
+  const int* ltab = nullptr;
+  int pages = -1;           // lane i: the page of granule (li & ~31) + i
+  auto read_pages = [&]() {
+    const int key = lkey + (li + lane) * kRowBlk;
+    const bool in = li + lane < ln && key < lhi && key + kGran > llo;
+    pages = in ? ltab[key >> b.page_shift] : -1;
+    if (in && (unsigned)pages >= (unsigned)b.num_pages) {
+      record_index_error(b.status);
+      pages = -1;
+    }
+  };
+  auto fetch = [&]() {
+    Seg s;
+    ln = li = 0;
+    if (!it.next(s)) return;
+    if (lane == 0) queue[fetched % L::kSlots] = s;
+    __syncwarp();
+    ++fetched;
+    ln = s.n;
+    lhead = s.head;
+    lkey = s.blk * kRowBlk + warp * kGran;  // first key of this warp's granule 0
+    key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, llo, lhi);
+    ltab = b.table + (long long)s.seq * b.table_stride;
+    read_pages();
+  };
+  auto issue = [&]() {  // the next granule's copies, one group (an empty one once all are issued)
+    if (li < ln) {
+      const int page = __shfl_sync(0xffffffffu, pages, li & 31);
+      const int key = lkey + li * kRowBlk;
+      const int slot = key & (b.page_size - 1);
+      const uint32_t st = ring + (copied % L::kStages) * 2 * L::kTile;
+      const long long pg = page < 0 ? 0 : page;
+      const __nv_bfloat16* kp = p.c.k + pg * p.c.k_page + lhead * p.c.k_head + cchunk * 8;
+      const __nv_bfloat16* vp = p.c.v + pg * p.c.v_page + lhead * p.c.v_head + cchunk * 8;
+#pragma unroll
+      for (int r = 0; r < kGran; r += kRowsPer) {
+        const int row = r + crow;
+        const bool in = page >= 0 && key + row >= llo && key + row < lhi;
+        const uint32_t dst = st + row * (D * 2) + ((cchunk ^ (row & 7)) << 4);
+        cp_async16(dst, kp + (in ? (slot + row) * p.c.k_tok : 0), in);
+      }
+#pragma unroll
+      for (int r = 0; r < kGran; r += kRowsPer) {
+        const int row = r + crow;
+        const bool in = page >= 0 && key + row >= llo && key + row < lhi;
+        const uint32_t dst = st + L::kTile + row * (D * 2) + ((cchunk ^ (row & 7)) << 4);
+        cp_async16(dst, vp + (in ? (slot + row) * p.c.v_tok : 0), in);
+      }
+      ++copied;
+      if (++li == ln) fetch();  // (the look-ups of the next stretch are under way before they are needed)
+      else if ((li & 31) == 0) read_pages();
+    }
+    cp_async_commit();
+  };
+
+  // The computing side: queries as A operands, zero rows past the tile; visible keys [klo, klim] of the
+  // lane's two rows, and those that every row sees (a granule inside them needs no mask).
+  uint32_t qa[D / 16][4];
+  int klo[2], klim[2], all_lo = 0, all_lim = 0;
+  auto load_q = [&](const Seg& s) {
+    const unsigned r0 = (unsigned)s.tile * kRowTile;
     const int rows = (int)min((unsigned)kRowTile, (unsigned)s.ql * G - r0);
-    int lo, hi;
-    key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
-    const int* tab = b.table + (long long)s.seq * b.table_stride;
-    const int key0 = s.blk * kRowBlk + warp * kGran;  // first key of this warp's granule 0
-    int pages = 0;                                    // lane i: the page of granule (i0 & ~31) + i
-    const __nv_bfloat16* kh = p.c.k + s.head * p.c.k_head + cchunk * 8;
-    const __nv_bfloat16* vh = p.c.v + s.head * p.c.v_head + cchunk * 8;
-
-    auto issue = [&](int i) {
-      if ((i & 31) == 0) {
-        const int key = key0 + (i + lane) * kRowBlk;
-        const bool in = i + lane < s.n && key < hi && key + kGran > lo;
-        pages = in ? tab[key >> b.page_shift] : -1;
-        if (in && (unsigned)pages >= (unsigned)b.num_pages) {
-          record_index_error(b.status);
-          pages = -1;
-        }
-      }
-      if (i < s.n) {
-        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-        const int key = key0 + i * kRowBlk;
-        const int slot = key & (b.page_size - 1);
-        const uint32_t st = ring + (i % L::kStages) * 2 * L::kTile;
-        const long long pg = page < 0 ? 0 : page;
-#pragma unroll
-        for (int r = 0; r < kGran; r += kRowsPer) {
-          const int row = r + crow;
-          const bool in = page >= 0 && key + row >= lo && key + row < hi;
-          const uint32_t dst = st + row * (D * 2) + ((cchunk ^ (row & 7)) << 4);
-          cp_async16(dst, kh + pg * p.c.k_page + (in ? (slot + row) * p.c.k_tok : 0), in);
-        }
-#pragma unroll
-        for (int r = 0; r < kGran; r += kRowsPer) {
-          const int row = r + crow;
-          const bool in = page >= 0 && key + row >= lo && key + row < hi;
-          const uint32_t dst = st + L::kTile + row * (D * 2) + ((cchunk ^ (row & 7)) << 4);
-          cp_async16(dst, vh + pg * p.c.v_page + (in ? (slot + row) * p.c.v_tok : 0), in);
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < L::kStages - 1; ++i) issue(i);
-
-    // Queries as A operands, zero rows past the tile; visible keys [klo, klim] of the lane's two rows.
-    uint32_t qa[D / 16][4];
-    int klo[2], klim[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = g + 8 * h;
@@ -400,28 +430,36 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
       klim[h] = b.causal ? pos : s.kvl - 1;
       klo[h] = b.window > 0 ? pos - b.window + 1 : 0;
     }
-    // Granules inside every row's range need no mask.
-    const int all_lo = __reduce_max_sync(0xffffffffu, max(klo[0], klo[1]));
-    const int all_lim = __reduce_min_sync(0xffffffffu, min(klim[0], klim[1]));
+    all_lo = __reduce_max_sync(0xffffffffu, max(klo[0], klo[1]));
+    all_lim = __reduce_min_sync(0xffffffffu, min(klim[0], klim[1]));
+  };
 
+  fetch();
+#pragma unroll
+  for (int i = 0; i < L::kStages - 1; ++i) issue();
+  if (fetched > 0) load_q(queue[0]);
+  uint32_t done = 0;  // granules computed, of all stretches
+  for (uint32_t k = 0; k < fetched; ++k) {
+    const Seg& s = queue[k % L::kSlots];
+    const int n = s.n, key0 = s.blk * kRowBlk + warp * kGran;
     float o[kNT][4];
 #pragma unroll
     for (int j = 0; j < kNT; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+      for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lr[2] = {0.f, 0.f};
 
-    for (int i = 0; i < s.n; ++i) {
-      issue(i + L::kStages - 1);
+    for (int i = 0; i < n; ++i, ++done) {
+      issue();
       cp_async_wait<L::kStages - 1>();
       __syncwarp();
-      const uint32_t sk = ring + (i % L::kStages) * 2 * L::kTile, sv = sk + L::kTile;
+      const uint32_t sk = ring + (done % L::kStages) * 2 * L::kTile, sv = sk + L::kTile;
       const int key = key0 + i * kRowBlk;
       float x[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[t][k] = 0.f;
+        for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t kb[4];
@@ -433,9 +471,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int kx = key + 8 * t + c2 + (k & 1);
-            if (kx > klim[k >> 1] || kx < klo[k >> 1]) x[t][k] = -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            const int kx = key + 8 * t + c2 + (e & 1);
+            if (kx > klim[e >> 1] || kx < klo[e >> 1]) x[t][e] = -INFINITY;
           }
       }
       float mt[2];
@@ -486,7 +524,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
       __syncwarp();  // the stage is read: the next copies may overwrite it
     }
 
-    // ---- join the four warps: each leaves o in its own ring (drained), m and the sums in `stat`
+    // ---- join the four warps, rows 0-7, then rows 8-15 where there are any
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -494,14 +532,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
       lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], 1);
       lr[h] += __shfl_xor_sync(0xffffffffu, lr[h], 2);
     }
-    cp_async_wait<0>();
-    __syncwarp();
-    float* mine = reinterpret_cast<float*>(smem + warp * L::kWarp);
-#pragma unroll
-    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(mine + (g + 8 * h) * D + j * 8 + c2) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+    const unsigned r0 = (unsigned)s.tile * kRowTile;
+    const int rows = (int)min((unsigned)kRowTile, (unsigned)s.ql * G - r0);
+    const bool whole = s.first && s.last;
+    const int c0 = s.c0, c1 = s.c1, q0 = s.q0, head = s.head;
+    float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * kRowPart<D>;
+    auto put = [&](int row, int col, float4 v, float sum) {  // four columns of a row of o
+      const unsigned rr = r0 + row;
+      const int tok = (int)(rr / G), hd = (int)(rr - tok * G);
+      const long long out = (long long)(q0 + tok) * b.Hq + head * (int)G + hd;
+      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees nothing: o = 0
+      uint2 w;
+      w.x = pack_bf16(v.x * inv, v.y * inv);
+      w.y = pack_bf16(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(p.o + out * D + col) = w;
+      return out;
+    };
+    __syncthreads();  // the last join has been read
     if ((lane & 3) == 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -510,66 +557,63 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
         stat[(warp * 3 + 2) * kRowTile + g + 8 * h] = lr[h];
       }
     }
-    __syncthreads();
-    // Eight threads per row, D / 8 columns each.
-    constexpr int kCols = D / 8;
-    const int row = threadIdx.x >> 3, col0 = (threadIdx.x & 7) * 4;  // columns col0 + 32 * i .. + 3
-    float M = -INFINITY, Ls = 0.f, Lr = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, stat[(w * 3) * kRowTile + row]);
-    const float Mu = M == -INFINITY ? 0.f : M;
-    float acc[kCols];
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-      const float f = ex2(stat[(w * 3) * kRowTile + row] - Mu);
-      Ls += f * stat[(w * 3 + 1) * kRowTile + row];
-      Lr += f * stat[(w * 3 + 2) * kRowTile + row];
-      const float* src = reinterpret_cast<const float*>(smem + w * L::kWarp) + row * D + col0;
-#pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(src + 32 * i);
-        acc[4 * i] += f * v.x;
-        acc[4 * i + 1] += f * v.y;
-        acc[4 * i + 2] += f * v.z;
-        acc[4 * i + 3] += f * v.w;
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1) {
+        if (rows <= kHalfRows) break;
+        __syncthreads();  // the first half has been read
       }
-    }
-    auto put = [&](int row, int col, float4 v, float sum) {  // four columns of a row of o
-      const unsigned rr = r0 + row;
-      const int tok = (int)(rr / G), hd = (int)(rr - tok * G);
-      const long long out = (long long)(s.q0 + tok) * b.Hq + s.head * (int)G + hd;
-      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees nothing: o = 0
-      uint2 w;
-      w.x = pack_bf16(v.x * inv, v.y * inv);
-      w.y = pack_bf16(v.z * inv, v.w * inv);
-      *reinterpret_cast<uint2*>(p.o + out * D + col) = w;
-      return out;
-    };
-    if (s.first && s.last) {
-      if (row < rows) {
-        long long out = 0;
+      // Columns 8 j .. of row g at block j ^ g: the rows of a column are in different banks.
 #pragma unroll
-        for (int i = 0; i < kCols / 4; ++i)
-          out = put(row, col0 + 32 * i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]), Lr);
-        if ((threadIdx.x & 7) == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
-      }
-    } else {
-      // A tile that other CTAs share: leave the partial result; the last of them to arrive joins all.
-      const int c0 = s.c0, c1 = s.c1;
-      float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * kRowPart<D>;
-      if (row < rows) {
+      for (int j = 0; j < kNT; ++j)
+        *reinterpret_cast<float2*>(merge + (warp * kHalfRows + g) * D + (j ^ g) * 8 + c2) =
+            make_float2(o[j][2 * h], o[j][2 * h + 1]);
+      __syncthreads();
+      // Sixteen threads per row, columns col0 + 64 i .. + 3.
+      const int hr = threadIdx.x >> 4, row = hr + 8 * h, col0 = (threadIdx.x & 15) * 4;
+      float M = -INFINITY, Ls = 0.f, Lr = 0.f;
 #pragma unroll
-        for (int i = 0; i < kCols / 4; ++i)
-          *reinterpret_cast<float4*>(slot + row * D + col0 + 32 * i) =
-              make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-        if ((threadIdx.x & 7) == 0) {
-          slot[kRowTile * D + row] = M;
-          slot[kRowTile * (D + 1) + row] = Ls;
-          slot[kRowTile * (D + 2) + row] = Lr;
+      for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, stat[(w * 3) * kRowTile + row]);
+      const float Mu = M == -INFINITY ? 0.f : M;
+      float4 acc[D / 64];
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) {
+        const float f = ex2(stat[(w * 3) * kRowTile + row] - Mu);
+        Ls += f * stat[(w * 3 + 1) * kRowTile + row];
+        Lr += f * stat[(w * 3 + 2) * kRowTile + row];
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const int col = col0 + 64 * i;
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * kHalfRows + hr) * D + ((col >> 3) ^ hr) * 8 +
+                                                            (col & 7));
+          acc[i].x = fmaf(f, v.x, acc[i].x);
+          acc[i].y = fmaf(f, v.y, acc[i].y);
+          acc[i].z = fmaf(f, v.z, acc[i].z);
+          acc[i].w = fmaf(f, v.w, acc[i].w);
         }
       }
+      if (row < rows) {
+        if (whole) {
+          long long out = 0;
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) out = put(row, col0 + 64 * i, acc[i], Lr);
+          if (col0 == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) *reinterpret_cast<float4*>(slot + row * D + col0 + 64 * i) = acc[i];
+          if (col0 == 0) {
+            slot[kRowTile * D + row] = M;
+            slot[kRowTile * (D + 1) + row] = Ls;
+            slot[kRowTile * (D + 2) + row] = Lr;
+          }
+        }
+      }
+    }
+    if (k + 1 < fetched) load_q(queue[(k + 1) % L::kSlots]);  // on its way beside what follows
+    if (!whole) {
+      // A tile that other CTAs share: the partial result is left; the last of them to arrive joins all.
       __syncthreads();
       if (threadIdx.x == 0) {
         // The barrier orders the CTA's stores before this thread's release, which covers them all.
@@ -592,14 +636,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
           constexpr int kAtOnce = 8;
           for (int c = c0; c <= c1; c += kAtOnce) {
             float4 v[kAtOnce];
-            float mi[kAtOnce], li[kAtOnce], ri[kAtOnce], mx = m0;
+            float mi[kAtOnce], si[kAtOnce], ri[kAtOnce], mx = m0;
 #pragma unroll
             for (int y = 0; y < kAtOnce; ++y) {
               const int cc = min(c + y, c1);
               const float* src = p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * kRowPart<D>;
               v[y] = __ldcg(reinterpret_cast<const float4*>(src + rw * D + col));
               mi[y] = c + y <= c1 ? __ldcg(src + kRowTile * D + rw) : -INFINITY;
-              li[y] = __ldcg(src + kRowTile * (D + 1) + rw);
+              si[y] = __ldcg(src + kRowTile * (D + 1) + rw);
               ri[y] = __ldcg(src + kRowTile * (D + 2) + rw);
             }
 #pragma unroll
@@ -617,7 +661,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
               a.y = fmaf(f, v[y].y, a.y);
               a.z = fmaf(f, v[y].z, a.z);
               a.w = fmaf(f, v[y].w, a.w);
-              ls = fmaf(f, li[y], ls);
+              ls = fmaf(f, si[y], ls);
               lsr = fmaf(f, ri[y], lsr);
             }
           }
@@ -626,7 +670,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
         }
       }
     }
-    __syncthreads();  // the rings and `stat` are free for the next stretch
   }
   if (p.tile_ctas > 0) join_pairs<D>(p);
 }
