@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
         int t0, t1, b0, nb;
         tile_tokens<false>(i, ps.ql, b.G, b.pair_tokens, t0, t1);
         tile_blocks<false>(t0, t1, ps.ql, ps.kvl, b.causal, b.window, b0, nb);
-        w[0] += nb;
+        w[0] += tile_units<false>(t0, t1, b, nb);
       }
     }
     // Long chunks: the warp counts each one's tiles together.

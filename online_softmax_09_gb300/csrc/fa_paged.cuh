@@ -136,10 +136,18 @@ __host__ __device__ __forceinline__ void tile_blocks(int t0, int t1, int ql, int
 __host__ __device__ __forceinline__ bool halves(int t0, int t1, const PagedBatch& b) {
   return b.d == 64 && t1 - t0 + 1 <= b.pair_tokens / 2;
 }
+// Every tile starts with some units for what it costs besides its blocks (queries in, sums out), so that
+// CTAs with many short tiles get fewer blocks: three blocks' time for a pair (2089 tokens of 32 heads at d = 64:
+// 45 us, 59 without), two for a 16-row tile (109 sequences of up to 421 keys: 30 us, 46 without).
+template <bool kPairs>
+__host__ __device__ __forceinline__ int tile_start(const PagedBatch& b) {
+  return kPairs ? (b.d == 64 ? 6 : 3) : 2;
+}
 template <bool kPairs>
 __host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBatch& b, int n) {
-  if (!kPairs || b.d != 64) return n;
-  return halves(t0, t1, b) ? (n + 1) & ~1 : 2 * n;
+  const int at = tile_start<kPairs>(b);
+  if (!kPairs || b.d != 64) return at + n;
+  return at + (halves(t0, t1, b) ? (n + 1) & ~1 : 2 * n);
 }
 
 // One stretch of key blocks of one row tile, as a CTA works it off.
@@ -150,6 +158,7 @@ struct Seg {
   int blk, n;      // key blocks [blk, blk + n) of this stretch
   bool first, last;  // holds the tile's first / last block (both: no other CTA shares the tile)
   int c0, c1;        // the first and last CTA with a stretch of the tile
+  int turn;          // pairs: the block to begin with, from `blk` on; the blocks before it come last
 };
 
 // Walk of one CTA's units, made by whole warps (the searches are warp-wide). The entries of 32
@@ -159,7 +168,7 @@ template <bool kPairs>
 struct SegIter {
   const PagedBatch& b;
   const long long* U;
-  long long u, u_end, per, tile_u0;
+  long long u, u_end, per, tile_u0, u_begin;
   long long wU;  // lane i: U[w0 + i], past the end the largest value
   PlanSeq wS;    // lane i: sequence w0 + i
   int w0, seq, head, tile, ntiles, t0, t1;
@@ -179,6 +188,7 @@ struct SegIter {
     if (kPairs && b.d == 64) per = (per + 1) & ~1LL;
     u = min(W, per * blockIdx.x);
     u_end = min(W, u + per);
+    u_begin = u;
     head = b.Hkv;  // no sequence yet
   }
   __device__ __forceinline__ int owner(long long unit) const {
@@ -252,47 +262,59 @@ struct SegIter {
   }
 
   __device__ __forceinline__ bool next(Seg& s) {
-    if (u >= u_end) return false;
-    if (head == b.Hkv) find_seq();
-    s.seq = seq;
-    s.head = head;
-    s.tile = tile;
-    s.q0 = ps.q0;
-    s.ql = ps.ql;
-    s.kvl = ps.kvl;
-    s.t0 = t0;
-    s.t1 = t1;
-    const int off = (int)(u - tile_u0);
-    const int take = (int)min((long long)(nb - off), u_end - u);  // units of this stretch
-    if (kPairs && b.d == 64 && !halves(t0, t1, b)) {
-      s.blk = b0 + off / 2;
-      s.n = take / 2;
-    } else {
-      s.blk = b0 + off;
-      s.n = min(take, nblk - off);
-    }
-    s.first = off == 0;
-    s.last = off + take == nb;
-    // A tile that is not this CTA's alone is shared by the CTAs that own its first to its last unit.
-    s.c0 = s.first ? (int)blockIdx.x : owner(tile_u0);
-    s.c1 = s.last ? (int)blockIdx.x : owner(tile_u0 + nb - 1);
-    u += take;
-    if (s.last) {  // on to the next tile, head or (at the next call) sequence
-      tile_u0 += nb;
-      if (ntiles > 1) {
-        if (++tile == ntiles) {
-          tile = 0;
-          ++head;
-        }
-        if (head < b.Hkv) {
-          tile_tokens<kPairs>(tile, ps.ql, b.G, b.pair_tokens, t0, t1);
-          measure();
-        }
+    while (u < u_end) {
+      if (head == b.Hkv) find_seq();
+      // The tile's blocks are its units [first_u, end_u); this CTA has those from `from` to `to`.
+      const long long first_u = tile_u0 + tile_start<kPairs>(b), end_u = tile_u0 + nb;
+      const long long from = max(u, first_u), to = min(u_end, end_u);
+      const bool last = to == end_u;
+      s.seq = seq;
+      s.head = head;
+      s.tile = tile;
+      s.q0 = ps.q0;
+      s.ql = ps.ql;
+      s.kvl = ps.kvl;
+      s.t0 = t0;
+      s.t1 = t1;
+      const int off = (int)(from - first_u), take = (int)(to - from);
+      if (kPairs && b.d == 64 && !halves(t0, t1, b)) {
+        s.blk = b0 + off / 2;
+        s.n = take / 2;
       } else {
-        ++head;  // one tile per head: the same blocks again
+        s.blk = b0 + off;
+        s.n = min(take, nblk - off);
       }
+      s.first = off == 0;
+      s.last = last;
+      s.turn = 0;
+      if (kPairs) {
+        const int w = b.d == 64 ? 2 : 1;
+        const unsigned round = (unsigned)(per / w), now = (unsigned)((from - u_begin) / w);
+        const unsigned turn = (now + round - (unsigned)s.blk % round) % round;
+        if (turn < (unsigned)s.n) s.turn = (int)turn;
+      }
+      // A tile that is not this CTA's alone is shared by the CTAs that own its first to its last block.
+      s.c0 = s.first ? (int)blockIdx.x : owner(first_u);
+      s.c1 = last ? (int)blockIdx.x : owner(end_u - 1);
+      u = to;
+      if (last) {  // on to the next tile, head or (at the next call) sequence
+        tile_u0 += nb;
+        if (ntiles > 1) {
+          if (++tile == ntiles) {
+            tile = 0;
+            ++head;
+          }
+          if (head < b.Hkv) {
+            tile_tokens<kPairs>(tile, ps.ql, b.G, b.pair_tokens, t0, t1);
+            measure();
+          }
+        } else {
+          ++head;  // one tile per head: the same blocks again
+        }
+      }
+      if (take > 0) return true;  // (else the CTA's units ended before the tile's first block)
     }
-    return true;
+    return false;
   }
 };
 

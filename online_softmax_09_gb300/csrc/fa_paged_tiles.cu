@@ -38,6 +38,7 @@ struct TileSeg {
   int n_max;  // blocks that some tile has work in; -1: the end of the CTA's stretches
   int j0, a[2], cnt[2], step, exists[2];
   int head, q0, ql, kvl, t0;
+  int turn;  // block j of the order is j0 + (j + turn) mod n_max
   int first, last, c0, c1;
 };
 
@@ -73,6 +74,7 @@ struct TileSmem {
   static constexpr int kAlloc = kBytes + 1024;
 };
 
+template <bool kTurn>
 __device__ __forceinline__ TileSeg tile_seg(const Seg& s, const PagedBatch& p) {
   TileSeg it;
   const int tpt = p.pair_tokens >> 1;
@@ -110,6 +112,10 @@ __device__ __forceinline__ TileSeg tile_seg(const Seg& s, const PagedBatch& p) {
     it.cnt[1] = it.n_max / 2;
     it.exists[1] = 1;
   }
+  // Where both tiles have all the blocks, their order is free. CTAs that work on other rows of the same keys
+  // then start at the same keys (Seg::turn), which so come from memory about once instead of once per pair.
+  const bool both = it.step == 1 && it.exists[1] && it.a[0] + it.a[1] == 0 && it.cnt[0] == it.n_max && it.cnt[1] == it.n_max;
+  it.turn = kTurn && both && it.n_max == s.n ? s.turn : 0;
   it.head = s.head;
   it.q0 = s.q0;
   it.ql = s.ql;
@@ -143,7 +149,7 @@ __device__ __forceinline__ float max64f(const uint32_t (&a)[32], const uint32_t 
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), max3f(m[6], m[7], init));
 }
 
-template <int D>
+template <int D, bool kTurn>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const PagedFwd p) {
@@ -239,10 +245,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto look = [&]() {
     it.n_max = -1;
     if (!walk.next(s)) return;
-    it = tile_seg(s, b);
+    it = tile_seg<kTurn>(s, b);
     key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, cur.lo, cur.hi);
     cur.tab = b.table + (long long)s.seq * b.table_stride;
-    if (it.n_max > 0) read_entry(it.j0);
+    if (it.n_max > 0) read_entry(it.j0 + it.turn);
   };
   if (warp == 8) look();
   tc_fence_before();
@@ -278,7 +284,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     };
     ok = hand_out();
     while (ok && it.n_max >= 0) {
-      const int head = s.head, tok = s.q0 + s.t0, j0 = it.j0, n_max = it.n_max;
+      const int head = s.head, tok = s.q0 + s.t0, j0 = it.j0, n_max = it.n_max, turn = it.turn;
+      int blk = kTurn ? j0 + turn : j0;
       const bool with[2] = {it.cnt[0] > 0, it.cnt[1] > 0};
       const int tile_tok = it.step == 1 ? tpt : 0;  // from tile 0's tokens to tile 1's
 #pragma unroll
@@ -300,9 +307,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         continue;
       }
       for (int j = 0; ok && j < n_max; ++j) {
-        const int slot = ((j0 + j) * kPairBlk + lane * box) & (b.page_size - 1);
+        const int slot = (blk * kPairBlk + lane * box) & (b.page_size - 1);
         const int pg = page_at();
-        if (j + 1 < n_max) read_entry(j0 + j + 1);
+                ++blk;
+        if (kTurn && blk == j0 + n_max) blk = j0;
+        if (j + 1 < n_max) read_entry(blk);
         const uint32_t sk = gk % NK, sv = gv % NV;
         if (!(ok = mbar_wait_warp(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
         if (lane == 0) mbar_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
@@ -511,7 +520,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       const int a_t = s.a[t], n_kv = s.cnt[t], step = kHalves ? s.step : 1;
       const bool twin = kHalves && step == 2;
-      const int kv_first = (s.j0 + a_t) * kPairBlk, kvl = s.kvl;
+      const int kv_first = (s.j0 + a_t) * kPairBlk, kvl = s.kvl, turn = s.turn;
       const int tok0 = s.t0 + (twin ? 0 : t * tpt);
       const int tok = tok0 + r_tok;
       const int pos = kvl - s.ql + tok;
@@ -540,7 +549,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           break;
         }
         tc_fence_after();
-        const int kv0 = kv_first + j * step * kPairBlk;
+        // (turn > 0: step is 1, and both tiles have all the blocks)
+        const int x = !kTurn ? j : (j + turn < n_kv ? j + turn : j + turn - n_kv);
+        const int kv0 = kv_first + x * step * kPairBlk;
         const bool tail = kv0 + kPairBlk > kvl;
         if (idle) {
           if (tail && !(ok = clear_tail(j, kv0))) break;
@@ -720,14 +731,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool kTurn>
 static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, int num_sms, cudaStream_t st) {
   constexpr int smem = TileSmem<D>::kAlloc;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-CTA limit");
   static unsigned long long known[kMaxGpus];
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_tiles_kernel<D>), smem, known);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_tiles_kernel<D, kTurn>), smem, known);
   if (e != cudaSuccess) return e;
-  fa_paged_tiles_kernel<D><<<num_sms, kTileThreads, smem, st>>>(m.q, m.k, m.v, p);
+  fa_paged_tiles_kernel<D, kTurn><<<num_sms, kTileThreads, smem, st>>>(m.q, m.k, m.v, p);
   return cudaGetLastError();
 }
 
@@ -735,8 +746,14 @@ size_t paged_tiles_workspace_bytes(int d) {
   return plan_up((size_t)2 * kPagedSms * tile_part(d) * 4) + plan_up((size_t)2 * kPagedSms * sizeof(TileShare));
 }
 
+// The turned order of blocks is for sequences whose keys and values may not stay in L2 (129 MB; counted as
+// half of it, from the table's width): 512 tokens over 32768 keys of 8 kv heads take 190 us with it, 193 to
+// 217 without, as the CTAs' starts happen to fall. Below that the order is free of cost, and the choice of a
+// block per step is not: 16 x 1743 tokens take 232 us without it, 242 with.
 cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
-  return d == 128 ? launch_tiles<128>(m, p, num_sms, st) : launch_tiles<64>(m, p, num_sms, st);
+  const bool turn = (long long)p.b.max_pages * p.b.page_size * p.b.Hkv * d * 4 > (64LL << 20);
+  if (d == 128) return turn ? launch_tiles<128, true>(m, p, num_sms, st) : launch_tiles<128, false>(m, p, num_sms, st);
+  return turn ? launch_tiles<64, true>(m, p, num_sms, st) : launch_tiles<64, false>(m, p, num_sms, st);
 }
 
 }  // namespace fa
