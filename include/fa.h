@@ -311,8 +311,9 @@ typedef struct {
   void *plan;              /* device, >= fa_paged_plan_bytes(S) bytes, 16-byte aligned; see fa_paged_plan */
   size_t plan_bytes;
   int S, T;                /* sequences, and rows of the step's token tensors (>= cu_q[S]); both may be 0 */
-  int max_q;               /* no sequence has more new tokens than this; max_q * Hq / Hkv must fit an int */
-  int max_pages;           /* columns of the table; max_pages * page_size must fit an int */
+  int max_q;               /* no sequence has more new tokens than this; max_q * Hq / Hkv
+                              and T at most 2^31 - 2^16 - 1 */
+  int max_pages;           /* columns of the table; max_pages * page_size at most 2^31 - 2^16 - 1 */
   int page_size;           /* 16, 32, 64, 128 or 256 */
   int Hq, Hkv, d;          /* Hq % Hkv == 0; d 64 or 128 */
   int causal;              /* a query sees keys up to its own position (else all of its sequence's) */
@@ -363,8 +364,11 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, co
  *       o = 0 and lse = -inf.
  *   workspace: >= fa_fwd_paged_workspace_bytes(batch) bytes (of Hq, Hkv, d and max_q alone), 16-byte
  *       aligned; contents on entry do not matter.
- * Cache slots that no query of the sequence sees, and table entries for them, may hold anything. The
- * result does not depend on scheduling: the same call gives the same bits.
+ * Cache slots that no query of the sequence sees, and table entries for pages of such slots alone, may
+ * hold anything. A NaN or infinity in a key that a query does not see does not reach it; one in a value
+ * that some new token of the sequence sees may reach its other new tokens (0 * NaN), as in fa_fwd. o must
+ * not overlap q. The result does not depend on scheduling: the same call gives the same bits.
+ * After FA_ERR_TIMEOUT the plan has to be laid out anew.
  */
 size_t fa_fwd_paged_workspace_bytes(const fa_paged_batch *batch);
 int fa_fwd_paged(const void *q, const long long *q_strides, const fa_paged_cache *cache, const fa_paged_batch *batch,

@@ -18,7 +18,7 @@ namespace fa {
 // and raises the status word.
 __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restrict__ cu_q,
                                                              const int* __restrict__ kv_len, PagedBatch b,
-                                                             int max_q, int pair_rows) {
+                                                             int pair_rows) {
   __shared__ long long sums[2][32];
   __shared__ long long carry[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
     long long w[2] = {0, 0};
     if (s < b.S) {
       const int a = cu_q[s], e = cu_q[s + 1], n = kv_len[s];
-      const bool ok = a >= 0 && e >= a && e <= b.T && e - a <= max_q && n >= 0 &&
+      const bool ok = a >= 0 && e >= a && e <= b.T && e - a <= b.max_q && n >= 0 &&
                       (long long)n <= (long long)b.max_pages * b.page_size;
       if (ok) ps = {a, e - a, n, 0};
       bad |= !ok;
@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
     h.magic = kPlanMagic;
     h.S = b.S;
     h.T = b.T;
+    h.max_q = b.max_q;
     h.Hq = b.Hq;
     h.Hkv = b.Hkv;
     h.d = b.d;
@@ -106,9 +107,8 @@ __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restri
   }
 }
 
-cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int max_q, int pair_rows,
-                              cudaStream_t st) {
-  fa_paged_plan_kernel<<<1, 1024, 0, st>>>(cu_q, kv_len, b, max_q, pair_rows);
+cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int pair_rows, cudaStream_t st) {
+  fa_paged_plan_kernel<<<1, 1024, 0, st>>>(cu_q, kv_len, b, pair_rows);
   return cudaGetLastError();
 }
 
@@ -145,16 +145,15 @@ __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(_
 constexpr int kRowWarps = 4, kRowThreads = 32 * kRowWarps;
 constexpr int kGran = kRowBlk / kRowWarps;  // keys that one warp takes at a time: 16, within one page
 
-constexpr int kHalfRows = kRowTile / 2;  // rows that the warps join at a time
-
 template <int D>
 struct RowSmem {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kJoinRows = D == 128 ? 8 : 16;  // rows that the warps join at a time
   static constexpr int kSlots = D == 128 ? 4 : 8;   // stretches in the queue: the one before, the present one, those ahead
   static constexpr int kTile = kGran * D * 2;        // K or V of one granule
   static constexpr int kWarp = kStages * 2 * kTile;  // ring of one warp
-  static constexpr int kMerge = kRowWarps * kWarp;   // 8 rows of o of each warp
-  static constexpr int kStat = kMerge + kRowWarps * kHalfRows * D * 4;  // m, l, rounded l of each warp's 16 rows
+  static constexpr int kMerge = kRowWarps * kWarp;   // kJoinRows rows of o of each warp
+  static constexpr int kStat = kMerge + kRowWarps * kJoinRows * D * 4;  // m, l, rounded l of each warp's 16 rows
   static constexpr int kQueue = kStat + kRowWarps * 3 * kRowTile * 4;
   static constexpr int kFlag = kQueue + kSlots * (int)sizeof(Seg);
   static constexpr int kBytes = (kFlag + 4 + 15) / 16 * 16;
@@ -310,8 +309,7 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
 // own cp.async copies, forms the 16 x 16 scores (m16n8k16), carries its own running max and sums, and
 // adds P V. The ring runs on across the CTA's stretches: the copies of the next ones are under way while
 // one is finished (a stretch of a short sequence is a few granules, and its chain of table, keys, join and
-// store would stand in the open each time). The four warps' results are joined once per stretch, eight rows
-// at a time, and the stretches of a tile that several CTAs share by the CTA that finishes last, in the order
+// store would stand in the open each time). The four warps' results are joined once per stretch, and the stretches of a tile that several CTAs share by the CTA that finishes last, in the order
 // of the keys.
 //
 // Weights are rounded to bf16 for the product with V; o is divided by the sum of the rounded weights,
@@ -524,7 +522,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
       __syncwarp();  // the stage is read: the next copies may overwrite it
     }
 
-    // ---- join the four warps, rows 0-7, then rows 8-15 where there are any
+    // ---- join the four warps; at d = 128 rows 0-7, then rows 8-15 where there are any
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
@@ -557,36 +555,40 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
         stat[(warp * 3 + 2) * kRowTile + g + 8 * h] = lr[h];
       }
     }
+    constexpr int kJoin = L::kJoinRows, kPer = kRowThreads / kJoin;  // threads per row, 8 columns each
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1) {
-        if (rows <= kHalfRows) break;
-        __syncthreads();  // the first half has been read
+    for (int pass = 0; pass < kRowTile / kJoin; ++pass) {
+      if (pass == 1) {
+        if (rows <= kJoin) break;
+        __syncthreads();  // the first rows have been read
       }
       // Columns 8 j .. of row g at block j ^ g: the rows of a column are in different banks.
 #pragma unroll
-      for (int j = 0; j < kNT; ++j)
-        *reinterpret_cast<float2*>(merge + (warp * kHalfRows + g) * D + (j ^ g) * 8 + c2) =
-            make_float2(o[j][2 * h], o[j][2 * h + 1]);
+      for (int h = 0; h < 2; ++h) {
+        if (kJoin == 8 && h != pass) continue;
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+          *reinterpret_cast<float2*>(merge + (warp * kJoin + g + (kJoin == 16 ? 8 * h : 0)) * D + (j ^ g) * 8 + c2) =
+              make_float2(o[j][2 * h], o[j][2 * h + 1]);
+      }
       __syncthreads();
-      // Sixteen threads per row, columns col0 + 64 i .. + 3.
-      const int hr = threadIdx.x >> 4, row = hr + 8 * h, col0 = (threadIdx.x & 15) * 4;
+      const int hr = threadIdx.x / kPer, row = hr + kJoin * pass, col0 = (threadIdx.x % kPer) * 4;
       float M = -INFINITY, Ls = 0.f, Lr = 0.f;
 #pragma unroll
       for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, stat[(w * 3) * kRowTile + row]);
       const float Mu = M == -INFINITY ? 0.f : M;
-      float4 acc[D / 64];
+      float4 acc[2];  // columns col0 + 4 kPer i .. + 3
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < 2; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kRowWarps; ++w) {
         const float f = ex2(stat[(w * 3) * kRowTile + row] - Mu);
         Ls += f * stat[(w * 3 + 1) * kRowTile + row];
         Lr += f * stat[(w * 3 + 2) * kRowTile + row];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const int col = col0 + 64 * i;
-          const float4 v = *reinterpret_cast<const float4*>(merge + (w * kHalfRows + hr) * D + ((col >> 3) ^ hr) * 8 +
+        for (int i = 0; i < 2; ++i) {
+          const int col = col0 + 4 * kPer * i;
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * kJoin + hr) * D + ((col >> 3) ^ (hr & 7)) * 8 +
                                                             (col & 7));
           acc[i].x = fmaf(f, v.x, acc[i].x);
           acc[i].y = fmaf(f, v.y, acc[i].y);
@@ -598,11 +600,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
         if (whole) {
           long long out = 0;
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) out = put(row, col0 + 64 * i, acc[i], Lr);
+          for (int i = 0; i < 2; ++i) out = put(row, col0 + 4 * kPer * i, acc[i], Lr);
           if (col0 == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
         } else {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i) *reinterpret_cast<float4*>(slot + row * D + col0 + 64 * i) = acc[i];
+          for (int i = 0; i < 2; ++i) *reinterpret_cast<float4*>(slot + row * D + col0 + 4 * kPer * i) = acc[i];
           if (col0 == 0) {
             slot[kRowTile * D + row] = M;
             slot[kRowTile * (D + 1) + row] = Ls;

@@ -25,8 +25,8 @@ constexpr int kPairBlk = 128;
 
 struct PlanHeader {  // 64 words; what the plan was built for, checked by every kernel that reads it
   uint32_t magic;
-  int S, T, Hq, Hkv, d, page_size, max_pages, causal, window;
-  int pad[54];
+  int S, T, max_q, Hq, Hkv, d, page_size, max_pages, causal, window;
+  int pad[53];
 };
 
 struct PlanSeq {
@@ -68,7 +68,7 @@ struct PagedBatch {
   PlanView plan;
   const int* table;  // [S][table_stride]
   long long table_stride;
-  int S, T, Hq, Hkv, G, d, page_size, page_shift, max_pages, num_pages, causal, window;
+  int S, T, max_q, Hq, Hkv, G, d, page_size, page_shift, max_pages, num_pages, causal, window;
   int pair_tokens;  // tokens of a pair of 128-row tiles: 2 * (128 / G)
   uint32_t* status;
 };
@@ -78,8 +78,9 @@ __device__ __forceinline__ void record_index_error(uint32_t* status) { atomicCAS
 // The plan was built for this batch (a stale or unset buffer would send indexes out of range).
 __device__ __forceinline__ bool plan_matches(const PagedBatch& b, int d) {
   const PlanHeader* h = b.plan.head;
-  return h->magic == kPlanMagic && h->S == b.S && h->T == b.T && h->Hq == b.Hq && h->Hkv == b.Hkv && h->d == d &&
-         h->page_size == b.page_size && h->max_pages == b.max_pages && h->causal == b.causal && h->window == b.window;
+  return h->magic == kPlanMagic && h->S == b.S && h->T == b.T && h->max_q == b.max_q && h->Hq == b.Hq &&
+         h->Hkv == b.Hkv && h->d == d && h->page_size == b.page_size && h->max_pages == b.max_pages &&
+         h->causal == b.causal && h->window == b.window;
 }
 
 // Keys [lo, hi) that some query of tokens [t0, t1] sees: token j stands at position kvl - ql + j and
@@ -366,8 +367,7 @@ struct RopeLaunch {
   PagedBatch b;
 };
 
-cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int max_q, int pair_rows,
-                              cudaStream_t st);
+cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int pair_rows, cudaStream_t st);
 size_t paged_rows_workspace_bytes(int d);
 cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
 

@@ -17,6 +17,7 @@ namespace {
   } while (0)
 
 constexpr int kMaxHeads = 1 << 16;
+constexpr int kMaxTokens = 0x7fffffff - (1 << 16);
 
 int check_ptr(const void* p, uintptr_t align) {
   if (p == nullptr) return FA_ERR_INVALID;
@@ -95,10 +96,11 @@ int check_batch(const fa_paged_batch* b) {
   if (b == nullptr) return FA_ERR_INVALID;
   if (b->S < 0 || b->T < 0 || b->max_q < 0 || b->max_pages < 1 || b->window < 0) return FA_ERR_INVALID;
   if (b->Hq < 1 || b->Hkv < 1 || b->Hq % b->Hkv != 0 || b->Hq > kMaxHeads) return FA_ERR_INVALID;
-  if ((long long)b->max_q * (b->Hq / b->Hkv) > 0x7fffffffLL - fa::kRowTile) return FA_ERR_INVALID;
+  if ((long long)b->max_q * (b->Hq / b->Hkv) > kMaxTokens) return FA_ERR_INVALID;
   FA_TRY(check_d(b->d));
   if (b->page_size < 16 || b->page_size > 256 || (b->page_size & (b->page_size - 1))) return FA_ERR_UNSUPPORTED;
-  if ((long long)b->max_pages * b->page_size > 0x7fffffffLL - 1024) return FA_ERR_INVALID;
+  // Tokens and keys are ints, with room for the last block of either.
+  if ((long long)b->max_pages * b->page_size > kMaxTokens || b->T > kMaxTokens) return FA_ERR_INVALID;
   if (b->plan == nullptr || b->plan_bytes < fa::plan_layout(nullptr, b->S, nullptr)) return FA_ERR_WORKSPACE;
   FA_TRY(check_ptr(b->plan, 16));
   return FA_OK;
@@ -125,6 +127,7 @@ fa::PagedBatch device_batch(const fa_paged_batch* b, int num_pages, uint32_t* st
   x.table_stride = b->table_stride;
   x.S = b->S;
   x.T = b->T;
+  x.max_q = b->max_q;
   x.Hq = b->Hq;
   x.Hkv = b->Hkv;
   x.G = b->Hq / b->Hkv;
@@ -199,7 +202,7 @@ int fa_paged_plan(const int* cu_q, const int* kv_len, const fa_paged_batch* batc
   if (batch->S > 0) FA_TRY(check_ptr(kv_len, 4));
   uint32_t* status = nullptr;
   FA_TRY(fa::device_state(&status, nullptr));
-  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status), batch->max_q,
+  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status),
                                fa::pair_rows_of(batch->Hq / batch->Hkv, batch->d), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_LAUNCH;

@@ -67,7 +67,7 @@ def _cache(fa, k=P, v=P, ks=(4096, 2048, 128), vs=(4096, 2048, 128), pages=10):
 
 
 BAD_BATCH = [({"S": -1}, -1), ({"T": -1}, -1), ({"max_q": -1}, -1), ({"max_pages": 0}, -1), ({"window": -1}, -1),
-             ({"max_q": 1 << 30}, -1), ({"Hq": 0}, -1), ({"Hkv": 0}, -1), ({"Hq": 3}, -1), ({"d": 96}, -2), ({"page_size": 8}, -2),
+             ({"max_q": 1 << 30}, -1), ({"T": (1 << 31) - 1}, -1), ({"max_pages": (1 << 27) - 1}, -1), ({"Hq": 0}, -1), ({"Hkv": 0}, -1), ({"Hq": 3}, -1), ({"d": 96}, -2), ({"page_size": 8}, -2),
              ({"page_size": 48}, -2), ({"page_size": 512}, -2), ({"max_pages": 1 << 28}, -1), ({"plan": None}, -6),
              ({"plan_bytes": 64}, -6), ({"plan": P + 8}, -3)]
 

@@ -109,6 +109,17 @@ def test_long_axis_is_split_and_joined_in_a_fixed_order(lens):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,window", [([(200, 5000)], 0), ([(150, 3000), (1, 40), (257, 2000)], 0),
+                                         ([(300, 4000)], 1500), ([(129, 129), (64, 6000)], 0)])
+def test_wide_tables(lens, window, d):
+    # A table wide enough for sequences beyond L2: blocks that both tiles see are worked off in a turned order.
+    b = Batch(lens, 4, 2, d, 16, seed=d + len(lens), extra_cols=40000)
+    o, lse = _run(b, window=window)
+    o2, lse2 = _run(b, window=window)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_many_sequences():
     r = np.random.default_rng(3)
     lens = [(int(r.integers(0, 4)), int(r.integers(0, 90))) for _ in range(1500)]
@@ -187,6 +198,66 @@ def test_captured_step_follows_new_lengths():
             assert_within(lse[i:i + 1], rl, tl, f"cut {cut} lse {i}")
 
 
+def test_captured_chunks_follow_new_lengths():
+    # Both kernels of a batch with chunks, captured with the plan: the cached part grows from replay to replay.
+    fa = fa_mod()
+    b = Batch([(40, 300), (1, 100), (200, 900)], 8, 2, 128, 16, seed=24)
+    o = torch.full((b.T, b.Hq, b.d), FILL, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((b.T, b.Hq), FILL, device="cuda")
+    plan = b.plan(fa)
+    fa.forward_paged(b.dev["q"], b.kc, b.vc, plan, out=o, lse=lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.plan(fa, plan=plan)
+        for _ in range(2):
+            fa.forward_paged(b.dev["q"], b.kc, b.vc, plan, out=o, lse=lse)
+    for cut in (0, 1, 70):
+        lens = [(ql, n - cut) for ql, n in b.lens]
+        b.dev["kv_lens"].copy_(torch.tensor([n for _, n in lens], dtype=torch.int32))
+        o.fill_(FILL)
+        lse.fill_(FILL)
+        graph.replay()
+        fa.check()
+        for i, (ql, n) in enumerate(lens):
+            a = b.cu[i]
+            ro, rl, to, tl = attention_ref(f64(b.q[a:a + ql]), f64(b.K[i][:n]), f64(b.V[i][:n]), n, True, 0, 128 ** -0.5)
+            assert_within(o[a:a + ql], ro, to, f"cut {cut} o {i}")
+            assert_within(lse[a:a + ql], rl, tl, f"cut {cut} lse {i}")
+
+
+def test_values_beyond_a_query_do_not_reach_it_across_sequences():
+    # NaN in one sequence's visible keys and values leaves the others as they are, tokens in the same tile too.
+    fa = fa_mod()
+    for lens in ([(1, 50), (1, 60)], [(30, 50), (30, 60)]):
+        b = Batch(lens, 4, 2, 64, 16, seed=25)
+        first = b.dev["table"][0, 0].item()
+        b.kc[first, :, 3] = float("nan")
+        b.vc[first, :, 5] = float("inf")
+        o, lse = fa.forward_paged(b.dev["q"], b.kc, b.vc, b.plan(fa))
+        fa.check()
+        a, ql, n = b.cu[1], *lens[1]
+        ro, rl, to, tl = attention_ref(f64(b.q[a:]), f64(b.K[1]), f64(b.V[1]), n, True, 0, 1 / 8)
+        assert_within(o[a:], ro, to, "o")
+        assert_within(lse[a:], rl, tl, "lse")
+        assert torch.isnan(o[0].float()).any()
+
+
+def test_keys_that_a_query_does_not_see_may_be_nan():
+    # A key of a later new token of the same chunk (its value is finite): masked, whatever it holds.
+    fa = fa_mod()
+    for new in (4, 60):
+        b = Batch([(new, 100)], 4, 2, 64, 16, seed=26)
+        last = b.dev["table"][0, 99 // 16].item()
+        b.kc[last, :, 99 % 16] = float("nan")
+        o, lse = fa.forward_paged(b.dev["q"], b.kc, b.vc, b.plan(fa))
+        fa.check()
+        ro, rl, to, tl = attention_ref(f64(b.q), f64(b.K[0]), f64(b.V[0]), 100, True, 0, 1 / 8)
+        assert_within(o[:new - 1], ro[:new - 1], to[:new - 1], "o")
+        assert_within(lse[:new - 1], rl[:new - 1], tl[:new - 1], "lse")
+        assert torch.isnan(o[new - 1].float()).all()
+
+
 def test_agrees_with_the_dense_forward():
     # One sequence whose every token is new is fa_fwd's causal case.
     fa = fa_mod()
@@ -240,11 +311,26 @@ def test_more_new_tokens_than_promised_is_reported():
     _expect_index_error(fa, lambda: fa.forward_paged(b.dev["q"], b.kc, b.vc, b.plan(fa)))
 
 
-def test_plan_of_another_batch_is_reported():
+@pytest.mark.parametrize("field,value", [("window", 5), ("max_q", 2), ("causal", 0), ("max_pages", 8), ("T", 1)])
+@pytest.mark.parametrize("lens", [[(1, 100)], [(50, 100)]])
+def test_plan_of_another_batch_is_reported(field, value, lens):
     fa = fa_mod()
-    b = Batch([(1, 100)], 4, 2, 64, 16, seed=19)
+    b = Batch(lens, 4, 2, 64, 16, seed=19, pad=1)
     plan = b.plan(fa)
-    plan._c.window = 5
+    setattr(plan._c, field, value)  # the call says something else than the plan was laid out for
+    k = torch.zeros(b.T, 2, 64, dtype=torch.bfloat16, device="cuda")
+    before = f64(b.kc)
+    _expect_index_error(fa, lambda: fa.forward_paged(b.dev["q"], b.kc, b.vc, plan))
+    _expect_index_error(fa, lambda: fa.paged_append(None, k, k, b.kc, b.vc, plan))
+    assert np.array_equal(before, f64(b.kc), equal_nan=True)
+
+
+def test_plan_that_was_never_laid_out_is_reported():
+    fa = fa_mod()
+    b = Batch([(1, 100)], 4, 2, 64, 16, seed=20)
+    plan = b.plan(fa)
+    fa.check()
+    plan.buffer.zero_()
     _expect_index_error(fa, lambda: fa.forward_paged(b.dev["q"], b.kc, b.vc, plan))
 
 
