@@ -442,35 +442,42 @@ def _rope(name, fn, q, k, positions, rotary, q_out, k_out, stream):
     if len(shape) != 4 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [B, Hq, N, d]")
     B, Hq, N, d = shape
-    i = _dev_index(q)
-    qs = _strides_of("q", q, shape, i)
+    i = q.get_device()
+    if i != torch._C._cuda_getDevice():
+        _dev_index(q)
+    A, n, pshape = rotary.naxes, positions.numel(), positions.shape
+    if positions.dtype != torch.int32 or positions.get_device() != i or rotary.index != i or pshape[-1:] != (N,) \
+            or (n != A * N and n != A * B * N) or (A > 1 and pshape[0] != A) or len(pshape) > 3 \
+            or not positions.is_contiguous():
+        want = f"[{A}, {N}] or [{A}, {B}, {N}]" if A > 1 else f"[{N}] or [{B}, {N}]"
+        raise ValueError(f"positions must be a contiguous int32 CUDA tensor {want}, and the rotary on q's device")
+    st = _strides_of("q", q, shape, i)[:3]
     if k is not None:
         kshape = k.shape
         if len(kshape) != 4 or kshape[0] != B or kshape[2:] != shape[2:]:
             raise ValueError("k must be [B, Hkv, N, d] with the same B, N, d as q")
-        ks = _strides_of("k", k, kshape, i)
+        ks = _strides_of("k", k, kshape, i)[:3]
+        Hkv, kp = kshape[1], k.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    A = rotary.naxes
-    n = positions.numel()
-    want = ((A, N), (A, B, N)) if A > 1 else ((N,), (B, N), (1, N), (1, B, N))
-    if positions.dtype != torch.int32 or positions.get_device() != i or not positions.is_contiguous() \
-            or positions.shape not in want or rotary.index != i:
-        raise ValueError(f"positions must be a contiguous int32 CUDA tensor of shape {want[0]} or {want[1]}")
+    else:
+        Hkv, kp, kop = 0, None, None
     if q_out is None:
         q_out = _empty(shape, torch.bfloat16, q.device, stream)
-    st = qs[:3] + _strides_of("q_out", q_out, shape, i)[:3]
-    kp = kop = None
+        st += (Hq * N * d, N * d, d)
+    else:
+        st += _strides_of("q_out", q_out, shape, i)[:3]
     if k is not None:
         if k_out is None:
             k_out = _empty(kshape, torch.bfloat16, q.device, stream)
-        st += ks[:3] + _strides_of("k_out", k_out, kshape, i)[:3]
-        kp, kop = k.data_ptr(), k_out.data_ptr()
+            st += ks + (Hkv * N * d, N * d, d)
+        else:
+            st += ks + _strides_of("k_out", k_out, kshape, i)[:3]
+        kop = k_out.data_ptr()
     if N == 0 or B == 0:
         return q_out, k_out
     r = fn(q.data_ptr(), q_out.data_ptr(), kp, kop, _ll12(*st), positions.data_ptr(), n // A,
-           N if B > 1 and n == A * B * N else 0, rotary._ref, B, Hq, kshape[1] if k is not None else 0, N, d,
-           _stream_of(stream, i))
+           N if B > 1 and n == A * B * N else 0, rotary._ref, B, Hq, Hkv, N, d, _stream_of(stream, i))
     if r != FA_OK:
         raise FAError(r, name)
     return q_out, k_out
@@ -480,12 +487,12 @@ def rope(q, k, positions, rotary, q_out=None, k_out=None, stream=None):
     """Rotated (q, k) (fa_rope). q [B,Hq,N,d], k [B,Hkv,N,d] or None: bf16 CUDA, any strides with contiguous
     last dim (e.g. views of a fused projection); outputs are contiguous unless given. positions: int32 CUDA
     [N] or [B,N]; with several axes [A,N] or [A,B,N]. An output may be its input."""
-    return _rope("fa_rope", lib().fa_rope, q, k, positions, rotary, q_out, k_out, stream)
+    return _rope("fa_rope", (_lib or lib()).fa_rope, q, k, positions, rotary, q_out, k_out, stream)
 
 
 def rope_backward(dq, dk, positions, rotary, q_out=None, k_out=None, stream=None):
     """Gradients of rope's q and k from those of its outputs (fa_rope_bwd); arguments as for rope."""
-    return _rope("fa_rope_bwd", lib().fa_rope_bwd, dq, dk, positions, rotary, q_out, k_out, stream)
+    return _rope("fa_rope_bwd", (_lib or lib()).fa_rope_bwd, dq, dk, positions, rotary, q_out, k_out, stream)
 
 
 class PagedPlan:
@@ -576,7 +583,9 @@ def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q
         qs = _strides_of("q", q, shape, i)
         if q_out is None:
             q_out = _empty(shape, torch.bfloat16, q.device, stream)
-        st = qs[:2] + _strides_of("q_out", q_out, shape, i)[:2]
+            st = qs[:2] + (shape[1] * shape[2], shape[2])
+        else:
+            st = qs[:2] + _strides_of("q_out", q_out, shape, i)[:2]
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
