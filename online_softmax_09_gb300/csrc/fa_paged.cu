@@ -5,7 +5,11 @@
 //     x_t = scale * q_j . k_t  for t < kv_len, t <= p (causal), t > p - window (window > 0)
 //     o_j = sum_t exp(x_t - lse_j) v_t,  lse_j = log sum_t exp(x_t);  nothing visible: o = 0, lse = -inf.
 //
-// fa_paged_plan_kernel lays the batch out (fa_paged.cuh); fa_paged_rows_kernel attends.
+// fa_paged_plan_kernel lays the batch out (fa_paged.cuh). Sequences with few rows (new tokens times heads
+// per kv head) are attended by fa_paged_rows_kernel in tiles of 16, the others by fa_paged_tiles_kernel
+// (fa_paged_tiles.cu) in pairs of 128, after which the rows' kernel also joins what several CTAs share.
+//
+// What has to be read is each key and value that some query sees, once: 4 d bytes per key and kv head.
 #include <math.h>
 
 #include "fa_paged.cuh"
@@ -15,7 +19,8 @@ namespace fa {
 // ------------------------------------------------------------------------------------------ plan
 // One CTA: checks every sequence's place and lengths, counts its work in both kinds of unit and
 // forms the running sums. A sequence out of range gets no tokens (nothing of it is read or written)
-// and raises the status word.
+// and raises the status word. (8 us for 24 sequences, once per step for all layers; nothing is read back, so a
+// captured step lays itself out.)
 __global__ void __launch_bounds__(1024) fa_paged_plan_kernel(const int* __restrict__ cu_q,
                                                              const int* __restrict__ kv_len, PagedBatch b,
                                                              int pair_rows) {
@@ -314,6 +319,12 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
 //
 // Weights are rounded to bf16 for the product with V; o is divided by the sum of the rounded weights,
 // so a row that one key dominates is not off by that rounding, and lse holds the unrounded sum.
+//
+// Bound by HBM: 64 sequences of 200 to 8192 keys (32 query heads, 8 kv heads, d = 128, 1.11 GB) take 172 us,
+// 6.45 TB/s, 96 % of the measured copy rate, two of 131072 keys 162 us (96 %), with 96 KB of copies under way
+// per CTA. mma.sync and not tcgen05, because 4 to 16 rows would leave most of a 128-row tile empty while its
+// scores still pass through the softmax's threads; the tensor pipe is 19 % busy. A single token over 1000 keys
+// takes 8.1 us, a chain of latencies (plan, table, keys, join, release, partial results).
 template <int D>
 __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const PagedFwd p) {
   using L = RowSmem<D>;
