@@ -17,10 +17,10 @@ constexpr uint32_t kPlanMagic = 0x70a6ed01u;
 constexpr int kPlanCtas = 512;  // most CTAs that a kernel over a plan may have (its merge counters)
 constexpr int kPagedSms = 160;  // most SMs that are used: bounds the partial results without asking the device
 
-// Row tiles of two kinds: 16 rows against 64-key blocks, and pairs of 128 rows against 128-key
+// Row tiles of two kinds: 16 or 32 rows against 64-key blocks, and pairs of 128 rows against 128-key
 // blocks. A row is one query head of one new token: row r of a (sequence, kv head) is token r / G,
 // head r % G, so the heads that share keys share a tile.
-constexpr int kRowTile = 16, kRowBlk = 64;
+constexpr int kRowBlk = 64;
 constexpr int kPairBlk = 128;
 
 struct PlanHeader {  // 64 words; what the plan was built for, checked by every kernel that reads it
@@ -36,8 +36,8 @@ struct PlanSeq {
 struct PlanView {
   PlanHeader* head;
   PlanSeq* seq;               // [S]
-  long long* units[2];        // [S + 1] running sums: 16-row tiles, 256-row pairs
-  uint32_t* counters;         // [kPlanCtas] arrivals at 16-row tiles that several CTAs share; zero between calls
+  long long* units[2];        // [S + 1] running sums: tiles of few rows, pairs
+  uint32_t* counters;         // [kPlanCtas] arrivals at tiles of few rows that several CTAs share; zero between calls
 };
 
 __host__ __device__ inline size_t plan_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -70,6 +70,8 @@ struct PagedBatch {
   long long table_stride;
   int S, T, max_q, Hq, Hkv, G, d, page_size, page_shift, max_pages, num_pages, causal, window;
   int pair_tokens;  // tokens of a pair of 128-row tiles: 2 * (128 / G)
+  int sms;          // SMs in use: one CTA each for the pairs, two for the small tiles
+  int row_tile;     // rows of the small tiles: 16, or 32 in batches with a sequence of more than 16
   uint32_t* status;
 };
 
@@ -95,25 +97,26 @@ __host__ __device__ __forceinline__ void key_range(int t0, int t1, int ql, int k
 
 // Row tile `i` of a sequence: its tokens [t0, t1], and how many tiles there are. (ql * G fits an int:
 // max_q * G is checked on the host.)
-template <bool kPairs>
-__host__ __device__ __forceinline__ int tile_count(int ql, int G, int pair_tokens) {
-  return kPairs ? (ql + pair_tokens - 1) / pair_tokens : (int)(((unsigned)ql * G + kRowTile - 1) / kRowTile);
+template <bool kPairs, int kRows = 0>  // kRows: the small tiles' rows, where the caller knows them
+__host__ __device__ __forceinline__ int tile_count(int ql, const PagedBatch& b) {
+  const unsigned rows = kRows ? kRows : b.row_tile;
+  return kPairs ? (ql + b.pair_tokens - 1) / b.pair_tokens : (int)(((unsigned)ql * b.G + rows - 1) / rows);
 }
-template <bool kPairs>
-__host__ __device__ __forceinline__ void tile_tokens(int i, int ql, int G, int pair_tokens, int& t0, int& t1) {
+template <bool kPairs, int kRows = 0>
+__host__ __device__ __forceinline__ void tile_tokens(int i, int ql, const PagedBatch& b, int& t0, int& t1) {
   if (kPairs) {
-    t0 = i * pair_tokens;
-    t1 = (t0 + pair_tokens < ql ? t0 + pair_tokens : ql) - 1;
+    t0 = i * b.pair_tokens;
+    t1 = (t0 + b.pair_tokens < ql ? t0 + b.pair_tokens : ql) - 1;
   } else {
-    const unsigned r0 = (unsigned)i * kRowTile, R = (unsigned)ql * G;
-    if (R <= kRowTile) {  // one tile: no divisions
+    const unsigned rows = kRows ? kRows : b.row_tile, r0 = (unsigned)i * rows, R = (unsigned)ql * b.G;
+    if (R <= rows) {  // one tile: no divisions
       t0 = 0;
       t1 = ql - 1;
       return;
     }
-    const unsigned r1 = (r0 + kRowTile < R ? r0 + kRowTile : R) - 1;
-    t0 = (int)(r0 / G);
-    t1 = (int)(r1 / G);
+    const unsigned r1 = (r0 + rows < R ? r0 + rows : R) - 1;
+    t0 = (int)(r0 / b.G);
+    t1 = (int)(r1 / b.G);
   }
 }
 // Key blocks [b0, b0 + n) of tokens [t0, t1]; one block at least, so that rows that see nothing are
@@ -165,7 +168,7 @@ struct Seg {
 // Walk of one CTA's units, made by whole warps (the searches are warp-wide). The entries of 32
 // sequences are held across the lanes, read together when the walk starts, so that finding the first
 // stretch and moving on to the next sequence cost no chain of loads.
-template <bool kPairs>
+template <bool kPairs, int kRows = 0>
 struct SegIter {
   const PagedBatch& b;
   const long long* U;
@@ -223,7 +226,7 @@ struct SegIter {
     ps.q0 = __shfl_sync(0xffffffffu, wS.q0, src);
     ps.ql = __shfl_sync(0xffffffffu, wS.ql, src);
     ps.kvl = __shfl_sync(0xffffffffu, wS.kvl, src);
-    ntiles = tile_count<kPairs>(ps.ql, b.G, b.pair_tokens);
+    ntiles = tile_count<kPairs, kRows>(ps.ql, b);
     long long per_head;
     if (units <= 0x7fffffffLL) {  // the usual case, without 64-bit divisions
       per_head = (unsigned)units / (unsigned)b.Hkv;
@@ -237,7 +240,7 @@ struct SegIter {
     for (int i0 = 0;; i0 += 32) {
       int x0 = 0, x1 = 0, y0 = 0, yn = 0;
       if (i0 + lane < ntiles) {
-        tile_tokens<kPairs>(i0 + lane, ps.ql, b.G, b.pair_tokens, x0, x1);
+        tile_tokens<kPairs, kRows>(i0 + lane, ps.ql, b, x0, x1);
         tile_blocks<kPairs>(x0, x1, ps.ql, ps.kvl, b.causal, b.window, y0, yn);
         yn = tile_units<kPairs>(x0, x1, b, yn);
       }
@@ -306,7 +309,7 @@ struct SegIter {
             ++head;
           }
           if (head < b.Hkv) {
-            tile_tokens<kPairs>(tile, ps.ql, b.G, b.pair_tokens, t0, t1);
+            tile_tokens<kPairs, kRows>(tile, ps.ql, b, t0, t1);
             measure();
           }
         } else {
@@ -332,6 +335,13 @@ struct TileShare {
   int q0, ql, tok0, head;
 };
 
+// A small tile that CTA c (the index in PagedFwd::row_share) began, CTAs up to c1 went on with, and the
+// kernel after theirs joins.
+struct RowShare {
+  int c1;  // -1: none
+  int q0, r0, rows, head;
+};
+
 struct PagedFwd {
   PagedBatch b;
   PagedCache c;
@@ -339,12 +349,16 @@ struct PagedFwd {
   long long q_tok, q_head;
   __nv_bfloat16* o;  // [T][Hq][d]
   float* lse;        // [T][Hq]
-  float* part;       // partial results of the 16-row tiles: 2 slots per CTA
+  float* part;       // partial results of the small tiles: 2 slots per CTA
+  RowShare* row_share;  // [2 * sms], or NULL: no kernel follows, every tile is joined by its last CTA
   float* tile_part;  // and of the pairs, with what each CTA shares with those after it
   TileShare* share;  // [tile_ctas][2 tiles]
   int tile_ctas;     // CTAs of the pairs' kernel (0: it does not run)
   float scale_log2;
 };
+
+// One partial result of a small tile: o [rows][D], then m, l, rounded l of the rows.
+__host__ __device__ constexpr int row_part(int D, int rows) { return rows * (D + 3); }
 
 // One partial result of a pair: per tile o [D / 4][128][4], unnormalised, and m, l, e [128].
 __host__ __device__ constexpr int tile_part(int D) { return 2 * kTile * (D + 3); }
@@ -368,7 +382,7 @@ struct RopeLaunch {
 };
 
 cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int pair_rows, cudaStream_t st);
-size_t paged_rows_workspace_bytes(int d);
+size_t paged_rows_workspace_bytes(int d, int row_tile);
 cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
 
 struct TileMaps {
@@ -378,11 +392,21 @@ struct TileMaps {
 size_t paged_tiles_workspace_bytes(int d);
 cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st);
 
+// Rows of the small tiles. 32 where no sequence of the batch can have more, and some may have more than 16
+// (a few drafted tokens): the keys are read once for them (8 tokens of 32 heads, 8 kv heads, 48 sequences of
+// 3000 keys: 109 us against 125 in pairs at d = 128, 66 against 97 in two 16-row tiles at d = 64). Where
+// longer sequences may be there too the batch's single tokens count more, which the 16-row kernel, with the
+// queries in registers, has done a little sooner (the mixed batch of 24 sequences: 367 us against 373).
+inline int row_tile_of(int G, int max_q) { return (long long)max_q * G > 16 && (long long)max_q * G <= 32 ? 32 : 16; }
 // Sequences of more rows (new tokens times heads per kv head) than this are worked off in pairs of 128-row
-// tiles, the others in 16-row tiles (with more than 128 heads per kv head, all of them).
-// At d = 64 two 16-row tiles, which read the keys twice, still beat a 128-row one: 41 us against 49 at 32
-// rows over 60000 keys of 8 kv heads, 53 against 50 at 48 rows; at d = 128 they do not: 85 against 64.
-inline int pair_rows_of(int G, int d) { return G > kTile ? 0x7fffffff : (d == 64 ? 32 : 16); }
+// tiles, the others in the small tiles (with more than 128 heads per kv head, all of them). 17 to 32 rows
+// beside longer sequences: two 16-row tiles, which read the keys twice, beat a 128-row one at d = 64 (41 us
+// against 49 at 32 rows over 60000 keys of 8 kv heads), at d = 128 they do not (85 against 64). 64 rows:
+// pairs (48 sequences as above: 126 us at d = 128, 77 at d = 64, against 195 and 120 in two 32-row tiles).
+inline int pair_rows_of(int G, int d, int max_q) {
+  return G > kTile ? 0x7fffffff : (d == 64 || row_tile_of(G, max_q) == 32 ? 32 : 16);
+}
+
 cudaError_t launch_rope(RopeLaunch& p, int d, bool paged, int num_sms, cudaStream_t st);
 
 }  // namespace fa

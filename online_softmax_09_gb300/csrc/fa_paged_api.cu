@@ -139,19 +139,21 @@ fa::PagedBatch device_batch(const fa_paged_batch* b, int num_pages, uint32_t* st
   x.causal = b->causal || b->window > 0;
   x.window = b->window;
   x.pair_tokens = x.G <= 128 ? 2 * (128 / x.G) : 1;
+  x.row_tile = fa::row_tile_of(x.G, b->max_q);
   x.status = status;
   return x;
 }
 
-// Some sequence may have more rows than a 16-row tile: pairs of 128-row tiles are launched as well.
+// Some sequence may have more rows than the small tiles are for: pairs of 128-row tiles are launched as well.
 bool with_pairs(const fa_paged_batch* b) {
   const int G = b->Hq / b->Hkv;
-  return (long long)b->max_q * G > fa::pair_rows_of(G, b->d);
+  return (long long)b->max_q * G > fa::pair_rows_of(G, b->d, b->max_q);
 }
 
 // Workspace: the partial results of the two kernels.
 size_t workspace_bytes(const fa_paged_batch* b) {
-  return fa::paged_rows_workspace_bytes(b->d) + (with_pairs(b) ? fa::paged_tiles_workspace_bytes(b->d) : 0);
+  return fa::paged_rows_workspace_bytes(b->d, fa::row_tile_of(b->Hq / b->Hkv, b->max_q)) +
+         (with_pairs(b) ? fa::paged_tiles_workspace_bytes(b->d) : 0);
 }
 
 // Tensor map of bf16 data with 128-byte swizzled boxes of 64 elements; `strides` in elements.
@@ -203,7 +205,7 @@ int fa_paged_plan(const int* cu_q, const int* kv_len, const fa_paged_batch* batc
   uint32_t* status = nullptr;
   FA_TRY(fa::device_state(&status, nullptr));
   return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status),
-                               fa::pair_rows_of(batch->Hq / batch->Hkv, batch->d), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                               fa::pair_rows_of(batch->Hq / batch->Hkv, batch->d, batch->max_q), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_LAUNCH;
 }
@@ -286,6 +288,8 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   FA_TRY(fa::device_state(&status, &num_sms));
   fa::PagedFwd p = {};
   p.b = device_batch(batch, cache->num_pages, status);
+  num_sms = num_sms < fa::kPagedSms ? num_sms : fa::kPagedSms;
+  p.b.sms = num_sms;
   p.c.k = static_cast<const __nv_bfloat16*>(cache->k);
   p.c.v = static_cast<const __nv_bfloat16*>(cache->v);
   p.c.k_page = cache->k_strides[0];
@@ -302,9 +306,22 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   p.part = static_cast<float*>(workspace);
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt((float)batch->d);
   p.scale_log2 = s * 1.4426950408889634f;
+  // Few tiles among many CTAs: a tile's partial results are many, and a kernel of its own joins them, spread
+  // over the GPU, in place of the tile's last CTA alone. Its launch costs 2 us. It pays from 9 results of a
+  // tile on (16 rows at d = 128, 4000 keys: 19.7 us without, 16.7 with it at 28 tiles, 22.1 and 23.0 at 36),
+  // with up to 1024 values in a result, which the last CTA joins in two rounds, from 16 on (4 rows: 13.1 and
+  // 12.4 us at 16 tiles, 13.1 and 13.5 at 20). One sequence and pairs: no small tiles but for what a captured
+  // batch leaves.
+  const bool pairs = with_pairs(batch);
+  const long long most = (long long)batch->max_q * p.b.G, rows = most < p.b.row_tile ? most : p.b.row_tile;
+  const bool few = (batch->S > 1 || !pairs) &&
+                   (long long)batch->S * batch->Hkv * (rows * batch->d <= 1024 ? 16 : 9) < 2 * p.b.sms;
+  p.row_share = few ? reinterpret_cast<fa::RowShare*>(
+                          static_cast<char*>(workspace) +
+                          fa::plan_up((size_t)4 * fa::kPagedSms * fa::row_part(batch->d, p.b.row_tile) * 4))
+                    : nullptr;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  num_sms = num_sms < fa::kPagedSms ? num_sms : fa::kPagedSms;
-  if (with_pairs(batch)) {
+  if (pairs) {
     fa::TileMaps m;
     const int d = batch->d;
     const long long qd[3] = {d, batch->Hq, batch->T}, qs[2] = {q_strides[1], q_strides[0]};
@@ -315,7 +332,7 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
     const int cb[4] = {64, batch->page_size < 128 ? batch->page_size : 128, 1, 1};
     FA_TRY(make_map(&m.k, cache->k, 4, cd, ks, cb));
     FA_TRY(make_map(&m.v, cache->v, 4, cd, vs, cb));
-    char* ws = static_cast<char*>(workspace) + fa::paged_rows_workspace_bytes(d);
+    char* ws = static_cast<char*>(workspace) + fa::paged_rows_workspace_bytes(d, p.b.row_tile);
     p.tile_part = reinterpret_cast<float*>(ws);
     p.share = reinterpret_cast<fa::TileShare*>(ws + fa::plan_up((size_t)2 * fa::kPagedSms * fa::tile_part(d) * 4));
     p.tile_ctas = num_sms;

@@ -10,8 +10,9 @@ attention: a score is off by e_s = 2 d 2^-24 scale sum|q k| (fp32 accumulation i
   weight therefore by 2 e_s + 2^-20 (exp2 and the reference's rescales), and by 2^-8 once rounded for the product
   with V. o is the weighted mean under the rounded weights, so with eps = 2^-8 + 2 e_s + 2^-20 and weights p:
   |o - ref| <= 1.02 eps sum_j p_j |v_j - ref| + 2^-8 |ref| + 2^-20 max|v|  (fp32 sums of the products: the last).
-  So it is in the 16-row tiles, whose rounded weights are summed. The pairs of 128-row tiles (sequences of more
-  than 16 rows, new tokens times heads per kv head, or 32 at d = 64) divide
+  So it is in the tiles of 16 or 32 rows, whose rounded weights are summed. The pairs of 128-row tiles (sequences of
+  more than 32 rows, new tokens times heads per kv head; at d = 128 of more than 16, if the batch's limit of new tokens
+  allows more than 32) divide
   by the sum of the weights before rounding, plus the rounding of each block's largest one: with p'_j = p_j (1 + d_j),
   |d_j| <= 2^-8, and M the blocks' largest,
       o' - ref = sum_j p_j d_j v_j - ref sum_{j in M} p_j d_j  (to first order),
@@ -68,11 +69,11 @@ def assert_within(got, ref, tol, what=""):
                              f"(tolerance {np.broadcast_to(tol, bad.shape)[i]})")
 
 
-def attention_ref(q, K, V, n, causal, window, scale):
+def attention_ref(q, K, V, n, causal, window, scale, max_q=None):
     """One sequence: q [ql, Hq, d], K, V [n, Hkv, d] fp64 -> o, lse and their tolerances."""
     ql, Hq, d = q.shape
     G = Hq // K.shape[1] if n else 1
-    pairs = G <= 128 and ql * G > (32 if d == 64 else 16)
+    pairs = G <= 128 and ql * G > (16 if d == 128 and (max_q or ql) * G > 32 else 32)
     o = np.zeros((ql, Hq, d))
     lse = np.full((ql, Hq), -np.inf)
     to, tl = np.zeros((ql, Hq, d)), np.zeros((ql, Hq))
@@ -162,7 +163,7 @@ class Batch:
             a = self.cu[i]
             inside[a:a + ql] = True
             ro, rl, to, tl = attention_ref(f64(self.q[a:a + ql]), f64(self.K[i]), f64(self.V[i]), n,
-                                           causal or window > 0, window, scale)
+                                           causal or window > 0, window, scale, self.max_q)
             assert_within(lse[a:a + ql], rl, tl, f"lse of sequence {i} {self.lens[i]}")
             assert_within(o[a:a + ql], ro, to, f"o of sequence {i} {self.lens[i]}")
         if fill is not None:

@@ -83,6 +83,50 @@ def test_one_and_two_tiles_and_single_tokens_in_one_batch(heads, d):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("new", [2, 3, 4, 5, 6, 7, 8, 9])
+@pytest.mark.parametrize("d", [64, 128])
+def test_drafted_tokens(new, d):
+    # 8 to 36 rows per kv head: 16-row tiles, 32-row tiles with any part of the second half, and pairs.
+    r = np.random.default_rng(new)
+    lens = [(int(r.integers(1, new + 1)), int(r.integers(new, 1200))) for _ in range(12)] + [(new, 3000), (new, new)]
+    _run(Batch(lens, 8, 2, d, 16, seed=new), window=0)
+    _run(Batch(lens, 12, 3, d, 64, seed=new + 50), window=700)
+
+
+@pytest.mark.parametrize("lens", [[(1, 20000)], [(1, 9000), (1, 30)], [(2, 7000), (1, 1), (0, 5), (3, 0), (1, 2500)],
+                                  [(60, 800), (1, 9000), (2, 3)], [(1, 100)], [(0, 40)]])
+@pytest.mark.parametrize("heads", [(1, 1), (8, 1), (6, 2), (32, 1), (130, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_tiles_over_all_ctas(lens, heads, d):
+    # One to a few tiles with up to all CTAs' partial results each, joined by a kernel of their own; the same bits
+    # each time.
+    b = Batch(lens, *heads, d, 64, seed=len(lens) + heads[0], pad=2)
+    o, lse = _run(b)
+    o2, lse2 = _run(b)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _run(b, window=2100)
+
+
+def test_few_tiles_with_nan_infinities_and_masked_starts():
+    # A NaN in a visible key makes its head's rows NaN through the join; rows before the first key stay empty.
+    fa = fa_mod()
+    b = Batch([(4, 6000), (6, 3)], 8, 2, 128, 32)
+    page, slot = int(b.table[0, 5990 // 32]), 5990 % 32
+    b.kc[page, 0, slot] = float("nan")
+    plan = b.plan(fa)
+    o, lse = fa.forward_paged(b.dev["q"], b.kc, b.vc, plan)
+    fa.check()
+    assert torch.isnan(o[:4, :4].float()).all() and torch.isnan(lse[:4, :4]).all()
+    b.K[0][5990, 0] = 0
+    for h in (slice(4, 8), slice(0, 8)):
+        rows = slice(0, 4) if h.start else slice(4, 10)
+        i = 0 if h.start else 1
+        ro, rl, to, tl = attention_ref(f64(b.q[rows]), f64(b.K[i]), f64(b.V[i]), b.lens[i][1], True, 0, 128 ** -0.5,
+                                       max_q=b.max_q)
+        assert_within(o[rows, h], ro[:, h], to[:, h], "o")
+        assert_within(lse[rows, h], rl[:, h], tl[:, h], "lse")
+
+
 @pytest.mark.parametrize("layout", ["pshd", "both"])
 @pytest.mark.parametrize("lens", [[(1, 100), (1, 333)], [(90, 300), (1, 77)]])
 def test_cache_layouts_and_strided_queries(layout, lens):
@@ -221,7 +265,8 @@ def test_captured_chunks_follow_new_lengths():
         fa.check()
         for i, (ql, n) in enumerate(lens):
             a = b.cu[i]
-            ro, rl, to, tl = attention_ref(f64(b.q[a:a + ql]), f64(b.K[i][:n]), f64(b.V[i][:n]), n, True, 0, 128 ** -0.5)
+            ro, rl, to, tl = attention_ref(f64(b.q[a:a + ql]), f64(b.K[i][:n]), f64(b.V[i][:n]), n, True, 0, 128 ** -0.5,
+                                           max_q=b.max_q)
             assert_within(o[a:a + ql], ro, to, f"cut {cut} o {i}")
             assert_within(lse[a:a + ql], rl, tl, f"cut {cut} lse {i}")
 
