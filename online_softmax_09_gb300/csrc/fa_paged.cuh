@@ -353,6 +353,8 @@ struct PagedFwd {
   RowShare* row_share;  // [2 * sms], or NULL: no kernel follows, every tile is joined by its last CTA
   float* tile_part;  // and of the pairs, with what each CTA shares with those after it
   TileShare* share;  // [tile_ctas][2 tiles]
+  int o_wide;        // o starts at a multiple of 32 bytes
+  int warp_out;      // (d = 128) 32 rows of a tile are whole tokens, and TileMaps::o has boxes of them
   int tile_ctas;     // CTAs of the pairs' kernel (0: it does not run)
   float scale_log2;
 };
@@ -388,6 +390,7 @@ cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_
 struct TileMaps {
   CUtensorMap q;     // [T][Hq][d], box 64 dims x G heads x 128 / G tokens
   CUtensorMap k, v;  // [pages][Hkv][page_size][d], box 64 dims x min(page_size, 128) slots
+  CUtensorMap o;     // [T][Hq][d], box 64 dims x G heads x 32 / G tokens, if PagedFwd::warp_out
 };
 size_t paged_tiles_workspace_bytes(int d);
 cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st);

@@ -303,6 +303,7 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   p.q_head = q_strides[1];
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
+  p.o_wide = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
   p.part = static_cast<float*>(workspace);
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt((float)batch->d);
   p.scale_log2 = s * 1.4426950408889634f;
@@ -332,6 +333,13 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
     const int cb[4] = {64, batch->page_size < 128 ? batch->page_size : 128, 1, 1};
     FA_TRY(make_map(&m.k, cache->k, 4, cd, ks, cb));
     FA_TRY(make_map(&m.v, cache->v, 4, cd, vs, cb));
+    p.warp_out = d == 128 && 32 % p.b.G == 0;
+    m.o = m.q;
+    if (p.warp_out) {
+      const long long os[2] = {d, (long long)batch->Hq * d};
+      const int ob[3] = {64, p.b.G, 32 / p.b.G};
+      FA_TRY(make_map(&m.o, o, 3, qd, os, ob));
+    }
     char* ws = static_cast<char*>(workspace) + fa::paged_rows_workspace_bytes(d, p.b.row_tile);
     p.tile_part = reinterpret_cast<float*>(ws);
     p.share = reinterpret_cast<fa::TileShare*>(ws + fa::plan_up((size_t)2 * fa::kPagedSms * fa::tile_part(d) * 4));

@@ -54,8 +54,9 @@ struct TileSmem {
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + 2 * kTileBytes;
   static constexpr int kV = kK + NK * kTileBytes;
-  static constexpr int kOStage = kV + NV * kTileBytes;  // 4 KB per softmax warp: 32 rows x 64 columns
-  static constexpr int kBar = kOStage + 8 * 4096;
+  static constexpr int kOStage = kV + NV * kTileBytes;  // d = 128: 4 KB per softmax warp, 32 rows x 64 columns
+  static constexpr int kHalf = kOStage;  // d = 64: m, l, e of tile 1's half, one row per thread
+  static constexpr int kBar = kOStage + (D == 128 ? 8 * 4096 : kTile * 16);
   static constexpr int bQ = 0;
   static constexpr int bKFull = bQ + 2;
   static constexpr int bKEmpty = bKFull + NK;
@@ -157,9 +158,11 @@ __device__ __forceinline__ float max64f(const uint32_t (&a)[32], const uint32_t 
 template <int D, bool kTurn>
 __global__ void __launch_bounds__(kTileThreads, 1)
     fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const PagedFwd p) {
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                          const PagedFwd p) {
   using L = TileSmem<D>;
   constexpr bool kHalves = D == 64;  // see halves() in fa_paged.cuh
+  constexpr bool kBoxOut = D == 128;
   constexpr int NK = L::NK, NV = L::NV;
   const PagedBatch& b = p.b;
   SegIter<true> walk(b);  // (its loads and the plan's check go out together)
@@ -214,6 +217,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    if (kBoxOut && p.warp_out) tma_prefetch_desc(&tm_o);
   }
   // Rows that no load fills are zero, so that their scores are.
   for (int i = threadIdx.x; i < 2 * (D / 64) * (kTile - used) * 8; i += kTileThreads) {
@@ -476,35 +480,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t tS = tmem + 128 * t + lane_off;
     const uint32_t tO = tmem + 256 + 128 * t + lane_off;
     const float sl2 = p.scale_log2;
-    const uint32_t o_stage = sbase + L::kOStage + (uint32_t)warp * 4096;
     uint32_t sc = 0, on = 0, gv = 0;
     uint32_t twins = 0;  // stretches so far whose two halves were joined here
     bool owed = false;   // (tile 1) its half of the last one has not been taken over yet
     bool ok = true;
-    // 64 columns of this warp's rows of o, through its buffer, so that eight lanes write 128 neighbouring
-    // bytes of a row; `out`: this thread's row (-1: none).
-    auto store_cols = [&](const uint4 (&w)[2][4], int c, long long out) {
-      __syncwarp();
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const uint4 v4 = w[g >> 2][g & 3];
-        st_shared_v4(o_stage + (uint32_t)lane * 128 + ((g ^ (lane & 7)) << 4), v4.x, v4.y, v4.z, v4.w);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = 4 * i + (lane >> 3), g = lane & 7;
-        const long long ro = __shfl_sync(0xffffffffu, out, row);
-        const uint4 v4 = *reinterpret_cast<const uint4*>(smem + L::kOStage + warp * 4096 + row * 128 +
-                                                         ((g ^ (row & 7)) << 4));
-        if (ro >= 0) *reinterpret_cast<uint4*>(p.o + ro * D + c * 64 + g * 8) = v4;
-      }
-    };
-    auto pack = [](uint4 (&w)[4], const float* f, float x) {
-      uint32_t* wp = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) wp[i] = pack_bf16(f[2 * i] * x, f[2 * i + 1] * x);
-    };
     auto row_out = [&](int q0, int tok, int ql, int head) -> long long {
       return r < used && tok < ql ? (long long)(q0 + tok) * b.Hq + head * b.G + r_head : -1;
     };
@@ -640,7 +619,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!(ok = mbar_wait_warp(bar(L::bTwinFree), (twins - 1) & 1, ctl))) break;
         owed = false;
       }
-      float4* half = reinterpret_cast<float4*>(smem + L::kOStage + (4 + (warp & 3)) * 4096) + lane;
+      float4* half = reinterpret_cast<float4*>(smem + L::kHalf) + r;
       if (twin && t == 1) {  // over to tile 0: o stays in tensor memory
         *half = make_float4(m_run, l_run, e_run, 0.f);
         tc_fence_before();
@@ -662,20 +641,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         l_run = l_run * f0 + h.y * f1;
         e_run = e_run * f0 + h.z * f1;
       }
-      auto read_o = [&](int c, float (&f)[32]) {  // 32 columns of the row's sums
-        uint32_t o[32];
-        tmem_ld32(tO + c * 32, o);
+      auto read_o = [&](uint32_t (&o)[D / 32][32]) {  // the row's sums
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + c * 32, o[c]);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_ld_wait(o[c]);
         if (twin) {
-          uint32_t o1[32];
-          tmem_ld32(tO + 128 + c * 32, o1);
-          tmem_ld_wait(o1);
-          tmem_ld_wait(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1;
-        } else {
-          tmem_ld_wait(o);
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o1[32];
+            tmem_ld32(tO + 128 + c * 32, o1);
+            tmem_ld_wait(o1);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(o[k]);
+            for (int k = 0; k < 32; ++k)
+              o[c][k] = __float_as_uint(__uint_as_float(o[c][k]) * f0 + __uint_as_float(o1[k]) * f1);
+          }
         }
       };
       auto o_read = [&]() {  // the accumulators may be overwritten
@@ -690,35 +670,64 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         o_read();
       } else if (e.first && e.last) {
         const float inv = (l_run > 0.f || l_run != l_run) ? 1.f / (l_run + e_run) : 0.f;  // nothing seen: o = 0
-        uint4 w[D / 64][2][4];
+        uint32_t w[D / 2] = {};
+        if (n_kv > 0) {
+          uint32_t o[D / 32][32];
+          read_o(o);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float f[32];
-          if (n_kv > 0) {
-            read_o(c, f);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) f[k] = 0.f;
+          for (int k = 0; k < D / 2; ++k) {
+            const float2 v = mul2(make_float2(__uint_as_float(o[k >> 4][2 * k & 31]), __uint_as_float(o[k >> 4][(2 * k & 31) + 1])),
+                                  make_float2(inv, inv));
+            w[k] = pack_bf16(v.x, v.y);
           }
-          pack(w[c >> 1][c & 1], f, inv);
         }
         o_read();
         const long long out = row_out(e.q0, tok, e.ql, e.head);
+        const int z = kBoxOut && p.warp_out && __all_sync(0xffffffffu, out >= 0) ? e.q0 + tok0 + (warp & 3) * 32 / b.G : -1;
+        // Out by a bulk tensor store where the warp's rows are a box of o, else each thread its row, 32 bytes (whole
+        // sectors) at a time. At d = 128 the box is sooner for rows that it takes, at d = 64 no box is (16 x 2048
+        // tokens, 32 heads, 8 kv heads, d = 128: 479 us, 501 without it; 16 x 1743 tokens, 16 heads, d = 64: 187,
+        // 194 with it); both beat rows that go through shared memory to be stored by neighbouring threads (504, 199).
+        if (kBoxOut && z >= 0) {
+          const uint32_t o_stage = sbase + L::kOStage + (uint32_t)warp * 4096;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) store_cols(w[c], c, out);
-        if (out >= 0) p.lse[out] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+          for (int c = 0; c < D / 64; ++c) {
+            if (lane == 0) bulk_wait_read_all();  // the last store from this buffer has read it
+            __syncwarp();
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              st_shared_v4(o_stage + (uint32_t)lane * 128 + ((g ^ (lane & 7)) << 4), w[32 * c + 4 * g], w[32 * c + 4 * g + 1],
+                           w[32 * c + 4 * g + 2], w[32 * c + 4 * g + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tm_o, o_stage, c * 64, e.head * b.G, z);
+              bulk_commit_group();
+            }
+          }
+          p.lse[out] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+        } else if (out >= 0) {
+          uint8_t* dst = reinterpret_cast<uint8_t*>(p.o + out * D);
+          if (p.o_wide) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) st_global_v8(dst + 32 * k, w + 8 * k);
+          } else {
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k)
+              *reinterpret_cast<uint4*>(dst + 16 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          }
+          p.lse[out] = (m_run + log2f(l_run)) * 0.6931471805599453f;
+        }
       } else {
         float* slot = p.tile_part + (size_t)(2 * blockIdx.x + (e.first ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
         if (n_kv > 0) {
+          uint32_t o[D / 32][32];
+          read_o(o);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float f[32];
-            read_o(c, f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(slot + ((c * 8 + k) * kTile + r) * 4) =
-                  make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-          }
+          for (int k = 0; k < D / 4; ++k)
+            *reinterpret_cast<uint4*>(slot + (k * kTile + r) * 4) =
+                make_uint4(o[k >> 3][4 * k & 31], o[k >> 3][(4 * k & 31) + 1], o[k >> 3][(4 * k & 31) + 2],
+                           o[k >> 3][(4 * k & 31) + 3]);
         }
         o_read();
         slot[D * kTile + r] = m_run;  // -inf: nothing seen here, and o is not there
@@ -728,6 +737,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
   }
+  if (kBoxOut && warp < 8 && lane == 0) bulk_wait_read_all();  // before the CTA gives its shared memory up
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -743,7 +753,7 @@ static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, int num_sm
   static unsigned long long known[kMaxGpus];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_tiles_kernel<D, kTurn>), smem, known);
   if (e != cudaSuccess) return e;
-  fa_paged_tiles_kernel<D, kTurn><<<num_sms, kTileThreads, smem, st>>>(m.q, m.k, m.v, p);
+  fa_paged_tiles_kernel<D, kTurn><<<num_sms, kTileThreads, smem, st>>>(m.q, m.k, m.v, m.o, p);
   return cudaGetLastError();
 }
 

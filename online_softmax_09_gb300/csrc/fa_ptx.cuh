@@ -165,6 +165,13 @@ __device__ __forceinline__ void bulk_wait_read_all() {
 // Every committed bulk group has completed (its writes to global memory included).
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// 32 bytes to global memory, 32-byte aligned.
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // ------------------------------------------------------------------------------------------
 // Shared memory written by threads, read by the async proxy
 // ------------------------------------------------------------------------------------------

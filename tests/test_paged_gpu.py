@@ -93,6 +93,20 @@ def test_drafted_tokens(new, d):
     _run(Batch(lens, 12, 3, d, 64, seed=new + 50), window=700)
 
 
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 8, 16, 32, 40])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("offset", [0, 8])
+def test_outputs_of_any_group_and_alignment(G, d, offset):
+    # Rows of o leave in boxes, or 32 or 16 bytes at a time: chunks that end inside a warp's rows, o 16 bytes off.
+    fa = fa_mod()
+    b = Batch([(131, 131), (70, 333), (0, 9), (33, 40), (1, 100)], 2 * G, 2, d, 32, seed=G, pad=3, lead=1)
+    o = torch.full((b.T * b.Hq * d + offset,), FILL, dtype=torch.bfloat16, device="cuda")[offset:].view(b.T, b.Hq, d)
+    lse = torch.full((b.T, b.Hq), FILL, device="cuda")
+    fa.forward_paged(b.dev["q"], b.kc, b.vc, b.plan(fa), out=o, lse=lse)
+    fa.check()
+    b.check(o, lse, fill=FILL)
+
+
 @pytest.mark.parametrize("lens", [[(1, 20000)], [(1, 9000), (1, 30)], [(2, 7000), (1, 1), (0, 5), (3, 0), (1, 2500)],
                                   [(60, 800), (1, 9000), (2, 3)], [(1, 100)], [(0, 40)]])
 @pytest.mark.parametrize("heads", [(1, 1), (8, 1), (6, 2), (32, 1), (130, 1)])
