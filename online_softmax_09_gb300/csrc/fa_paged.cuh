@@ -141,15 +141,18 @@ __host__ __device__ __forceinline__ bool halves(int t0, int t1, const PagedBatch
   return b.d == 64 && t1 - t0 + 1 <= b.pair_tokens / 2;
 }
 // Every tile starts with some units for what it costs besides its blocks (queries in, sums out), so that
-// CTAs with many short tiles get fewer blocks: three blocks' time for a pair (2089 tokens of 32 heads at d = 64:
-// 45 us, 59 without), two for a 16-row tile (109 sequences of up to 421 keys: 30 us, 46 without).
+// CTAs with many short tiles get fewer blocks: three blocks' time for a pair at d = 128 (512 tokens over 32768
+// keys: 191 us, 193 with two), two at d = 64 (2089 tokens of 32 heads: 44 us, 45 with three, 59 without) or three
+// in halves (64 sequences of 128 tokens over 1000 keys: 56 us, 59 with two), two for a small tile (109 sequences
+// of up to 421 keys: 30 us, 46 without).
 template <bool kPairs>
-__host__ __device__ __forceinline__ int tile_start(const PagedBatch& b) {
-  return kPairs ? (b.d == 64 ? 6 : 3) : 2;
+__host__ __device__ __forceinline__ int tile_start(int t0, int t1, const PagedBatch& b) {
+  if (!kPairs) return 2;
+  return b.d == 64 && !halves(t0, t1, b) ? 4 : (b.d == 64 ? 6 : 3);
 }
 template <bool kPairs>
 __host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBatch& b, int n) {
-  const int at = tile_start<kPairs>(b);
+  const int at = tile_start<kPairs>(t0, t1, b);
   if (!kPairs || b.d != 64) return at + n;
   return at + (halves(t0, t1, b) ? (n + 1) & ~1 : 2 * n);
 }
@@ -269,7 +272,7 @@ struct SegIter {
     while (u < u_end) {
       if (head == b.Hkv) find_seq();
       // The tile's blocks are its units [first_u, end_u); this CTA has those from `from` to `to`.
-      const long long first_u = tile_u0 + tile_start<kPairs>(b), end_u = tile_u0 + nb;
+      const long long first_u = tile_u0 + tile_start<kPairs>(t0, t1, b), end_u = tile_u0 + nb;
       const long long from = max(u, first_u), to = min(u_end, end_u);
       const bool last = to == end_u;
       s.seq = seq;
