@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
   Seg* queue = reinterpret_cast<Seg*>(smem + L::kQueue);
   int* flag = reinterpret_cast<int*>(smem + L::kFlag);
   const PagedBatch& b = p.b;
-  SegIter<false, kRows> it(b);  // (its loads and the plan's check go out together)
+  // (Its loads and the check of the plan go out together.)
+  SegIter<false, kRows> it(b, p.tile_ctas > 0 ? max(1, 2 * (b.sms - pair_sms(b))) : gridDim.x);
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
     if (p.tile_ctas > 0) asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -157,6 +157,19 @@ __host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBa
   return at + (halves(t0, t1, b) ? (n + 1) & ~1 : 2 * n);
 }
 
+// SMs for the pairs where a batch has both kinds of tiles; the small ones have the others, at the same time: the
+// pairs are bound by the tensor cores and the small tiles by HBM (an SM alone draws twice its share of that). Of
+// as many as end both soonest, with the time of a small tile's unit on an SM counted as 0.31 of a pair's at
+// d = 128, and 0.43 of a half block's at d = 64. 4097 new tokens beside 23 single ones over 300 to 9000 keys: 347 us,
+// 366 one after the other (with 0.28: 377, 0.34: 346, 0.40: 351); 4 x 30000 keys beside 1024 over 16000: 253, 287.
+__device__ __forceinline__ int pair_sms(const PagedBatch& b) {
+  const long long rows = b.plan.units[0][b.S], pairs = b.plan.units[1][b.S];
+  if (rows == 0 || pairs == 0) return pairs == 0 ? 0 : b.sms;
+  const float r = (float)rows * (b.d == 64 ? 0.43f : 0.31f), p = (float)pairs;
+  const int n = max(1, min(b.sms - 2, (int)(b.sms * p / (p + r)))), m = b.sms - n;  // or one more: what ends sooner
+  return fmaxf(p / n, r / m) <= fmaxf(p / (n + 1), r / (m - 1)) ? n : n + 1;
+}
+
 // One stretch of key blocks of one row tile, as a CTA works it off.
 struct Seg {
   int seq, head, tile;
@@ -188,10 +201,10 @@ struct SegIter {
     wU = i <= b.S ? U[i] : 0x7fffffffffffffffLL;
     wS = i < b.S ? b.plan.seq[i] : PlanSeq{0, 0, 0, 0};
   }
-  __device__ __forceinline__ SegIter(const PagedBatch& batch) : b(batch), U(batch.plan.units[kPairs ? 1 : 0]) {
+  __device__ __forceinline__ SegIter(const PagedBatch& batch, unsigned ctas) : b(batch), U(batch.plan.units[kPairs ? 1 : 0]) {
     load_window(0);
     const long long W = U[b.S];
-    per = W <= 0x7fffffffLL ? (long long)(((unsigned)W + gridDim.x - 1) / gridDim.x) : (W + gridDim.x - 1) / gridDim.x;
+    per = W <= 0x7fffffffLL ? (long long)(((unsigned)W + ctas - 1) / ctas) : (W + ctas - 1) / ctas;
     if (kPairs && b.d == 64) per = (per + 1) & ~1LL;
     u = min(W, per * blockIdx.x);
     u_end = min(W, u + per);

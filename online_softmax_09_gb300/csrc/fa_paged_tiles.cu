@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr bool kBoxOut = D == 128;
   constexpr int NK = L::NK, NV = L::NV;
   const PagedBatch& b = p.b;
-  SegIter<true> walk(b);  // (its loads and the plan's check go out together)
+  SegIter<true> walk(b, max(1, pair_sms(b)));  // (its loads and the plan's check go out together)
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
     return;

@@ -93,6 +93,18 @@ def test_drafted_tokens(new, d):
     _run(Batch(lens, 12, 3, d, 64, seed=new + 50), window=700)
 
 
+@pytest.mark.parametrize("lens", [[(1, 400)] * 40 + [(40, 41)], [(300, 300)] * 7 + [(1, 2)], [(1, 3000), (70, 70)],
+                                  [(0, 5)] * 3 + [(64, 700)] * 20 + [(2, 90)] * 20, [(90, 300), (0, 7)]])
+@pytest.mark.parametrize("heads", [(8, 2), (7, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_tokens_beside_chunks(lens, heads, d):
+    # Both kinds of tiles at once, from nearly all SMs for the one to nearly all for the other.
+    b = Batch(lens, *heads, d, 32, seed=len(lens), pad=1)
+    o, lse = _run(b)
+    o2, lse2 = _run(b)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("G", [1, 2, 3, 4, 8, 16, 32, 40])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("offset", [0, 8])
