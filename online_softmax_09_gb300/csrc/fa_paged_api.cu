@@ -308,15 +308,17 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   const float s = scale > 0.f ? scale : 1.0f / std::sqrt((float)batch->d);
   p.scale_log2 = s * 1.4426950408889634f;
   // Few tiles among many CTAs: a tile's partial results are many, and a kernel of its own joins them, spread
-  // over the GPU, in place of the tile's last CTA alone. Its launch costs 2 us. It pays from 9 results of a
-  // tile on (16 rows at d = 128, 4000 keys: 19.7 us without, 16.7 with it at 28 tiles, 22.1 and 23.0 at 36),
-  // with up to 1024 values in a result, which the last CTA joins in two rounds, from 16 on (4 rows: 13.1 and
-  // 12.4 us at 16 tiles, 13.1 and 13.5 at 20). One sequence and pairs: no small tiles but for what a captured
-  // batch leaves.
+  // over the GPU, in place of the tile's last CTA alone. Its launch costs 2 us of the GPU's time and as much of
+  // the host's. It pays from 9 results of a tile on (16 rows at d = 128, 4000 keys: 19.7 us without, 16.7 with it
+  // at 28 tiles, 22.1 and 23.0 at 36); with up to 1024 values in a result, which the last CTA joins in two
+  // rounds, 16 bring as much as the host pays (4 rows: 13.1 and 12.4 us at 16 tiles), 24 and more 1.5 to 4 us
+  // (8 tiles: 12.5 and 10.2 over 4000 keys, 32.0 and 27.9 over 30000). One sequence and pairs: no small tiles
+  // but for what a captured batch leaves.
   const bool pairs = with_pairs(batch);
   const long long most = (long long)batch->max_q * p.b.G, rows = most < p.b.row_tile ? most : p.b.row_tile;
-  const bool few = (batch->S > 1 || !pairs) &&
-                   (long long)batch->S * batch->Hkv * (rows * batch->d <= 1024 ? 16 : 9) < 2 * p.b.sms;
+  const long long tiles = (long long)batch->S * batch->Hkv, need = rows * batch->d <= 1024 ? 24 : 9;
+  const bool few = (batch->S > 1 || !pairs) && tiles * need < 2 * p.b.sms &&
+                   (long long)batch->max_pages * batch->page_size >= need * fa::kRowBlk;
   p.row_share = few ? reinterpret_cast<fa::RowShare*>(
                           static_cast<char*>(workspace) +
                           fa::plan_up((size_t)4 * fa::kPagedSms * fa::row_part(batch->d, p.b.row_tile) * 4))
