@@ -118,7 +118,7 @@ cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBat
   return cudaGetLastError();
 }
 
-// ------------------------------------------------------------------------------- 16-row tiles
+// -------------------------------------------------------------------------------- small tiles
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
   const int n = full ? 16 : 0;  // 0: the 16 bytes are zero-filled and nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");

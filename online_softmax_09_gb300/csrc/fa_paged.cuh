@@ -158,8 +158,8 @@ __host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBa
 }
 
 // SMs for the pairs where a batch has both kinds of tiles; the small ones have the others, at the same time: the
-// pairs are bound by the tensor cores and the small tiles by HBM (an SM alone draws twice its share of that). Of
-// as many as end both soonest, with the time of a small tile's unit on an SM counted as 0.31 of a pair's at
+// pairs are bound by the tensor cores and the small tiles by HBM, of which 15 of
+// the 152 SMs still draw 1.4 times their share. As many as end both soonest, with the time of a small tile's unit on an SM counted as 0.31 of a pair's at
 // d = 128, and 0.43 of a half block's at d = 64. 4097 new tokens beside 23 single ones over 300 to 9000 keys: 347 us,
 // 366 one after the other (with 0.28: 377, 0.34: 346, 0.40: 351); 4 x 30000 keys beside 1024 over 16000: 253, 287.
 __device__ __forceinline__ int pair_sms(const PagedBatch& b) {
