@@ -158,16 +158,17 @@ __host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBa
 }
 
 // SMs for the pairs where a batch has both kinds of tiles; the small ones have the others, at the same time: the
-// pairs are bound by the tensor cores and the small tiles by HBM, of which 15 of
-// the 152 SMs still draw 1.4 times their share. As many as end both soonest, with the time of a small tile's unit on an SM counted as 0.31 of a pair's at
-// d = 128, and 0.43 of a half block's at d = 64. 4097 new tokens beside 23 single ones over 300 to 9000 keys: 347 us,
-// 366 one after the other (with 0.28: 377, 0.34: 346, 0.40: 351); 4 x 30000 keys beside 1024 over 16000: 253, 287.
+// pairs are bound by the tensor cores and the small tiles by HBM, of which 15 of the 152 SMs still draw 1.4 times
+// their share. As many as end both soonest, with the time of a small tile's unit on an SM counted as 0.31 of a
+// pair's at d = 128, and 0.43 of a half block's at d = 64. 4097 new tokens beside 23 single ones over 300 to 9000
+// keys: 347 us, 366 one after the other (with 0.34: 346, 0.40: 351; too low costs more, 0.28 took 377); 4 x 30000
+// keys beside 1024 new tokens over 16000: 255 us, 287 one after the other (0.34: 259, 0.40: 268).
 __device__ __forceinline__ int pair_sms(const PagedBatch& b) {
   const long long rows = b.plan.units[0][b.S], pairs = b.plan.units[1][b.S];
   if (rows == 0 || pairs == 0) return pairs == 0 ? 0 : b.sms;
   const float r = (float)rows * (b.d == 64 ? 0.43f : 0.31f), p = (float)pairs;
   const int n = max(1, min(b.sms - 2, (int)(b.sms * p / (p + r)))), m = b.sms - n;  // or one more: what ends sooner
-  return fmaxf(p / n, r / m) <= fmaxf(p / (n + 1), r / (m - 1)) ? n : n + 1;
+  return m < 2 || fmaxf(p / n, r / m) <= fmaxf(p / (n + 1), r / (m - 1)) ? n : n + 1;
 }
 
 // One stretch of key blocks of one row tile, as a CTA works it off.

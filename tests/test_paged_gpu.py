@@ -91,6 +91,8 @@ def test_drafted_tokens(new, d):
     lens = [(int(r.integers(1, new + 1)), int(r.integers(new, 1200))) for _ in range(12)] + [(new, 3000), (new, new)]
     _run(Batch(lens, 8, 2, d, 16, seed=new), window=0)
     _run(Batch(lens, 12, 3, d, 64, seed=new + 50), window=700)
+    _run(Batch(lens, 4, 1, d, 128, seed=new + 90), causal=False)
+    _run(Batch(lens, 4, 1, d, 32, seed=new + 90), causal=False, window=90)
 
 
 @pytest.mark.parametrize("lens", [[(1, 400)] * 40 + [(40, 41)], [(300, 300)] * 7 + [(1, 2)], [(1, 3000), (70, 70)],
@@ -154,7 +156,7 @@ def test_few_tiles_with_nan_infinities_and_masked_starts():
 
 
 @pytest.mark.parametrize("layout", ["pshd", "both"])
-@pytest.mark.parametrize("lens", [[(1, 100), (1, 333)], [(90, 300), (1, 77)]])
+@pytest.mark.parametrize("lens", [[(1, 100), (1, 333)], [(90, 300), (1, 77)], [(7, 100), (5, 333), (1, 40)]])
 def test_cache_layouts_and_strided_queries(layout, lens):
     fa = fa_mod()
     b = Batch(lens, 8, 2, 128, 32, seed=5, layout=layout)
