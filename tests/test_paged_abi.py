@@ -20,6 +20,11 @@ def _ll(*v):
     return (ctypes.c_longlong * len(v))(*v)
 
 
+def test_packed_cache_is_the_struct(fa):
+    c = fa._Cache(*range(1, 10))
+    assert fa._pack_cache(*range(1, 10)) == bytes(c) and ctypes.sizeof(c) == 72
+
+
 def _rot(fa, rot=128, axes=None, naxes=1, inv=P):
     return fa._Rotary(inv, axes, naxes, rot, 0)
 
