@@ -155,7 +155,7 @@ template <int D>
 struct RowSmem {
   static constexpr int kStages = D == 128 ? 3 : 5;
   static constexpr int kJoinRows = D == 128 ? 8 : 16;  // rows that the warps join at a time
-  static constexpr int kSlots = D == 128 ? 4 : 8;   // stretches in the queue: the one before, the present one, those ahead
+  static constexpr int kSlots = D == 128 ? 4 : 8;  // stretches queued: the one before, the present one, those ahead
   static constexpr int kTile = kGran * D * 2;        // K or V of one granule
   static constexpr int kWarp = kStages * 2 * kTile;  // ring of one warp
   static constexpr int kMerge = kRowWarps * kWarp;   // kJoinRows rows of o of each warp
@@ -257,7 +257,8 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    if (mine[i].c1 >= 0) list[at + __popc(some[i] & ((1u << lane) - 1))] = Entry{mine[i], i * kRowThreads + (int)threadIdx.x};
+    if (mine[i].c1 >= 0)
+      list[at + __popc(some[i] & ((1u << lane) - 1))] = Entry{mine[i], i * kRowThreads + (int)threadIdx.x};
     at += __popc(some[i]);
   }
   __syncthreads();
@@ -311,9 +312,9 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
 // fourth granule of 16 keys with a ring of its own, so no barrier stands in the loop: it waits for its
 // own cp.async copies, forms the 16 MT x 16 scores (m16n8k16), carries its own running max and sums, and
 // adds P V. (The queries stand in registers at MT = 1; at MT = 2 there is no room for them beside o, and they
-// are read from shared memory.) The ring runs on across the CTA's stretches: the copies of the next ones are under way while
-// one is finished (a stretch of a short sequence is a few granules, and its chain of table, keys, join and
-// store would stand in the open each time). The four warps' results are joined once per stretch, and the
+// are read from shared memory.) The ring runs on across the CTA's stretches: the copies of the next ones are
+// under way while one is finished (a stretch of a short sequence is a few granules, and its chain of table,
+// keys, join and store would stand in the open each time). The four warps' results are joined once per stretch, and the
 // stretches of a tile that several CTAs share by the CTA that finishes last, or by a kernel that follows,
 // in the order of the keys.
 //

@@ -202,7 +202,8 @@ struct SegIter {
     wU = i <= b.S ? U[i] : 0x7fffffffffffffffLL;
     wS = i < b.S ? b.plan.seq[i] : PlanSeq{0, 0, 0, 0};
   }
-  __device__ __forceinline__ SegIter(const PagedBatch& batch, unsigned ctas) : b(batch), U(batch.plan.units[kPairs ? 1 : 0]) {
+  __device__ __forceinline__ SegIter(const PagedBatch& batch, unsigned ctas)
+      : b(batch), U(batch.plan.units[kPairs ? 1 : 0]) {
     load_window(0);
     const long long W = U[b.S];
     per = W <= 0x7fffffffLL ? (long long)(((unsigned)W + ctas - 1) / ctas) : (W + ctas - 1) / ctas;

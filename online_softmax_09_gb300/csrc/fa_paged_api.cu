@@ -204,8 +204,9 @@ int fa_paged_plan(const int* cu_q, const int* kv_len, const fa_paged_batch* batc
   if (batch->S > 0) FA_TRY(check_ptr(kv_len, 4));
   uint32_t* status = nullptr;
   FA_TRY(fa::device_state(&status, nullptr));
-  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status),
-                               fa::pair_rows_of(batch->Hq / batch->Hkv, batch->d, batch->max_q), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  const int pair_rows = fa::pair_rows_of(batch->Hq / batch->Hkv, batch->d, batch->max_q);
+  return fa::launch_paged_plan(cu_q, kv_len, device_batch(batch, 0, status), pair_rows,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_LAUNCH;
 }

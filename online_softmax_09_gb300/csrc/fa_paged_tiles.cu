@@ -120,7 +120,8 @@ __device__ __forceinline__ TileSeg tile_seg(const Seg& s, const PagedBatch& p) {
   }
   // Where both tiles have all the blocks, their order is free. CTAs that work on other rows of the same keys
   // then start at the same keys (Seg::turn), which so come from memory about once instead of once per pair.
-  const bool both = it.step == 1 && it.exists[1] && it.a[0] + it.a[1] == 0 && it.cnt[0] == it.n_max && it.cnt[1] == it.n_max;
+  const bool both = it.step == 1 && it.exists[1] && it.a[0] + it.a[1] == 0 && it.cnt[0] == it.n_max &&
+                    it.cnt[1] == it.n_max;
   it.turn = kTurn && both && it.n_max == s.n ? s.turn : 0;
   it.head = s.head;
   it.q0 = s.q0;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // lane's box of the next block to load. Found here for the first time, beside the setup.
   Seg s;
   TileSeg it;
-    struct Look {
+  struct Look {
     const int* tab;
     int lo, hi;
   } cur = {nullptr, 0, 0};
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int j = 0; ok && j < n_max; ++j) {
         const int slot = (blk * kPairBlk + lane * box) & (b.page_size - 1);
         const int pg = page_at();
-                ++blk;
+        ++blk;
         if (kTurn && blk == j0 + n_max) blk = j0;
         if (j + 1 < n_max) read_entry(blk);
         const uint32_t sk = gk % NK, sv = gv % NV;
@@ -426,7 +427,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (it.n_max == 0) continue;
       const int step = kHalves ? it.step : 1;
       const int end[2] = {it.a[0] + (it.cnt[0] - 1) * step, it.a[1] + (it.cnt[1] - 1) * step};  // last blocks
-      auto has = [&](int t, int j) { return it.cnt[t] > 0 && it.a[t] <= j && j <= end[t] && !((j - it.a[t]) & (step - 1)); };
+      auto has = [&](int t, int j) {
+        return it.cnt[t] > 0 && it.a[t] <= j && j <= end[t] && !((j - it.a[t]) & (step - 1));
+      };
       bool k_ready = false;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -676,28 +679,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           read_o(o);
 #pragma unroll
           for (int k = 0; k < D / 2; ++k) {
-            const float2 v = mul2(make_float2(__uint_as_float(o[k >> 4][2 * k & 31]), __uint_as_float(o[k >> 4][(2 * k & 31) + 1])),
-                                  make_float2(inv, inv));
+            const uint32_t* pair = &o[k >> 4][2 * k & 31];
+            const float2 v = mul2(make_float2(__uint_as_float(pair[0]), __uint_as_float(pair[1])), make_float2(inv, inv));
             w[k] = pack_bf16(v.x, v.y);
           }
         }
         o_read();
         const long long out = row_out(e.q0, tok, e.ql, e.head);
-        const int z = kBoxOut && p.warp_out && __all_sync(0xffffffffu, out >= 0) ? e.q0 + tok0 + (warp & 3) * 32 / b.G : -1;
+        const bool box_out = kBoxOut && p.warp_out && __all_sync(0xffffffffu, out >= 0);
         // Out by a bulk tensor store where the warp's rows are a box of o, else each thread its row, 32 bytes (whole
         // sectors) at a time. At d = 128 the box is sooner for rows that it takes, at d = 64 no box is (16 x 2048
         // tokens, 32 heads, 8 kv heads, d = 128: 479 us, 501 without it; 16 x 1743 tokens, 16 heads, d = 64: 187,
         // 194 with it); both beat rows that go through shared memory to be stored by neighbouring threads (504, 199).
-        if (kBoxOut && z >= 0) {
+        if (box_out) {
           const uint32_t o_stage = sbase + L::kOStage + (uint32_t)warp * 4096;
+          const int z = e.q0 + tok0 + (warp & 3) * 32 / b.G;  // the first row's token
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             if (lane == 0) bulk_wait_read_all();  // the last store from this buffer has read it
             __syncwarp();
 #pragma unroll
             for (int g = 0; g < 8; ++g)
-              st_shared_v4(o_stage + (uint32_t)lane * 128 + ((g ^ (lane & 7)) << 4), w[32 * c + 4 * g], w[32 * c + 4 * g + 1],
-                           w[32 * c + 4 * g + 2], w[32 * c + 4 * g + 3]);
+              st_shared_v4(o_stage + (uint32_t)lane * 128 + ((g ^ (lane & 7)) << 4), w[32 * c + 4 * g],
+                           w[32 * c + 4 * g + 1], w[32 * c + 4 * g + 2], w[32 * c + 4 * g + 3]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
