@@ -151,9 +151,10 @@ __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(_
 constexpr int kRowWarps = 4, kRowThreads = 32 * kRowWarps;
 constexpr int kGran = kRowBlk / kRowWarps;  // keys that one warp takes at a time: 16, within one page
 
-template <int D>
+template <int D, int MT>
 struct RowSmem {
-  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kCtas = row_ctas(D, 16 * MT);
+  static constexpr int kStages = D == 128 || kCtas == 3 ? 3 : 5;
   static constexpr int kJoinRows = D == 128 ? 8 : 16;  // rows that the warps join at a time
   static constexpr int kSlots = D == 128 ? 4 : 8;  // stretches queued: the one before, the present one, those ahead
   static constexpr int kTile = kGran * D * 2;        // K or V of one granule
@@ -163,7 +164,7 @@ struct RowSmem {
   static constexpr int kQueue = kStat + kRowWarps * 3 * kJoinRows * 4;
   static constexpr int kFlag = kQueue + kSlots * (int)sizeof(Seg);
   static constexpr int kBytes = (kFlag + 4 + 15) / 16 * 16;
-  static_assert(kBytes <= 115712, "two CTAs must fit an SM");
+  static_assert(kBytes <= 231424 / kCtas, "kCtas CTAs must fit an SM");
 };
 
 
@@ -308,7 +309,7 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
   }
 }
 
-// fa_paged_rows_kernel: tiles of 16 MT rows. Four warps per CTA, two CTAs per SM; each warp takes every
+// fa_paged_rows_kernel: tiles of 16 MT rows. Four warps per CTA, two or three CTAs per SM; each warp takes every
 // fourth granule of 16 keys with a ring of its own, so no barrier stands in the loop: it waits for its
 // own cp.async copies, forms the 16 MT x 16 scores (m16n8k16), carries its own running max and sums, and
 // adds P V. (The queries stand in registers at MT = 1; at MT = 2 there is no room for them beside o, and they
@@ -327,8 +328,8 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
 // scores still pass through the softmax's threads; the tensor pipe is 19 % busy. A single token over 1000 keys
 // takes 8.1 us, a chain of latencies (plan, table, keys, join, release, partial results).
 template <int D, int MT>
-__global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const PagedFwd p) {
-  using L = RowSmem<D>;
+__global__ void __launch_bounds__(kRowThreads, row_ctas(D, 16 * MT)) fa_paged_rows_kernel(const PagedFwd p) {
+  using L = RowSmem<D, MT>;
   constexpr int kRows = 16 * MT;        // rows of a tile
   constexpr int kChunks = D / 8;        // 16-byte chunks of a row
   constexpr int kRowsPer = 32 / kChunks;  // rows that one copy instruction of a warp covers
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
   int* flag = reinterpret_cast<int*>(smem + L::kFlag);
   const PagedBatch& b = p.b;
   // (Its loads and the check of the plan go out together.)
-  SegIter<false, kRows> it(b, p.tile_ctas > 0 ? max(1, 2 * (b.sms - pair_sms(b))) : gridDim.x);
+  SegIter<false, kRows> it(b, p.tile_ctas > 0 ? max(1, L::kCtas * (b.sms - pair_sms(b))) : gridDim.x);
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
     if (p.tile_ctas > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -777,7 +778,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) fa_paged_rows_kernel(const Pag
 // all, against 52.7 with the last CTA joining them alone.
 template <int D>
 __global__ void __launch_bounds__(128) fa_paged_join_rows_kernel(const PagedFwd p) {
-  constexpr int kPieces = D / 32, kMost = 2 * kPagedSms, kParts = 16;
+  constexpr int kPieces = D / 32, kMost = row_ctas(D, 16) * kPagedSms, kParts = 16;
   __shared__ RowShare share[kMost];
   __shared__ short first[kMost];  // of the tiles that are shared: their first CTA
   __shared__ int count[4];
@@ -785,7 +786,8 @@ __global__ void __launch_bounds__(128) fa_paged_join_rows_kernel(const PagedFwd 
   __shared__ float stat_s[kParts][3];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' kernel is complete
   const PagedBatch& b = p.b;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ctas = 2 * b.sms, rows_max = b.row_tile;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows_max = b.row_tile;
+  const int ctas = row_ctas(D, rows_max) * b.sms;
   constexpr int kEach = (kMost + 127) / 128;
   RowShare mine[kEach];
   uint32_t some[kEach];
@@ -899,12 +901,12 @@ __global__ void __launch_bounds__(128) fa_paged_join_rows_kernel(const PagedFwd 
 
 template <int D, int MT>
 static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) {
-  constexpr int smem = RowSmem<D>::kBytes;
+  constexpr int smem = RowSmem<D, MT>::kBytes;
   static unsigned long long known[kMaxGpus];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_rows_kernel<D, MT>), smem, known);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * num_sms);
+  cfg.gridDim = dim3(RowSmem<D, MT>::kCtas * num_sms);
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -924,7 +926,8 @@ static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) 
 }
 
 size_t paged_rows_workspace_bytes(int d, int row_tile) {
-  return plan_up((size_t)4 * kPagedSms * row_part(d, row_tile) * 4) + plan_up((size_t)2 * kPagedSms * sizeof(RowShare));
+  const size_t ctas = (size_t)row_ctas(d, row_tile) * kPagedSms;
+  return plan_up(2 * ctas * row_part(d, row_tile) * 4) + plan_up(ctas * sizeof(RowShare));
 }
 
 cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st) {

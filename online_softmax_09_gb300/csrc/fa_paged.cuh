@@ -70,7 +70,7 @@ struct PagedBatch {
   long long table_stride;
   int S, T, max_q, Hq, Hkv, G, d, page_size, page_shift, max_pages, num_pages, causal, window;
   int pair_tokens;  // tokens of a pair of 128-row tiles: 2 * (128 / G)
-  int sms;          // SMs in use: one CTA each for the pairs, two for the small tiles
+  int sms;          // SMs in use: one CTA each for the pairs, two or three for the small tiles
   int row_tile;     // rows of the small tiles: 16, or 32 in batches with a sequence of more than 16
   uint32_t* status;
 };
@@ -160,13 +160,13 @@ __host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBa
 // SMs for the pairs where a batch has both kinds of tiles; the small ones have the others, at the same time: the
 // pairs are bound by the tensor cores and the small tiles by HBM, of which 15 of the 152 SMs still draw 1.4 times
 // their share. As many as end both soonest, with the time of a small tile's unit on an SM counted as 0.31 of a
-// pair's at d = 128, and 0.43 of a half block's at d = 64. 4097 new tokens beside 23 single ones over 300 to 9000
+// pair's at d = 128, and 0.37 of a half block's at d = 64. 4097 new tokens beside 23 single ones over 300 to 9000
 // keys: 347 us, 366 one after the other (with 0.34: 346, 0.40: 351; too low costs more, 0.28 took 377); 4 x 30000
 // keys beside 1024 new tokens over 16000: 255 us, 287 one after the other (0.34: 259, 0.40: 268).
 __device__ __forceinline__ int pair_sms(const PagedBatch& b) {
   const long long rows = b.plan.units[0][b.S], pairs = b.plan.units[1][b.S];
   if (rows == 0 || pairs == 0) return pairs == 0 ? 0 : b.sms;
-  const float r = (float)rows * (b.d == 64 ? 0.43f : 0.31f), p = (float)pairs;
+  const float r = (float)rows * (b.d == 64 ? 0.37f : 0.31f), p = (float)pairs;
   const int n = max(1, min(b.sms - 2, (int)(b.sms * p / (p + r)))), m = b.sms - n;  // or one more: what ends sooner
   return m < 2 || fmaxf(p / n, r / m) <= fmaxf(p / (n + 1), r / (m - 1)) ? n : n + 1;
 }
@@ -368,7 +368,7 @@ struct PagedFwd {
   __nv_bfloat16* o;  // [T][Hq][d]
   float* lse;        // [T][Hq]
   float* part;       // partial results of the small tiles: 2 slots per CTA
-  RowShare* row_share;  // [2 * sms], or NULL: no kernel follows, every tile is joined by its last CTA
+  RowShare* row_share;  // [row_ctas * sms], or NULL: no kernel follows, every tile is joined by its last CTA
   float* tile_part;  // and of the pairs, with what each CTA shares with those after it
   TileShare* share;  // [tile_ctas][2 tiles]
   int o_wide;        // o starts at a multiple of 32 bytes
@@ -376,6 +376,10 @@ struct PagedFwd {
   int tile_ctas;     // CTAs of the pairs' kernel (0: it does not run)
   float scale_log2;
 };
+
+// CTAs per SM of the small tiles' kernel: what its registers leave room for (16 rows at d = 64: 109 single tokens
+// over up to 421 keys of 16 heads 25.8 us, 29.7 with two CTAs and deeper rings; 256 over 500 keys 29.8, 33.0).
+__host__ __device__ constexpr int row_ctas(int d, int row_tile) { return d == 64 && row_tile == 16 ? 3 : 2; }
 
 // One partial result of a small tile: o [rows][D], then m, l, rounded l of the rows.
 __host__ __device__ constexpr int row_part(int D, int rows) { return rows * (D + 3); }

@@ -318,11 +318,13 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   const bool pairs = with_pairs(batch);
   const long long most = (long long)batch->max_q * p.b.G, rows = most < p.b.row_tile ? most : p.b.row_tile;
   const long long tiles = (long long)batch->S * batch->Hkv, need = rows * batch->d <= 1024 ? 24 : 9;
-  const bool few = (batch->S > 1 || !pairs) && tiles * need < 2 * p.b.sms &&
+  const long long ctas = (long long)fa::row_ctas(batch->d, p.b.row_tile) * p.b.sms;
+  const bool few = (batch->S > 1 || !pairs) && tiles * need < ctas &&
                    (long long)batch->max_pages * batch->page_size >= need * fa::kRowBlk;
   p.row_share = few ? reinterpret_cast<fa::RowShare*>(
                           static_cast<char*>(workspace) +
-                          fa::plan_up((size_t)4 * fa::kPagedSms * fa::row_part(batch->d, p.b.row_tile) * 4))
+                          fa::plan_up((size_t)2 * fa::row_ctas(batch->d, p.b.row_tile) * fa::kPagedSms *
+                                      fa::row_part(batch->d, p.b.row_tile) * 4))
                     : nullptr;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (pairs) {
