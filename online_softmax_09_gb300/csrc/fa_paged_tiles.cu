@@ -15,8 +15,9 @@
 //              reference max moved only when a row outgrows it by 2^8, P as bf16 over the scores'
 //              columns, and the rounding of each tile's largest weight carried along as in the dense
 //              forward, so that o is not off where one key dominates.
-// Slots of the last page past the sequence hold anything, NaN too, and 0 * NaN is NaN: the rows of V
-// past the last key are set to zero in shared memory before the product.
+// Slots past the sequence, and before the window of its first new token, hold anything, NaN too, and 0 * NaN is
+// NaN: pages of such slots alone are not read (zeros stand for them), and where a page holds both, the rows of V
+// past the last key and before the pair's first are set to zero in shared memory before the product.
 // A pair that several CTAs share leaves unnormalised sums in the workspace, the rows of a warp side by
 // side; the kernel that follows joins them in the order of the keys (fa_paged.cu).
 //
@@ -517,15 +518,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // A warp whose rows all lie past the tile's tokens only keeps the barriers going. (At d = 128 such a
       // CTA waits for memory, and the test cost long chunks 2 %.)
       const bool idle = kHalves && (warp & 3) * 32 >= min(used, (s.ql - tok0) * b.G);
-      // Rows of V past the last key (both tiles may write the same zeros): after the copy has landed,
-      // before the product that the arrival at bPFull lets start.
-      auto clear_tail = [&](int j, int kv0) -> bool {
+      // Rows of V that no row of the pair sees, past the last key and before the first token's window (both tiles
+      // may write the same zeros): after the copy has landed, before the product that the arrival at bPFull lets
+      // start. Called for masked blocks; most have no such rows.
+      auto clear_unseen = [&](int j, int kv0) -> bool {
+        const int past = kvl - kv0, p0 = kvl - s.ql + s.t0;
+        const int before = b.window > 0 && p0 >= b.window ? min(p0 - b.window + 1 - kv0, kPairBlk) : 0;
+        if (past >= kPairBlk && before <= 0) return true;
         const uint32_t g = gv0 + a_t + j * step, sv = g % NV;
         if (!mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
-        for (int row = kvl - kv0 + (r >> 3); row < kPairBlk; row += 16)
+        auto clear = [&](int row) {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
             st_shared_v4(sV + sv * L::kTileBytes + c * 16384 + row * 128 + (r & 7) * 16, 0, 0, 0, 0);
+        };
+        for (int row = r >> 3; row < before; row += 16) clear(row);
+        for (int row = past + (r >> 3); row < kPairBlk; row += 16) clear(row);
         fence_proxy_async_smem();
         return true;
       };
@@ -539,14 +547,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // (turn > 0: step is 1, and both tiles have all the blocks)
         const int x = !kTurn ? j : (j + turn < n_kv ? j + turn : j + turn - n_kv);
         const int kv0 = kv_first + x * step * kPairBlk;
-        const bool tail = kv0 + kPairBlk > kvl;
+        const bool need_mask = kv0 + kPairBlk > kvl || (b.causal && kv0 + kPairBlk - 1 > pos0) ||
+                               (b.window > 0 && kv0 < pos1 - b.window + 1);
         if (idle) {
-          if (tail && !(ok = clear_tail(j, kv0))) break;
+          if (need_mask && !(ok = clear_unseen(j, kv0))) break;
           mbar_arrive(bar(L::bPFull + t));
           continue;
         }
-        const bool need_mask = tail || (b.causal && kv0 + kPairBlk - 1 > pos0) ||
-                               (b.window > 0 && kv0 < pos1 - b.window + 1);
         uint32_t sr[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         l_run = l_run * corr + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
-        if (tail && !(ok = clear_tail(j, kv0))) break;
+        if (need_mask && !(ok = clear_unseen(j, kv0))) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar(L::bPFull + t));
