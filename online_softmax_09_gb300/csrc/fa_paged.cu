@@ -228,7 +228,11 @@ struct JoinPiece {
     if (!on) return;
 #pragma unroll
     for (int y = 0; y < kAtOnce; ++y) {
-      if (c + y > s.c1 || mi[y] == -INFINITY) continue;  // nothing seen there: o was not written
+      if (c + y > s.c1) continue;
+      if (mi[y] == -INFINITY) {  // nothing seen there, o was not written: l = 0; or every score was NaN, as l is
+        Ls += li[y];
+        continue;
+      }
       const float mn = fmaxf(M, mi[y]);
       const float fa = ex2(M - mn), fb = ex2(mi[y] - mn);
       M = mn;
