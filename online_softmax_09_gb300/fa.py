@@ -512,7 +512,7 @@ class PagedPlan:
         self.device, self.index = device, device.index
         self.q_shape, self.kv_shape, self.lse_shape, self.page_shape = (T, Hq, d), (T, Hkv, d), (T, Hq), (Hkv, page_size, d)
         self.buffer = _empty(int(L.fa_paged_plan_bytes(S)), torch.uint8, device, stream)
-        self.home = _stream_of(stream, device.index)
+        self._kept = None  # the last stream on whose account the buffers and the table are kept
         self._c = _Batch(None, 0, self.buffer.data_ptr(), self.buffer.numel(), S, T, max_q, max_pages, page_size, Hq,
                          Hkv, d, causal, window)
         self._ref = ctypes.addressof(self._c)
@@ -520,12 +520,14 @@ class PagedPlan:
         self.workspace = _empty(max(self.ws_bytes, 16), torch.uint8, device, stream)
 
     def _use(self, stream, index):
-        """The raw stream of a call; the buffers outlive their use on a stream that they were not made on."""
+        """The raw stream of a call; what the plan holds outlives its use on a stream that it does not belong to
+        (the table is the caller's and may belong to any)."""
         raw = _stream_of(stream, index)
-        if raw != self.home and not torch.cuda.is_current_stream_capturing():
+        if raw != self._kept and not torch.cuda.is_current_stream_capturing():
             s = stream if stream is not None else torch.cuda.current_stream(index)
             for t in (self.buffer, self.workspace, self.table):
                 t.record_stream(s)
+            self._kept = raw
         return raw
 
     def _cache(self, k_cache, v_cache):
@@ -564,6 +566,7 @@ def paged_plan(cu_q, kv_lens, block_table, num_tokens: int, max_q: int, page_siz
     elif plan.key != key:
         raise ValueError("plan was made for other sizes")
     plan.table = block_table
+    plan._kept = None
     plan._c.block_table = block_table.data_ptr()
     plan._c.table_stride = block_table.stride(0)
     r = lib().fa_paged_plan(cu_q.data_ptr(), kv_lens.data_ptr(), plan._ref, plan._use(stream, i))
