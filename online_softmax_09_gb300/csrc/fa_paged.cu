@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(D, 16 * MT)) fa_paged_ro
         }
         const int pos = s.kvl - s.ql + tok;
         klim[t][h] = b.causal ? pos : s.kvl - 1;
-        klo[t][h] = b.window > 0 ? pos - b.window + 1 : 0;
+        klo[t][h] = mask_from(pos, b.window);
         top = max(top, klo[t][h]);
         low = min(low, klim[t][h]);
       }

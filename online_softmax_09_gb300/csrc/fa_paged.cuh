@@ -85,13 +85,25 @@ __device__ __forceinline__ bool plan_matches(const PagedBatch& b, int d) {
          h->causal == b.causal && h->window == b.window;
 }
 
+// The first key that a query at `pos` sees. (No difference is formed for a window that reaches back to the first
+// key: positions may be negative, and windows as large as an int.)
+__host__ __device__ __forceinline__ int first_key(int pos, int window) {
+  return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+// The same as a bound for masks, without the test: keys from it on are in the window. Negative where all are; it
+// wraps only where pos is negative too, and such a query sees no key anyway. (first_key in its place: 191.9 us
+// for 512 tokens over 32768 keys, 191.0 with this.)
+__host__ __device__ __forceinline__ int mask_from(int pos, int window) {
+  return window > 0 ? (int)((unsigned)pos - (unsigned)window + 1u) : 0;
+}
+
 // Keys [lo, hi) that some query of tokens [t0, t1] sees: token j stands at position kvl - ql + j and
 // sees keys up to its own (causal) and after position - window (window > 0).
 __host__ __device__ __forceinline__ void key_range(int t0, int t1, int ql, int kvl, int causal, int window, int& lo,
                                                    int& hi) {
   const int p0 = kvl - ql + t0, p1 = kvl - ql + t1;
   hi = causal ? (p1 + 1 < 0 ? 0 : p1 + 1) : kvl;
-  lo = (window > 0 && p0 - window + 1 > 0) ? p0 - window + 1 : 0;
+  lo = first_key(p0, window);
   if (lo > hi) lo = hi;
 }
 

@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const int tok = tok0 + r_tok;
       const int pos = kvl - s.ql + tok;
       const int klim = min(kvl - 1, b.causal ? pos : kvl - 1);
-      const int klo = b.window > 0 ? pos - b.window + 1 : 0;
+      const int klo = mask_from(pos, b.window);
       const int pos0 = kvl - s.ql + tok0, pos1 = pos0 + tpt - 1;
       // A warp whose rows all lie past the tile's tokens only keeps the barriers going. (At d = 128 such a
       // CTA waits for memory, and the test cost long chunks 2 %.)
@@ -522,8 +522,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // may write the same zeros): after the copy has landed, before the product that the arrival at bPFull lets
       // start. Called for masked blocks; most have no such rows.
       auto clear_unseen = [&](int j, int kv0) -> bool {
-        const int past = kvl - kv0, p0 = kvl - s.ql + s.t0;
-        const int before = b.window > 0 && p0 >= b.window ? min(p0 - b.window + 1 - kv0, kPairBlk) : 0;
+        const int past = kvl - kv0, before = min(first_key(kvl - s.ql + s.t0, b.window) - kv0, kPairBlk);
         if (past >= kPairBlk && before <= 0) return true;
         const uint32_t g = gv0 + a_t + j * step, sv = g % NV;
         if (!mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
@@ -548,7 +547,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int x = !kTurn ? j : (j + turn < n_kv ? j + turn : j + turn - n_kv);
         const int kv0 = kv_first + x * step * kPairBlk;
         const bool need_mask = kv0 + kPairBlk > kvl || (b.causal && kv0 + kPairBlk - 1 > pos0) ||
-                               (b.window > 0 && kv0 < pos1 - b.window + 1);
+                               (b.window > 0 && kv0 < mask_from(pos1, b.window));
         if (idle) {
           if (need_mask && !(ok = clear_unseen(j, kv0))) break;
           mbar_arrive(bar(L::bPFull + t));
