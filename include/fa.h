@@ -368,7 +368,7 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, co
  * Cache slots that no query of the sequence sees, and table entries for pages of such slots alone, may
  * hold anything. A NaN or infinity in a key that a query does not see does not reach it; one in a value
  * that some new token of the sequence sees may reach its other new tokens (0 * NaN), as in fa_fwd. o must
- * not overlap q. The result does not depend on scheduling: the same call gives the same bits.
+ * not overlap q: FA_ERR_INVALID. The result does not depend on scheduling: the same call gives the same bits.
  * After FA_ERR_TIMEOUT the plan has to be laid out anew.
  */
 size_t fa_fwd_paged_workspace_bytes(const fa_paged_batch *batch);

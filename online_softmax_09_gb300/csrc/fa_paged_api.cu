@@ -120,6 +120,23 @@ int check_cache(const fa_paged_cache* c, const fa_paged_batch* b) {
   return check_strides(c->v_strides, extent, 3, true);
 }
 
+// Queries [T][Hq][d] with strides (token, head) share memory with the dense o. (Rows along the larger stride are
+// taken as solid, so that o may lie between them.)
+bool overlaps(const void* q, const long long* strides, const void* o, const fa_paged_batch* b) {
+  const long long n[2] = {b->T, b->Hq}, s[2] = {n[0] > 1 ? strides[0] * 2 : 0, n[1] > 1 ? strides[1] * 2 : 0};
+  const int outer = s[0] >= s[1] ? 0 : 1, inner = 1 - outer;
+  constexpr long long kFar = 1LL << 60;  // beyond any address
+  const long long row = b->d * 2LL;
+  const long long span = s[inner] > 0 && n[inner] - 1 > kFar / s[inner] ? kFar : (n[inner] - 1) * s[inner] + row;
+  const long long from = static_cast<long long>(reinterpret_cast<uintptr_t>(o) - reinterpret_cast<uintptr_t>(q));
+  const long long to = from + n[0] * n[1] * row;
+  // The first piece that ends after `from`, and whether it begins before `to`.
+  if (from < span) return to > 0;
+  if (n[outer] <= 1) return false;
+  const long long i = (from - span) / s[outer] + 1;
+  return i < n[outer] && i * s[outer] < to;
+}
+
 fa::PagedBatch device_batch(const fa_paged_batch* b, int num_pages, uint32_t* status) {
   fa::PagedBatch x = {};
   fa::plan_layout(b->plan, b->S, &x.plan);
@@ -284,6 +301,7 @@ int fa_fwd_paged(const void* q, const long long* q_strides, const fa_paged_cache
   FA_TRY(check_ptr(lse, 4));
   const long long extent[2] = {batch->T, batch->Hq};
   FA_TRY(check_strides(q_strides, extent, 2, true));
+  if (overlaps(q, q_strides, o, batch)) return FA_ERR_INVALID;
   uint32_t* status = nullptr;
   int num_sms = 0;
   FA_TRY(fa::device_state(&status, &num_sms));

@@ -620,7 +620,8 @@ def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q
 
 def forward_paged(q, k_cache, v_cache, plan, scale: float | None = None, out=None, lse=None, stream=None):
     """O [T,Hq,d], LSE [T,Hq]: attention of a step's new tokens over the paged cache (fa_fwd_paged). q [T,Hq,d] bf16
-    CUDA, any strides with contiguous last dim. Rows that belong to no sequence are left as they were."""
+    CUDA, any strides with contiguous last dim. Rows that belong to no sequence are left as they were. ``out`` must
+    not overlap q (refused)."""
     shape, i = plan.q_shape, plan.index
     st = _strides_of("q", q, shape, i)
     if i != torch._C._cuda_getDevice():
