@@ -508,6 +508,8 @@ class PagedPlan:
         L = lib()
         if S < 0:
             raise ValueError("cu_q must hold S + 1 values")
+        if any(not -2 ** 31 <= n < 2 ** 31 for n in (S, T, max_q, max_pages, page_size, Hq, Hkv, d, window)):
+            raise ValueError("sizes and window must fit 32 bits")  # ctypes would cut them off
         self.key = (S, T, max_q, max_pages, page_size, Hq, Hkv, d, causal, window, device)
         self.device, self.index = device, device.index
         self.q_shape, self.kv_shape, self.lse_shape, self.page_shape = (T, Hq, d), (T, Hkv, d), (T, Hq), (Hkv, page_size, d)
