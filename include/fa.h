@@ -267,9 +267,10 @@ int fa_softmax_rows(const float *x, float *p, float *lse, long long rows, int n,
  * Rotary positions. Pair i < rot/2 of a head is turned by the angle
  *     phi = position[axis(i)] * inv_freq[i]:  (a, b) -> (a cos phi - b sin phi, b cos phi + a sin phi),
  * the pair being dims (i, i + rot/2), or (2i, 2i + 1) when `interleaved`; dims from rot on pass
- * through. One axis is text; several (time, height, width) are images and video. The angle is exact to
- * about 2^-32 of a turn for every 32-bit position (whole turns are dropped in integers), the products
- * are fp32, and each output is rounded to bf16 once.
+ * through. One axis is text; several (time, height, width) are images and video. Whole turns are dropped
+ * in integers, for every 32-bit position; what is left of the angle is off by at most 2^-26 of a turn plus
+ * |position| * max(|inv_freq|, 1) * 2^-53 turns (the second term passes the first from about 2^27 on). The
+ * products are fp32, and each output is rounded to bf16 once.
  */
 typedef struct {
   const float *inv_freq;      /* device, [rot/2], finite: radians per position */
@@ -289,7 +290,8 @@ typedef struct {
  *              So q and k may be views of a fused projection's output while q_out and k_out are the
  *              dense tensors that fa_fwd takes, and the other way round for their gradients.
  *   positions: device int32; axis a of token n of batch element b is at a * pos_axis + b * pos_batch + n.
- * An output may be its own input (same pointer and strides); it must not overlap anything else.
+ * An output may be its own input (same pointer and strides); it must not overlap anything else. Inputs may
+ * have strides of 0, outputs not.
  */
 int fa_rope(const void *q, void *q_out, const void *k, void *k_out, const long long *strides, const int *positions,
             long long pos_axis, long long pos_batch, const fa_rotary *rotary, int B, int Hq, int Hkv, int N, int d,
@@ -303,7 +305,7 @@ int fa_rope_bwd(const void *dq_out, void *dq, const void *dk_out, void *dk, cons
  * tokens cu_q[s] .. cu_q[s + 1] - 1 of the step's T, and has kv_len[s] tokens in the cache once they
  * are appended: new token j stands at position kv_len - q_len + j, and position x lives in page
  * block_table[s][x / page_size], slot x % page_size. Sequences may share pages (a common prefix).
- * Tokens outside every sequence (padding) are neither read nor written.
+ * Tokens outside every sequence (padding) are not written, and what they hold reaches no result.
  */
 typedef struct {
   const int *block_table;  /* device int32 [S][max_pages]; read only where a visible key or a new token lives */
@@ -350,7 +352,7 @@ int fa_paged_plan(const int *cu_q, const int *kv_len, const fa_paged_batch *batc
  *   rotary   : NULL: no rotation (q must then be NULL).
  *   positions: device int32, axis a of token t at a * pos_axis + t; NULL (one axis only): the token's
  *              position in its sequence.
- * q_out may be q. Two tokens with the same page and slot leave either one's values there.
+ * q_out may be q. Two tokens with the same page and slot leave parts of either one's values there.
  */
 int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, const long long *strides,
                     const fa_paged_cache *cache, const fa_paged_batch *batch, const fa_rotary *rotary,
@@ -360,7 +362,7 @@ int fa_paged_append(const void *q, void *q_out, const void *k, const void *v, co
  * Attention of a step's new tokens over the cache (their own keys and values included, so after
  * fa_paged_append): one token per sequence, chunks, or both in one batch. Same mathematics as fa_fwd
  * (and fa_fwd_window, with the window).
- *   q : [T][Hq][d] bf16; q_strides: HOST, (token, head) in elements, multiples of 8.
+ *   q : [T][Hq][d] bf16; q_strides: HOST, (token, head) in elements, positive multiples of 8.
  *   o : [T][Hq][d] bf16 and lse: [T][Hq] fp32 (natural log), contiguous. A query that sees no key gets
  *       o = 0 and lse = -inf.
  *   workspace: >= fa_fwd_paged_workspace_bytes(batch) bytes (of Hq, Hkv, d and max_q alone), 16-byte

@@ -357,7 +357,7 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
 // 6.45 TB/s, 96 % of the measured copy rate, two of 131072 keys 162 us (96 %), with 96 KB of copies under way
 // per CTA. mma.sync and not tcgen05, because 4 to 16 rows would leave most of a 128-row tile empty while its
 // scores still pass through the softmax's threads; the tensor pipe is 19 % busy. A single token over 1000 keys
-// takes 8.1 us, a chain of latencies (plan, table, keys, join, release, partial results).
+// takes 8.6 to 9 us, a chain of latencies (plan, table, keys, join, release, partial results).
 template <int D, int MT>
 __global__ void __launch_bounds__(kRowThreads, row_ctas(D, 16 * MT)) fa_paged_rows_kernel(const PagedFwd p) {
   using L = RowSmem<D, MT>;

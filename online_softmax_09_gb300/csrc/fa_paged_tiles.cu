@@ -22,9 +22,10 @@
 // side; the kernel that follows joins them in the order of the keys (fa_paged.cu).
 //
 // Bound by the loop of score product, softmax and P V, as in the dense forward: 1.52 us per block of both
-// tiles at d = 128, where the products alone take 1.3 at the measured bf16 peak. 512 tokens over 32768 keys
-// (32 query heads, 8 kv heads) take 191 us, 1430 TFLOP/s or 74 % of that peak: 4.4 us until the first scores,
-// 165 in the loop, 3 to 4 per further stretch, 9 for the join. L2 serves 71 % of what the loop loads.
+// tiles at d = 128 (1.55 in a mixed batch, beside the small tiles' reads), where the products alone take 1.3 at the
+// measured bf16 peak. 512 tokens over 32768 keys (32 query heads, 8 kv heads) take 191 us, 1430 TFLOP/s or 74 % of
+// that peak: 4.4 us until the first scores, 165 in the loop, 3 to 4 per further stretch, 9 for the join. L2 serves
+// 71 % of what the loop loads.
 #include <cudaTypedefs.h>
 #include <math.h>
 

@@ -6,9 +6,10 @@
 // the gradient is the same with -phi. The other dims pass through.
 //
 // Angles. inv_freq / 2 pi is kept as a fraction of a turn in 64-bit fixed point, w = inv_freq / 2 pi * 2^64,
-// so pos * w in 64-bit integers drops whole turns exactly, for any 32-bit position: what is lost is
-// pos * 2^-53 of the angle per position (the double that w comes from), 2^-32 of a turn when the top
-// half is taken, and 2^-24 of the remainder as a float. cos and sin follow from cospi and sinpi.
+// so pos * w in 64-bit integers drops whole turns exactly, for any 32-bit position. What is lost: the double that
+// w comes from is off by 2^-52.3 of itself (the product and the constant; below 0, by 2^-54 of a turn more), times
+// pos; the top half keeps 2^-32 of a turn; and as a float the remainder, at most half a turn, keeps 2^-26 of one.
+// In all 2^-26 of a turn up to positions of about 2^27, 2^-24 at 2^31. cos and sin follow from cospi and sinpi.
 //
 // Memory-bound: 2 bytes in and 2 out per element. A thread takes 8 pairs of one head (two 16-byte
 // chunks in, two out); the cos and sin of a CTA's tokens are made once, in shared memory, for all heads.

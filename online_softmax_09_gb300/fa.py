@@ -392,7 +392,7 @@ def softmax_rows(x, out=None, lse=None, with_lse: bool = True, stream=None):
 
 class Rotary:
     """Frequencies of a rotary position embedding (fa_rotary): ``inv_freq`` fp32 CUDA [rot / 2] in radians per
-    position; dims from rot on pass through. ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + rot / 2).
+    position, rot a multiple of 16; dims from rot on pass through. ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + rot / 2).
     ``axes``: the axis of each pair, for positions with several axes (e.g. time, height, width)."""
 
     def __init__(self, inv_freq, interleaved: bool = False, axes=None):
@@ -490,8 +490,9 @@ def _rope(name, fn, q, k, positions, rotary, q_out, k_out, stream):
 
 def rope(q, k, positions, rotary, q_out=None, k_out=None, stream=None):
     """Rotated (q, k) (fa_rope). q [B,Hq,N,d], k [B,Hkv,N,d] or None: bf16 CUDA, any strides with contiguous
-    last dim (e.g. views of a fused projection); outputs are contiguous unless given. positions: int32 CUDA
-    [N] or [B,N]; with several axes [A,N] or [A,B,N]. An output may be its input."""
+    last dim (e.g. views of a fused projection), 16-byte aligned; outputs are contiguous unless given. positions:
+    int32 CUDA [N] or [B,N]; with several axes [A,N] or [A,B,N]. An output may be its input, the same tensor; it
+    must not overlap anything else."""
     return _rope("fa_rope", (_lib or lib()).fa_rope, q, k, positions, rotary, q_out, k_out, stream)
 
 
@@ -502,7 +503,9 @@ def rope_backward(dq, dk, positions, rotary, q_out=None, k_out=None, stream=None
 
 class PagedPlan:
     """The layout of one serving step over a paged cache (fa_paged_batch, its plan and a workspace); made by
-    paged_plan and taken by paged_append and forward_paged of every layer of the step."""
+    paged_plan and taken by paged_append and forward_paged of every layer of the step. It holds the workspace and
+    counters of forward_paged, so calls that overlap on the GPU (two streams, two captured graphs replayed at once)
+    need a plan each; a captured graph needs its plan for as long as it is replayed."""
 
     def __init__(self, S, T, max_q, max_pages, page_size, Hq, Hkv, d, causal, window, device, stream):
         L = lib()
@@ -550,7 +553,7 @@ def paged_plan(cu_q, kv_lens, block_table, num_tokens: int, max_q: int, page_siz
     sequence s are rows cu_q[s] .. cu_q[s+1]-1 of the step's num_tokens; kv_lens int32 CUDA [S]: its cached tokens,
     the new ones included; block_table int32 CUDA [S, max_pages]; max_q bounds the new tokens of a sequence.
     ``plan``: an earlier plan of the same sizes, laid out anew in place (as a captured graph needs). Lengths stay on
-    the device; out of range, they are reported by check()."""
+    the device; a sequence whose lengths are out of range is left out, and check() reports it."""
     for name, t in (("cu_q", cu_q), ("kv_lens", kv_lens)):
         if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
@@ -622,8 +625,8 @@ def paged_append(q, k, v, k_cache, v_cache, plan, rotary=None, positions=None, q
 
 def forward_paged(q, k_cache, v_cache, plan, scale: float | None = None, out=None, lse=None, stream=None):
     """O [T,Hq,d], LSE [T,Hq]: attention of a step's new tokens over the paged cache (fa_fwd_paged). q [T,Hq,d] bf16
-    CUDA, any strides with contiguous last dim. Rows that belong to no sequence are left as they were. ``out`` must
-    not overlap q (refused)."""
+    CUDA, any strides with contiguous last dim, 16-byte aligned. Rows that belong to no sequence are left as they
+    were. ``out`` must not overlap q (refused). Calls that overlap on the GPU need a plan each."""
     shape, i = plan.q_shape, plan.index
     st = _strides_of("q", q, shape, i)
     if i != torch._C._cuda_getDevice():

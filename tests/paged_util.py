@@ -3,8 +3,9 @@
 Tolerances, derived from the kernels' arithmetic (bf16 half step: 2^-8 relative; fp32: 2^-24):
 
 rotation: y = a cos + b sin is formed in fp32 from bf16 a, b and rounded to bf16 once. The angle is off by
-  2^-32 of a turn and by half a float step of at most half a turn (9.4e-8 rad); cos and sin by two float steps
-  (2.4e-7); two products and a sum by 3 * 2^-24. So |y - ref| <= 2^-8 |ref| + 6e-7 (|a| + |b|).
+  half a float step of at most half a turn (9.4e-8 rad); cos and sin by two float steps (2.4e-7); two products and a
+  sum by 3 * 2^-24. So |y - ref| <= 2^-8 |ref| + 6e-7 (|a| + |b|). (The angle is off by 2^-52.3 of itself as well,
+  3.4e-7 rad at position 2^31: not counted, and inside what the other parts leave of their bounds.)
 
 attention: a score is off by e_s = 2 d 2^-24 scale sum|q k| (fp32 accumulation in any order, truncating), its
   weight therefore by 2 e_s + 2^-20 (exp2 and the reference's rescales), and by 2^-8 once rounded for the product
@@ -102,8 +103,8 @@ def attention_ref(q, K, V, n, causal, window, scale, max_q=None):
 
 
 class Batch:
-    """A ragged batch: lens [(new, cached)], a page table over shuffled pages, everything that no query may see set
-    to NaN or to numbers out of range."""
+    """A ragged batch: lens [(new, cached)], a page table over shuffled pages, everything past a sequence's cached
+    tokens set to NaN or to numbers out of range (what stands before a window is finite)."""
 
     def __init__(self, lens, Hq, Hkv, d, page, seed=0, layout="phsd", pad=0, lead=0, poison=True, extra_cols=2):
         g = torch.Generator().manual_seed(seed)

@@ -1,7 +1,7 @@
 """Attention over a paged cache (fa_paged_plan, fa_fwd_paged) against an fp64 reference.
 
-Unused slots of the cache hold NaN and infinities and unused table entries numbers out of range, so that whatever
-is read past a sequence or before its window shows.
+Slots of the cache past a sequence hold NaN and infinities and unused table entries numbers out of range, so that
+whatever is read past a sequence shows. (Before its window: test_paged_unseen_gpu.py.)
 """
 
 import numpy as np
