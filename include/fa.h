@@ -339,7 +339,7 @@ typedef struct {
  *   cu_q: device int32 [S + 1]; kv_len: device int32 [S].
  * Lengths out of range (cu_q falling or beyond T, a start before an earlier sequence's end, more than max_q
  * new tokens, kv_len beyond the table) are reported by fa_check as FA_ERR_INDEX, and that sequence is left
- * out: nothing of it is read or written, and the others are as they would be without it.
+ * out: nothing of it is written, and the others are as they would be without it.
  */
 size_t fa_paged_plan_bytes(int S);
 int fa_paged_plan(const int *cu_q, const int *kv_len, const fa_paged_batch *batch, fa_stream_t stream);

@@ -521,9 +521,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const bool idle = kHalves && (warp & 3) * 32 >= min(used, (s.ql - tok0) * b.G);
       // Rows of V that no row of the pair sees, past the last key and before the first token's window (both tiles
       // may write the same zeros): after the copy has landed, before the product that the arrival at bPFull lets
-      // start. Called for masked blocks; most have no such rows.
+      // start. At d = 128 it is called for all masked blocks and looks for such rows itself: a bound held in a
+      // register all along costs 0.3 % there. At d = 64 that is sooner (4 x 512 tokens over 8192 keys: 175.1 us, 176.2 the
+      // other way; 48 x 40 over 3000 with a window of 200: 40.7 and 41.5).
+      auto pair_lo = [&]() { return first_key(kvl - s.ql + s.t0, b.window); };
+      const int vlo = kHalves ? pair_lo() : 0;
       auto clear_unseen = [&](int j, int kv0) -> bool {
-        const int past = kvl - kv0, before = min(first_key(kvl - s.ql + s.t0, b.window) - kv0, kPairBlk);
+        const int past = kvl - kv0, before = min((kHalves ? vlo : pair_lo()) - kv0, kPairBlk);
         if (past >= kPairBlk && before <= 0) return true;
         const uint32_t g = gv0 + a_t + j * step, sv = g % NV;
         if (!mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
@@ -549,8 +553,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int kv0 = kv_first + x * step * kPairBlk;
         const bool need_mask = kv0 + kPairBlk > kvl || (b.causal && kv0 + kPairBlk - 1 > pos0) ||
                                (b.window > 0 && kv0 < mask_from(pos1, b.window));
+        const bool edge = kHalves ? kv0 + kPairBlk > kvl || kv0 < vlo : need_mask;
         if (idle) {
-          if (need_mask && !(ok = clear_unseen(j, kv0))) break;
+          if (edge && !(ok = clear_unseen(j, kv0))) break;
           mbar_arrive(bar(L::bPFull + t));
           continue;
         }
@@ -610,7 +615,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         l_run = l_run * corr + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
-        if (need_mask && !(ok = clear_unseen(j, kv0))) break;
+        if (edge && !(ok = clear_unseen(j, kv0))) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar(L::bPFull + t));
