@@ -44,3 +44,45 @@ def test_a_table_of_another_stream_is_kept_while_it_is_read(anew, chunk):
     fa.check(stream=s)
     b.check(o, lse)
     assert busy and not taken
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("lens", [[(1, 3000)] * 20, [(160, 2000), (1, 900), (40, 500)], [(1, 9000)]])
+def test_calls_at_once_with_a_plan_each(lens, captured):
+    # Two streams, each with batches of its own plan under way at the same time, eager or as captured graphs.
+    fa = fa_mod()
+    batches = [Batch(lens, 8, 2, d, 32, seed=52 + d) for d in (64, 128)]
+    streams = [torch.cuda.Stream() for _ in batches]
+    plans = [b.plan(fa) for b in batches]
+    outs = [fa.forward_paged(b.dev["q"], b.kc, b.vc, p) for b, p in zip(batches, plans)]
+    fa.check()
+    want = [(o.clone(), lse.clone()) for o, lse in outs]
+
+    def call(i, stream=None):
+        b = batches[i]
+        b.plan(fa, plan=plans[i], stream=stream)
+        fa.forward_paged(b.dev["q"], b.kc, b.vc, plans[i], out=outs[i][0], lse=outs[i][1], stream=stream)
+
+    graphs = []
+    if captured:
+        for i in range(2):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[i]):
+                for _ in range(3):
+                    call(i)
+    for o, lse in outs:
+        o.zero_()
+        lse.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            if captured:
+                with torch.cuda.stream(s):
+                    graphs[i].replay()
+            else:
+                call(i, s)
+    for s in streams:
+        fa.check(stream=s)
+    for b, (o, lse), (wo, wl) in zip(batches, outs, want):
+        b.check(o, lse)
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
