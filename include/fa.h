@@ -378,6 +378,93 @@ int fa_fwd_paged(const void *q, const long long *q_strides, const fa_paged_cache
                  void *o, float *lse, float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * A paged cache in 4 bits. A group of 32 dims of a key or value has a scale s, bf16 with four significant bits, and
+ * a code u in 1..15 per dim, which stands for (u - 8) s, a number that bf16 holds exactly. For a group x, s is max|x| / 7
+ * rounded to four significant bits and u = 8 + x / s rounded (ties to even), so that a value is off by s / 2 at most. A group
+ * with a NaN, an infinity or a magnitude of 2^120 or more is NaN throughout, one whose largest magnitude is below 2^-100 zero.
+ * The 32-bit word i of a group holds dims 8 i .. 8 i + 7, dim 8 i + 2 j + e in the bits from 4 j + 16 e on.
+ * Slots of a page and head are dense: codes [page_size][d / 2] bytes, scales [page_size][d / 32] bf16; 0.56 bytes per dim
+ * in all, where a bf16 cache takes 2.
+ */
+typedef struct {
+  void *k, *v;              /* device, 16-byte aligned: codes */
+  void *k_scale, *v_scale;  /* device, 16-byte aligned: scales */
+  long long k_strides[2], v_strides[2];              /* (page, head) in BYTES, multiples of 16 */
+  long long k_scale_strides[2], v_scale_strides[2];
+  int num_pages;            /* page numbers outside [0, num_pages) are reported, not followed */
+} fa_paged_cache4;
+
+/*
+ * fa_paged_append into a 4-bit cache: keys are rotated (with a rotary), rounded to bf16 as a bf16 cache would hold them, and
+ * quantised; values are quantised.
+ *   k_out, v_out : [T][Hkv][d] bf16, each may be NULL: the values that the cache now stands for, so that dense
+ *                  attention over a prompt can see what later steps will see. May be k and v themselves.
+ *   strides      : HOST, 12 values in elements, multiples of 8: (token, head) of q, q_out, k, v, k_out, v_out.
+ * Otherwise as fa_paged_append.
+ */
+int fa_paged_append4(const void *q, void *q_out, const void *k, const void *v, void *k_out, void *v_out,
+                     const long long *strides, const fa_paged_cache4 *cache, const fa_paged_batch *batch,
+                     const fa_rotary *rotary, const int *positions, long long pos_axis, fa_stream_t stream);
+
+/*
+ * fa_fwd_paged over a 4-bit cache: the same attention over the values that it stands for (the same bits as over a bf16 cache
+ * that holds them, where a sequence has more than 32 rows; else sums in another order). Plans are fa_paged_plan's. The
+ * workspace is of its own size; calls that overlap on the GPU need a plan and a workspace each.
+ */
+size_t fa_fwd_paged4_workspace_bytes(const fa_paged_batch *batch);
+int fa_fwd_paged4(const void *q, const long long *q_strides, const fa_paged_cache4 *cache, const fa_paged_batch *batch,
+                  void *o, float *lse, float scale, void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * The attention weight that cached tokens receive from a step's new tokens, for the batch, queries, scale and lse of
+ * fa_fwd_paged (or fa_fwd_paged4): for each slot t of a sequence's page and kv head that some new token sees
+ *     out[t] = weights[t] + sum of exp(scale q . k_t - lse) over the new tokens that see t and the query heads that share
+ *              its kv head,
+ * where weights[t] counts as 0 for the step's own tokens, so that a page needs no clearing when it is given to a sequence
+ * (call it once for every step). Other slots are not written.
+ *   lse      : [T][Hq] fp32, contiguous, as fa_fwd_paged writes it. A query with lse = -inf gives no weight.
+ *   weights, out : fp32, element (page, head, slot) at page * stride + head * stride + slot; weight_strides: HOST,
+ *              (page, head) of weights, then of out, in elements. out may be weights (with its strides); it must not overlap it
+ *              otherwise. Where sequences of the batch share pages, what they add to a slot is all there only if out is weights,
+ *              in no fixed order; else the same call gives the same bits.
+ *   cache    : of fa_paged_weights, only k is looked at (v may be NULL); of fa_paged_weights4, only k and k_scale.
+ */
+int fa_paged_weights(const void *q, const long long *q_strides, const float *lse, const fa_paged_cache *cache,
+                     const fa_paged_batch *batch, const float *weights, float *out, const long long *weight_strides,
+                     float scale, fa_stream_t stream);
+int fa_paged_weights4(const void *q, const long long *q_strides, const float *lse, const fa_paged_cache4 *cache,
+                      const fa_paged_batch *batch, const float *weights, float *out, const long long *weight_strides,
+                      float scale, fa_stream_t stream);
+
+/* Slots of a tensor that pages index: slot (page, head, slot) has `bytes` bytes at base + page * strides[0] + head *
+ * strides[1] + slot * strides[2] (strides in bytes). */
+typedef struct {
+  void *base;  /* device */
+  long long strides[3];
+  int bytes;
+} fa_paged_rows;
+
+/*
+ * Eviction by weight: for every sequence and kv head of the batch, n = kv_len tokens are cut down to new = min(n, keep[s]),
+ * and those that stay are copied, in their order, into the pages of another table, slots 0 .. new - 1. The first min(sinks, new)
+ * tokens stay, the last min(recent, what is left of new), and of the others the heaviest, among equal weights those at lower
+ * places; NaN is heaviest. Heads choose for themselves. The pages read are not written, so sequences may share them (and
+ * keep them); out_table's pages must not be among those that the call reads, nor stand there twice.
+ *   weights  : fp32, weight_strides: HOST, (page, head) in elements, slots dense.
+ *   rows     : HOST, n_rows (0..8) tensors to copy: keys, values, scales, the weights themselves, positions, ...
+ *              16 bytes are copied at a time where base, strides and bytes are multiples of 16 (else 4, 2 or 1).
+ *   num_pages: of all these tensors; page numbers of either table outside [0, num_pages) are reported, not followed.
+ *   keep     : device int32 [S], 0..max_keep, or the sequence keeps nothing and FA_ERR_INDEX is reported.
+ *   out_table: device int32 [S][out_pages], out_stride elements from row to row; max_keep <= out_pages * page_size.
+ *   kept     : device int32 [S][Hkv][max_keep]: the places that stay, -1 behind them.
+ *   kv_len_out: device int32 [S]: new. Since keys keep their rotation, later tokens need their true positions
+ *              (fa_paged_append's `positions`).
+ * The batch's plan gives the lengths. Lengths stay on the device, so the call can be captured. */
+int fa_paged_evict(const float *weights, const long long *weight_strides, const fa_paged_rows *rows, int n_rows, int num_pages,
+                   const fa_paged_batch *batch, const int *keep, int max_keep, int sinks, int recent, const int *out_table,
+                   long long out_stride, int out_pages, int *kept, int *kv_len_out, fa_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status word:
  * FA_OK, FA_ERR_TIMEOUT (a kernel gave up waiting), FA_ERR_INDEX (a length, page number or plan in
  * device memory was out of range) or FA_ERR_LAUNCH (the stream reported

@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_noalloc.cu", "fa_softmax.cu", "fa_naive.cu", "fa_host_step.cu",
-           "fa_rope.cu", "fa_paged.cu", "fa_paged_tiles.cu", "fa_paged_api.cu"]
+           "fa_rope.cu", "fa_paged.cu", "fa_paged_tiles.cu", "fa_paged_api.cu", "fa_append4.cu", "fa_paged4.cu",
+           "fa_paged4_api.cu", "fa_paged_weights.cu", "fa_paged_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
                 "--expt-relaxed-constexpr"]

@@ -13,7 +13,7 @@
 // What has to be read is each key and value that some query sees, once: 4 d bytes per key and kv head.
 #include <math.h>
 
-#include "fa_paged.cuh"
+#include "fa_paged_join.cuh"
 
 namespace fa {
 
@@ -167,16 +167,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
-
-constexpr int kRowWarps = 4, kRowThreads = 32 * kRowWarps;
-constexpr int kGran = kRowBlk / kRowWarps;  // keys that one warp takes at a time: 16, within one page
 
 template <int D, int MT>
 struct RowSmem {
@@ -194,151 +184,6 @@ struct RowSmem {
   static_assert(kBytes <= 231424 / kCtas, "kCtas CTAs must fit an SM");
 };
 
-
-// The tiles of 128 rows that several CTAs of the kernel before shared: their partial results joined in the
-// order of the keys, 16 rows at a time, all of this grid's CTAs together, two such pieces per CTA under way
-// at once. (512 tokens over 32768 keys: about 9 us; joined by the last CTA to finish each tile, on 64 of 152
-// SMs, 18 us.)
-template <int D>
-struct JoinPiece {
-  static constexpr int kAtOnce = 4;  // partial results whose loads go out together
-  TileShare s;
-  int c0, t, r, tok;
-  bool on;
-  float4 v[kAtOnce][D / 32];
-  float mi[kAtOnce], li[kAtOnce], ei[kAtOnce];
-  float M, Ls, Es, acc[D / 8];
-  __device__ __forceinline__ const float* part(const PagedFwd& p, int c) const {
-    return p.tile_part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
-  }
-  __device__ __forceinline__ void load(const PagedFwd& p, int c) {
-    if (!on) return;
-    const int g0 = threadIdx.x >> 4;  // columns 4 * (g0 + 8 i) ..
-#pragma unroll
-    for (int y = 0; y < kAtOnce; ++y) {
-      const float* src = part(p, min(c + y, s.c1));
-      mi[y] = src[D * kTile + r];
-      li[y] = src[(D + 1) * kTile + r];
-      ei[y] = src[(D + 2) * kTile + r];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) v[y][i] = *reinterpret_cast<const float4*>(src + ((g0 + 8 * i) * kTile + r) * 4);
-    }
-  }
-  __device__ __forceinline__ void add(int c) {
-    if (!on) return;
-#pragma unroll
-    for (int y = 0; y < kAtOnce; ++y) {
-      if (c + y > s.c1) continue;
-      if (mi[y] == -INFINITY) {  // nothing seen there, o was not written: l = 0; or every score was NaN, as l is
-        Ls += li[y];
-        continue;
-      }
-      const float mn = fmaxf(M, mi[y]);
-      const float fa = ex2(M - mn), fb = ex2(mi[y] - mn);
-      M = mn;
-      Ls = Ls * fa + fb * li[y];
-      Es = Es * fa + fb * ei[y];
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        acc[4 * i] = acc[4 * i] * fa + fb * v[y][i].x;
-        acc[4 * i + 1] = acc[4 * i + 1] * fa + fb * v[y][i].y;
-        acc[4 * i + 2] = acc[4 * i + 2] * fa + fb * v[y][i].z;
-        acc[4 * i + 3] = acc[4 * i + 3] * fa + fb * v[y][i].w;
-      }
-    }
-  }
-};
-
-template <int D>
-__device__ __forceinline__ void join_pairs(const PagedFwd& p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before is complete
-  const PagedBatch& b = p.b;
-  const int tpt = b.pair_tokens >> 1, used = tpt * b.G;
-  // The shared tiles, listed by every CTA for itself: all descriptors are read at once.
-  extern __shared__ __align__(1024) uint8_t smem[];
-  struct Entry {
-    TileShare s;
-    int x;  // 2 * first CTA + tile
-  };
-  Entry* list = reinterpret_cast<Entry*>(smem);
-  int* counts = reinterpret_cast<int*>(smem + 2 * kPagedSms * sizeof(Entry));  // of each warp
-  constexpr int kEach = (2 * kPagedSms + kRowThreads - 1) / kRowThreads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  TileShare mine[kEach];
-  uint32_t some[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int x = i * kRowThreads + threadIdx.x;
-    mine[i].c1 = -1;
-    if (x < 2 * p.tile_ctas) mine[i] = p.share[x];
-  }
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    some[i] = __ballot_sync(0xffffffffu, mine[i].c1 >= 0);
-    n += __popc(some[i]);
-  }
-  __syncthreads();  // the rows' use of this memory is over
-  if (lane == 0) counts[warp] = n;
-  __syncthreads();
-  int at = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kRowWarps; ++w) {
-    at += w < warp ? counts[w] : 0;
-    total += counts[w];
-  }
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    if (mine[i].c1 >= 0)
-      list[at + __popc(some[i] & ((1u << lane) - 1))] = Entry{mine[i], i * kRowThreads + (int)threadIdx.x};
-    at += __popc(some[i]);
-  }
-  __syncthreads();
-  const int units = total * (kTile / 16);
-  const int g0 = threadIdx.x >> 4;
-  for (int x = blockIdx.x; x < units; x += 2 * gridDim.x) {
-    JoinPiece<D> j[2];
-    int longest = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int u = x + k * gridDim.x;
-      j[k].on = u < units;
-      if (!j[k].on) continue;
-      const Entry& e = list[u >> 3];
-      j[k].s = e.s;
-      j[k].c0 = e.x >> 1;
-      j[k].t = e.x & 1;
-      j[k].r = (u & 7) * 16 + (threadIdx.x & 15);
-      j[k].tok = e.s.tok0 + j[k].r / b.G;
-      j[k].on = j[k].r < used && j[k].tok < e.s.ql;
-      j[k].M = -INFINITY;
-      j[k].Ls = j[k].Es = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) j[k].acc[i] = 0.f;
-      longest = max(longest, e.s.c1 - j[k].c0 + 1);
-    }
-    for (int c = 0; c < longest; c += JoinPiece<D>::kAtOnce) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) j[k].load(p, j[k].c0 + c);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) j[k].add(j[k].c0 + c);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!j[k].on) continue;
-      const float inv = (j[k].Ls > 0.f || j[k].Ls != j[k].Ls) ? 1.f / (j[k].Ls + j[k].Es) : 0.f;
-      const long long out = (long long)(j[k].s.q0 + j[k].tok) * b.Hq + j[k].s.head * b.G + j[k].r % b.G;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint2 w;
-        w.x = pack_bf16(j[k].acc[4 * i] * inv, j[k].acc[4 * i + 1] * inv);
-        w.y = pack_bf16(j[k].acc[4 * i + 2] * inv, j[k].acc[4 * i + 3] * inv);
-        *reinterpret_cast<uint2*>(p.o + out * D + (g0 + 8 * i) * 4) = w;
-      }
-      if (g0 == 0) p.lse[out] = (j[k].M + log2f(j[k].Ls)) * 0.6931471805599453f;
-    }
-  }
-}
 
 // fa_paged_rows_kernel: tiles of 16 MT rows. Four warps per CTA, two or three CTAs per SM; each warp takes every
 // fourth granule of 16 keys with a ring of its own, so no barrier stands in the loop: it waits for its
@@ -656,16 +501,8 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(D, 16 * MT)) fa_paged_ro
     const bool whole = s.first && s.last;
     const int c0 = s.c0, c1 = s.c1, q0 = s.q0, head = s.head;
     float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * row_part(D, kRows);
-    auto put = [&](int row, int col, float4 v, float sum) {  // four columns of a row of o
-      const unsigned rr = r0 + row;
-      const int tok = (int)(rr / G), hd = (int)(rr - tok * G);
-      const long long out = (long long)(q0 + tok) * b.Hq + head * (int)G + hd;
-      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees nothing: o = 0
-      uint2 w;
-      w.x = pack_bf16(v.x * inv, v.y * inv);
-      w.y = pack_bf16(v.z * inv, v.w * inv);
-      *reinterpret_cast<uint2*>(p.o + out * D + col) = w;
-      return out;
+    auto put = [&](int row, int col, float4 v, float sum) {
+      return put_row<D>(p, q0, head, r0 + row, col, v, sum);
     };
     constexpr int kJoin = L::kJoinRows, kPer = kRowThreads / kJoin;  // threads per row, 8 columns each
 #pragma unroll
@@ -753,46 +590,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(D, 16 * MT)) fa_paged_ro
       }
       __syncthreads();
       if (*flag != 0) {
-        // Four columns of a row per thread, eight results' loads at a time.
-        for (int x = threadIdx.x; x < rows * (D / 4); x += kRowThreads) {
-          const int rw = x / (D / 4), col = (x - rw * (D / 4)) * 4;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-          float m0 = -INFINITY, ls = 0.f, lsr = 0.f;
-          constexpr int kAtOnce = 8;
-          for (int c = c0; c <= c1; c += kAtOnce) {
-            float4 v[kAtOnce];
-            float mi[kAtOnce], si[kAtOnce], ri[kAtOnce], mx = m0;
-#pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) {
-              const int cc = min(c + y, c1);
-              const float* src = p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * row_part(D, kRows);
-              v[y] = __ldcg(reinterpret_cast<const float4*>(src + rw * D + col));
-              mi[y] = c + y <= c1 ? __ldcg(src + kRows * D + rw) : -INFINITY;
-              si[y] = __ldcg(src + kRows * (D + 1) + rw);
-              ri[y] = __ldcg(src + kRows * (D + 2) + rw);
-            }
-#pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) mx = fmaxf(mx, mi[y]);
-            const float mu = mx == -INFINITY ? 0.f : mx, f0 = ex2(m0 - mu);
-            m0 = mx;
-            a = make_float4(a.x * f0, a.y * f0, a.z * f0, a.w * f0);
-            ls *= f0;
-            lsr *= f0;
-#pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) {
-              if (c + y > c1) continue;
-              const float f = ex2(mi[y] - mu);
-              a.x = fmaf(f, v[y].x, a.x);
-              a.y = fmaf(f, v[y].y, a.y);
-              a.z = fmaf(f, v[y].z, a.z);
-              a.w = fmaf(f, v[y].w, a.w);
-              ls = fmaf(f, si[y], ls);
-              lsr = fmaf(f, ri[y], lsr);
-            }
-          }
-          const long long out = put(rw, col, a, lsr);
-          if (col == 0) p.lse[out] = (m0 + log2f(ls)) * 0.6931471805599453f;
-        }
+        join_row_tile<D, kRows>(p, c0, c1, q0, head, r0, rows);
       }
     }
     if (k + 1 < fetched) place_q();
@@ -809,7 +607,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(D, 16 * MT)) fa_paged_ro
 // all, against 52.7 with the last CTA joining them alone.
 template <int D>
 __global__ void __launch_bounds__(128) fa_paged_join_rows_kernel(const PagedFwd p) {
-  constexpr int kPieces = D / 32, kMost = row_ctas(D, 16) * kPagedSms, kParts = 16;
+  constexpr int kPieces = D / 32, kMost = kMostRowGrid, kParts = 16;
   __shared__ RowShare share[kMost];
   __shared__ short first[kMost];  // of the tiles that are shared: their first CTA
   __shared__ int count[4];
@@ -818,7 +616,7 @@ __global__ void __launch_bounds__(128) fa_paged_join_rows_kernel(const PagedFwd 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' kernel is complete
   const PagedBatch& b = p.b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows_max = b.row_tile;
-  const int ctas = row_ctas(D, rows_max) * b.sms;
+  const int ctas = p.row_grid;
   constexpr int kEach = (kMost + 127) / 128;
   RowShare mine[kEach];
   uint32_t some[kEach];
@@ -930,14 +728,29 @@ __global__ void __launch_bounds__(128) fa_paged_join_rows_kernel(const PagedFwd 
   }
 }
 
+cudaError_t launch_paged_join_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(8 * num_sms);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return d == 128 ? cudaLaunchKernelEx(&cfg, fa_paged_join_rows_kernel<128>, p)
+                  : cudaLaunchKernelEx(&cfg, fa_paged_join_rows_kernel<64>, p);
+}
+
 template <int D, int MT>
-static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) {
+static cudaError_t launch_rows(PagedFwd& p, int num_sms, cudaStream_t st) {
   constexpr int smem = RowSmem<D, MT>::kBytes;
   static unsigned long long known[kMaxGpus];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_rows_kernel<D, MT>), smem, known);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(RowSmem<D, MT>::kCtas * num_sms);
+  p.row_grid = RowSmem<D, MT>::kCtas * num_sms;
+  cfg.gridDim = dim3(p.row_grid);
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -949,11 +762,7 @@ static cudaError_t launch_rows(const PagedFwd& p, int num_sms, cudaStream_t st) 
   cfg.numAttrs = p.tile_ctas > 0 ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, fa_paged_rows_kernel<D, MT>, p);
   if (e != cudaSuccess || p.row_share == nullptr) return e;
-  cfg.gridDim = dim3(8 * num_sms);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_paged_join_rows_kernel<D>, p);
+  return launch_paged_join_rows(p, D, num_sms, st);
 }
 
 size_t paged_rows_workspace_bytes(int d, int row_tile) {
@@ -961,7 +770,7 @@ size_t paged_rows_workspace_bytes(int d, int row_tile) {
   return plan_up(2 * ctas * row_part(d, row_tile) * 4) + plan_up(ctas * sizeof(RowShare));
 }
 
-cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
+cudaError_t launch_paged_rows(PagedFwd& p, int d, int num_sms, cudaStream_t st) {
   if (d == 128) return p.b.row_tile == 16 ? launch_rows<128, 1>(p, num_sms, st) : launch_rows<128, 2>(p, num_sms, st);
   return p.b.row_tile == 16 ? launch_rows<64, 1>(p, num_sms, st) : launch_rows<64, 2>(p, num_sms, st);
 }

@@ -72,6 +72,7 @@ struct PagedBatch {
   int pair_tokens;  // tokens of a pair of 128-row tiles: 2 * (128 / G)
   int sms;          // SMs in use: one CTA each for the pairs, two or three for the small tiles
   int row_tile;     // rows of the small tiles: 16, or 32 in batches with a sequence of more than 16
+  float row_cost;   // time of a small tile's unit on an SM, counted in a pair's (pair_sms)
   uint32_t* status;
 };
 
@@ -175,10 +176,11 @@ __host__ __device__ __forceinline__ int tile_units(int t0, int t1, const PagedBa
 // pair's at d = 128, and 0.37 of a half block's at d = 64. 4097 new tokens beside 23 single ones over 300 to 9000
 // keys: 347 us, 366 one after the other (with 0.34: 346, 0.40: 351; too low costs more, 0.28 took 377); 4 x 30000
 // keys beside 1024 new tokens over 16000: 255 us, 287 one after the other (0.34: 259, 0.40: 268).
+__host__ __device__ constexpr float row_cost_of(int d) { return d == 64 ? 0.37f : 0.31f; }
 __device__ __forceinline__ int pair_sms(const PagedBatch& b) {
   const long long rows = b.plan.units[0][b.S], pairs = b.plan.units[1][b.S];
   if (rows == 0 || pairs == 0) return pairs == 0 ? 0 : b.sms;
-  const float r = (float)rows * (b.d == 64 ? 0.37f : 0.31f), p = (float)pairs;
+  const float r = (float)rows * b.row_cost, p = (float)pairs;
   const int n = max(1, min(b.sms - 2, (int)(b.sms * p / (p + r)))), m = b.sms - n;  // or one more: what ends sooner
   return m < 2 || fmaxf(p / n, r / m) <= fmaxf(p / (n + 1), r / (m - 1)) ? n : n + 1;
 }
@@ -380,7 +382,8 @@ struct PagedFwd {
   __nv_bfloat16* o;  // [T][Hq][d]
   float* lse;        // [T][Hq]
   float* part;       // partial results of the small tiles: 2 slots per CTA
-  RowShare* row_share;  // [row_ctas * sms], or NULL: no kernel follows, every tile is joined by its last CTA
+  int row_grid;      // CTAs of the small tiles' kernel
+  RowShare* row_share;  // [row_grid], or NULL: no kernel follows, every tile is joined by its last CTA
   float* tile_part;  // and of the pairs, with what each CTA shares with those after it
   TileShare* share;  // [tile_ctas][2 tiles]
   int o_wide;        // o starts at a multiple of 32 bytes
@@ -419,7 +422,10 @@ struct RopeLaunch {
 
 cudaError_t launch_paged_plan(const int* cu_q, const int* kv_len, const PagedBatch& b, int pair_rows, cudaStream_t st);
 size_t paged_rows_workspace_bytes(int d, int row_tile);
-cudaError_t launch_paged_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
+cudaError_t launch_paged_rows(PagedFwd& p, int d, int num_sms, cudaStream_t st);
+// The kernel that joins the small tiles left in PagedFwd::row_share, behind the kernel that leaves them.
+constexpr int kMostRowGrid = 3 * kPagedSms;
+cudaError_t launch_paged_join_rows(const PagedFwd& p, int d, int num_sms, cudaStream_t st);
 
 struct TileMaps {
   CUtensorMap q;     // [T][Hq][d], box 64 dims x G heads x 128 / G tokens

@@ -29,11 +29,12 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include "fa_paged.cuh"
+#include "fa_paged4.cuh"
 
 namespace fa {
 
 constexpr int kTileThreads = 320;
+constexpr int kUnpackThreads = 64;  // more of them over a 4-bit cache
 constexpr uint32_t kTileTmemCols = 512;
 constexpr float kTileRescale = 8.f;
 
@@ -47,6 +48,7 @@ struct TileSeg {
   int head, q0, ql, kvl, t0;
   int turn;  // block j of the order is j0 + (j + turn) mod n_max
   int first, last, c0, c1;
+  int lo, hi, seq;  // keys [lo, hi) that some row sees, and the sequence (for the warps that unpack a 4-bit cache)
 };
 
 template <int D>
@@ -134,6 +136,8 @@ __device__ __forceinline__ TileSeg tile_seg(const Seg& s, const PagedBatch& p) {
   it.last = s.last;
   it.c0 = s.c0;
   it.c1 = s.c1;
+  it.seq = s.seq;
+  key_range(s.t0, s.t1, s.ql, s.kvl, p.causal, p.window, it.lo, it.hi);
   return it;
 }
 
@@ -158,12 +162,13 @@ __device__ __forceinline__ float max64f(const uint32_t (&a)[32], const uint32_t 
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), max3f(m[6], m[7], init));
 }
 
-template <int D, bool kTurn>
-__global__ void __launch_bounds__(kTileThreads, 1)
+template <int D, bool kTurn, bool kPacked>
+__global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTileThreads, 1)
     fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                          const PagedFwd p) {
+                          const PagedFwd p, const PagedCache4 cache) {
   using L = TileSmem<D>;
+  constexpr int kThreads = kPacked ? kTileThreads + kUnpackThreads : kTileThreads;
   constexpr bool kHalves = D == 64;  // see halves() in fa_paged.cuh
   constexpr bool kBoxOut = D == 128;
   constexpr int NK = L::NK, NV = L::NV;
@@ -199,16 +204,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(bar(L::bOFree + t), 128);
     }
     for (int s = 0; s < NK; ++s) {
-      mbar_init(bar(L::bKFull + s), 1);
+      mbar_init(bar(L::bKFull + s), kPacked ? kUnpackThreads : 1);
       mbar_init(bar(L::bKEmpty + s), 1);
     }
     for (int s = 0; s < NV; ++s) {
-      mbar_init(bar(L::bVFull + s), 1);
+      mbar_init(bar(L::bVFull + s), kPacked ? kUnpackThreads : 1);
       mbar_init(bar(L::bVEmpty + s), 1);
     }
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(bar(L::bSegFull + s), 1);
-      mbar_init(bar(L::bSegEmpty + s), 9);  // the MMA warp and the eight softmax warps
+      mbar_init(bar(L::bSegEmpty + s), kPacked ? 11 : 9);  // the MMA warp, the softmax warps, those that unpack
     }
     mbar_init(bar(L::bTwin), 128);
     mbar_init(bar(L::bTwinFree), 128);
@@ -218,12 +223,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    if constexpr (!kPacked) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
     if (kBoxOut && p.warp_out) tma_prefetch_desc(&tm_o);
   }
   // Rows that no load fills are zero, so that their scores are.
-  for (int i = threadIdx.x; i < 2 * (D / 64) * (kTile - used) * 8; i += kTileThreads) {
+  for (int i = threadIdx.x; i < 2 * (D / 64) * (kTile - used) * 8; i += kThreads) {
     const int part = i / ((kTile - used) * 8), at = i - part * ((kTile - used) * 8);
     st_shared_v4(sQ + part * 16384 + used * 128 + at * 16, 0, 0, 0, 0);
   }
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     it = tile_seg<kTurn>(s, b);
     key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, cur.lo, cur.hi);
     cur.tab = b.table + (long long)s.seq * b.table_stride;
-    if (it.n_max > 0) read_entry(it.j0 + it.turn);
+    if (!kPacked && it.n_max > 0) read_entry(it.j0 + it.turn);
   };
   if (warp == 8) look();
   tc_fence_before();
@@ -313,12 +320,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         ++qn[t];
       }
-      if (n_max == 0) {  // no tile sees a key: nothing to load
+      if (n_max == 0 || kPacked) {  // no tile sees a key, or others load them
         look();
         if (ok) ok = hand_out();
         continue;
       }
-      for (int j = 0; ok && j < n_max; ++j) {
+      for (int j = 0; ok && j < (kPacked ? 0 : n_max); ++j) {
         const int slot = (blk * kPairBlk + lane * box) & (b.page_size - 1);
         const int pg = page_at();
         ++blk;
@@ -368,6 +375,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (*abort_flag && lane == 0) {  // every copy in flight lands before shared memory is freed
       for (int t = 0; t < 2; ++t)
         if (qn[t] > 0) drain_wait(bar(L::bQ + t), (qn[t] - 1) & 1);
+      // (Of a 4-bit cache none is: gk = gv = 0.)
       for (uint32_t g = gk > NK ? gk - NK : 0; g < gk; ++g) drain_wait(bar(L::bKFull + g % NK), (g / NK) & 1);
       for (uint32_t g = gv > NV ? gv - NV : 0; g < gv; ++g) drain_wait(bar(L::bVFull + g % NV), (g / NV) & 1);
     }
@@ -476,6 +484,104 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       __syncwarp();
     }
+  } else if (kPacked && warp >= 10) {
+    // ------------------------------------------------------------------ codes to bf16 keys and values
+    // A thread has two rows of a block: it reads their codes a block ahead (and the page entries another one), and
+    // writes the operands as a bulk copy of a bf16 cache would (128-byte swizzled). Rows that no row of the pair sees
+    // are zero.
+    constexpr int kQ = D / 32;  // 16-byte pieces of a row's codes, one scale each
+    const int u = threadIdx.x - kTileThreads;  // rows u and u + 64
+    uint32_t gk = 0, gv = 0;
+    bool ok = true;
+    for (uint32_t i = 0; ok; ++i) {
+      const TileSeg* sp = take(i);
+      if (sp == nullptr) break;
+      const int n_max = sp->n_max, j0 = sp->j0, turn = sp->turn, lo = sp->lo, hi = sp->hi, head = sp->head;
+      const int* tab = b.table + (long long)sp->seq * b.table_stride;
+      give_back(i);
+      if (n_max < 0) break;
+      if (n_max == 0) continue;
+      struct Half {  // two rows of K or V
+        uint4 w[2][kQ];
+        uint32_t s[2][kQ / 2];
+      } kr, vr;
+      int entry[2], page[2];  // of the block after the next, of the next one
+      auto block_at = [&](int j) { return j0 + (j + turn < n_max ? j + turn : j + turn - n_max); };
+      auto read_entries = [&](int j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = block_at(j) * kPairBlk + u + 64 * h;
+          entry[h] = -1;
+          if (j < n_max && key >= lo && key < hi) {
+            entry[h] = tab[key >> b.page_shift];
+            if ((unsigned)entry[h] >= (unsigned)b.num_pages) {
+              record_index_error(b.status);
+              entry[h] = -1;
+            }
+          }
+        }
+      };
+      auto read_rows = [&](Half& x, int j, const uint8_t* codes, const uint8_t* scales, long long c_page, long long c_head,
+                           long long s_page, long long s_head) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int slot = (block_at(j) * kPairBlk + u + 64 * h) & (b.page_size - 1);
+          const bool in = page[h] >= 0;
+          const long long pg = in ? page[h] : 0;
+          const uint4* cp = reinterpret_cast<const uint4*>(codes + pg * c_page + head * c_head + slot * code_bytes(D));
+          const uint32_t* scp =
+              reinterpret_cast<const uint32_t*>(scales + pg * s_page + head * s_head + slot * scale_bytes(D));
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) x.w[h][q] = in ? cp[q] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < kQ / 2; ++q) x.s[h][q] = in ? scp[q] : 0u;
+        }
+      };
+      auto write_rows = [&](const Half& x, uint32_t dst) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = u + 64 * h;
+#pragma unroll
+          for (int q = 0; q < kQ; ++q) {
+            const uint32_t sc = (q & 1) ? x.s[h][q >> 1] >> 16 : x.s[h][q >> 1] & 0xffffu;
+            const uint32_t s2 = sc * 0x10001u, cs = scale_shift(s2);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&x.w[h][q]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {  // 8 dims: one 16-byte chunk
+              const int ch = 4 * q + y;
+              st_shared_v4(dst + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                           fma_bf16x2(code_pair(w[y], 0), s2, cs), fma_bf16x2(code_pair(w[y], 1), s2, cs),
+                           fma_bf16x2(code_pair(w[y], 2), s2, cs), fma_bf16x2(code_pair(w[y], 3), s2, cs));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+      };
+      auto read_k = [&](int j) { read_rows(kr, j, cache.k, cache.k_scale, cache.k_page, cache.k_head, cache.ks_page, cache.ks_head); };
+      auto read_v = [&](int j) { read_rows(vr, j, cache.v, cache.v_scale, cache.v_page, cache.v_head, cache.vs_page, cache.vs_head); };
+      read_entries(0);
+      page[0] = entry[0];
+      page[1] = entry[1];
+      read_k(0);
+      read_v(0);
+      read_entries(1);
+      for (int j = 0; j < n_max; ++j) {
+        const uint32_t sk = gk % NK, sv = gv % NV;
+        if (!(ok = mbar_wait_warp(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
+        write_rows(kr, sK + sk * L::kTileBytes);
+        mbar_arrive(bar(L::bKFull + sk));
+        ++gk;
+        page[0] = entry[0];
+        page[1] = entry[1];
+        if (j + 1 < n_max) read_k(j + 1);
+        if (!(ok = mbar_wait_warp(bar(L::bVEmpty + sv), ((gv / NV) & 1) ^ 1, ctl))) break;
+        write_rows(vr, sV + sv * L::kTileBytes);
+        mbar_arrive(bar(L::bVFull + sv));
+        ++gv;
+        if (j + 1 < n_max) read_v(j + 1);
+        read_entries(j + 2);
+      }
+    }
   } else {
     // ------------------------------------------------------------------ softmax
     const int t = warp >> 2;
@@ -527,6 +633,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto pair_lo = [&]() { return first_key(kvl - s.ql + s.t0, b.window); };
       const int vlo = kHalves ? pair_lo() : 0;
       auto clear_unseen = [&](int j, int kv0) -> bool {
+        if (kPacked) return true;  // (the warps that unpack have done it)
         const int past = kvl - kv0, before = min((kHalves ? vlo : pair_lo()) - kv0, kPairBlk);
         if (past >= kPairBlk && before <= 0) return true;
         const uint32_t g = gv0 + a_t + j * step, sv = g % NV;
@@ -762,14 +869,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
-template <int D, bool kTurn>
-static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, int num_sms, cudaStream_t st) {
+template <int D, bool kTurn, bool kPacked>
+static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, const PagedCache4& cache, int num_sms,
+                                cudaStream_t st) {
   constexpr int smem = TileSmem<D>::kAlloc;
   static_assert(smem <= 232448, "shared memory exceeds the 227 KB per-CTA limit");
   static unsigned long long known[kMaxGpus];
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_tiles_kernel<D, kTurn>), smem, known);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_tiles_kernel<D, kTurn, kPacked>), smem, known);
   if (e != cudaSuccess) return e;
-  fa_paged_tiles_kernel<D, kTurn><<<num_sms, kTileThreads, smem, st>>>(m.q, m.k, m.v, m.o, p);
+  fa_paged_tiles_kernel<D, kTurn, kPacked>
+      <<<num_sms, kPacked ? kTileThreads + kUnpackThreads : kTileThreads, smem, st>>>(m.q, m.k, m.v, m.o, p, cache);
   return cudaGetLastError();
 }
 
@@ -783,8 +892,19 @@ size_t paged_tiles_workspace_bytes(int d) {
 // block per step is not: 16 x 1743 tokens take 232 us without it, 242 with.
 cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int num_sms, cudaStream_t st) {
   const bool turn = (long long)p.b.max_pages * p.b.page_size * p.b.Hkv * d * 4 > (64LL << 20);
-  if (d == 128) return turn ? launch_tiles<128, true>(m, p, num_sms, st) : launch_tiles<128, false>(m, p, num_sms, st);
-  return turn ? launch_tiles<64, true>(m, p, num_sms, st) : launch_tiles<64, false>(m, p, num_sms, st);
+  const PagedCache4 none = {};
+  if (d == 128)
+    return turn ? launch_tiles<128, true, false>(m, p, none, num_sms, st)
+                : launch_tiles<128, false, false>(m, p, none, num_sms, st);
+  return turn ? launch_tiles<64, true, false>(m, p, none, num_sms, st)
+              : launch_tiles<64, false, false>(m, p, none, num_sms, st);
+}
+
+// Over a 4-bit cache (m.k and m.v are not read) the keys of fewer than a quarter of the bytes stay in L2.
+cudaError_t launch_paged4_tiles(const TileMaps& m, const PagedFwd& p, const PagedCache4& cache, int d, int num_sms,
+                                cudaStream_t st) {
+  return d == 128 ? launch_tiles<128, false, true>(m, p, cache, num_sms, st)
+                  : launch_tiles<64, false, true>(m, p, cache, num_sms, st);
 }
 
 }  // namespace fa

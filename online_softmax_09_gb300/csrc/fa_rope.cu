@@ -15,95 +15,12 @@
 // chunks in, two out); the cos and sin of a CTA's tokens are made once, in shared memory, for all heads.
 // q and k of 4 x 4096 tokens (40 heads, d = 128) and their gradients back, 671 MB, take 109 us: 6.16 TB/s,
 // 92 % of the measured copy rate; 8500 prompt tokens into the cache 34.5 us, 5.9 TB/s; one token 3.8 us.
-#include "fa_paged.cuh"
+#include "fa_rope.cuh"
 
 namespace fa {
 
 constexpr int kRopeThreads = 256;  // most threads per CTA
 constexpr int kRopeTokens = 2;     // most tokens per CTA
-
-template <int D>
-__device__ __forceinline__ void turn8(uint4& va, uint4& vb, const float4* t, bool interleaved) {
-  constexpr int kStep = D / 16;  // t[kStep * i]: cos, sin of this thread's pairs 2i, 2i + 1
-  uint32_t* a = reinterpret_cast<uint32_t*>(&va);
-  uint32_t* c = reinterpret_cast<uint32_t*>(&vb);
-  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
-  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
-  if (!interleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = t[kStep * i];
-      const float x0 = lo(a[i]), x1 = hi(a[i]), y0 = lo(c[i]), y1 = hi(c[i]);
-      a[i] = pack_bf16(x0 * f.x - y0 * f.y, x1 * f.z - y1 * f.w);
-      c[i] = pack_bf16(y0 * f.x + x0 * f.y, y1 * f.z + x1 * f.w);
-    }
-  } else {  // words a[0..3], c[0..3] hold pairs 8j .. 8j + 7
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = t[kStep * i];
-      uint32_t& w0 = i < 2 ? a[2 * i] : c[2 * i - 4];
-      uint32_t& w1 = i < 2 ? a[2 * i + 1] : c[2 * i - 3];
-      const float x0 = lo(w0), y0 = hi(w0), x1 = lo(w1), y1 = hi(w1);
-      w0 = pack_bf16(x0 * f.x - y0 * f.y, y0 * f.x + x0 * f.y);
-      w1 = pack_bf16(x1 * f.z - y1 * f.w, y1 * f.z + x1 * f.w);
-    }
-  }
-}
-
-struct RopeToken {
-  long long in[3];   // element offset of the token in q, k, v
-  long long out[3];  // and in their outputs; v and k of a paged batch: in the cache
-  int pos;           // paged batch without given positions
-  int state;         // bit 0: a token of the batch, bit 1: its cache slot exists
-};
-
-// Token t of the grid's dense batch, or of the plan's ragged one.
-template <bool kPaged>
-__device__ __forceinline__ RopeToken rope_token(const RopeLaunch& p, long long t) {
-  RopeToken k = {};
-  if (t >= p.tokens) return k;
-  if constexpr (!kPaged) {
-    const long long bi = t / p.N, n = t - bi * p.N;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      k.in[i] = bi * p.in[i].batch + n * p.in[i].tok;
-      k.out[i] = bi * p.out[i].batch + n * p.out[i].tok;
-    }
-    k.state = 3;
-  } else {
-    const PagedBatch& b = p.b;
-    // The last sequence that starts at or before the token; sequences without tokens share a start.
-    int lo = 0, hi = b.S;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (b.plan.seq[mid].q0 <= t) lo = mid;
-      else hi = mid;
-    }
-    const PlanSeq s = b.plan.seq[lo];
-    const long long j = t - s.q0;
-    if (j < 0 || j >= s.ql) return k;
-    k.state = 1;
-    k.pos = s.kvl - s.ql + (int)j;
-    k.in[0] = t * p.in[0].tok;
-    k.out[0] = t * p.out[0].tok;
-    k.in[1] = t * p.in[1].tok;
-    k.in[2] = t * p.in[2].tok;
-    if (k.pos >= 0) {
-      const int page = b.table[(long long)lo * b.table_stride + (k.pos >> b.page_shift)];
-      if ((unsigned)page < (unsigned)b.num_pages) {
-        const int slot = k.pos & (b.page_size - 1);
-        k.out[1] = page * p.out[1].batch + slot * p.out[1].tok;
-        k.out[2] = page * p.out[2].batch + slot * p.out[2].tok;
-        k.state = 3;
-      } else {
-        record_index_error(b.status);
-      }
-    } else {
-      record_index_error(b.status);  // more new tokens than the sequence has
-    }
-  }
-  return k;
-}
 
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeLaunch p) {
@@ -157,8 +74,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeLaunch 
     const int per = blockDim.x / np;  // tokens at a time
     const int i = tid % np, first = tid / np;
     if (first < per && first < p.tile) {
-      const double turns = (double)p.inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
-      const uint64_t w = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+      const uint64_t w = turn_fraction(p, i);
       const int axis = (int)(p.axes[i >> 5] >> ((i & 31) * 2)) & 3;
       for (int k = first; k < p.tile; k += per) {
         long long pos = 0;
@@ -170,10 +86,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeLaunch 
             pos = p.positions[axis * p.pos_axis + bi * p.pos_batch + (t0 + k - bi * p.N)];
           }
         }
-        const int phase = (int)(uint32_t)(((uint64_t)pos * w) >> 32);  // 2^-32 turns, signed
-        float s, c;
-        sincospif((float)phase * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-        cs[k][(i >> 1) & 3][i >> 3][i & 1] = make_float2(c, p.inverse ? -s : s);
+        cs[k][(i >> 1) & 3][i >> 3][i & 1] = turn_angle(p, w, pos);
       }
     }
   }

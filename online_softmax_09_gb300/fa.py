@@ -41,8 +41,18 @@ class _Cache(ctypes.Structure):  # fa_paged_cache
         ("num_pages", _i)]
 
 
+class _Cache4(ctypes.Structure):  # fa_paged_cache4
+    _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (f"{x}_stride{i}", ctypes.c_longlong) for x in ("k", "v", "k_scale", "v_scale") for i in range(2)] + [
+        ("num_pages", _i)]
+
+
+class _Rows(ctypes.Structure):  # fa_paged_rows
+    _fields_ = [("base", _vp)] + [(f"stride{i}", ctypes.c_longlong) for i in range(3)] + [("bytes", _i)]
+
+
 # Arguments that change with each call are packed into bytes, in a third of the time that ctypes takes for an array.
-_ll2, _ll8, _ll12 = (struct.Struct(f"{n}q").pack for n in (2, 8, 12))
+_ll2, _ll4, _ll8, _ll12 = (struct.Struct(f"{n}q").pack for n in (2, 4, 8, 12))
 _pack_cache = struct.Struct("PP6qi4x").pack  # _Cache
 
 
@@ -112,6 +122,17 @@ def lib() -> ctypes.CDLL:
         L.fa_fwd_paged_workspace_bytes.restype = ctypes.c_size_t
         L.fa_fwd_paged.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, ctypes.c_size_t, _vp]
         L.fa_fwd_paged.restype = _i
+        L.fa_paged_append4.argtypes = [_vp] * 11 + [ll, _vp]
+        L.fa_paged_append4.restype = _i
+        L.fa_fwd_paged4_workspace_bytes.argtypes = [_vp]
+        L.fa_fwd_paged4_workspace_bytes.restype = ctypes.c_size_t
+        L.fa_fwd_paged4.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, ctypes.c_size_t, _vp]
+        L.fa_fwd_paged4.restype = _i
+        for fn in (L.fa_paged_weights, L.fa_paged_weights4):
+            fn.argtypes = [_vp] * 8 + [_f, _vp]
+            fn.restype = _i
+        L.fa_paged_evict.argtypes = [_vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, ll, _i, _vp, _vp, _vp]
+        L.fa_paged_evict.restype = _i
         L.fa_check.argtypes = [_vp]
         L.fa_check.restype = _i
         L.fa_strerror.argtypes = [_i]
@@ -521,7 +542,8 @@ class PagedPlan:
         self._c = _Batch(None, 0, self.buffer.data_ptr(), self.buffer.numel(), S, T, max_q, max_pages, page_size, Hq,
                          Hkv, d, causal, window)
         self._ref = ctypes.addressof(self._c)
-        self.ws_bytes = int(L.fa_fwd_paged_workspace_bytes(self._ref))
+        self.ws_bytes = max(int(L.fa_fwd_paged_workspace_bytes(self._ref)),
+                            int(L.fa_fwd_paged4_workspace_bytes(self._ref)))  # for either kind of cache
         self.workspace = _empty(max(self.ws_bytes, 16), torch.uint8, device, stream)
 
     def _use(self, stream, index):
@@ -648,6 +670,197 @@ def forward_paged(q, k_cache, v_cache, plan, scale: float | None = None, out=Non
     if r != FA_OK:
         raise FAError(r, "fa_fwd_paged")
     return out, lse
+
+
+class PagedCache4:
+    """A paged cache in 4 bits (fa_paged_cache4, which has its layout): codes ``k``, ``v`` uint8 CUDA
+    [pages, Hkv, page_size, d / 2] and scales ``k_scale``, ``v_scale`` bf16 CUDA [pages, Hkv, page_size, d / 32], the slots of
+    a page and head dense. ``PagedCache4.empty`` allocates one."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        shape, i = tuple(k.shape), k.get_device()
+        if len(shape) != 4:
+            raise ValueError("codes must be [pages, Hkv, page_size, d / 2]")
+        pages, Hkv, page, half = shape
+        for name, t, dt, width in (("k", k, torch.uint8, half), ("v", v, torch.uint8, half),
+                                   ("k_scale", k_scale, torch.bfloat16, half // 16),
+                                   ("v_scale", v_scale, torch.bfloat16, half // 16)):
+            if not t.is_cuda or t.get_device() != i or t.dtype != dt or tuple(t.shape) != (pages, Hkv, page, width) \
+                    or t.stride(3) != 1 or t.stride(2) != width:
+                raise ValueError(f"{name} must be a CUDA tensor {[pages, Hkv, page, width]} of {dt} with dense slots, on the "
+                                 "device of the others")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_shape, self.num_pages, self.index = (Hkv, page, 2 * half), pages, i
+        st = [n * t.element_size() for t in (k, v, k_scale, v_scale) for n in t.stride()[:2]]
+        self._c = _Cache4(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *st, pages)
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, num_pages: int, Hkv: int, page_size: int, d: int, device="cuda"):
+        """A new cache; its contents are undefined."""
+        code = [torch.empty(num_pages, Hkv, page_size, d // 2, dtype=torch.uint8, device=device) for _ in "kv"]
+        scale = [torch.empty(num_pages, Hkv, page_size, d // 32, dtype=torch.bfloat16, device=device) for _ in "kv"]
+        return cls(*code, *scale)
+
+    def _for(self, plan):
+        if self.page_shape != plan.page_shape or self.index != plan.index:
+            raise ValueError(f"the cache holds pages {list(self.page_shape)} (Hkv, page_size, d) on cuda:{self.index}, the plan "
+                             f"is for {list(plan.page_shape)} on cuda:{plan.index}")
+        return self._ref
+
+
+def paged_append4(q, k, v, cache, plan, rotary=None, positions=None, q_out=None, k_out=None, v_out=None, stream=None):
+    """paged_append into a PagedCache4 (fa_paged_append4). ``k_out``, ``v_out`` bf16 CUDA [T,Hkv,d], if given, receive the values
+    that the cache now stands for; they may be k and v."""
+    i = plan.index
+    if i != torch._C._cuda_getDevice():
+        _dev_index(k)
+    ref = cache._for(plan)
+    qp = qop = None
+    st = (0, 0, 0, 0)
+    if q is not None:
+        if rotary is None:
+            raise ValueError("q is only rotated: it needs a rotary")
+        shape = plan.q_shape
+        st = _strides_of("q", q, shape, i)[:2]
+        if q_out is None:
+            q_out = _empty(shape, torch.bfloat16, q.device, stream)
+            st += (shape[1] * shape[2], shape[2])
+        else:
+            st += _strides_of("q_out", q_out, shape, i)[:2]
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    shape = plan.kv_shape
+    T = shape[0]
+    st += _strides_of("k", k, shape, i)[:2] + _strides_of("v", v, shape, i)[:2]
+    out = [None, None]
+    for j, (name, t) in enumerate((("k_out", k_out), ("v_out", v_out))):
+        if t is None:
+            st += (0, 0)
+        else:
+            st += _strides_of(name, t, shape, i)[:2]
+            out[j] = t.data_ptr()
+    pp = None
+    if positions is not None:
+        A = rotary.naxes if rotary is not None else 0
+        if positions.dtype != torch.int32 or positions.get_device() != i or not positions.is_contiguous() \
+                or positions.shape not in (((T,), (1, T)) if A == 1 else ((A, T),)):
+            raise ValueError("positions must be a contiguous int32 CUDA tensor [T], or [A, T] for several axes")
+        pp = positions.data_ptr()
+    if rotary is not None and rotary.index != i:
+        raise ValueError("rotary is on another device")
+    r = (_lib or lib()).fa_paged_append4(qp, qop, k.data_ptr(), v.data_ptr(), out[0], out[1], _ll12(*st), ref, plan._ref,
+                                         rotary._ref if rotary is not None else None, pp, T, plan._use(stream, i))
+    if r != FA_OK:
+        raise FAError(r, "fa_paged_append4")
+    return q_out
+
+
+def forward_paged4(q, cache, plan, scale: float | None = None, out=None, lse=None, stream=None):
+    """forward_paged over a PagedCache4 (fa_fwd_paged4): O [T,Hq,d], LSE [T,Hq]. Arguments and what is left unwritten as there."""
+    shape, i = plan.q_shape, plan.index
+    st = _strides_of("q", q, shape, i)
+    if i != torch._C._cuda_getDevice():
+        _dev_index(q)
+    ref = cache._for(plan)
+    if out is not None and not (_strides_of("out", out, shape, i) and out.is_contiguous()):
+        raise ValueError("out must be contiguous")
+    if lse is not None and (lse.dtype != torch.float32 or lse.get_device() != i or lse.shape != plan.lse_shape
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
+    raw = plan._use(stream, i)
+    if out is None:
+        out = _empty(shape, torch.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _empty(plan.lse_shape, torch.float32, q.device, stream)
+    r = (_lib or lib()).fa_fwd_paged4(q.data_ptr(), _ll2(st[0], st[1]), ref, plan._ref, out.data_ptr(), lse.data_ptr(),
+                                      0.0 if scale is None else float(scale), plan.workspace.data_ptr(), plan.ws_bytes, raw)
+    if r != FA_OK:
+        raise FAError(r, "fa_fwd_paged4")
+    return out, lse
+
+
+def _check_weights(name, t, plan, pages):
+    if t.dtype != torch.float32 or t.get_device() != plan.index or tuple(t.shape) != (pages,) + plan.page_shape[:2] \
+            or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a float32 CUDA tensor {[pages, *plan.page_shape[:2]]} with dense slots, on the plan's "
+                         "device")
+    return t.stride()[:2]
+
+
+def paged_weights(q, lse, keys, weights, plan, scale: float | None = None, out=None, stream=None):
+    """Add the attention weight that cached tokens receive from a step's new tokens (fa_paged_weights, fa_paged_weights4).
+    q and scale as given to forward_paged (or forward_paged4) and lse [T,Hq] as it returned it; keys: the bf16 k_cache or
+    the PagedCache4; weights fp32 CUDA [pages, Hkv, page_size]. Returns ``out``: by default weights itself, added to in
+    place; else a tensor like it, of which only the slots that some new token sees are written. The step's own tokens start from
+    0, so call it once per step."""
+    i = plan.index
+    if i != torch._C._cuda_getDevice():
+        _dev_index(q)
+    qs = _strides_of("q", q, plan.q_shape, i)
+    if lse.dtype != torch.float32 or lse.get_device() != i or lse.shape != plan.lse_shape or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [T, Hq]")
+    if isinstance(keys, PagedCache4):
+        cache, pages, fn, name = keys._for(plan), keys.num_pages, (_lib or lib()).fa_paged_weights4, "fa_paged_weights4"
+    else:
+        cache, pages, fn, name = plan._cache(keys, keys), keys.shape[0], (_lib or lib()).fa_paged_weights, "fa_paged_weights"
+    if out is None:
+        out = weights
+    ws = _check_weights("weights", weights, plan, pages) + _check_weights("out", out, plan, pages)
+    r = fn(q.data_ptr(), _ll2(qs[0], qs[1]), lse.data_ptr(), cache, plan._ref, weights.data_ptr(), out.data_ptr(), _ll4(*ws),
+           0.0 if scale is None else float(scale), plan._use(stream, i))
+    if r != FA_OK:
+        raise FAError(r, name)
+    return out
+
+
+def paged_evict(weights, caches, plan, keep, out_table, max_keep: int, sinks: int = 4, recent: int = 64, kept=None,
+                kv_lens=None, stream=None):
+    """Cut every sequence of the plan down to its keep heaviest tokens per kv head, copied in order into the pages of
+    ``out_table`` (fa_paged_evict). weights fp32 CUDA [pages, Hkv, page_size] (moved along); caches: a PagedCache4, or the
+    tensors to move, CUDA [pages, Hkv, page_size, ...] with dense slots, e.g. (k_cache, v_cache); keep int32 CUDA [S], at most
+    max_keep; out_table int32 CUDA [S, out_pages] of pages that the plan's table does not name. The first ``sinks`` and the last
+    ``recent`` tokens stay whatever their weight. Returns kept int32 [S,Hkv,max_keep] (the places that stay, then -1) and
+    kv_lens int32 [S]. Later tokens need their true positions (paged_append's ``positions``)."""
+    i, S = plan.index, plan.key[0]
+    if i != torch._C._cuda_getDevice():
+        _dev_index(weights)
+    pages = weights.shape[0]
+    ws = _check_weights("weights", weights, plan, pages)
+    if isinstance(caches, PagedCache4):
+        caches._for(plan)
+        caches = (caches.k, caches.v, caches.k_scale, caches.v_scale)
+    rows = (_Rows * (len(caches) + 1))()
+    for row, t in zip(rows, (*caches, weights)):
+        if t.get_device() != i or t.dim() < 3 or tuple(t.shape[:3]) != (pages,) + plan.page_shape[:2] \
+                or (t.numel() > 0 and not t[0, 0, 0].is_contiguous()):
+            raise ValueError(f"what is moved must be CUDA tensors {[pages, *plan.page_shape[:2]]} [, ...] with dense slots, on the "
+                             "plan's device")
+        e = t.element_size()
+        row.base, row.bytes = t.data_ptr(), e * math.prod(t.shape[3:])
+        row.stride0, row.stride1, row.stride2 = (n * e for n in t.stride()[:3])
+    for name, t, shape in (("keep", keep, (S,)), ("out_table", out_table, (S, *out_table.shape[1:2]))):
+        if t.dtype != torch.int32 or t.get_device() != i or tuple(t.shape) != shape or (S > 0 and t.stride(-1) != 1):
+            raise ValueError(f"{name} must be an int32 CUDA tensor {list(shape)} with contiguous last dim, on the plan's device")
+    max_keep, sinks, recent = int(max_keep), int(sinks), int(recent)
+    if any(not 0 <= n < 2 ** 31 for n in (max_keep, sinks, recent)):
+        raise ValueError("max_keep, sinks and recent must be at least 0 and fit 32 bits")
+    raw = plan._use(stream, i)
+    shape = (S, plan.page_shape[0], max_keep)
+    if kept is None:
+        kept = _empty(shape, torch.int32, weights.device, stream)
+    if kv_lens is None:
+        kv_lens = _empty((S,), torch.int32, weights.device, stream)
+    for name, t, want in (("kept", kept, shape), ("kv_lens", kv_lens, (S,))):
+        if t.dtype != torch.int32 or t.get_device() != i or tuple(t.shape) != want or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(want)}")
+    r = (_lib or lib()).fa_paged_evict(weights.data_ptr(), _ll2(*ws), rows, len(rows), pages, plan._ref, keep.data_ptr(), max_keep,
+                                       sinks, recent, out_table.data_ptr(), out_table.stride(0), out_table.shape[1],
+                                       kept.data_ptr(), kv_lens.data_ptr(), raw)
+    if r != FA_OK:
+        raise FAError(r, "fa_paged_evict")
+    return kept, kv_lens
 
 
 def check(stream=None, device=None) -> None:
