@@ -389,7 +389,7 @@ int fa_fwd_paged(const void *q, const long long *q_strides, const fa_paged_cache
 typedef struct {
   void *k, *v;              /* device, 16-byte aligned: codes */
   void *k_scale, *v_scale;  /* device, 16-byte aligned: scales */
-  long long k_strides[2], v_strides[2];              /* (page, head) in BYTES, multiples of 16 */
+  long long k_strides[2], v_strides[2];              /* (page, head) in BYTES, multiples of 16; the page's below 2^32 */
   long long k_scale_strides[2], v_scale_strides[2];
   int num_pages;            /* page numbers outside [0, num_pages) are reported, not followed */
 } fa_paged_cache4;

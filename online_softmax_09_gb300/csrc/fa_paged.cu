@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kRowThreads, row_ctas(D, 16 * MT)) fa_paged_ro
     }
     if (k + 1 < fetched) place_q();
   }
-  if (p.tile_ctas > 0) join_pairs<D>(p);
+  if (p.tile_ctas > 0) join_pairs<D>(p, [] { __syncthreads(); });
 }
 
 // fa_paged_join_rows_kernel: the small tiles that the rows' kernel left, spread over the GPU. A CTA takes 32

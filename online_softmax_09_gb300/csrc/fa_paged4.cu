@@ -19,22 +19,25 @@ namespace fa {
 template <int D, int NT>
 struct Row4Smem {
   static constexpr int kRows = NT <= 2 ? 16 : 32;
-  static constexpr int kCtas = row4_ctas(kRows);
+  static constexpr int kWarps = row4_warps(NT), kThreads = 32 * (kWarps + 1);  // those that compute, and one that copies
+  static constexpr int kCtas = row4_ctas(NT);
   static constexpr int kCodes = kGran * code_bytes(D), kScales = kGran * scale_bytes(D);
-  static constexpr int kStage = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales of a granule
-  static constexpr int kStages = D == 128 ? 6 : 8;
-  static constexpr int kSlots = 16;                // stretches queued: kStages + 1 at least
+  static constexpr int kPart = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales of a granule
+  static constexpr int kStage = 2 * kPart;              // two granules: what a warp takes at a time
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kSlots = kStages + 3;  // stretches handed out
   static constexpr int kWarp = kStages * kStage;
-  static constexpr int kMerge = kRowWarps * kWarp;               // 8 rows of o of each warp
-  static constexpr int kStat = kMerge + kRowWarps * 8 * D * 4;   // their m, l, rounded l
-  static constexpr int kQ = kStat + kRowWarps * 3 * 8 * 4;       // queries of 32 rows
+  static constexpr int kMerge = kWarps * kWarp;               // 4 rows of o of each warp
+  static constexpr int kStat = kMerge + kWarps * 4 * D * 4;   // their m, l, rounded l
+  static constexpr int kQ = kStat + kWarps * 3 * 4 * 4;       // queries of 32 rows
   static constexpr int kQueue = kQ + (NT > 2 ? kRows * D * 2 : 0);
   static constexpr int kBar = kQueue + kSlots * (int)sizeof(Seg);
-  static constexpr int kSkip = kBar + kRowWarps * kStages * 8;   // granules that hold nothing to see
-  static constexpr int kFlag = kSkip + kRowWarps * kStages * 4;
-  static constexpr int kAbort = kFlag + 4;
+  static constexpr int bSegFull = 0, bSegEmpty = bSegFull + kSlots;
+  static constexpr int kNumBars = bSegEmpty + kSlots;
+  static constexpr int kFlag = kBar + kNumBars * 8;
+  static constexpr int kAbort = kFlag + 8;
   static constexpr int kBytes = (kAbort + 4 + 15) / 16 * 16;
-  static_assert(kSlots > kStages && kBar % 8 == 0 && kQueue % 16 == 0, "layout");
+  static_assert(kBar % 8 == 0 && kQueue % 16 == 0, "layout");
   static_assert(kBytes <= 231424 / kCtas, "kCtas CTAs must fit an SM");
 };
 
@@ -63,11 +66,20 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   return x;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kRowThreads, Row4Smem<D, NT>::kCtas)
+__global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kCtas)
     fa_paged4_rows_kernel(const PagedFwd p, const PagedCache4 cache) {
   using L = Row4Smem<D, NT>;
-  constexpr int kRows = L::kRows;
+  constexpr int kRows = L::kRows, kWarps = L::kWarps, kStages = L::kStages;
   constexpr int kSteps = D / 16;       // MMA steps over the dims of a score
   constexpr int kMT = D / 16;          // 16-dim tiles of o
   constexpr int kKW = D / 32;          // words of a key that a lane takes
@@ -76,17 +88,11 @@ __global__ void __launch_bounds__(kRowThreads, Row4Smem<D, NT>::kCtas)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const uint32_t ring = sbase + warp * L::kWarp;
-  float* merge = reinterpret_cast<float*>(smem + L::kMerge);
-  float* stat = reinterpret_cast<float*>(smem + L::kStat);
   Seg* queue = reinterpret_cast<Seg*>(smem + L::kQueue);
-  volatile int* skip = reinterpret_cast<volatile int*>(smem + L::kSkip) + warp * L::kStages;
-  int* flag = reinterpret_cast<int*>(smem + L::kFlag);
+  volatile int* flag = reinterpret_cast<volatile int*>(smem + L::kFlag);
   const PagedBatch& b = p.b;
   const Ctl ctl{reinterpret_cast<volatile int*>(smem + L::kAbort), b.status};
-  auto bar = [&](uint32_t stage) -> uint32_t { return sbase + L::kBar + (warp * L::kStages + stage) * 8; };
-  SegIter<false, kRows> it(b, p.tile_ctas > 0 ? max(1, L::kCtas * (b.sms - pair_sms(b))) : gridDim.x);
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
     if (p.tile_ctas > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -97,77 +103,49 @@ __global__ void __launch_bounds__(kRowThreads, Row4Smem<D, NT>::kCtas)
     if (threadIdx.x == 0) p.row_share[blockIdx.x].c1 = -1;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
-  if (threadIdx.x == 0) *ctl.abort = 0;
-  if (lane == 0) {
-    for (int i = 0; i < L::kStages; ++i) mbar_init(bar(i), 1);
-    fence_mbar_init();
+  if (threadIdx.x < L::kSlots) {
+    mbar_init(bar(L::bSegFull + threadIdx.x), 1);
+    mbar_init(bar(L::bSegEmpty + threadIdx.x), kWarps);
   }
+  if (threadIdx.x == 0) *ctl.abort = 0;
+  fence_mbar_init();
   __syncthreads();
   const unsigned G = b.G;
 
-  // The copying side, as in fa_paged_rows_kernel: stretches from the walk into the queue, granules into the ring. A
-  // granule that no row of the tile sees, or whose page does not exist, takes a stage without a copy.
-  uint32_t fetched = 0, copied = 0;
-  int ln = 0, li = 0, lkey = 0, llo = 0, lhi = 0, lhead = 0;
-  const int* ltab = nullptr;
-  int pages = -1;
-  auto read_pages = [&]() {
-    const int key = lkey + (li + lane) * kRowBlk;
-    const bool in = li + lane < ln && key < lhi && key + kGran > llo;
-    pages = in ? ltab[key >> b.page_shift] : -1;
-    if (in && (unsigned)pages >= (unsigned)b.num_pages) {
-      record_index_error(b.status);
-      pages = -1;
-    }
-  };
-  auto fetch = [&]() {
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- walk
+    // One warp finds the CTA's stretches and hands them out, a few ahead of those that are worked on.
+    SegIter<false, kRows> it(b, p.tile_ctas > 0 ? max(1, L::kCtas * (b.sms - pair_sms(b))) : gridDim.x);
     Seg s;
-    ln = li = 0;
-    if (!it.next(s)) return;
-    if (lane == 0) queue[fetched % L::kSlots] = s;
-    __syncwarp();
-    ++fetched;
-    ln = s.n;
-    lhead = s.head;
-    lkey = s.blk * kRowBlk + warp * kGran;
-    key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, llo, lhi);
-    ltab = b.table + (long long)s.seq * b.table_stride;
-    read_pages();
-  };
-  auto issue = [&]() {
-    if (li < ln) {
-      const int page = __shfl_sync(0xffffffffu, pages, li & 31);
-      const uint32_t stage = copied % L::kStages;
+    for (uint32_t i = 0;; ++i) {
+      const bool some = it.next(s);
+      const uint32_t at = i % L::kSlots;
+      if (!mbar_wait_warp(bar(L::bSegEmpty + at), ((i / L::kSlots) & 1) ^ 1, ctl)) return;
       if (lane == 0) {
-        skip[stage] = page < 0;
-        if (page < 0) {
-          mbar_arrive(bar(stage));
-        } else {
-          const int slot = (lkey + li * kRowBlk) & (b.page_size - 1);
-          const uint32_t st = ring + stage * L::kStage;
-          mbar_expect_tx(bar(stage), L::kStage);
-          bulk_load(st, cache.k + page * cache.k_page + lhead * cache.k_head + slot * code_bytes(D), L::kCodes, bar(stage));
-          bulk_load(st + 2 * L::kCodes, cache.k_scale + page * cache.ks_page + lhead * cache.ks_head + slot * scale_bytes(D),
-                    L::kScales, bar(stage));
-          bulk_load(st + L::kCodes, cache.v + page * cache.v_page + lhead * cache.v_head + slot * code_bytes(D), L::kCodes,
-                    bar(stage));
-          bulk_load(st + 2 * L::kCodes + L::kScales,
-                    cache.v_scale + page * cache.vs_page + lhead * cache.vs_head + slot * scale_bytes(D), L::kScales,
-                    bar(stage));
-        }
+        queue[at] = s;
+        if (!some) queue[at].n = -1;
+        mbar_arrive(bar(L::bSegFull + at));
       }
-      __syncwarp();
-      ++copied;
-      if (++li == ln) fetch();
-      else if ((li & 31) == 0) read_pages();
+      if (!some) return;
     }
+  }
+
+  // ------------------------------------------------------------------ products and softmax
+  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); };
+  const int g = lane >> 2, c = lane & 3;
+  float* merge = reinterpret_cast<float*>(smem + L::kMerge);
+  float* stat = reinterpret_cast<float*>(smem + L::kStat);
+  const uint32_t magic = 0x43004300u, nibble = 0x000f000fu;
+  // Codes 2 j and 2 j + 1 of a word as values: the masks stand in registers, so that they take one instruction.
+  auto value_pair = [&](uint32_t w, int j, uint32_t s2, uint32_t cs) {
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w >> (4 * j)), "r"(nibble), "r"(magic));
+    return fma_bf16x2(x, s2, cs);
   };
 
   // Queries as B operands: column g of tile t is row 8 t + g, and lane c holds its quarter of the dims. (Zero past the
   // tile's rows.) With 32 rows they stand in shared memory, 16-byte chunk x of row r at x ^ (r & 7).
   uint32_t qb[kQRegs ? NT : 1][kQRegs ? D / 8 : 1];
-  constexpr int kQLoads = kRows * (D / 8) / kRowThreads;
-  uint4 qv[kQRegs ? 1 : kQLoads];
   int klo[NT][2], klim[NT][2], all_lo = 0, all_lim = 0;  // of rows 8 t + 2 c and the next
   auto load_q = [&](const Seg& s) {
     const unsigned r0 = (unsigned)s.tile * kRows;
@@ -178,6 +156,17 @@ __global__ void __launch_bounds__(kRowThreads, Row4Smem<D, NT>::kCtas)
       const int hd = (int)(rr - tok * G);
       return p.q + (long long)(s.q0 + tok) * p.q_tok + (long long)(s.head * G + hd) * p.q_head;
     };
+    if constexpr (!kQRegs) {
+      meet();  // the queries that stood there have been used
+      for (int x = threadIdx.x; x < kRows * (D / 8); x += 32 * kWarps) {
+        const int r = x / (D / 8), ch = x % (D / 8);
+        int tok;
+        const __nv_bfloat16* qp = row_of(r, tok);
+        const uint4 v = r < rows ? *reinterpret_cast<const uint4*>(qp + ch * 8) : make_uint4(0, 0, 0, 0);
+        st_shared_v4(sbase + L::kQ + r * (D * 2) + ((ch ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+      }
+      meet();
+    }
     int top = -0x7fffffff, low = 0x7fffffff;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -206,298 +195,388 @@ __global__ void __launch_bounds__(kRowThreads, Row4Smem<D, NT>::kCtas)
     }
     all_lo = __reduce_max_sync(0xffffffffu, top);
     all_lim = __reduce_min_sync(0xffffffffu, low);
-    if constexpr (!kQRegs) {
-#pragma unroll
-      for (int i = 0; i < kQLoads; ++i) {
-        const int x = i * kRowThreads + threadIdx.x, r = x / (D / 8);
-        int tok;
-        const __nv_bfloat16* qp = row_of(r, tok);
-        qv[i] = r < rows ? *reinterpret_cast<const uint4*>(qp + (x % (D / 8)) * 8) : make_uint4(0, 0, 0, 0);
-      }
-    }
-  };
-  auto place_q = [&]() {  // by all threads, where nothing reads the place any more
-    if constexpr (!kQRegs) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kQLoads; ++i) {
-        const int x = i * kRowThreads + threadIdx.x, r = x / (D / 8), ch = x % (D / 8);
-        st_shared_v4(sbase + L::kQ + r * (D * 2) + ((ch ^ (r & 7)) << 4), qv[i].x, qv[i].y, qv[i].z, qv[i].w);
-      }
-      __syncthreads();
-    }
   };
 
-  fetch();
-#pragma unroll
-  for (int i = 0; i < L::kStages - 1; ++i) issue();
-  if (fetched > 0) {
-    load_q(queue[0]);
-    place_q();
-  }
-  uint32_t done = 0;  // granules computed, of all stretches
-  for (uint32_t k = 0; k < fetched; ++k) {
-    const Seg& s = queue[k % L::kSlots];
-    const int n = s.n, key0 = s.blk * kRowBlk + warp * kGran;
-    const unsigned r0 = (unsigned)s.tile * kRows;
-    const int rows = (int)min((unsigned)kRows, (unsigned)s.ql * G - r0);
-    int lo, hi;
-    key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
-    float o[kMT][NT][4];
-#pragma unroll
-    for (int j = 0; j < kMT; ++j)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][t][i] = 0.f;
-    float m[NT][2], l[NT][2], lr[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        m[t][h] = -INFINITY;
-        l[t][h] = lr[t][h] = 0.f;
+  {
+    const uint32_t ring = sbase + warp * L::kWarp;
+    // The copying side: units of 32 keys, number warp, warp + kWarps, .. of a stretch's, up to kStages ahead of the products,
+    // on into the next stretches. A unit is two granules of 16 keys, each within a page. 16 bytes per lane: two rounds for a
+    // granule's codes of keys and of values (one at d = 64), and one for its scales, of keys in the first lanes and of values
+    // in the next. (Bulk copies of these four pieces, of 64 bytes to 1 KB, came to one per 60 cycles and SM and bound the
+    // kernel: 111 us for 64 sequences of 200 to 8192 keys.) A granule that no row sees, or whose page does not exist, is
+    // left out.
+    constexpr int kPieces = L::kScales / 16, kRounds = L::kCodes / 512;
+    constexpr int kUnit = 2 * kGran;
+    uint32_t fetched = 0, in = 0, none = 0;  // stretches taken; the stage that is filled next; bits 2 i, 2 i + 1: left out in stage i
+    int key_in = 0, end_in = 0, lo_in = 0, hi_in = 0;
+    const int* tab = nullptr;
+    const uint8_t *kp = nullptr, *vp = nullptr, *sp = nullptr;
+    int pages = -1;  // lane i: the page of granule i of this warp's next 16 units
+    int batch = 0;
+    bool more = true;
+    auto read_pages = [&]() {
+      const int key = key_in + (lane >> 1) * (kWarps * kUnit) + (lane & 1) * kGran;
+      const bool seen = key < end_in && key < hi_in && key + kGran > lo_in;
+      pages = seen ? tab[key >> b.page_shift] : -1;
+      if (seen && (unsigned)pages >= (unsigned)b.num_pages) {
+        record_index_error(b.status);
+        pages = -1;
       }
-
-    for (int i = 0; i < n; ++i, ++done) {
-      issue();
-      const uint32_t stage = done % L::kStages;
-      if (!mbar_wait_warp(bar(stage), (done / L::kStages) & 1, ctl)) continue;
-      if (skip[stage]) continue;
-      const uint32_t st = ring + stage * L::kStage;
-      const int key = key0 + i * kRowBlk;
-      const bool masked = key < all_lo || key + kGran - 1 > all_lim;
-      // ---- scores
-      float x[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-      {
-        uint32_t w[2][kKW], s2[2], cs[2];
+      batch = 0;
+    };
+    // The next stretch with units for this warp, while stretch k is worked on: no further than the slots reach without
+    // k's being given back (a warp may have none in many short stretches).
+    auto fetch = [&](uint32_t k) {
+      while (more && key_in >= end_in && fetched - k < L::kSlots - 1) {
+        const uint32_t at = fetched % L::kSlots;
+        if (!mbar_wait_warp(bar(L::bSegFull + at), (fetched / L::kSlots) & 1, ctl)) more = false;
+        const Seg& s = queue[at];
+        if (!more || s.n < 0) {
+          more = false;
+          break;
+        }
+        ++fetched;
+        key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo_in, hi_in);
+        key_in = s.blk * kRowBlk + warp * kUnit;
+        end_in = (s.blk + s.n) * kRowBlk;
+        tab = b.table + (long long)s.seq * b.table_stride;
+        kp = cache.k + (long long)s.head * cache.k_head + lane * 16;
+        vp = cache.v + (long long)s.head * cache.v_head + lane * 16;
+        sp = lane < kPieces ? cache.k_scale + (long long)s.head * cache.ks_head + lane * 16
+                            : cache.v_scale + (long long)s.head * cache.vs_head + (lane - kPieces) * 16;
+        read_pages();
+      }
+    };
+    const uint32_t s_page = (uint32_t)(lane < kPieces ? cache.ks_page : cache.vs_page);
+    uint32_t issued = 0, done = 0;  // units, of all stretches; a group of copies each
+    auto fill = [&](uint32_t k) {   // the ring, as far as units are at hand
+      while (issued - done < kStages) {
+        if (key_in >= end_in) fetch(k);
+        if (key_in >= end_in) break;
+        none &= ~(3u << 2 * in);
+        const uint32_t st = ring + in * L::kStage + lane * 16;
+        const uint32_t slot0 = key_in & (b.page_size - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          lds_words<kKW>(st + (g + 8 * h) * code_bytes(D) + c * (4 * kKW), w[h]);
-          const uint32_t sc = lds_u16(st + 2 * L::kCodes + (g + 8 * h) * scale_bytes(D) + (c * (D / 4) / kGroup4) * 2);
-          s2[h] = sc * 0x10001u;
-          cs[h] = scale_shift(s2[h]);
-        }
-#pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) {
-          uint32_t a[4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              a[2 * e + h] = fma_bf16x2(code_pair(w[h][kk >> 1], 2 * (kk & 1) + e), s2[h], cs[h]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if constexpr (kQRegs) {
-              mma16816(x[t], a, qb[t][2 * kk], qb[t][2 * kk + 1]);
-            } else {
-              const int r = 8 * t + g, byte = c * (D / 2) + 8 * kk;  // within the row
-              uint32_t q2[2];
-              lds_words<2>(sbase + L::kQ + r * (D * 2) + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15), q2);
-              mma16816(x[t], a, q2[0], q2[1]);
-            }
+          const int page = __shfl_sync(0xffffffffu, pages, 2 * batch + h);
+          if (page < 0) {
+            none |= 1u << (2 * in + h);
+            continue;
           }
+          const uint32_t slot = b.page_size == kGran ? 0 : slot0 + h * kGran;
+          const uint8_t* kx = kp + (uint64_t)(uint32_t)page * (uint32_t)cache.k_page + slot * code_bytes(D);
+          const uint8_t* vx = vp + (uint64_t)(uint32_t)page * (uint32_t)cache.v_page + slot * code_bytes(D);
+          const uint8_t* sx = sp + (uint64_t)(uint32_t)page * s_page + slot * scale_bytes(D);
+#pragma unroll
+          for (int i = 0; i < kRounds; ++i) {
+            cp_async16(st + h * L::kPart + i * 512, kx + i * 512);
+            cp_async16(st + h * L::kPart + L::kCodes + i * 512, vx + i * 512);
+          }
+          if (lane < 2 * kPieces) cp_async16(st + h * L::kPart + 2 * L::kCodes, sx);
         }
+        cp_async_commit();
+        ++issued;
+        in = in + 1 == kStages ? 0 : in + 1;
+        key_in += kWarps * kUnit;
+        if (++batch == 16 && key_in < end_in) read_pages();
       }
-      // ---- weights
-      uint32_t pb[NT][2];
+    };
+    fill(0);
+    uint32_t out = 0;  // the stage that is used next
+    const uint32_t k_at = g * code_bytes(D) + c * (4 * kKW);
+    const uint32_t ks_at = 2 * L::kCodes + g * scale_bytes(D) + (c * (D / 4) / kGroup4) * 2;
+    const uint32_t v_at = L::kCodes + 2 * c * code_bytes(D) + g * (4 * kVW);
+    const uint32_t vs_at = 2 * L::kCodes + L::kScales + 2 * c * scale_bytes(D) + (g * (D / 8) / kGroup4) * 2;
+    for (uint32_t k = 0;; ++k) {
+      // One warp waits for the stretch, so that all of them go on or none.
+      if (warp == 0) {
+        const bool go = mbar_wait_warp(bar(L::bSegFull + k % L::kSlots), (k / L::kSlots) & 1, ctl);
+        if (lane == 0) flag[0] = go;
+      }
+      meet();
+      if (!flag[0]) break;
+      const Seg& s = queue[k % L::kSlots];
+      if (s.n < 0) break;
+      fill(k);
+      load_q(s);
+      const int end = (s.blk + s.n) * kRowBlk;
+      const unsigned r0 = (unsigned)s.tile * kRows;
+      const int rows = (int)min((unsigned)kRows, (unsigned)s.ql * G - r0);
+      int lo, hi;
+      key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
+      float o[kMT][NT][4];
+#pragma unroll
+      for (int j = 0; j < kMT; ++j)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][t][i] = 0.f;
+      float m[NT][2], l[NT][2], lr[NT][4];  // lr: a product of ones and the weights as they are rounded
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kx = key + g + 8 * (e >> 1);
-            if (kx > klim[t][e & 1] || kx < klo[t][e & 1]) x[t][e] = -INFINITY;
-          }
-        }
-        float mt[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float v = fmaxf(x[t][h], x[t][2 + h]);
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          mt[h] = v * p.scale_log2;
+          m[t][h] = -INFINITY;
+          l[t][h] = 0.f;
         }
-        if (__any_sync(0xffffffffu, mt[0] > m[t][0] + 8.f || mt[1] > m[t][1] + 8.f)) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mn = fmaxf(m[t][h], mt[h]);
-            const float corr = mn > m[t][h] ? ex2(m[t][h] - mn) : 1.f;
-            m[t][h] = mn;
-            l[t][h] *= corr;
-            lr[t][h] *= corr;
+        for (int i = 0; i < 4; ++i) lr[t][i] = 0.f;
+      }
+
+      for (int key = s.blk * kRowBlk + warp * kUnit; key < end; key += kWarps * kUnit) {
+        fill(k);
+        if (issued - done == kStages) cp_async_wait<kStages - 1>();
+        else cp_async_wait<0>();
+        __syncwarp();
+        ++done;
+        const uint32_t st = ring + out * L::kStage, left_out = none >> 2 * out & 3;
+        out = out + 1 == kStages ? 0 : out + 1;
+        if (left_out == 3) continue;
+        const bool masked = key < all_lo || key + kUnit - 1 > all_lim || left_out;
+        // ---- scores
+        float x[2][NT][4];
 #pragma unroll
-            for (int j = 0; j < kMT; ++j) {
-              o[j][t][h] *= corr;
-              o[j][t][2 + h] *= corr;
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[u][t][e] = 0.f;
+        {
+          uint32_t w[2][2][kKW], s2[2][2], cs[2][2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              lds_words<kKW>(st + u * L::kPart + k_at + 8 * h * code_bytes(D), w[u][h]);
+              s2[u][h] = lds_u16(st + u * L::kPart + ks_at + 8 * h * scale_bytes(D)) * 0x10001u;
+              cs[u][h] = scale_shift(s2[u][h]);
+            }
+#pragma unroll
+          for (int kk = 0; kk < kSteps; ++kk) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t a[4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  a[2 * e + h] = value_pair(w[u][h][kk >> 1], 2 * (kk & 1) + e, s2[u][h], cs[u][h]);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                if constexpr (kQRegs) {
+                  mma16816(x[u][t], a, qb[t][2 * kk], qb[t][2 * kk + 1]);
+                } else {
+                  const int r = 8 * t + g, byte = c * (D / 2) + 8 * kk;  // within the row
+                  uint32_t q2[2];
+                  lds_words<2>(sbase + L::kQ + r * (D * 2) + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15), q2);
+                  mma16816(x[u][t], a, q2[0], q2[1]);
+                }
+              }
             }
           }
         }
-        const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
+        // ---- weights
+        uint32_t pb[NT][2][2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {  // keys g and g + 8
-          const float e0 = ex2(fmaf(x[t][2 * y], p.scale_log2, -mu[0]));
-          const float e1 = ex2(fmaf(x[t][2 * y + 1], p.scale_log2, -mu[1]));
-          const uint32_t pk = pack_bf16(e0, e1);
-          l[t][0] += e0;
-          l[t][1] += e1;
-          lr[t][0] += __uint_as_float(pk << 16);
-          lr[t][1] += __uint_as_float(pk & 0xffff0000u);
-          pb[t][y] = transpose8x8(pk);
-        }
-      }
-      // ---- values
-      {
-        uint32_t w[4][kVW], sc[4];  // values 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+        for (int t = 0; t < NT; ++t) {
+          if (masked) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int kx = 2 * c + (y & 1) + 8 * (y >> 1);
-          lds_words<kVW>(st + L::kCodes + kx * code_bytes(D) + g * (4 * kVW), w[y]);
-          sc[y] = lds_u16(st + 2 * L::kCodes + L::kScales + kx * scale_bytes(D) + (g * (D / 8) / kGroup4) * 2);
-          if (masked && (key + kx < lo || key + kx >= hi)) sc[y] = 0;  // slots that no row sees may hold NaN
-        }
-        uint32_t s2[2], cs[2];
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          s2[y] = sc[2 * y] | sc[2 * y + 1] << 16;
-          cs[y] = scale_shift(s2[y]);
-        }
-        // The same half words of two values side by side: pairs of keys for dims 2 j (low halves) and 2 j + 1.
-        uint32_t z[2][kVW][2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int v = 0; v < kVW; ++v) {
-            z[y][v][0] = __byte_perm(w[2 * y][v], w[2 * y + 1][v], 0x5410);
-            z[y][v][1] = __byte_perm(w[2 * y][v], w[2 * y + 1][v], 0x7632);
+              for (int e = 0; e < 4; ++e) {
+                const int kx = key + u * kGran + g + 8 * (e >> 1);
+                if (kx > klim[t][e & 1] || kx < klo[t][e & 1] || (left_out >> u & 1)) x[u][t][e] = -INFINITY;
+              }
           }
+          float mt[2];
 #pragma unroll
-        for (int j = 0; j < kMT; ++j) {
-          uint32_t a[4];
+          for (int h = 0; h < 2; ++h) {
+            float v = max3f(fmaxf(x[0][t][h], x[0][t][2 + h]), x[1][t][h], x[1][t][2 + h]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            mt[h] = v * p.scale_log2;
+          }
+          // The reference max moves only when a row has outgrown it by 2^8 (any reference gives the same softmax).
+          if (__any_sync(0xffffffffu, mt[0] > m[t][0] + 8.f || mt[1] > m[t][1] + 8.f)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float mn = fmaxf(m[t][h], mt[h]);
+              const float corr = mn > m[t][h] ? ex2(m[t][h] - mn) : 1.f;
+              m[t][h] = mn;
+              l[t][h] *= corr;
+              lr[t][h] *= corr;
+#pragma unroll
+              for (int j = 0; j < kMT; ++j) {
+                o[j][t][h] *= corr;
+                o[j][t][2 + h] *= corr;
+              }
+            }
+          }
+          const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {  // keys g and g + 8
+              const float e0 = ex2(fmaf(x[u][t][2 * y], p.scale_log2, -mu[0]));
+              const float e1 = ex2(fmaf(x[u][t][2 * y + 1], p.scale_log2, -mu[1]));
+              l[t][0] += e0;
+              l[t][1] += e1;
+              pb[t][u][y] = transpose8x8(pack_bf16(e0, e1));
+            }
+        }
+        // ---- values
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t w[4][kVW], sc[4];  // values 2 c, 2 c + 1, 2 c + 8, 2 c + 9
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int kx = (y & 1) + 8 * (y >> 1);
+            lds_words<kVW>(st + u * L::kPart + v_at + kx * code_bytes(D), w[y]);
+            sc[y] = lds_u16(st + u * L::kPart + vs_at + kx * scale_bytes(D));
+          }
+          if (masked) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int kx = key + u * kGran + 2 * c + (y & 1) + 8 * (y >> 1);
+              if (kx < lo || kx >= hi || (left_out >> u & 1)) sc[y] = 0;  // slots that no row sees may hold NaN
+            }
+          }
+          uint32_t s2[2], cs[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            s2[y] = sc[2 * y] | sc[2 * y + 1] << 16;
+            cs[y] = scale_shift(s2[y]);
+          }
+          // The same half words of two values side by side: pairs of keys for dims 2 j (low halves) and 2 j + 1.
+          uint32_t z[2][kVW][2];
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              // d = 128: tile j has dims 16 g + j and 16 g + 8 + j; d = 64: 8 g + 2 j and 8 g + 2 j + 1.
-              const uint32_t src = D == 128 ? z[y][h & (kVW - 1)][j & 1] : z[y][0][h];
-              a[2 * y + h] = fma_bf16x2(code_pair(src, D == 128 ? j >> 1 : j), s2[y], cs[y]);
+            for (int v = 0; v < kVW; ++v) {
+              z[y][v][0] = __byte_perm(w[2 * y][v], w[2 * y + 1][v], 0x5410);
+              z[y][v][1] = __byte_perm(w[2 * y][v], w[2 * y + 1][v], 0x7632);
             }
+          const uint32_t ones[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma16816(o[j][t], a, pb[t][0], pb[t][1]);
+          for (int t = 0; t < NT; ++t) mma16816(lr[t], ones, pb[t][u][0], pb[t][u][1]);
+#pragma unroll
+          for (int j = 0; j < kMT; ++j) {
+            uint32_t a[4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                // d = 128: tile j has dims 16 g + j and 16 g + 8 + j; d = 64: 8 g + 2 j and 8 g + 2 j + 1.
+                const uint32_t src = D == 128 ? z[y][h & (kVW - 1)][j & 1] : z[y][0][h];
+                a[2 * y + h] = value_pair(src, D == 128 ? j >> 1 : j, s2[y], cs[y]);
+              }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816(o[j][t], a, pb[t][u][0], pb[t][u][1]);
+          }
         }
+        __syncwarp();  // the stage is read: the next copies may overwrite it
       }
-      __syncwarp();  // the stage is read: the next copies may overwrite it
-    }
 
-    // ---- join the four warps, 8 rows at a time
+      // ---- join the warps, 4 rows at a time
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], off);
-          lr[t][h] += __shfl_xor_sync(0xffffffffu, lr[t][h], off);
-        }
-    const bool whole = s.first && s.last;
-    const int c0 = s.c0, c1 = s.c1, q0 = s.q0, head = s.head;
-    float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * row_part(D, kRows);
+          for (int off = 4; off < 32; off <<= 1) l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], off);
+      const bool whole = s.first && s.last;
+      const int c0 = s.c0, c1 = s.c1, q0 = s.q0, head = s.head;
+      float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * row_part(D, kRows);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::bSegEmpty + k % L::kSlots));  // (nothing of s is read below)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (8 * t >= rows) break;
-      __syncthreads();  // the rows that stood here have been read
-      // Rows 2 c and 2 c + 1 of this lane, dims from g * D / 8 on; 16-byte chunk x of row r at x ^ r.
+      for (int half = 0; half < 2 * NT; ++half) {
+        const int t = half >> 1;
+        if (4 * half >= rows) break;
+        if (half > 0) meet();  // the rows that stood here have been read
+        // Rows 2 c and 2 c + 1 of this lane, dims from g * D / 8 on; 16-byte chunk x of row r at x ^ 2 r.
+        if (c >> 1 == (half & 1)) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 2 * c + h, at = warp * 8 + r;
+          for (int h = 0; h < 2; ++h) {
+            const int r = 2 * (c & 1) + h, at = warp * 4 + r;
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {  // dims 4 q .. of the lane's
-          float4 v;
-          float* f = reinterpret_cast<float*>(&v);
+            for (int q = 0; q < D / 32; ++q) {  // dims 4 q .. of the lane's
+              float4 v;
+              float* f = reinterpret_cast<float*>(&v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int dim = 4 * q + i;
-            f[i] = D == 128 ? o[(dim & 7) % kMT][t][2 * (dim >> 3) + h] : o[(dim >> 1) % kMT][t][2 * (dim & 1) + h];
+              for (int i = 0; i < 4; ++i) {
+                const int dim = 4 * q + i;
+                f[i] = D == 128 ? o[(dim & 7) % kMT][t][2 * (dim >> 3) + h] : o[(dim >> 1) % kMT][t][2 * (dim & 1) + h];
+              }
+              *reinterpret_cast<float4*>(merge + at * D + (((g * (D / 32) + q) ^ (2 * r)) << 2)) = v;
+            }
+            if (g == 0) {
+              stat[at * 3] = m[t][h];
+              stat[at * 3 + 1] = l[t][h];
+              stat[at * 3 + 2] = lr[t][h];
+            }
           }
-          *reinterpret_cast<float4*>(merge + at * D + (((g * (D / 32) + q) ^ r) << 2)) = v;
         }
-        if (g == 0) {
-          stat[at * 3] = m[t][h];
-          stat[at * 3 + 1] = l[t][h];
-          stat[at * 3 + 2] = lr[t][h];
-        }
-      }
-      __syncthreads();
-      const int hr = threadIdx.x >> 4, row = hr + 8 * t, ch = threadIdx.x & 15;  // 16 threads per row
-      float M = -INFINITY, Ls = 0.f, Lr = 0.f;
+        meet();
+        for (int x = threadIdx.x; x < 4 * (D / 4); x += 32 * kWarps) {  // four columns of a row
+          const int hr = x / (D / 4), row = hr + 4 * half, ch = x % (D / 4);
+          if (row >= rows) continue;
+          float M = -INFINITY, Ls = 0.f, Lr = 0.f;
 #pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, stat[(w * 8 + hr) * 3]);
-      const float Mu = M == -INFINITY ? 0.f : M;
-      float4 acc[D / 64];
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[(w * 4 + hr) * 3]);
+          const float Mu = M == -INFINITY ? 0.f : M;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) {
-        const float* sw = stat + (w * 8 + hr) * 3;
-        const float f = ex2(sw[0] - Mu);
-        Ls += f * sw[1];
-        Lr += f * sw[2];
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + hr) * D + (((ch + 16 * i) ^ hr) << 2));
-          acc[i].x = fmaf(f, v.x, acc[i].x);
-          acc[i].y = fmaf(f, v.y, acc[i].y);
-          acc[i].z = fmaf(f, v.z, acc[i].z);
-          acc[i].w = fmaf(f, v.w, acc[i].w);
-        }
-      }
-      if (row < rows) {
-        if (whole) {
-          long long out = 0;
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) out = put_row<D>(p, q0, head, r0 + row, 4 * (ch + 16 * i), acc[i], Lr);
-          if (ch == 0) p.lse[out] = (M + log2f(Ls)) * 0.6931471805599453f;
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) *reinterpret_cast<float4*>(slot + row * D + 4 * (ch + 16 * i)) = acc[i];
-          if (ch == 0) {
-            slot[kRows * D + row] = M;
-            slot[kRows * (D + 1) + row] = Ls;
-            slot[kRows * (D + 2) + row] = Lr;
+          for (int w = 0; w < kWarps; ++w) {
+            const float* sw = stat + (w * 4 + hr) * 3;
+            const float f = ex2(sw[0] - Mu);
+            Ls += f * sw[1];
+            Lr += f * sw[2];
+            const float4 v = *reinterpret_cast<const float4*>(merge + (w * 4 + hr) * D + ((ch ^ (2 * hr)) << 2));
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+          if (whole) {
+            const long long place = put_row<D>(p, q0, head, r0 + row, 4 * ch, acc, Lr);
+            if (ch == 0) p.lse[place] = (M + log2f(Ls)) * 0.6931471805599453f;
+          } else {
+            *reinterpret_cast<float4*>(slot + row * D + 4 * ch) = acc;
+            if (ch == 0) {
+              slot[kRows * D + row] = M;
+              slot[kRows * (D + 1) + row] = Ls;
+              slot[kRows * (D + 2) + row] = Lr;
+            }
           }
         }
       }
-    }
-    if (k + 1 < fetched) load_q(queue[(k + 1) % L::kSlots]);  // on its way beside what follows
-    if (!whole && p.row_share != nullptr) {
-      if (c0 == (int)blockIdx.x && threadIdx.x == 0) p.row_share[c0] = RowShare{c1, q0, (int)r0, rows, head};
-    } else if (!whole) {
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        // The barrier orders the CTA's stores before this thread's release, which covers them all.
-        uint32_t before;
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                     : "=r"(before)
-                     : "l"(&b.plan.counters[c0])
-                     : "memory");
-        const bool last = before == (uint32_t)(c1 - c0);
-        if (last) b.plan.counters[c0] = 0;
-        *flag = last;
+      if (!whole && p.row_share != nullptr) {
+        if (c0 == (int)blockIdx.x && threadIdx.x == 0) p.row_share[c0] = RowShare{c1, q0, (int)r0, rows, head};
+      } else if (!whole) {
+        meet();
+        if (threadIdx.x == 0) {
+          // The barrier orders the CTA's stores before this thread's release, which covers them all.
+          uint32_t before;
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                       : "=r"(before)
+                       : "l"(&b.plan.counters[c0])
+                       : "memory");
+          const bool last = before == (uint32_t)(c1 - c0);
+          if (last) b.plan.counters[c0] = 0;
+          flag[1] = last;
+        }
+        meet();
+        if (flag[1]) join_row_tile<D, kRows, 32 * kWarps>(p, c0, c1, q0, head, r0, rows);
       }
-      __syncthreads();
-      if (*flag != 0) join_row_tile<D, kRows>(p, c0, c1, q0, head, r0, rows);
     }
-    if (k + 1 < fetched) place_q();
   }
-  if (*ctl.abort)  // every copy in flight lands before shared memory is given up
-    for (uint32_t x = copied > L::kStages ? copied - L::kStages : 0; x < copied; ++x)
-      drain_wait(bar(x % L::kStages), (x / L::kStages) & 1);
-  if (p.tile_ctas > 0) join_pairs<D>(p);
+  if constexpr (NT == 2) {  // (a batch of tiles of 8 or of 32 rows has no pairs)
+    // (All warps that compute have met since the last wait, so they see one answer.)
+    if (p.tile_ctas > 0 && !*ctl.abort && warp < kRowWarps)
+      join_pairs<D>(p, [] { asm volatile("bar.sync 2, %0;" ::"n"(kRowThreads) : "memory"); });
+  }
 }
 
 template <int D, int NT>
@@ -509,7 +588,7 @@ static cudaError_t launch_rows4(PagedFwd& p, const PagedCache4& cache, int num_s
   cudaLaunchConfig_t cfg = {};
   p.row_grid = L::kCtas * num_sms;
   cfg.gridDim = dim3(p.row_grid);
-  cfg.blockDim = dim3(kRowThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = L::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute early;  // beside the pairs' kernel, as in launch_paged_rows
@@ -522,20 +601,19 @@ static cudaError_t launch_rows4(PagedFwd& p, const PagedCache4& cache, int num_s
   return launch_paged_join_rows(p, D, num_sms, st);
 }
 
+// Tiles of 8 columns: one where no tile of the batch can have more than 8 rows, two for 16, four for 32.
 size_t paged4_rows_workspace_bytes(int d, int row_tile) {
-  const size_t ctas = (size_t)row4_ctas(row_tile) * kPagedSms;
+  const size_t ctas = (size_t)kMostRow4Ctas * kPagedSms;
   return plan_up(2 * ctas * row_part(d, row_tile) * 4) + plan_up(ctas * sizeof(RowShare));
 }
 
-// Tiles of 8 columns: one where no tile of the batch can have more than 8 rows, two for 16, four for 32.
 cudaError_t launch_paged4_rows(PagedFwd& p, const PagedCache4& cache, int d, int num_sms, cudaStream_t st) {
-  const bool few = (long long)p.b.max_q * p.b.G <= 8;
-  if (d == 128) {
-    if (p.b.row_tile == 32) return launch_rows4<128, 4>(p, cache, num_sms, st);
-    return few ? launch_rows4<128, 1>(p, cache, num_sms, st) : launch_rows4<128, 2>(p, cache, num_sms, st);
-  }
-  if (p.b.row_tile == 32) return launch_rows4<64, 4>(p, cache, num_sms, st);
-  return few ? launch_rows4<64, 1>(p, cache, num_sms, st) : launch_rows4<64, 2>(p, cache, num_sms, st);
+  const int nt = row4_columns(p.b.row_tile, p.b.max_q, p.b.G);
+  if (d == 128)
+    return nt == 4 ? launch_rows4<128, 4>(p, cache, num_sms, st)
+                   : (nt == 2 ? launch_rows4<128, 2>(p, cache, num_sms, st) : launch_rows4<128, 1>(p, cache, num_sms, st));
+  return nt == 4 ? launch_rows4<64, 4>(p, cache, num_sms, st)
+                 : (nt == 2 ? launch_rows4<64, 2>(p, cache, num_sms, st) : launch_rows4<64, 1>(p, cache, num_sms, st));
 }
 
 }  // namespace fa

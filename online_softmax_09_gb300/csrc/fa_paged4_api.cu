@@ -5,12 +5,12 @@
 
 namespace {
 
-// Strides (page, head) in bytes of a part of the cache.
+// Strides (page, head) in bytes of a part of the cache. (The kernels multiply a page's number and stride in 32 bits each.)
 int check_bytes(const long long* s, int pages, int heads) {
   const long long extent[2] = {pages, heads};
   for (int i = 0; i < 2; ++i) {
     if (extent[i] <= 1) continue;
-    if (s[i] <= 0 || s[i] > (1LL << 46)) return FA_ERR_INVALID;
+    if (s[i] <= 0 || s[i] > (i == 0 ? 0xffffffffLL : 1LL << 46)) return FA_ERR_INVALID;
     if (s[i] & 15) return FA_ERR_ALIGN;
   }
   return FA_OK;
@@ -197,11 +197,11 @@ int fa_fwd_paged4(const void* q, const long long* q_strides, const fa_paged_cach
   p.b.sms = num_sms;
   set_fwd(p, q, q_strides, o, lse, scale, workspace, batch);
   const fa::PagedCache4 c = device_cache4(cache);
-  const int d = batch->d, ctas = fa::row4_ctas(p.b.row_tile);
+  const int d = batch->d, ctas = fa::row4_ctas(fa::row4_columns(p.b.row_tile, p.b.max_q, p.b.G));
   p.row_share = few_tiles(batch, p.b, (long long)ctas * num_sms)
                     ? reinterpret_cast<fa::RowShare*>(
                           static_cast<char*>(workspace) +
-                          fa::plan_up((size_t)2 * ctas * fa::kPagedSms * fa::row_part(d, p.b.row_tile) * 4))
+                          fa::plan_up((size_t)2 * fa::kMostRow4Ctas * fa::kPagedSms * fa::row_part(d, p.b.row_tile) * 4))
                     : nullptr;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (with_pairs(batch)) {

@@ -35,11 +35,11 @@ __device__ __forceinline__ long long put_row(const PagedFwd& p, int q0, int head
 
 // The partial results that CTAs c0 to c1 left of a small tile, joined in the order of the keys by one CTA (the last of
 // them to arrive).
-template <int D, int kRows>
+template <int D, int kRows, int kThreads = kRowThreads>
 __device__ __forceinline__ void join_row_tile(const PagedFwd& p, int c0, int c1, int q0, int head, unsigned r0,
                                               int rows) {
   // Four columns of a row per thread, eight results' loads at a time.
-  for (int x = threadIdx.x; x < rows * (D / 4); x += kRowThreads) {
+  for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
     const int rw = x / (D / 4), col = (x - rw * (D / 4)) * 4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float m0 = -INFINITY, ls = 0.f, lsr = 0.f;
@@ -134,8 +134,9 @@ struct JoinPiece {
   }
 };
 
-template <int D>
-__device__ __forceinline__ void join_pairs(const PagedFwd& p) {
+// By kRowThreads threads (the first of the CTA) that meet in `sync`.
+template <int D, class Sync>
+__device__ __forceinline__ void join_pairs(const PagedFwd& p, Sync sync) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before is complete
   const PagedBatch& b = p.b;
   const int tpt = b.pair_tokens >> 1, used = tpt * b.G;
@@ -163,9 +164,9 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
     some[i] = __ballot_sync(0xffffffffu, mine[i].c1 >= 0);
     n += __popc(some[i]);
   }
-  __syncthreads();  // the rows' use of this memory is over
+  sync();  // the rows' use of this memory is over
   if (lane == 0) counts[warp] = n;
-  __syncthreads();
+  sync();
   int at = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kRowWarps; ++w) {
@@ -178,7 +179,7 @@ __device__ __forceinline__ void join_pairs(const PagedFwd& p) {
       list[at + __popc(some[i] & ((1u << lane) - 1))] = Entry{mine[i], i * kRowThreads + (int)threadIdx.x};
     at += __popc(some[i]);
   }
-  __syncthreads();
+  sync();
   const int units = total * (kTile / 16);
   const int g0 = threadIdx.x >> 4;
   for (int x = blockIdx.x; x < units; x += 2 * gridDim.x) {
