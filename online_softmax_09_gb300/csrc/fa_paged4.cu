@@ -20,11 +20,12 @@ template <int D, int NT>
 struct Row4Smem {
   static constexpr int kRows = NT <= 2 ? 16 : 32;
   static constexpr int kWarps = row4_warps(NT), kThreads = 32 * (kWarps + 1);  // those that compute, and one that copies
+  static constexpr int kShares = kWarps == 7 ? 8 : kWarps;
   static constexpr int kCtas = row4_ctas(NT);
   static constexpr int kCodes = kGran * code_bytes(D), kScales = kGran * scale_bytes(D);
   static constexpr int kPart = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales of a granule
   static constexpr int kStage = 2 * kPart;              // two granules: what a warp takes at a time
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? 3 : (NT == 2 ? 4 : 6);
   static constexpr int kSlots = kStages + 3;  // stretches handed out
   static constexpr int kWarp = kStages * kStage;
   static constexpr int kMerge = kWarps * kWarp;               // 4 rows of o of each warp
@@ -75,6 +76,15 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void cp_async16_if(bool go, uint32_t dst, const void* src) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}\n" ::"r"(dst),
+      "l"(src), "r"((uint32_t)go)
+      : "memory");
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kCtas)
     fa_paged4_rows_kernel(const PagedFwd p, const PagedCache4 cache) {
@@ -85,24 +95,17 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
   constexpr int kKW = D / 32;          // words of a key that a lane takes
   constexpr int kVW = D / 64;          // and of a value
   constexpr bool kQRegs = NT <= 2;     // queries in registers
+  constexpr int kUnit = 2 * kGran;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (A value that all lanes have, from lane 0: the compiler then knows it, and needs no care for lanes that part.)
+  auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   Seg* queue = reinterpret_cast<Seg*>(smem + L::kQueue);
   volatile int* flag = reinterpret_cast<volatile int*>(smem + L::kFlag);
   const PagedBatch& b = p.b;
   const Ctl ctl{reinterpret_cast<volatile int*>(smem + L::kAbort), b.status};
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
-  if (!plan_matches(b, D)) {
-    if (threadIdx.x == 0) record_index_error(b.status);
-    if (p.tile_ctas > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (p.row_share != nullptr && threadIdx.x == 0) p.row_share[blockIdx.x].c1 = -1;
-    return;
-  }
-  if (p.row_share != nullptr) {
-    if (threadIdx.x == 0) p.row_share[blockIdx.x].c1 = -1;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  }
   if (threadIdx.x < L::kSlots) {
     mbar_init(bar(L::bSegFull + threadIdx.x), 1);
     mbar_init(bar(L::bSegEmpty + threadIdx.x), kWarps);
@@ -110,24 +113,35 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
   if (threadIdx.x == 0) *ctl.abort = 0;
   fence_mbar_init();
   __syncthreads();
+  if (p.row_share != nullptr) {
+    if (threadIdx.x == 0) p.row_share[blockIdx.x].c1 = -1;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   const unsigned G = b.G;
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- walk
-    // One warp finds the CTA's stretches and hands them out, a few ahead of those that are worked on.
+    // One warp finds the CTA's stretches and hands them out, a few ahead of those that are worked on. (Done between the
+    // stretches by a warp that computes, its state in shared memory: 110 us where this takes 91 for 64 sequences of 200 to
+    // 8192 keys, 15 where it takes 10 for one of 1000.)
     SegIter<false, kRows> it(b, p.tile_ctas > 0 ? max(1, L::kCtas * (b.sms - pair_sms(b))) : gridDim.x);
     Seg s;
-    for (uint32_t i = 0;; ++i) {
-      const bool some = it.next(s);
+    bool some = plan_matches(b, D);  // (its loads go out beside the walk's)
+    for (uint32_t i = 0; some; ++i) {
+      some = it.next(s);
       const uint32_t at = i % L::kSlots;
-      if (!mbar_wait_warp(bar(L::bSegEmpty + at), ((i / L::kSlots) & 1) ^ 1, ctl)) return;
+      if (!mbar_wait_warp(bar(L::bSegEmpty + at), ((i / L::kSlots) & 1) ^ 1, ctl)) break;
       if (lane == 0) {
         queue[at] = s;
         if (!some) queue[at].n = -1;
         mbar_arrive(bar(L::bSegFull + at));
       }
-      if (!some) return;
     }
+  }
+  if (!plan_matches(b, D)) {
+    if (threadIdx.x == 0) record_index_error(b.status);
+    if (p.tile_ctas > 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
   }
 
   // ------------------------------------------------------------------ products and softmax
@@ -152,7 +166,7 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     const int rows = (int)min((unsigned)kRows, (unsigned)s.ql * G - r0);
     auto row_of = [&](int r, int& tok) {
       const unsigned rr = r0 + (r < rows ? r : 0);
-      tok = (int)(rr / G);
+      tok = s.ql == 1 ? 0 : (int)(rr / G);
       const int hd = (int)(rr - tok * G);
       return p.q + (long long)(s.q0 + tok) * p.q_tok + (long long)(s.head * G + hd) * p.q_head;
     };
@@ -197,31 +211,36 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     all_lim = __reduce_min_sync(0xffffffffu, low);
   };
 
-  {
+  if (warp < kWarps) {
     const uint32_t ring = sbase + warp * L::kWarp;
-    // The copying side: units of 32 keys, number warp, warp + kWarps, .. of a stretch's, up to kStages ahead of the products,
+    // Units are dealt to kWarps + 1 shares. The walking warp's is taken by the one in the middle of seven, which is on the
+    // same quarter of the SM and would have half of it to itself.
+    const int step = kWarps * kUnit;
+    // The copying side: units of 32 keys, one of each round of shares, up to kStages ahead of the products,
     // on into the next stretches. A unit is two granules of 16 keys, each within a page. 16 bytes per lane: two rounds for a
     // granule's codes of keys and of values (one at d = 64), and one for its scales, of keys in the first lanes and of values
     // in the next. (Bulk copies of these four pieces, of 64 bytes to 1 KB, came to one per 60 cycles and SM and bound the
     // kernel: 111 us for 64 sequences of 200 to 8192 keys.) A granule that no row sees, or whose page does not exist, is
     // left out.
     constexpr int kPieces = L::kScales / 16, kRounds = L::kCodes / 512;
-    constexpr int kUnit = 2 * kGran;
     uint32_t fetched = 0, in = 0, none = 0;  // stretches taken; the stage that is filled next; bits 2 i, 2 i + 1: left out in stage i
     int key_in = 0, end_in = 0, lo_in = 0, hi_in = 0;
     const int* tab = nullptr;
     const uint8_t *kp = nullptr, *vp = nullptr, *sp = nullptr;
-    int pages = -1;  // lane i: the page of granule i of this warp's next 16 units
+    int pages = 0;  // lane i: the page of granule i of this warp's next 16 units
+    uint32_t have = 0;  // bit i: there is one
     int batch = 0;
     bool more = true;
     auto read_pages = [&]() {
-      const int key = key_in + (lane >> 1) * (kWarps * kUnit) + (lane & 1) * kGran;
+      const int key = key_in + (lane >> 1) * step + (lane & 1) * kGran;
       const bool seen = key < end_in && key < hi_in && key + kGran > lo_in;
-      pages = seen ? tab[key >> b.page_shift] : -1;
-      if (seen && (unsigned)pages >= (unsigned)b.num_pages) {
+      pages = seen ? tab[key >> b.page_shift] : 0;
+      const bool bad = (unsigned)pages >= (unsigned)b.num_pages;
+      if (bad) {
         record_index_error(b.status);
-        pages = -1;
+        pages = 0;
       }
+      have = __ballot_sync(0xffffffffu, seen && !bad);
       batch = 0;
     };
     // The next stretch with units for this warp, while stretch k is worked on: no further than the slots reach without
@@ -236,9 +255,12 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
           break;
         }
         ++fetched;
-        key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo_in, hi_in);
-        key_in = s.blk * kRowBlk + warp * kUnit;
-        end_in = (s.blk + s.n) * kRowBlk;
+        int lo, hi;
+        key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
+        lo_in = uniform(lo);
+        hi_in = uniform(hi);
+        key_in = uniform(s.blk) * kRowBlk + warp * kUnit;
+        end_in = uniform(s.blk + s.n) * kRowBlk;
         tab = b.table + (long long)s.seq * b.table_stride;
         kp = cache.k + (long long)s.head * cache.k_head + lane * 16;
         vp = cache.v + (long long)s.head * cache.v_head + lane * 16;
@@ -249,36 +271,41 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     };
     const uint32_t s_page = (uint32_t)(lane < kPieces ? cache.ks_page : cache.vs_page);
     uint32_t issued = 0, done = 0;  // units, of all stretches; a group of copies each
-    auto fill = [&](uint32_t k) {   // the ring, as far as units are at hand
+    auto issue = [&]() {            // the next unit's copies
+      const uint32_t st = ring + in * L::kStage + lane * 16, there = have >> 2 * batch & 3;
+      const uint32_t slot0 = b.page_size == kGran ? 0 : key_in & (b.page_size - 1);
+      const uint32_t slot_step = b.page_size == kGran ? 0 : kGran;
+      auto part = [&](int h) {
+        const uint32_t page = __shfl_sync(0xffffffffu, pages, 2 * batch + h), slot = slot0 + h * slot_step;
+        const uint8_t* kx = kp + (uint64_t)page * (uint32_t)cache.k_page + slot * code_bytes(D);
+        const uint8_t* vx = vp + (uint64_t)page * (uint32_t)cache.v_page + slot * code_bytes(D);
+        const uint8_t* sx = sp + (uint64_t)page * s_page + slot * scale_bytes(D);
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+          cp_async16(st + h * L::kPart + i * 512, kx + i * 512);
+          cp_async16(st + h * L::kPart + L::kCodes + i * 512, vx + i * 512);
+        }
+        cp_async16_if(lane < 2 * kPieces, st + h * L::kPart + 2 * L::kCodes, sx);
+      };
+      if (there == 3) {
+        part(0);
+        part(1);
+      } else if (there != 0) {
+        if (there & 1) part(0);
+        else part(1);
+      }
+      none = (none & ~(3u << 2 * in)) | (there ^ 3u) << 2 * in;
+      cp_async_commit();
+      ++issued;
+      in = in + 1 == kStages ? 0 : in + 1;
+      key_in += step;
+      if (++batch == 16 && key_in < end_in) read_pages();
+    };
+    auto fill = [&](uint32_t k) {  // the ring, as far as units are at hand
       while (issued - done < kStages) {
         if (key_in >= end_in) fetch(k);
         if (key_in >= end_in) break;
-        none &= ~(3u << 2 * in);
-        const uint32_t st = ring + in * L::kStage + lane * 16;
-        const uint32_t slot0 = key_in & (b.page_size - 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int page = __shfl_sync(0xffffffffu, pages, 2 * batch + h);
-          if (page < 0) {
-            none |= 1u << (2 * in + h);
-            continue;
-          }
-          const uint32_t slot = b.page_size == kGran ? 0 : slot0 + h * kGran;
-          const uint8_t* kx = kp + (uint64_t)(uint32_t)page * (uint32_t)cache.k_page + slot * code_bytes(D);
-          const uint8_t* vx = vp + (uint64_t)(uint32_t)page * (uint32_t)cache.v_page + slot * code_bytes(D);
-          const uint8_t* sx = sp + (uint64_t)(uint32_t)page * s_page + slot * scale_bytes(D);
-#pragma unroll
-          for (int i = 0; i < kRounds; ++i) {
-            cp_async16(st + h * L::kPart + i * 512, kx + i * 512);
-            cp_async16(st + h * L::kPart + L::kCodes + i * 512, vx + i * 512);
-          }
-          if (lane < 2 * kPieces) cp_async16(st + h * L::kPart + 2 * L::kCodes, sx);
-        }
-        cp_async_commit();
-        ++issued;
-        in = in + 1 == kStages ? 0 : in + 1;
-        key_in += kWarps * kUnit;
-        if (++batch == 16 && key_in < end_in) read_pages();
+        issue();
       }
     };
     fill(0);
@@ -294,16 +321,18 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
         if (lane == 0) flag[0] = go;
       }
       meet();
-      if (!flag[0]) break;
+      if (!uniform(flag[0])) break;
       const Seg& s = queue[k % L::kSlots];
-      if (s.n < 0) break;
+      if (uniform(s.n) < 0) break;
       fill(k);
       load_q(s);
-      const int end = (s.blk + s.n) * kRowBlk;
+      const int begin = uniform(s.blk) * kRowBlk, end = begin + uniform(s.n) * kRowBlk;
       const unsigned r0 = (unsigned)s.tile * kRows;
-      const int rows = (int)min((unsigned)kRows, (unsigned)s.ql * G - r0);
+      const int rows = uniform((int)min((unsigned)kRows, (unsigned)s.ql * G - r0));
       int lo, hi;
       key_range(s.t0, s.t1, s.ql, s.kvl, b.causal, b.window, lo, hi);
+      lo = uniform(lo);
+      hi = uniform(hi);
       float o[kMT][NT][4];
 #pragma unroll
       for (int j = 0; j < kMT; ++j)
@@ -323,8 +352,12 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
         for (int i = 0; i < 4; ++i) lr[t][i] = 0.f;
       }
 
-      for (int key = s.blk * kRowBlk + warp * kUnit; key < end; key += kWarps * kUnit) {
-        fill(k);
+#pragma unroll 1
+      for (int key = begin + warp * kUnit; key < end; key += step) {
+        if (issued - done < kStages) {  // (usually by the one that was used last)
+          if (key_in < end_in) issue();
+          else fill(k);
+        }
         if (issued - done == kStages) cp_async_wait<kStages - 1>();
         else cp_async_wait<0>();
         __syncwarp();
@@ -573,9 +606,12 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     }
   }
   if constexpr (NT == 2) {  // (a batch of tiles of 8 or of 32 rows has no pairs)
-    // (All warps that compute have met since the last wait, so they see one answer.)
-    if (p.tile_ctas > 0 && !*ctl.abort && warp < kRowWarps)
-      join_pairs<D>(p, [] { asm volatile("bar.sync 2, %0;" ::"n"(kRowThreads) : "memory"); });
+    static_assert(NT != 2 || kWarps + 1 == kRowWarps, "join_pairs is for kRowThreads");
+    if (p.tile_ctas > 0) {
+      asm volatile("cp.async.wait_all;" ::: "memory");  // (some are in flight after a wait that gave up)
+      __syncthreads();
+      join_pairs<D>(p, [] { __syncthreads(); });
+    }
   }
 }
 

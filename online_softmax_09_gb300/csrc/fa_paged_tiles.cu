@@ -34,7 +34,10 @@
 namespace fa {
 
 constexpr int kTileThreads = 320;
-constexpr int kUnpackThreads = 64;  // more of them over a 4-bit cache
+// Over a 4-bit cache: four warps that unpack stand before the producer, and two that do nothing behind it, so that registers
+// can be given from these eight to those of the softmax (a warpgroup at a time; 256 * (kSoftRegs + kOtherRegs) = 65536).
+constexpr int kUnpackThreads = 128, kPackedThreads = 512;
+constexpr int kSoftRegs = 168, kOtherRegs = 88;
 constexpr uint32_t kTileTmemCols = 512;
 constexpr float kTileRescale = 8.f;
 
@@ -162,13 +165,22 @@ __device__ __forceinline__ float max64f(const uint32_t (&a)[32], const uint32_t 
   return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), max3f(m[6], m[7], init));
 }
 
+// Registers can change hands only in a kernel without calls: there the slow part of a wait stands in line.
+template <bool kInLine>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, Ctl ctl) {
+  if constexpr (!kInLine) return mbar_wait_warp(bar, parity, ctl);
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = mbar_wait_loop(bar, parity, ctl);
+  return __all_sync(0xffffffffu, ok);
+}
+
 template <int D, bool kTurn, bool kPacked>
-__global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTileThreads, 1)
+__global__ void __launch_bounds__(kPacked ? kPackedThreads : kTileThreads, 1)
     fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                           const PagedFwd p, const PagedCache4 cache) {
   using L = TileSmem<D>;
-  constexpr int kThreads = kPacked ? kTileThreads + kUnpackThreads : kTileThreads;
+  constexpr int kThreads = kPacked ? kPackedThreads : kTileThreads, kLoad = kPacked ? 12 : 8, kMma = kLoad + 1;
   constexpr bool kHalves = D == 64;  // see halves() in fa_paged.cuh
   constexpr bool kBoxOut = D == 128;
   constexpr int NK = L::NK, NV = L::NV;
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
     }
     for (int s = 0; s < kSegSlots; ++s) {
       mbar_init(bar(L::bSegFull + s), 1);
-      mbar_init(bar(L::bSegEmpty + s), kPacked ? 11 : 9);  // the MMA warp, the softmax warps, those that unpack
+      mbar_init(bar(L::bSegEmpty + s), kPacked ? 13 : 9);  // the MMA warp, the softmax warps, those that unpack
     }
     mbar_init(bar(L::bTwin), 128);
     mbar_init(bar(L::bTwinFree), 128);
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kLoad && lane == 0) {
     tma_prefetch_desc(&tm_q);
     if constexpr (!kPacked) {
       tma_prefetch_desc(&tm_k);
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
     st_shared_v4(sQ + part * 16384 + used * 128 + at * 16, 0, 0, 0, 0);
   }
   fence_proxy_async_smem();
-  if (warp == 9) {
+  if (warp == kMma) {
     tmem_alloc(smem_u32(tmem_slot), kTileTmemCols);
     tmem_relinquish();
   }
@@ -269,7 +281,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
     cur.tab = b.table + (long long)s.seq * b.table_stride;
     if (!kPacked && it.n_max > 0) read_entry(it.j0 + it.turn);
   };
-  if (warp == 8) look();
+  if (warp == kLoad) look();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -278,13 +290,15 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
 
   // Stretch i of the CTA, once the producer has handed it out; and its slot given back.
   auto take = [&](uint32_t i) -> const TileSeg* {
-    return mbar_wait_warp(bar(L::bSegFull + i % kSegSlots), (i / kSegSlots) & 1, ctl) ? segs + i % kSegSlots : nullptr;
+    return wait_warp<kPacked>(bar(L::bSegFull + i % kSegSlots), (i / kSegSlots) & 1, ctl) ? segs + i % kSegSlots : nullptr;
   };
   auto give_back = [&](uint32_t i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(L::bSegEmpty + i % kSegSlots));
   };
-  if (warp == 8) {
+  if (warp >= 8) {
+  if constexpr (kPacked) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kLoad) {
     // ------------------------------------------------------------------ TMA producer
     const uint32_t q_bytes = (uint32_t)used * D * 2;
     uint32_t gk = 0, gv = 0, qn[2] = {0, 0};
@@ -293,7 +307,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
     int next_entry = 0;
     Look keep, nxt = cur;
     auto hand_out = [&]() -> bool {
-      if (!mbar_wait_warp(bar(L::bSegEmpty + handed % kSegSlots), ((handed / kSegSlots) & 1) ^ 1, ctl)) return false;
+      if (!wait_warp<kPacked>(bar(L::bSegEmpty + handed % kSegSlots), ((handed / kSegSlots) & 1) ^ 1, ctl)) return false;
       if (lane == 0) {
         segs[handed % kSegSlots] = it;
         mbar_arrive(bar(L::bSegFull + handed % kSegSlots));
@@ -310,7 +324,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || !with[t]) continue;
-        if (!(ok = mbar_wait_warp(bar(L::bQEmpty + t), (qn[t] & 1) ^ 1, ctl))) continue;
+        if (!(ok = wait_warp<kPacked>(bar(L::bQEmpty + t), (qn[t] & 1) ^ 1, ctl))) continue;
         if (lane == 0) {
           mbar_expect_tx(bar(L::bQ + t), q_bytes);
 #pragma unroll
@@ -332,7 +346,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
         if (kTurn && blk == j0 + n_max) blk = j0;
         if (j + 1 < n_max) read_entry(blk);
         const uint32_t sk = gk % NK, sv = gv % NV;
-        if (!(ok = mbar_wait_warp(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
+        if (!(ok = wait_warp<kPacked>(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
         if (lane == 0) mbar_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
         __syncwarp();
         if (lane < nbox) {
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
                         head, pg);
         }
         ++gk;
-        if (!(ok = mbar_wait_warp(bar(L::bVEmpty + sv), ((gv / NV) & 1) ^ 1, ctl))) break;
+        if (!(ok = wait_warp<kPacked>(bar(L::bVEmpty + sv), ((gv / NV) & 1) ^ 1, ctl))) break;
         if (lane == 0) mbar_expect_tx(bar(L::bVFull + sv), L::kTileBytes);
         __syncwarp();
         if (lane < nbox) {
@@ -380,7 +394,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       for (uint32_t g = gv > NV ? gv - NV : 0; g < gv; ++g) drain_wait(bar(L::bVFull + g % NV), (g / NV) & 1);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kMma) {
     // ------------------------------------------------------------------ MMA issue
     constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
     constexpr uint32_t idO = idesc_bf16_f32(128, D, false, true);
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
     };
     auto issue_s = [&](int t, uint32_t g, bool ready) -> bool {
       const uint32_t sk = g % NK;
-      if (!ready && !mbar_wait_warp(bar(L::bKFull + sk), (g / NK) & 1, ctl)) return false;
+      if (!ready && !wait_warp<kPacked>(bar(L::bKFull + sk), (g / NK) & 1, ctl)) return false;
       tc_fence_after();
       const uint64_t a = dQ + (uint32_t)(t * (L::kTileBytes >> 4));
       const uint64_t bk = dK + sk * (uint32_t)(L::kTileBytes >> 4);
@@ -411,9 +425,9 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
     };
     auto issue_pv = [&](int t, uint32_t g, bool first, bool last, bool ready) -> bool {
       const uint32_t sv = g % NV;
-      if (!mbar_wait_warp(bar(L::bPFull + t), pc[t] & 1, ctl)) return false;
-      if (!ready && !mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
-      if (first && qn[t] > 1 && !mbar_wait_warp(bar(L::bOFree + t), (qn[t] - 2) & 1, ctl)) return false;
+      if (!wait_warp<kPacked>(bar(L::bPFull + t), pc[t] & 1, ctl)) return false;
+      if (!ready && !wait_warp<kPacked>(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
+      if (first && qn[t] > 1 && !wait_warp<kPacked>(bar(L::bOFree + t), (qn[t] - 2) & 1, ctl)) return false;
       tc_fence_after();
       const uint64_t bv = dV + sv * (uint32_t)(L::kTileBytes >> 4);
       if (elect_one()) {
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || it.cnt[t] == 0) continue;
-        if (!(ok = mbar_wait_warp(bar(L::bQ + t), qn[t] & 1, ctl))) continue;
+        if (!(ok = wait_warp<kPacked>(bar(L::bQ + t), qn[t] & 1, ctl))) continue;
         ++qn[t];
         tc_fence_after();
         if (it.a[t] < step) {
@@ -484,13 +498,12 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       }
       __syncwarp();
     }
-  } else if (kPacked && warp >= 10) {
+  } else if (kPacked && warp >= 8 && warp < kLoad) {
     // ------------------------------------------------------------------ codes to bf16 keys and values
-    // A thread has two rows of a block: it reads their codes a block ahead (and the page entries another one), and
-    // writes the operands as a bulk copy of a bf16 cache would (128-byte swizzled). Rows that no row of the pair sees
-    // are zero.
+    // A thread has one row of a block: it reads its codes a block ahead (and the page entry another one), and writes the
+    // operands as a bulk copy of a bf16 cache would (128-byte swizzled). Rows that no row of the pair sees are zero.
     constexpr int kQ = D / 32;  // 16-byte pieces of a row's codes, one scale each
-    const int u = threadIdx.x - kTileThreads;  // rows u and u + 64
+    const int row = threadIdx.x - 256;
     uint32_t gk = 0, gv = 0;
     bool ok = true;
     for (uint32_t i = 0; ok; ++i) {
@@ -501,88 +514,78 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       give_back(i);
       if (n_max < 0) break;
       if (n_max == 0) continue;
-      struct Half {  // two rows of K or V
-        uint4 w[2][kQ];
-        uint32_t s[2][kQ / 2];
+      struct Row {  // of K or V
+        uint4 w[kQ];
+        uint32_t s[kQ / 2];
       } kr, vr;
-      int entry[2], page[2];  // of the block after the next, of the next one
-      auto block_at = [&](int j) { return j0 + (j + turn < n_max ? j + turn : j + turn - n_max); };
-      auto read_entries = [&](int j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = block_at(j) * kPairBlk + u + 64 * h;
-          entry[h] = -1;
-          if (j < n_max && key >= lo && key < hi) {
-            entry[h] = tab[key >> b.page_shift];
-            if ((unsigned)entry[h] >= (unsigned)b.num_pages) {
-              record_index_error(b.status);
-              entry[h] = -1;
-            }
+      int entry, page;  // of the block after the next, of the next one
+      auto key_of = [&](int j) { return (j0 + (j + turn < n_max ? j + turn : j + turn - n_max)) * kPairBlk + row; };
+      auto read_entry = [&](int j) {
+        const int key = key_of(j);
+        entry = -1;
+        if (j < n_max && key >= lo && key < hi) {
+          entry = tab[key >> b.page_shift];
+          if ((unsigned)entry >= (unsigned)b.num_pages) {
+            record_index_error(b.status);
+            entry = -1;
           }
         }
       };
-      auto read_rows = [&](Half& x, int j, const uint8_t* codes, const uint8_t* scales, long long c_page, long long c_head,
-                           long long s_page, long long s_head) {
+      auto read_row = [&](Row& x, int j, const uint8_t* codes, const uint8_t* scales, long long c_page, long long c_head,
+                          long long s_page, long long s_head) {
+        const int slot = key_of(j) & (b.page_size - 1);
+        const bool in = page >= 0;
+        const long long pg = in ? page : 0;
+        const uint4* cp = reinterpret_cast<const uint4*>(codes + pg * c_page + head * c_head + slot * code_bytes(D));
+        const uint32_t* scp =
+            reinterpret_cast<const uint32_t*>(scales + pg * s_page + head * s_head + slot * scale_bytes(D));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int slot = (block_at(j) * kPairBlk + u + 64 * h) & (b.page_size - 1);
-          const bool in = page[h] >= 0;
-          const long long pg = in ? page[h] : 0;
-          const uint4* cp = reinterpret_cast<const uint4*>(codes + pg * c_page + head * c_head + slot * code_bytes(D));
-          const uint32_t* scp =
-              reinterpret_cast<const uint32_t*>(scales + pg * s_page + head * s_head + slot * scale_bytes(D));
+        for (int q = 0; q < kQ; ++q) x.w[q] = in ? cp[q] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int q = 0; q < kQ; ++q) x.w[h][q] = in ? cp[q] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int q = 0; q < kQ / 2; ++q) x.s[h][q] = in ? scp[q] : 0u;
-        }
+        for (int q = 0; q < kQ / 2; ++q) x.s[q] = in ? scp[q] : 0u;
       };
-      auto write_rows = [&](const Half& x, uint32_t dst) {
+      auto write_row = [&](const Row& x, uint32_t dst) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = u + 64 * h;
+        for (int q = 0; q < kQ; ++q) {
+          const uint32_t sc = (q & 1) ? x.s[q >> 1] >> 16 : x.s[q >> 1] & 0xffffu;
+          const uint32_t s2 = sc * 0x10001u, cs = scale_shift(s2);
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&x.w[q]);
 #pragma unroll
-          for (int q = 0; q < kQ; ++q) {
-            const uint32_t sc = (q & 1) ? x.s[h][q >> 1] >> 16 : x.s[h][q >> 1] & 0xffffu;
-            const uint32_t s2 = sc * 0x10001u, cs = scale_shift(s2);
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(&x.w[h][q]);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {  // 8 dims: one 16-byte chunk
-              const int ch = 4 * q + y;
-              st_shared_v4(dst + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                           fma_bf16x2(code_pair(w[y], 0), s2, cs), fma_bf16x2(code_pair(w[y], 1), s2, cs),
-                           fma_bf16x2(code_pair(w[y], 2), s2, cs), fma_bf16x2(code_pair(w[y], 3), s2, cs));
-            }
+          for (int y = 0; y < 4; ++y) {  // 8 dims: one 16-byte chunk
+            const int ch = 4 * q + y;
+            st_shared_v4(dst + (ch >> 3) * 16384 + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                         fma_bf16x2(code_pair(w[y], 0), s2, cs), fma_bf16x2(code_pair(w[y], 1), s2, cs),
+                         fma_bf16x2(code_pair(w[y], 2), s2, cs), fma_bf16x2(code_pair(w[y], 3), s2, cs));
           }
         }
         fence_proxy_async_smem();
       };
-      auto read_k = [&](int j) { read_rows(kr, j, cache.k, cache.k_scale, cache.k_page, cache.k_head, cache.ks_page, cache.ks_head); };
-      auto read_v = [&](int j) { read_rows(vr, j, cache.v, cache.v_scale, cache.v_page, cache.v_head, cache.vs_page, cache.vs_head); };
-      read_entries(0);
-      page[0] = entry[0];
-      page[1] = entry[1];
+      auto read_k = [&](int j) { read_row(kr, j, cache.k, cache.k_scale, cache.k_page, cache.k_head, cache.ks_page, cache.ks_head); };
+      auto read_v = [&](int j) { read_row(vr, j, cache.v, cache.v_scale, cache.v_page, cache.v_head, cache.vs_page, cache.vs_head); };
+      read_entry(0);
+      page = entry;
       read_k(0);
       read_v(0);
-      read_entries(1);
+      read_entry(1);
       for (int j = 0; j < n_max; ++j) {
         const uint32_t sk = gk % NK, sv = gv % NV;
-        if (!(ok = mbar_wait_warp(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
-        write_rows(kr, sK + sk * L::kTileBytes);
+        if (!(ok = wait_warp<kPacked>(bar(L::bKEmpty + sk), ((gk / NK) & 1) ^ 1, ctl))) break;
+        write_row(kr, sK + sk * L::kTileBytes);
         mbar_arrive(bar(L::bKFull + sk));
         ++gk;
-        page[0] = entry[0];
-        page[1] = entry[1];
+        page = entry;
         if (j + 1 < n_max) read_k(j + 1);
-        if (!(ok = mbar_wait_warp(bar(L::bVEmpty + sv), ((gv / NV) & 1) ^ 1, ctl))) break;
-        write_rows(vr, sV + sv * L::kTileBytes);
+        if (!(ok = wait_warp<kPacked>(bar(L::bVEmpty + sv), ((gv / NV) & 1) ^ 1, ctl))) break;
+        write_row(vr, sV + sv * L::kTileBytes);
         mbar_arrive(bar(L::bVFull + sv));
         ++gv;
         if (j + 1 < n_max) read_v(j + 1);
-        read_entries(j + 2);
+        read_entry(j + 2);
       }
     }
+  }
   } else {
+    if constexpr (kPacked) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ------------------------------------------------------------------ softmax
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;  // row within the tile
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
         const int past = kvl - kv0, before = min((kHalves ? vlo : pair_lo()) - kv0, kPairBlk);
         if (past >= kPairBlk && before <= 0) return true;
         const uint32_t g = gv0 + a_t + j * step, sv = g % NV;
-        if (!mbar_wait_warp(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
+        if (!wait_warp<kPacked>(bar(L::bVFull + sv), (g / NV) & 1, ctl)) return false;
         auto clear = [&](int row) {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       };
       float m_run = -INFINITY, m_hi = -INFINITY, l_run = 0.f, e_run = 0.f;
       for (int j = 0; j < n_kv; ++j) {
-        if (!mbar_wait_warp(bar(L::bSFull + t), (sc + j) & 1, ctl)) {
+        if (!wait_warp<kPacked>(bar(L::bSFull + t), (sc + j) & 1, ctl)) {
           ok = false;
           break;
         }
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       if (!ok) break;
       // ---------------------------------------------------------------- epilogue
       if (n_kv > 0) {
-        if (!(ok = mbar_wait_warp(bar(L::bOFull + t), on & 1, ctl))) break;
+        if (!(ok = wait_warp<kPacked>(bar(L::bOFull + t), on & 1, ctl))) break;
         ++on;
         sc += n_kv;
         tc_fence_after();
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       const TileSeg e = s;
       give_back(i);  // before the stores: an arrival after them would wait for them
       if (kHalves && owed) {  // this warp's buffer still holds its half of an earlier stretch
-        if (!(ok = mbar_wait_warp(bar(L::bTwinFree), (twins - 1) & 1, ctl))) break;
+        if (!(ok = wait_warp<kPacked>(bar(L::bTwinFree), (twins - 1) & 1, ctl))) break;
         owed = false;
       }
       float4* half = reinterpret_cast<float4*>(smem + L::kHalf) + r;
@@ -752,7 +755,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       }
       float f0 = 1.f, f1 = 0.f;
       if (twin) {
-        if (!(ok = mbar_wait_warp(bar(L::bTwin), twins & 1, ctl))) break;
+        if (!(ok = wait_warp<kPacked>(bar(L::bTwin), twins & 1, ctl))) break;
         ++twins;
         tc_fence_after();
         const float4 h = *half;
@@ -780,6 +783,18 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
           }
         }
       };
+      auto read_chunk = [&](int c, uint32_t (&o)[32]) {  // 32 of them (kPacked: registers that the kernel is not built with
+        tmem_ld32(tO + c * 32, o);                       // cannot be spilled)
+        tmem_ld_wait(o);
+        if (twin) {
+          uint32_t o1[32];
+          tmem_ld32(tO + 128 + c * 32, o1);
+          tmem_ld_wait(o1);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+        }
+      };
       auto o_read = [&]() {  // the accumulators may be overwritten
         tc_fence_before();
         if (n_kv > 0) mbar_arrive(bar(L::bOFree + t));
@@ -793,7 +808,19 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
       } else if (e.first && e.last) {
         const float inv = (l_run > 0.f || l_run != l_run) ? 1.f / (l_run + e_run) : 0.f;  // nothing seen: o = 0
         uint32_t w[D / 2] = {};
-        if (n_kv > 0) {
+        if (kPacked && n_kv > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            read_chunk(c, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])),
+                                    make_float2(inv, inv));
+              w[16 * c + k] = pack_bf16(v.x, v.y);
+            }
+          }
+        } else if (n_kv > 0) {
           uint32_t o[D / 32][32];
           read_o(o);
 #pragma unroll
@@ -843,7 +870,17 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
         }
       } else {
         float* slot = p.tile_part + (size_t)(2 * blockIdx.x + (e.first ? 1 : 0)) * tile_part(D) + t * kTile * (D + 3);
-        if (n_kv > 0) {
+        if (kPacked && n_kv > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            read_chunk(c, o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(slot + ((8 * c + k) * kTile + r) * 4) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        } else if (n_kv > 0) {
           uint32_t o[D / 32][32];
           read_o(o);
 #pragma unroll
@@ -863,7 +900,7 @@ __global__ void __launch_bounds__(kPacked ? kTileThreads + kUnpackThreads : kTil
   if (kBoxOut && warp < 8 && lane == 0) bulk_wait_read_all();  // before the CTA gives its shared memory up
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTileTmemCols);
   }
@@ -878,7 +915,7 @@ static cudaError_t launch_tiles(const TileMaps& m, const PagedFwd& p, const Page
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_tiles_kernel<D, kTurn, kPacked>), smem, known);
   if (e != cudaSuccess) return e;
   fa_paged_tiles_kernel<D, kTurn, kPacked>
-      <<<num_sms, kPacked ? kTileThreads + kUnpackThreads : kTileThreads, smem, st>>>(m.q, m.k, m.v, m.o, p, cache);
+      <<<num_sms, kPacked ? kPackedThreads : kTileThreads, smem, st>>>(m.q, m.k, m.v, m.o, p, cache);
   return cudaGetLastError();
 }
 

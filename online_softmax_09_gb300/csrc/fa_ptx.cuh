@@ -63,7 +63,7 @@ struct Ctl {
   uint32_t* status;      // global, per device
 };
 
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl ctl) {
+__device__ __forceinline__ bool mbar_wait_loop(uint32_t bar, uint32_t parity, Ctl ctl) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -74,6 +74,9 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
       return false;
     }
   }
+}
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, Ctl ctl) {
+  return mbar_wait_loop(bar, parity, ctl);
 }
 
 // Single-thread wait (producer / MMA roles).
