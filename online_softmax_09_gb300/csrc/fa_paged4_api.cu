@@ -48,12 +48,12 @@ fa::PagedCache4 device_cache4(const fa_paged_cache4* c) {
 // Where a batch has both kinds of tiles: a unit of 64 keys is a quarter of a bf16 cache's bytes.
 float row4_cost(int d) { return d == 64 ? 0.18f : 0.15f; }
 
-// Strides (page, head) in elements of fp32 weights; `distinct`: they are written.
+// Strides (page, head) in elements of fp32 weights, the page's below 2^32; `distinct`: they are written.
 int check_weights(const float* w, const long long* s, int pages, int heads, bool distinct) {
   FA_TRY(check_ptr(w, 4));
   const long long extent[2] = {pages, heads};
   for (int i = 0; i < 2; ++i)
-    if (extent[i] > 1 && (s[i] < (distinct ? 1 : 0) || s[i] > (1LL << 46))) return FA_ERR_INVALID;
+    if (extent[i] > 1 && (s[i] < (distinct ? 1 : 0) || s[i] > (i == 0 ? 0xffffffffLL : 1LL << 46))) return FA_ERR_INVALID;
   return FA_OK;
 }
 

@@ -9,6 +9,7 @@
 // dims a step of the product takes is free as long as keys and queries agree, so a lane's 16-byte loads are its operands.
 // The queries go by as columns, 8 at a time. CTAs take blocks by their sequences' share of the plan's units.
 #include <math.h>
+#include <type_traits>
 
 #include "fa_paged_evict.cuh"
 #include "fa_paged_join.cuh"
@@ -16,17 +17,26 @@
 namespace fa {
 
 constexpr int kWeightThreads = 128;
-constexpr int kWeightKeys = 32;   // of a warp
-constexpr int kWeightBlk = kWeightThreads / 32 * kWeightKeys;
-constexpr int kWeightCtas = 4;    // per SM
+// Granules of 16 keys that a warp holds (64 registers of operands), and CTAs per SM (with four at d = 128 some of the loop's
+// values stand in local memory: 106 us for the decode step of 64 sequences of 200 to 8192 keys, 95 with three).
+__host__ __device__ constexpr int weight_grans(int D) { return D == 128 ? 2 : 4; }
+__host__ __device__ constexpr int weight_ctas(int D) { return 3 + 0 * D; }
 constexpr long long kPairShare = 16;  // a unit of the plan's pairs (256 rows of 128 keys), in units of its small tiles
 
+// a / b of numbers that are rarely beyond 32 bits (in 64 bits the division takes over a hundred instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 template <int D, bool kPacked>
-__global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_kernel(const PagedWeights p) {
+__global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
+    fa_paged_weights_kernel(const PagedWeights p) {
+  constexpr int kT = weight_grans(D), kKeys = 16 * kT, kBlk = kWeightThreads / 32 * kKeys;
+  constexpr bool kEarly = D == 64;  // the next queries are loaded beside the products (at d = 128 there is no room for them)
   const PagedBatch& b = p.b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   auto start = [&](long long s) { return b.plan.units[0][s] + kPairShare * b.plan.units[1][s]; };
-  const long long W = start(b.S), per = (W + gridDim.x - 1) / gridDim.x;
+  const long long W = start(b.S), per = quotient(W + gridDim.x - 1, gridDim.x);
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
     return;
@@ -42,82 +52,158 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
     hi = min(hi, seq + step);
   }
   const unsigned G = b.G;
-  const int q8 = (int)(8 / G), r8 = (int)(8 % G);  // 8 rows on: tokens and heads
+  // 8 rows on: tokens and heads, and what that moves a query's and a sum's place by (one more token: `wrap`).
+  const int q8 = (int)(8 / G), r8 = (int)(8 % G);
+  const int tok0[3] = {(int)(g / G), (int)(2 * c / G), (int)((2 * c + 1) / G)};  // tokens of the first rows
+  const long long q_on = q8 * p.q_tok + r8 * p.q_head, q_wrap = p.q_tok - (long long)G * p.q_head;
+  const int l_on = q8 * b.Hq + r8, l_wrap = b.Hq - (int)G;
   for (bool begin = true; seq < b.S; ++seq, begin = false) {
     const long long base = start(seq);
     if (base >= u_end) break;
-    const long long per_head = (start(seq + 1) - base) / b.Hkv;
+    const long long per_head = quotient(start(seq + 1) - base, b.Hkv);
     const PlanSeq ps = b.plan.seq[seq];
     if (per_head <= 0 || ps.ql <= 0) continue;
     int lo, hi;  // keys that some new token sees
     key_range(0, ps.ql - 1, ps.ql, ps.kvl, b.causal, b.window, lo, hi);
-    if (b.causal) hi = min(hi, ps.kvl);
+    hi = min(hi, ps.kvl);
     if (hi <= lo) continue;
-    const int blk0 = lo / kWeightBlk, nblk = (hi - 1) / kWeightBlk - blk0 + 1;
+    const int blk0 = lo / kBlk, nblk = (hi - 1) / kBlk - blk0 + 1;
     const int first_new = ps.kvl - ps.ql, rows_all = ps.ql * (int)G;
+    const bool few = rows_all <= 8;  // one tile of queries, held from block to block
     const int* tab = b.table + (long long)seq * b.table_stride;
     int head = 0;
-    long long k = 0;
+    int k = 0;
     if (begin && u > base) {  // block k of a head begins at unit floor(k per_head / nblk) of it
-      head = (int)((u - base) / per_head);
+      head = (int)quotient(u - base, per_head);
       const long long off = u - base - head * per_head;
-      k = (off * nblk + per_head - 1) / per_head;
+      k = (int)quotient(off * nblk + per_head - 1, per_head);
       if (k == nblk) {
         ++head;
         k = 0;
       }
     }
-    for (; head < b.Hkv; ++head, k = 0) {
-      for (; k < nblk; ++k) {
-        if (base + head * per_head + k * per_head / nblk >= u_end) return;
-        const int key0 = (blk0 + (int)k) * kWeightBlk + warp * kWeightKeys;
-        if (key0 >= hi || key0 + kWeightKeys <= lo) continue;
-        // ---- keys g, g + 8 of both halves as A operands
-        int page[2];
-        uint32_t a[2][D / 16][4];
+    // Table entries of a warp's granules of 16 keys, -1 for those that no token sees.
+    auto entries = [&](int key0, int (&page)[kT]) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int at = key0 + 16 * t;
-          page[t] = -1;
-          if (at < hi && at + 16 > lo) {
-            page[t] = tab[at >> b.page_shift];
-            if ((unsigned)page[t] >= (unsigned)b.num_pages) {
-              record_index_error(b.status);
-              page[t] = -1;
-            }
+      for (int t = 0; t < kT; ++t) {
+        const int at = key0 + 16 * t;
+        page[t] = at < hi && at + 16 > lo ? tab[at >> b.page_shift] : -1;
+      }
+    };
+    for (; head < b.Hkv; ++head, k = 0) {
+      // The queries that stand from row r on: row r + g as a column of the product, and rows r + 2 c, r + 2 c + 1 as sums.
+      struct Queries {
+        uint4 q[D / 32];
+        float z[2];
+      } now;
+      const __nv_bfloat16* qp = nullptr;
+      const float* zp[2];
+      int tok[3], hd[3];
+      auto set_rows = [&](unsigned r) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const unsigned rr = r + (i == 0 ? g : 2 * c + i - 1);
+          tok[i] = r == 0 ? tok0[i] : (int)(rr / G);
+          hd[i] = (int)(rr - tok[i] * G);
+        }
+        qp = p.q + (long long)(ps.q0 + tok[0]) * p.q_tok + ((long long)head * G + hd[0]) * p.q_head +
+             c * (kPacked ? D / 4 : 8);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          zp[e] = p.lse + (long long)(ps.q0 + tok[1 + e]) * b.Hq + head * (int)G + hd[1 + e];
+      };
+      auto load_rows = [&](Queries& x, bool every) {  // every: no row is past the last
+        const bool q_in = every || tok[0] < ps.ql;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          x.q[i] = q_in ? *reinterpret_cast<const uint4*>(qp + (kPacked ? 8 * i : 32 * i)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) x.z[e] = every || tok[1 + e] < ps.ql ? *zp[e] : -INFINITY;
+      };
+      auto next_rows = [&]() {
+        qp += q_on;
+        zp[0] += l_on;
+        zp[1] += l_on;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) tok[i] += q8;
+        if (r8 == 0) return;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          hd[i] += r8;
+          if (hd[i] >= (int)G) {
+            hd[i] -= (int)G;
+            ++tok[i];
+            if (i == 0) qp += q_wrap;
+            else zp[i - 1] += l_wrap;
           }
         }
+      };
+      // This lane's place in a key (and its scale's), and of keys g of each granule.
+      const long long k_tok = kPacked ? code_bytes(D) : p.c.k_tok * 2, k_page = kPacked ? p.c4.k_page : p.c.k_page * 2;
+      const uint8_t* k_head = kPacked ? p.c4.k + head * p.c4.k_head
+                                      : reinterpret_cast<const uint8_t*>(p.c.k + head * p.c.k_head);
+      const uint8_t* k_lane = k_head + c * (kPacked ? D / 8 : 16) + g * k_tok;
+      const uint8_t* s_lane =
+          kPacked ? p.c4.k_scale + head * p.c4.ks_head + g * scale_bytes(D) + c * (D / 4) / kGroup4 * 2 : nullptr;
+      float* out_lane = p.out + head * p.out_head;
+      const float* old_lane = p.old + head * p.old_head;
+      int page[kT], page_next[kT];
+      {
+        const int key0 = (blk0 + k) * kBlk + warp * kKeys;
+        entries(key0, page);
+        entries(key0 + kBlk, page_next);
+      }
+      if (few) {
+        set_rows(0);
+        load_rows(now, false);
+      }
+      const long long left = u_end - base - head * per_head;  // units of the head that are this CTA's
+      if (left <= 0) return;
+      const int k_end = left >= per_head ? nblk : (int)quotient(left * nblk + per_head - 1, per_head);
+      for (; k < k_end; ++k) {
+        const int key0 = (blk0 + k) * kBlk + warp * kKeys;
+        bool whole = key0 >= lo && key0 + kKeys <= hi;  // every key of the unit is seen
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kT; ++t) {
+          if (page[t] >= b.num_pages || page[t] < -1) {
+            record_index_error(b.status);
+            page[t] = -1;
+          }
+          whole = whole && page[t] >= 0;
+        }
+        // ---- keys g, g + 8 of each granule as A operands
+        uint32_t a[kT][D / 16][4];
+        auto read = [&](int t, auto all) {
+          const int at = key0 + 16 * t, slot = at & (b.page_size - 1);
+          const long long pg = decltype(all)::value || page[t] >= 0 ? page[t] : 0;
+          const uint8_t* row = k_lane + (kPacked ? (uint64_t)(uint32_t)pg * (uint32_t)k_page : (uint64_t)(pg * k_page)) +
+                               slot * k_tok;
+          [[maybe_unused]] const uint8_t* scale =
+              s_lane + (kPacked ? (uint64_t)(uint32_t)pg * (uint32_t)p.c4.ks_page + slot * scale_bytes(D) : 0);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = key0 + 16 * t + 8 * h + g;
-            const int slot = key & (b.page_size - 1);
-            const bool in = page[t] >= 0 && key >= lo && key < hi;
+          for (int h = 0; h < 2; ++h, row += 8 * k_tok) {
+            const int key = at + 8 * h + g;
+            const bool in = decltype(all)::value || (page[t] >= 0 && key >= lo && key < hi);
             if constexpr (kPacked) {
-              const uint8_t* kp = p.c4.k + (long long)page[t] * p.c4.k_page + head * p.c4.k_head + slot * code_bytes(D) + c * (D / 8);
-              const uint8_t* sp = p.c4.k_scale + (long long)page[t] * p.c4.ks_page + head * p.c4.ks_head +
-                                  slot * scale_bytes(D) + c * (D / 4) / kGroup4 * 2;
               uint32_t w[D / 32];
               if constexpr (D == 128) {
-                const uint4 v = in ? *reinterpret_cast<const uint4*>(kp) : make_uint4(0, 0, 0, 0);
+                const uint4 v = in ? *reinterpret_cast<const uint4*>(row) : make_uint4(0, 0, 0, 0);
                 w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
               } else {
-                const uint2 v = in ? *reinterpret_cast<const uint2*>(kp) : make_uint2(0, 0);
+                const uint2 v = in ? *reinterpret_cast<const uint2*>(row) : make_uint2(0, 0);
                 w[0] = v.x, w[1] = v.y;
               }
-              const uint32_t s2 = in ? *reinterpret_cast<const uint16_t*>(sp) * 0x10001u : 0u, cs = scale_shift(s2);
+              const uint32_t s2 = in ? *reinterpret_cast<const uint16_t*>(scale + 8 * h * scale_bytes(D)) * 0x10001u : 0u;
+              const uint32_t cs = scale_shift(s2);
 #pragma unroll
               for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                   a[t][i][2 * e + h] = fma_bf16x2(code_pair(w[i >> 1], 2 * (i & 1) + e), s2, cs);
             } else {
-              const uint4* kp = reinterpret_cast<const uint4*>(p.c.k + (long long)page[t] * p.c.k_page +
-                                                               head * p.c.k_head + (in ? slot : 0) * p.c.k_tok) + c;
 #pragma unroll
               for (int i = 0; i < D / 32; ++i) {
-                const uint4 v = in ? kp[4 * i] : make_uint4(0, 0, 0, 0);
+                const uint4 v = in ? *reinterpret_cast<const uint4*>(row + 64 * i) : make_uint4(0, 0, 0, 0);
                 a[t][2 * i][h] = v.x;
                 a[t][2 * i][2 + h] = v.y;
                 a[t][2 * i + 1][h] = v.z;
@@ -125,86 +211,128 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
               }
             }
           }
-        // This lane's key for the sum: (half c / 2, + 8 for odd c, g).
-        const int my = key0 + 8 * c + g, my_page = c < 2 ? page[0] : page[1];
-        const bool mine = my_page >= 0 && my >= lo && my < hi;
-        const long long my_slot = my & (b.page_size - 1);
-        float old = 0.f;
-        if (mine && my < first_new && p.old != p.out)
-          old = p.old[(long long)my_page * p.old_page + head * p.old_head + my_slot];
+        };
+        if (__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+          for (int t = 0; t < kT; ++t) read(t, std::true_type());
+        } else {
+#pragma unroll
+          for (int t = 0; t < kT; ++t) read(t, std::false_type());
+        }
+        // This lane's keys for the sums: number c + 4 y of (granule, first or second eight), of those the g-th.
+        float old[kT / 2];
+        float* out[kT / 2];
+        bool adds[kT / 2];
+#pragma unroll
+        for (int y = 0; y < kT / 2; ++y) {
+          const int my = key0 + 32 * y + 8 * c + g, pg = c < 2 ? page[2 * y] : page[2 * y + 1];
+          const unsigned slot = my & (b.page_size - 1);
+          const bool mine = pg >= 0 && my >= lo && my < hi, was = my < first_new;
+          out[y] = mine ? out_lane + (uint64_t)(uint32_t)pg * (uint32_t)p.out_page + slot : nullptr;
+          adds[y] = was && p.old == p.out;  // (pages may be shared by sequences)
+          old[y] = mine && was && !adds[y] ? old_lane[(uint64_t)(uint32_t)pg * (uint32_t)p.old_page + slot] : 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < kT; ++t) page[t] = page_next[t];
+        // The next block's keys on their way into L2: lane i brings key i.
+        if (!kPacked && k + 1 < nblk) {
+#pragma unroll
+          for (int y = 0; y < kT / 2; ++y) {
+          const int key = key0 + kBlk + 32 * y + lane, pg = lane < 16 ? page[2 * y] : page[2 * y + 1];
+          if (pg >= 0 && pg < b.num_pages && key < hi) {
+            const uint8_t* at = k_head + (long long)pg * k_page + (long long)(key & (b.page_size - 1)) * k_tok;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
+          }
+          }
+        }
+        entries(key0 + 2 * kBlk, page_next);
         // ---- rows [r, r_end) that may see them
-        long long r = 0, r_end = rows_all;
-        if (b.causal) {
-          r = max(0, key0 - first_new) * (long long)G & ~7LL;
-          if (b.window > 0) {
-            const long long past = (long long)key0 + kWeightKeys - 1 + b.window - first_new;  // tokens from here on do not
-            r_end = min(r_end, max(past, 0LL) * G);
-          }
-        }
-        float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-        int tok[3], hd[3];  // of row r + g (as a column of queries), and of rows r + 2 c, r + 2 c + 1
+        float sum[kT][2];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const unsigned rr = (unsigned)r + (i == 0 ? g : 2 * c + i - 1);
-          tok[i] = (int)(rr / G);
-          hd[i] = (int)(rr - tok[i] * G);
-        }
-        for (; r < r_end; r += 8) {
-          const __nv_bfloat16* qp = p.q + (long long)(ps.q0 + tok[0]) * p.q_tok + ((long long)head * G + hd[0]) * p.q_head;
-          const bool q_in = tok[0] < ps.ql;
-          uint4 qv[D / 32];
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            qv[i] = q_in ? *reinterpret_cast<const uint4*>(qp + (kPacked ? c * (D / 4) + 8 * i : 8 * (c + 4 * i)))
-                         : make_uint4(0, 0, 0, 0);
-          float l2[2];
-          int klim[2], klo[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool in = tok[1 + e] < ps.ql;
-            const float z = in ? p.lse[(long long)(ps.q0 + tok[1 + e]) * b.Hq + head * G + hd[1 + e]] : 0.f;
-            l2[e] = z == -INFINITY ? INFINITY : z * 1.4426950408889634f;  // a row that sees nothing gives nothing
-            const int pos = first_new + tok[1 + e];
-            klim[e] = !in ? -1 : (b.causal ? min(pos, ps.kvl - 1) : ps.kvl - 1);
-            klo[e] = mask_from(pos, b.window);
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              mma16816(x, a[t][2 * i], qv[i].x, qv[i].y);
-              mma16816(x, a[t][2 * i + 1], qv[i].z, qv[i].w);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + 16 * t + 8 * (e >> 1) + g;
-              const float w = ex2(fmaf(x[e], p.scale_log2, -l2[e & 1]));
-              sum[t][e >> 1] += key <= klim[e & 1] && key >= klo[e & 1] ? w : 0.f;
+        for (int t = 0; t < kT; ++t) sum[t][0] = sum[t][1] = 0.f;
+        if (key0 < hi && key0 + kKeys > lo) {
+          long long r = 0, r_end = rows_all;
+          if (b.causal && !few) {
+            r = max(0, key0 - first_new) * (long long)G & ~7LL;
+            if (b.window > 0) {
+              const long long past = (long long)key0 + kKeys - 1 + b.window - first_new;  // tokens from here on do not
+              r_end = min(r_end, max(past, 0LL) * G);
             }
           }
+          // Rows from `full` to `full_end` see every key of the unit.
+          const long long full = b.causal ? (long long)max(0, key0 + kKeys - 1 - first_new) * G
+                                          : (key0 + kKeys <= ps.kvl ? 0 : rows_all);
+          const long long full_end = b.window > 0 ? max(0LL, ((long long)key0 + b.window - first_new) * G) : rows_all;
+          if (!few && r < r_end) {
+            set_rows((unsigned)r);
+            if (kEarly) load_rows(now, false);
+          }
+          for (; r < r_end; r += 8) {
+            if (!few && !kEarly) load_rows(now, r + 8 <= rows_all);
+            const int at0 = tok[1], at1 = tok[2];
+            const bool masked = r < full || min(r + 8, (long long)rows_all) > full_end;
+            float l2[2];
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            tok[i] += q8;
-            hd[i] += r8;
-            if (hd[i] >= (int)G) {
-              hd[i] -= (int)G;
-              ++tok[i];
+            for (int e = 0; e < 2; ++e)  // nothing seen: nothing given
+              l2[e] = now.z[e] == -INFINITY ? INFINITY : now.z[e] * 1.4426950408889634f;
+            Queries next;
+            if (!few) next_rows();
+            if (kEarly) {
+              next = now;
+              if (!few && r + 8 < r_end) load_rows(next, r + 16 <= rows_all);
             }
+            auto add = [&](auto some) {
+              int klim[2], klo[2];
+              if (decltype(some)::value) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int pos = first_new + (e == 0 ? at0 : at1);
+                  klim[e] = b.causal ? min(pos, ps.kvl - 1) : ps.kvl - 1;
+                  klo[e] = mask_from(pos, b.window);
+                }
+              }
+              float x[kT][4];
+#pragma unroll
+              for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)  // (the granules' products take turns, not each its own sum's steps)
+#pragma unroll
+                for (int t = 0; t < kT; ++t)
+                  mma16816(x[t], a[t][i], (i & 1) ? now.q[i >> 1].z : now.q[i >> 1].x,
+                           (i & 1) ? now.q[i >> 1].w : now.q[i >> 1].y);
+#pragma unroll
+              for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float w = ex2(fmaf(x[t][e], p.scale_log2, -l2[e & 1]));
+                  if (decltype(some)::value) {
+                    const int key = key0 + 16 * t + 8 * (e >> 1) + g;
+                    w = key <= klim[e & 1] && key >= klo[e & 1] && l2[e & 1] != INFINITY ? w : 0.f;
+                  }
+                  sum[t][e >> 1] += w;
+                }
+            };
+            if (masked) add(std::true_type());
+            else add(std::false_type());
+            if (kEarly) now = next;
           }
         }
-        float total = 0.f;
+        float total[kT / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * kT; ++i) {
           float v = sum[i >> 1][i & 1];
           v += __shfl_xor_sync(0xffffffffu, v, 1);
           v += __shfl_xor_sync(0xffffffffu, v, 2);
-          if (i == c) total = v;
+          if ((i & 3) == c) total[i >> 2] = v;
         }
-        if (mine) {
-          float* out = p.out + (long long)my_page * p.out_page + head * p.out_head + my_slot;
-          if (p.old == p.out && my < first_new) atomicAdd(out, total);  // (pages may be shared by sequences)
-          else *out = old + total;
+#pragma unroll
+        for (int y = 0; y < kT / 2; ++y) {
+          if (out[y] == nullptr) continue;
+          if (adds[y]) atomicAdd(out[y], total[y]);
+          else *out[y] = old[y] + total[y];
         }
       }
     }
@@ -212,7 +340,7 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
 }
 
 cudaError_t launch_paged_weights(const PagedWeights& p, int d, bool packed, int num_sms, cudaStream_t st) {
-  const int grid = kWeightCtas * num_sms;
+  const int grid = weight_ctas(d) * num_sms;
   if (d == 128) {
     if (packed) fa_paged_weights_kernel<128, true><<<grid, kWeightThreads, 0, st>>>(p);
     else fa_paged_weights_kernel<128, false><<<grid, kWeightThreads, 0, st>>>(p);
