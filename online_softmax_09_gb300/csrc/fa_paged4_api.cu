@@ -266,7 +266,7 @@ int fa_paged_evict(const float* weights, const long long* weight_strides, const 
       (long long)out_pages * batch->page_size < max_keep)
     return FA_ERR_INVALID;
   const long long heads = (long long)batch->S * batch->Hkv;
-  if (heads > 0x7fffffffLL || heads * (max_keep / 32 + 1) > 0x7fffffffLL) return FA_ERR_INVALID;
+  if (heads * 8 > 0x7fffffffLL || heads * (max_keep / 32 + 1) > 0x7fffffffLL) return FA_ERR_INVALID;
   for (int i = 0; i < n_rows; ++i) {
     FA_TRY(check_ptr(rows[i].base, 1));
     if (rows[i].bytes < 1 || rows[i].bytes > (1 << 20)) return FA_ERR_INVALID;
@@ -284,7 +284,8 @@ int fa_paged_evict(const float* weights, const long long* weight_strides, const 
     FA_TRY(check_ptr(kept, 4));
   }
   uint32_t* status = nullptr;
-  FA_TRY(fa::device_state(&status, nullptr));
+  int num_sms = 0;
+  FA_TRY(fa::device_state(&status, &num_sms));
   fa::PagedEvict p = {};
   p.b = device_batch(batch, num_pages, status);
   p.weights = weights;
@@ -302,7 +303,7 @@ int fa_paged_evict(const float* weights, const long long* weight_strides, const 
   p.out_stride = out_stride;
   p.kept = kept;
   p.kv_len_out = kv_len_out;
-  return fa::launch_paged_evict(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return fa::launch_paged_evict(p, num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

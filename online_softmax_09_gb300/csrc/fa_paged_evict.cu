@@ -4,20 +4,23 @@
 // room, the first before the last), and of those between, the heaviest; among equal weights those at lower places. They keep
 // their order. A NaN counts as the heaviest.
 //
-// fa_paged_select_kernel, one CTA per sequence and head: the m-th largest weight by its digits (11, 11 and 10 bits of an
+// fa_paged_select_kernel, one to eight CTAs per sequence and head: the m-th largest weight by its digits (11, 11 and 10 bits of an
 // unsigned number in the weights' order, a histogram each), then two passes in order of place, one that counts and one that
 // writes the places kept, each warp over a stretch of its own. Weights that fit stay in shared memory between the passes.
 // fa_paged_move_kernel: a CTA moves 32 slots of one head, all tensors. The pages written are others than those read, so
 // the slots move independently, and pages that sequences share stay as they are.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "fa_paged_evict.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace fa {
 
 constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kSelectMost = 48 * 1024;  // weights held in shared memory
+constexpr int kSelectMost = 44 * 1024;  // weights held in shared memory
 constexpr int kMoveSlots = 32, kMoveThreads = 256;
 
 // What of a sequence's n tokens stays: places [0, a), [b, n), and m of those between.
@@ -46,68 +49,95 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
+// A cluster of CTAs per sequence and head, each with a stretch of the places of its own: the histograms and counts of all are
+// added up through distributed shared memory.
 __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const PagedEvict p, int held) {
   extern __shared__ __align__(16) uint32_t cache[];
-  __shared__ uint32_t bins[kBins];
+  __shared__ __align__(16) uint32_t bins[3][kBins];  // of each pass, so that no pass waits for the others' reading of the one before
   __shared__ uint32_t warp_sum[kSelectWarps];
   __shared__ uint32_t above_w[kSelectWarps], level_w[kSelectWarps];
-  __shared__ uint32_t found[2];  // the digit, and how many of its numbers stay
+  __shared__ __align__(8) uint32_t counts[2];  // of this CTA: numbers above the bound, and at it
+  __shared__ uint32_t found[2];   // the digit, and how many of its numbers stay
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const PagedBatch& b = p.b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int item = (int)(blockIdx.x / C), seq = item / b.Hkv, head = item - seq * b.Hkv;
+  const Split s = split_of(p, seq);  // (its loads and the check of the plan go out together)
   if (!plan_matches(b, b.d)) {
     if (tid == 0) record_index_error(b.status);
     return;
   }
-  const int seq = blockIdx.x / b.Hkv, head = blockIdx.x - seq * b.Hkv;
-  const Split s = split_of(p, seq);
-  int* kept = p.kept + (long long)blockIdx.x * p.max_keep;
-  if (head == 0 && tid == 0) p.kv_len_out[seq] = s.fresh;
-  for (int i = s.fresh + tid; i < p.max_keep; i += kSelectThreads) kept[i] = -1;
+  int* kept = p.kept + (long long)item * p.max_keep;
+  const int all = C * kSelectThreads, at = rank * kSelectThreads + tid;
+  if (head == 0 && at == 0) p.kv_len_out[seq] = s.fresh;
+  for (int i = s.fresh + at; i < p.max_keep; i += all) kept[i] = -1;
   if (s.m == s.b - s.a) {  // all stay
-    for (int i = tid; i < s.fresh; i += kSelectThreads) kept[i] = i;
+    for (int i = at; i < s.fresh; i += all) kept[i] = i;
     return;
   }
-  for (int i = tid; i < s.a; i += kSelectThreads) kept[i] = i;
-  for (int i = tid; i < s.n - s.b; i += kSelectThreads) kept[s.a + s.m + i] = s.b + i;
+  for (int i = at; i < s.a; i += all) kept[i] = i;
+  for (int i = at; i < s.n - s.b; i += all) kept[s.a + s.m + i] = s.b + i;
   if (s.m == 0) return;
   const int* tab = b.table + (long long)seq * b.table_stride;
   const float* w = p.weights + (long long)head * p.w_head;
-  const int n = s.b - s.a;
+  const int each = ((s.b - s.a + C - 1) / C + 31) & ~31;  // places of a CTA: those from s.a + rank * each on
+  const int a0 = s.a + min(rank * each, s.b - s.a), n = min(each, s.b - a0);
   const bool hold = n <= held;
   auto read = [&](int i) -> uint32_t {
-    const int key = s.a + i, page = tab[key >> b.page_shift];
+    const int key = a0 + i, page = tab[key >> b.page_shift];
     if ((unsigned)page >= (unsigned)b.num_pages) {
       record_index_error(b.status);
       return 0;
     }
     return order_of(w[(long long)page * p.w_page + (key & (b.page_size - 1))]);
   };
+  for (int i = tid; i < 3 * kBins; i += kSelectThreads) bins[0][i] = 0;
+  __syncthreads();
   uint32_t prefix = 0, mask = 0, left = (uint32_t)s.m;  // numbers whose bits under `mask` are `prefix`
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t digit = pass == 2 ? 1023 : 2047;
-    for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
-    __syncthreads();
+    if (hold && pass > 0) {
 #pragma unroll 4
-    for (int i = tid; i < n; i += kSelectThreads) {
-      uint32_t x;
-      if (hold && pass > 0) {
-        x = cache[i];
-      } else {
-        x = read(i);
-        if (hold) cache[i] = x;
+      for (int i = tid; i < n; i += kSelectThreads) {
+        const uint32_t x = cache[i];
+        if ((x & mask) == prefix) atomicAdd(&bins[pass][(x >> shift) & digit], 1u);
       }
-      if ((x & mask) == prefix) atomicAdd(&bins[(x >> shift) & digit], 1u);
-    }
-    __syncthreads();
-    // Numbers with a larger digit, for each: thread t has digits 2047 - 4 t and the three below.
-    uint32_t v[4], sum = 0;
+    } else {
+      constexpr int kAtOnce = 8;  // loads that go out together
+      for (int i0 = tid; i0 < n; i0 += kAtOnce * kSelectThreads) {
+        uint32_t x[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = bins[kBins - 1 - 4 * tid - i];
-      sum += v[i];
+        for (int y = 0; y < kAtOnce; ++y) x[y] = i0 + y * kSelectThreads < n ? read(i0 + y * kSelectThreads) : 0;
+#pragma unroll
+        for (int y = 0; y < kAtOnce; ++y) {
+          const int i = i0 + y * kSelectThreads;
+          if (i >= n) continue;
+          if (hold) cache[i] = x[y];
+          if ((x[y] & mask) == prefix) atomicAdd(&bins[pass][(x[y] >> shift) & digit], 1u);
+        }
+      }
     }
+    cluster.sync();
+    // Numbers with a larger digit, for each: thread t has digits 2047 - 4 t and the three below.
+    uint32_t v[4] = {0, 0, 0, 0}, sum = 0;
+    uint4 h[8];  // all CTAs' at once: a read from another SM takes about a microsecond
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      h[c] = c < C ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&bins[pass][kBins - 4 - 4 * tid], c))
+                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      v[0] += h[c].w;
+      v[1] += h[c].z;
+      v[2] += h[c].y;
+      v[3] += h[c].x;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += v[i];
     uint32_t x = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -133,7 +163,8 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     __syncthreads();
   }
   // prefix is the m-th largest number; of those equal to it the first `left` stay.
-  const int each = (n + kSelectWarps - 1) / kSelectWarps, from = min(n, warp * each), to = min(n, from + each);
+  const int each_w = ((n + kSelectWarps - 1) / kSelectWarps + 31) & ~31, from = min(n, warp * each_w),
+            to = min(n, from + each_w);
   uint32_t above = 0, level = 0;
   for (int i0 = from; i0 < to; i0 += 32) {
     const int i = i0 + lane;
@@ -146,7 +177,20 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     level_w[warp] = level;
   }
   __syncthreads();
+  if (tid < 2) {
+    uint32_t x = 0;
+    for (int i = 0; i < kSelectWarps; ++i) x += tid == 0 ? above_w[i] : level_w[i];
+    counts[tid] = x;
+  }
+  cluster.sync();
   uint32_t at_above = 0, at_level = 0;  // before this lane's place
+#pragma unroll
+  for (int c = 0; c < 7; ++c) {
+    if (c >= rank) continue;
+    const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(counts, c));
+    at_above += x.x;
+    at_level += x.y;
+  }
   for (int i = 0; i < warp; ++i) {
     at_above += above_w[i];
     at_level += level_w[i];
@@ -158,21 +202,22 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     const bool is_above = i < to && x > prefix, is_level = i < to && x == prefix;
     const uint32_t ma = __ballot_sync(0xffffffffu, is_above), ml = __ballot_sync(0xffffffffu, is_level);
     const uint32_t na = at_above + __popc(ma & under), nl = at_level + __popc(ml & under);
-    if (is_above || (is_level && nl < left)) kept[s.a + na + min(nl, left)] = s.a + i;
+    if (is_above || (is_level && nl < left)) kept[s.a + na + min(nl, left)] = a0 + i;
     at_above += __popc(ma);
     at_level += __popc(ml);
   }
+  cluster.sync();  // (until the others have read the counts)
 }
 
 __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const PagedEvict p) {
   __shared__ int page_s[kMoveSlots], slot_s[kMoveSlots], to_s[kMoveSlots];  // a page below 0: nothing to move
   const PagedBatch& b = p.b;
-  if (!plan_matches(b, b.d)) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the places are known
   const unsigned chunks = (p.max_keep + kMoveSlots - 1) / kMoveSlots, row = blockIdx.x / chunks;
   const int seq = (int)(row / b.Hkv), head = (int)(row - seq * b.Hkv), tid = threadIdx.x;
   const int i0 = (int)(blockIdx.x - row * chunks) * kMoveSlots;
   const int n = min(kMoveSlots, split_of(p, seq).fresh - i0);
-  if (n <= 0) return;
+  if (n <= 0 || !plan_matches(b, b.d)) return;
   if (tid < n) {
     const int i = i0 + tid, key = p.kept[((long long)seq * b.Hkv + head) * p.max_keep + i];
     int page = b.table[(long long)seq * b.table_stride + (key >> b.page_shift)];
@@ -220,19 +265,36 @@ __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const Paged
   }
 }
 
-cudaError_t launch_paged_evict(const PagedEvict& p, cudaStream_t st) {
-  if ((long long)(p.max_keep / kMoveSlots + 1) * p.b.Hkv * p.b.S > 0x7fffffffLL) return cudaErrorInvalidValue;
+cudaError_t launch_paged_evict(const PagedEvict& p, int num_sms, cudaStream_t st) {
+  const long long items = (long long)p.b.S * p.b.Hkv, chunks = (p.max_keep + kMoveSlots - 1) / kMoveSlots;
+  if (items * 8 > 0x7fffffffLL || items * chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
   static unsigned long long known[kMaxGpus];
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_select_kernel), kSelectMost * 4, known);
   if (e != cudaSuccess) return e;
+  // CTAs per sequence and head: as many as fill the GPU, with 1024 places each at least.
   const long long most = (long long)p.b.max_pages * p.b.page_size;
-  const int held = (int)(most < kSelectMost ? most : kSelectMost);
-  fa_paged_select_kernel<<<(unsigned)(p.b.S * p.b.Hkv), kSelectThreads, held * 4, st>>>(p, held);
-  e = cudaGetLastError();
+  int ctas = 1;
+  while (ctas < 8 && items * ctas * 2 <= 2LL * num_sms && most >= 2048LL * ctas) ctas *= 2;
+  const long long each = (most + ctas - 1) / ctas + 31;
+  const int held = (int)(each < kSelectMost ? each : kSelectMost);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * ctas));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = held * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {(unsigned)ctas, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fa_paged_select_kernel, p, held);
   if (e != cudaSuccess || p.max_keep == 0 || p.n_rows == 0) return e;
-  const long long grid = (long long)((p.max_keep + kMoveSlots - 1) / kMoveSlots) * p.b.Hkv * p.b.S;
-  fa_paged_move_kernel<<<(unsigned)grid, kMoveThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  cfg.gridDim = dim3((unsigned)(items * chunks));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = 0;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, fa_paged_move_kernel, p);
 }
 
 }  // namespace fa

@@ -40,6 +40,6 @@ struct PagedEvict {
   int* kept;        // [S][Hkv][max_keep]
   int* kv_len_out;  // [S]
 };
-cudaError_t launch_paged_evict(const PagedEvict& p, cudaStream_t st);
+cudaError_t launch_paged_evict(const PagedEvict& p, int num_sms, cudaStream_t st);
 
 }  // namespace fa

@@ -54,6 +54,7 @@ class _Rows(ctypes.Structure):  # fa_paged_rows
 # Arguments that change with each call are packed into bytes, in a third of the time that ctypes takes for an array.
 _ll2, _ll4, _ll8, _ll12 = (struct.Struct(f"{n}q").pack for n in (2, 4, 8, 12))
 _pack_cache = struct.Struct("PP6qi4x").pack  # _Cache
+_pack_rows = struct.Struct("P3qi4x").pack  # _Rows
 
 
 class FAError(RuntimeError):
@@ -831,32 +832,39 @@ def paged_evict(weights, caches, plan, keep, out_table, max_keep: int, sinks: in
     if isinstance(caches, PagedCache4):
         caches._for(plan)
         caches = (caches.k, caches.v, caches.k_scale, caches.v_scale)
-    rows = (_Rows * (len(caches) + 1))()
-    for row, t in zip(rows, (*caches, weights)):
-        if t.get_device() != i or t.dim() < 3 or tuple(t.shape[:3]) != (pages,) + plan.page_shape[:2] \
-                or (t.numel() > 0 and not t[0, 0, 0].is_contiguous()):
-            raise ValueError(f"what is moved must be CUDA tensors {[pages, *plan.page_shape[:2]]} [, ...] with dense slots, on the "
-                             "plan's device")
-        e = t.element_size()
-        row.base, row.bytes = t.data_ptr(), e * math.prod(t.shape[3:])
-        row.stride0, row.stride1, row.stride2 = (n * e for n in t.stride()[:3])
-    for name, t, shape in (("keep", keep, (S,)), ("out_table", out_table, (S, *out_table.shape[1:2]))):
-        if t.dtype != torch.int32 or t.get_device() != i or tuple(t.shape) != shape or (S > 0 and t.stride(-1) != 1):
-            raise ValueError(f"{name} must be an int32 CUDA tensor {list(shape)} with contiguous last dim, on the plan's device")
+    Hkv, page = plan.page_shape[:2]
+    rows = b""
+    for t in (*caches, weights):
+        sh, st, e, n = t.shape, t.stride(), t.element_size(), 1
+        dense = len(sh) >= 3
+        for j in range(len(sh) - 1, 2, -1):
+            dense = dense and (st[j] == n or sh[j] == 1)
+            n *= sh[j]
+        if not dense or sh[0] != pages or sh[1] != Hkv or sh[2] != page or t.get_device() != i:
+            raise ValueError(f"what is moved must be CUDA tensors {[pages, Hkv, page]} [, ...] with dense slots, on the plan's "
+                             "device")
+        rows += _pack_rows(t.data_ptr(), st[0] * e, st[1] * e, st[2] * e, n * e)
+    if keep.dtype != torch.int32 or keep.get_device() != i or keep.shape != (S,) or not keep.is_contiguous():
+        raise ValueError(f"keep must be a contiguous int32 CUDA tensor {[S]} on the plan's device")
+    ts = out_table.shape
+    if out_table.dtype != torch.int32 or out_table.get_device() != i or len(ts) != 2 or ts[0] != S \
+            or (out_table.stride(1) != 1 and ts[1] > 1):
+        raise ValueError(f"out_table must be an int32 CUDA tensor [{S}, out_pages] with contiguous last dim, on the plan's device")
     max_keep, sinks, recent = int(max_keep), int(sinks), int(recent)
-    if any(not 0 <= n < 2 ** 31 for n in (max_keep, sinks, recent)):
+    if not (0 <= max_keep < 2 ** 31 and 0 <= sinks < 2 ** 31 and 0 <= recent < 2 ** 31):
         raise ValueError("max_keep, sinks and recent must be at least 0 and fit 32 bits")
     raw = plan._use(stream, i)
-    shape = (S, plan.page_shape[0], max_keep)
+    shape = (S, Hkv, max_keep)
     if kept is None:
         kept = _empty(shape, torch.int32, weights.device, stream)
+    elif kept.dtype != torch.int32 or kept.get_device() != i or kept.shape != shape or not kept.is_contiguous():
+        raise ValueError(f"kept must be a contiguous int32 CUDA tensor {list(shape)}")
     if kv_lens is None:
         kv_lens = _empty((S,), torch.int32, weights.device, stream)
-    for name, t, want in (("kept", kept, shape), ("kv_lens", kv_lens, (S,))):
-        if t.dtype != torch.int32 or t.get_device() != i or tuple(t.shape) != want or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(want)}")
-    r = (_lib or lib()).fa_paged_evict(weights.data_ptr(), _ll2(*ws), rows, len(rows), pages, plan._ref, keep.data_ptr(), max_keep,
-                                       sinks, recent, out_table.data_ptr(), out_table.stride(0), out_table.shape[1],
+    elif kv_lens.dtype != torch.int32 or kv_lens.get_device() != i or kv_lens.shape != (S,) or not kv_lens.is_contiguous():
+        raise ValueError(f"kv_lens must be a contiguous int32 CUDA tensor {[S]}")
+    r = (_lib or lib()).fa_paged_evict(weights.data_ptr(), _ll2(*ws), rows, len(caches) + 1, pages, plan._ref, keep.data_ptr(), max_keep,
+                                       sinks, recent, out_table.data_ptr(), out_table.stride(0), ts[1],
                                        kept.data_ptr(), kv_lens.data_ptr(), raw)
     if r != FA_OK:
         raise FAError(r, "fa_paged_evict")
