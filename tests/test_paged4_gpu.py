@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from gpu_util import fa_mod
-from paged4_util import Batch4
+from paged4_util import Batch4, quantise
+from paged_util import f64
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +100,45 @@ def test_nan_in_a_seen_group_reaches_its_rows(fa, ql):
     fa.check()
     assert o[:ql, 2:].isnan().all() and lse[:ql, 2:].isnan().all()
     assert not o[:ql, :2].isnan().any() and not o[ql:].isnan().any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_heads_per_kv_head_and_many_sequences(fa, d):
+    run(fa, Batch4(fa, [(1, 70), (2, 33)], 130, 1, d, 16, seed=1))
+    r = torch.Generator().manual_seed(5)
+    lens = [(int(a), int(a) + int(n)) for a, n in zip(torch.randint(0, 3, (700,), generator=r), torch.randint(0, 60, (700,), generator=r))]
+    run(fa, Batch4(fa, lens, 2, 1, d, 16, seed=2))
+
+
+@pytest.mark.parametrize("ql", [4, 40])
+def test_more_new_tokens_than_cached_ones(fa, ql):
+    """The first of them stand before the sequence and see nothing."""
+    run(fa, Batch4(fa, [(ql, ql - 2), (1, 50)], 4, 2, 64, 16, seed=ql))
+
+
+def test_pages_beyond_four_gigabytes(fa):
+    Hkv, page, d = 8, 64, 128
+    b = Batch4(fa, [(1, 500), (20, 300)], 16, Hkv, d, page, seed=3)
+    pages = (1 << 32) // (Hkv * page * d // 2) + 40  # the last ones begin beyond 2^32 bytes of codes
+    big = fa.PagedCache4.empty(pages, Hkv, page, d)
+    shift = pages - b.num_pages
+    for x, y in zip((big.k, big.v, big.k_scale, big.v_scale), (b.cache.k, b.cache.v, b.cache.k_scale, b.cache.v_scale)):
+        x[shift:] = y
+    small = run(fa, b)
+    lse = small[1]
+    w = torch.rand(b.num_pages, Hkv, page, device="cuda")
+    want = fa.paged_weights(b.dev["q"], lse, b.cache, w, b.plan(fa), out=torch.zeros_like(w))
+    for i, (_, n) in enumerate(b.lens):
+        b.dev["table"][i, :(n + page - 1) // page] += shift
+    plan = b.plan(fa)
+    o, lse2 = fa.forward_paged4(b.dev["q"], big, plan)
+    wb = torch.zeros(pages, Hkv, page, device="cuda")
+    wb[shift:] = w
+    got = fa.paged_weights(b.dev["q"], lse, big, wb, plan, out=torch.zeros_like(wb))
+    x = torch.randn(21, 2 * Hkv, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    fa.paged_append4(None, x[:, :Hkv], x[:, Hkv:], big, plan)
+    fa.check()
+    assert torch.equal(o, small[0]) and torch.equal(lse2, lse) and torch.equal(got[shift:], want)
+    last = int(b.dev["table"][0, 7])
+    _, s, _ = quantise(f64(x[0, :Hkv]))
+    assert torch.equal(big.k_scale[last, :, 499 % page].cpu().double(), torch.from_numpy(s))
