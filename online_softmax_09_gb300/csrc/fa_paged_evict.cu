@@ -4,8 +4,8 @@
 // room, the first before the last), and of those between, the heaviest; among equal weights those at lower places. They keep
 // their order. A NaN counts as the heaviest.
 //
-// fa_paged_select_kernel, one to eight CTAs per sequence and head: the m-th largest weight by its digits (11, 11 and 10 bits of an
-// unsigned number in the weights' order, a histogram each), then two passes in order of place, one that counts and one that
+// fa_paged_select_kernel, one to eight CTAs per sequence and head: the m-th largest weight by its digits (11, 11 and 10 bits, or
+// four times 8, of an unsigned number in the weights' order, a histogram each), then two passes in order of place, one that counts and one that
 // writes the places kept, each warp over a stretch of its own. Weights that fit stay in shared memory between the passes.
 // fa_paged_move_kernel: a CTA moves 32 slots of one head, all tensors. The pages written are others than those read, so
 // the slots move independently, and pages that sequences share stay as they are.
@@ -19,7 +19,6 @@ namespace cg = cooperative_groups;
 namespace fa {
 
 constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
-constexpr int kBins = 2048;
 constexpr int kSelectMost = 44 * 1024;  // weights held in shared memory
 constexpr int kMoveSlots = 32, kMoveThreads = 256;
 
@@ -51,15 +50,22 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 
 // A cluster of CTAs per sequence and head, each with a stretch of the places of its own: the histograms and counts of all are
 // added up through distributed shared memory.
+template <bool kCluster>  // (else one CTA has all places)
 __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const PagedEvict p, int held) {
   extern __shared__ __align__(16) uint32_t cache[];
-  __shared__ __align__(16) uint32_t bins[3][kBins];  // of each pass, so that no pass waits for the others' reading of the one before
+  // Digits of 11 bits; of 8 in a cluster, whose CTAs all read all histograms (five thousand cycles each with 2048 numbers).
+  constexpr int kBits = kCluster ? 8 : 11, kBins = 1 << kBits, kPasses = (32 + kBits - 1) / kBits;
+  __shared__ __align__(16) uint32_t bins[kPasses][kBins];  // of each pass, so that no pass waits for the others' reading of the one before
   __shared__ uint32_t warp_sum[kSelectWarps];
   __shared__ uint32_t above_w[kSelectWarps], level_w[kSelectWarps];
   __shared__ __align__(8) uint32_t counts[2];  // of this CTA: numbers above the bound, and at it
   __shared__ uint32_t found[2];   // the digit, and how many of its numbers stay
   const cg::cluster_group cluster = cg::this_cluster();
-  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int C = kCluster ? (int)cluster.num_blocks() : 1, rank = kCluster ? (int)cluster.block_rank() : 0;
+  auto meet = [&]() {
+    if constexpr (kCluster) cluster.sync();
+    else __syncthreads();
+  };
   const PagedBatch& b = p.b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -93,13 +99,13 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     }
     return order_of(w[(long long)page * p.w_page + (key & (b.page_size - 1))]);
   };
-  for (int i = tid; i < 3 * kBins; i += kSelectThreads) bins[0][i] = 0;
+  for (int i = tid; i < kPasses * kBins; i += kSelectThreads) bins[0][i] = 0;
   __syncthreads();
   uint32_t prefix = 0, mask = 0, left = (uint32_t)s.m;  // numbers whose bits under `mask` are `prefix`
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-    const uint32_t digit = pass == 2 ? 1023 : 2047;
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int shift = max(0, 32 - kBits * (pass + 1));
+    const uint32_t digit = (1u << min(kBits, 32 - kBits * pass)) - 1;
     if (hold && pass > 0) {
 #pragma unroll 4
       for (int i = tid; i < n; i += kSelectThreads) {
@@ -121,16 +127,19 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
         }
       }
     }
-    cluster.sync();
-    // Numbers with a larger digit, for each: thread t has digits 2047 - 4 t and the three below.
+    meet();
+    // Numbers with a larger digit, for each: thread t has digits kBins - 1 - 4 t and the three below, if there are so many.
     uint32_t v[4] = {0, 0, 0, 0}, sum = 0;
-    uint4 h[8];  // all CTAs' at once: a read from another SM takes about a microsecond
+    constexpr int kMost = kCluster ? 8 : 1;
+    uint4 h[kMost];  // all CTAs' at once: a read from another SM takes about a microsecond
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      h[c] = c < C ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&bins[pass][kBins - 4 - 4 * tid], c))
-                   : make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < kMost; ++c) {
+      const uint32_t* own = &bins[pass][kBins - 4 - 4 * tid];
+      h[c] = make_uint4(0, 0, 0, 0);
+      if (c < C && 4 * tid < kBins) h[c] = *reinterpret_cast<const uint4*>(kCluster ? cluster.map_shared_rank(own, c) : own);
+    }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int c = 0; c < kMost; ++c) {
       v[0] += h[c].w;
       v[1] += h[c].z;
       v[2] += h[c].y;
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     for (int i = 0; i < warp; ++i) before += warp_sum[i];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (before < left && left <= before + v[i]) {
+      if (v[i] > 0 && before < left && left <= before + v[i]) {
         found[0] = kBins - 1 - 4 * tid - i;
         found[1] = left - before;
       }
@@ -182,10 +191,10 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     for (int i = 0; i < kSelectWarps; ++i) x += tid == 0 ? above_w[i] : level_w[i];
     counts[tid] = x;
   }
-  cluster.sync();
+  if constexpr (kCluster) cluster.sync();
   uint32_t at_above = 0, at_level = 0;  // before this lane's place
 #pragma unroll
-  for (int c = 0; c < 7; ++c) {
+  for (int c = 0; c < (kCluster ? 7 : 0); ++c) {
     if (c >= rank) continue;
     const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(counts, c));
     at_above += x.x;
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     at_above += __popc(ma);
     at_level += __popc(ml);
   }
-  cluster.sync();  // (until the others have read the counts)
+  if constexpr (kCluster) cluster.sync();  // (until the others have read the counts)
 }
 
 __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const PagedEvict p) {
@@ -231,52 +240,60 @@ __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const Paged
     to_s[tid] = to;
   }
   __syncthreads();
-  auto move = [&](const SlotRows& r, auto zero) {
+  // Two tensors whose slots are alike (keys and values, say), or one twice over: their loads go out together.
+  auto move = [&](const SlotRows& r0, const SlotRows& r1, int both, auto zero) {
     using V = decltype(zero);
-    const int per = r.bytes / (int)sizeof(V), total = n * per;
-    constexpr int kAtOnce = 4;
-    for (int x0 = tid; x0 < total; x0 += kAtOnce * kMoveThreads) {
-      V v[kAtOnce];
-      uint8_t* dst[kAtOnce];
+    const unsigned per = r0.bytes / (unsigned)sizeof(V), total = n * per;
+    constexpr int kAtOnce = 2;
+    for (unsigned x0 = tid; x0 < total; x0 += kAtOnce * kMoveThreads) {
+      V v[2][kAtOnce];
+      uint8_t* dst[2][kAtOnce];
 #pragma unroll
       for (int y = 0; y < kAtOnce; ++y) {
-        const int x = x0 + y * kMoveThreads;
-        dst[y] = nullptr;
-        if (x >= total) continue;
-        const int i = x / per, piece = x - i * per;
-        if (page_s[i] < 0) continue;
-        const uint8_t* src = r.base + (long long)page_s[i] * r.page + (long long)head * r.head +
-                             (long long)slot_s[i] * r.slot + piece * (int)sizeof(V);
-        v[y] = *reinterpret_cast<const V*>(src);
-        dst[y] = r.base + (long long)to_s[i] * r.page + (long long)head * r.head +
-                 (long long)((i0 + i) & (b.page_size - 1)) * r.slot + piece * (int)sizeof(V);
+        const unsigned x = x0 + y * kMoveThreads, i = x / per, piece = (x - i * per) * (unsigned)sizeof(V);
+        const bool on = x < total && page_s[x < total ? i : 0] >= 0;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const SlotRows& r = z == 0 ? r0 : r1;
+          dst[z][y] = nullptr;
+          if (!on || (z == 1 && !both)) continue;
+          uint8_t* base = r.base + (long long)head * r.head + piece;
+          v[z][y] = *reinterpret_cast<const V*>(base + page_s[i] * r.page + slot_s[i] * r.slot);
+          dst[z][y] = base + to_s[i] * r.page + (long long)((i0 + i) & (b.page_size - 1)) * r.slot;
+        }
       }
 #pragma unroll
       for (int y = 0; y < kAtOnce; ++y)
-        if (dst[y] != nullptr) *reinterpret_cast<V*>(dst[y]) = v[y];
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+          if (dst[z][y] != nullptr) *reinterpret_cast<V*>(dst[z][y]) = v[z][y];
     }
   };
-  for (int k = 0; k < p.n_rows; ++k) {
-    const SlotRows& r = p.rows[k];
-    if (r.vec == 16) move(r, uint4{});
-    else if (r.vec == 4) move(r, uint32_t{});
-    else if (r.vec == 2) move(r, uint16_t{});
-    else move(r, uint8_t{});
+  for (int k = 0; k < p.n_rows;) {
+    const SlotRows &r0 = p.rows[k], &r1 = p.rows[k + 1 < p.n_rows ? k + 1 : k];
+    const int both = k + 1 < p.n_rows && r1.bytes == r0.bytes && r1.vec == r0.vec;
+    if (r0.vec == 16) move(r0, r1, both, uint4{});
+    else if (r0.vec == 4) move(r0, r1, both, uint32_t{});
+    else if (r0.vec == 2) move(r0, r1, both, uint16_t{});
+    else move(r0, r1, both, uint8_t{});
+    k += 1 + both;
   }
 }
 
 cudaError_t launch_paged_evict(const PagedEvict& p, int num_sms, cudaStream_t st) {
   const long long items = (long long)p.b.S * p.b.Hkv, chunks = (p.max_keep + kMoveSlots - 1) / kMoveSlots;
   if (items * 8 > 0x7fffffffLL || items * chunks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  static unsigned long long known[kMaxGpus];
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_paged_select_kernel), kSelectMost * 4, known);
-  if (e != cudaSuccess) return e;
+  static unsigned long long known[2][kMaxGpus];
+  const void* kernels[2] = {reinterpret_cast<const void*>(fa_paged_select_kernel<false>),
+                            reinterpret_cast<const void*>(fa_paged_select_kernel<true>)};
   // CTAs per sequence and head: as many as fill the GPU, with 1024 places each at least.
   const long long most = (long long)p.b.max_pages * p.b.page_size;
   int ctas = 1;
   while (ctas < 8 && items * ctas * 2 <= 2LL * num_sms && most >= 2048LL * ctas) ctas *= 2;
   const long long each = (most + ctas - 1) / ctas + 31;
   const int held = (int)(each < kSelectMost ? each : kSelectMost);
+  cudaError_t e = allow_smem(kernels[ctas > 1], kSelectMost * 4, known[ctas > 1]);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * ctas));
   cfg.blockDim = dim3(kSelectThreads);
@@ -286,12 +303,14 @@ cudaError_t launch_paged_evict(const PagedEvict& p, int num_sms, cudaStream_t st
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim = {(unsigned)ctas, 1, 1};
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa_paged_select_kernel, p, held);
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  e = ctas > 1 ? cudaLaunchKernelEx(&cfg, fa_paged_select_kernel<true>, p, held)
+               : cudaLaunchKernelEx(&cfg, fa_paged_select_kernel<false>, p, held);
   if (e != cudaSuccess || p.max_keep == 0 || p.n_rows == 0) return e;
   cfg.gridDim = dim3((unsigned)(items * chunks));
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, fa_paged_move_kernel, p);
