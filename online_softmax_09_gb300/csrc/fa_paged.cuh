@@ -8,6 +8,8 @@
 // of a row tile that another CTA shares: at most two partial results per CTA, whatever the batch.
 #pragma once
 
+#include <stddef.h>
+
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
@@ -78,12 +80,15 @@ struct PagedBatch {
 
 __device__ __forceinline__ void record_index_error(uint32_t* status) { atomicCAS(status, kStatusOk, kStatusIndex); }
 
-// The plan was built for this batch (a stale or unset buffer would send indexes out of range).
+// The plan was built for this batch (a stale or unset buffer would send indexes out of range). Three loads that go out
+// together, and no branch between them.
 __device__ __forceinline__ bool plan_matches(const PagedBatch& b, int d) {
-  const PlanHeader* h = b.plan.head;
-  return h->magic == kPlanMagic && h->S == b.S && h->T == b.T && h->max_q == b.max_q && h->Hq == b.Hq &&
-         h->Hkv == b.Hkv && h->d == d && h->page_size == b.page_size && h->max_pages == b.max_pages &&
-         h->causal == b.causal && h->window == b.window;
+  static_assert(offsetof(PlanHeader, Hq) == 16 && offsetof(PlanHeader, max_pages) == 32, "the header is read by fours");
+  const int4* h = reinterpret_cast<const int4*>(b.plan.head);
+  const int4 x = h[0], y = h[1], z = h[2];
+  return (((uint32_t)x.x ^ kPlanMagic) | (uint32_t)((x.y ^ b.S) | (x.z ^ b.T) | (x.w ^ b.max_q) | (y.x ^ b.Hq) | (y.y ^ b.Hkv) |
+                                                    (y.z ^ d) | (y.w ^ b.page_size) | (z.x ^ b.max_pages) |
+                                                    (z.y ^ b.causal) | (z.z ^ b.window))) == 0;
 }
 
 // The first key that a query at `pos` sees. (No difference is formed for a window that reaches back to the first

@@ -19,18 +19,19 @@ namespace fa {
 template <int D, int NT>
 struct Row4Smem {
   static constexpr int kRows = NT <= 2 ? 16 : 32;
-  static constexpr int kWarps = row4_warps(NT), kThreads = 32 * (kWarps + 1);  // those that compute, and one that copies
+  static constexpr int kWarps = row4_warps(NT, D), kThreads = 32 * (kWarps + 1);  // those that compute, and one that copies
   static constexpr int kShares = kWarps == 7 ? 8 : kWarps;
-  static constexpr int kCtas = row4_ctas(NT);
+  static constexpr int kCtas = row4_ctas(NT, D);
   static constexpr int kCodes = kGran * code_bytes(D), kScales = kGran * scale_bytes(D);
   static constexpr int kPart = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales of a granule
   static constexpr int kStage = 2 * kPart;              // two granules: what a warp takes at a time
-  static constexpr int kStages = D == 128 ? 3 : (NT == 2 ? 4 : 6);
+  static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kSlots = kStages + 3;  // stretches handed out
   static constexpr int kWarp = kStages * kStage;
-  static constexpr int kMerge = kWarps * kWarp;               // 4 rows of o of each warp
-  static constexpr int kStat = kMerge + kWarps * 4 * D * 4;   // their m, l, rounded l
-  static constexpr int kQ = kStat + kWarps * 3 * 4 * 4;       // queries of 32 rows
+  static constexpr int kJoin = D == 128 && NT == 1 ? 4 : 8 * NT;  // rows that the warps join at a time
+  static constexpr int kMerge = kWarps * kWarp;                  // these of each warp
+  static constexpr int kStat = kMerge + kWarps * kJoin * D * 4;  // their m, l, rounded l
+  static constexpr int kQ = kStat + kWarps * 3 * kJoin * 4;      // queries of 32 rows
   static constexpr int kQueue = kQ + (NT > 2 ? kRows * D * 2 : 0);
   static constexpr int kBar = kQueue + kSlots * (int)sizeof(Seg);
   static constexpr int bSegFull = 0, bSegEmpty = bSegFull + kSlots;
@@ -106,13 +107,6 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
   const PagedBatch& b = p.b;
   const Ctl ctl{reinterpret_cast<volatile int*>(smem + L::kAbort), b.status};
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
-  if (threadIdx.x < L::kSlots) {
-    mbar_init(bar(L::bSegFull + threadIdx.x), 1);
-    mbar_init(bar(L::bSegEmpty + threadIdx.x), kWarps);
-  }
-  if (threadIdx.x == 0) *ctl.abort = 0;
-  fence_mbar_init();
-  __syncthreads();
   if (p.row_share != nullptr) {
     if (threadIdx.x == 0) p.row_share[blockIdx.x].c1 = -1;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -127,6 +121,7 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     SegIter<false, kRows> it(b, p.tile_ctas > 0 ? max(1, L::kCtas * (b.sms - pair_sms(b))) : gridDim.x);
     Seg s;
     bool some = plan_matches(b, D);  // (its loads go out beside the walk's)
+    __syncthreads();                 // the barriers are there
     for (uint32_t i = 0; some; ++i) {
       some = it.next(s);
       const uint32_t at = i % L::kSlots;
@@ -137,6 +132,15 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
         mbar_arrive(bar(L::bSegFull + at));
       }
     }
+  }
+  if (warp < kWarps) {
+    if (threadIdx.x < L::kSlots) {
+      mbar_init(bar(L::bSegFull + threadIdx.x), 1);
+      mbar_init(bar(L::bSegEmpty + threadIdx.x), kWarps);
+    }
+    if (threadIdx.x == 0) *ctl.abort = 0;
+    fence_mbar_init();
+    __syncthreads();
   }
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
@@ -157,6 +161,7 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     return fma_bf16x2(x, s2, cs);
   };
 
+  const uint32_t by_G = 0xffffffffu / G + 1;  // ceil(2^32 / G): a product's high half is the quotient of up to 2^16 rows
   // Queries as B operands: column g of tile t is row 8 t + g, and lane c holds its quarter of the dims. (Zero past the
   // tile's rows.) With 32 rows they stand in shared memory, 16-byte chunk x of row r at x ^ (r & 7).
   uint32_t qb[kQRegs ? NT : 1][kQRegs ? D / 8 : 1];
@@ -164,9 +169,10 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
   auto load_q = [&](const Seg& s) {
     const unsigned r0 = (unsigned)s.tile * kRows;
     const int rows = (int)min((unsigned)kRows, (unsigned)s.ql * G - r0);
+    const bool few_rows = (unsigned)s.ql * G <= 65536 && G > 1;
     auto row_of = [&](int r, int& tok) {
       const unsigned rr = r0 + (r < rows ? r : 0);
-      tok = s.ql == 1 ? 0 : (int)(rr / G);
+      tok = s.ql == 1 ? 0 : (int)(few_rows ? __umulhi(rr, by_G) : rr / G);
       const int hd = (int)(rr - tok * G);
       return p.q + (long long)(s.q0 + tok) * p.q_tok + (long long)(s.head * G + hd) * p.q_head;
     };
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
         __syncwarp();  // the stage is read: the next copies may overwrite it
       }
 
-      // ---- join the warps, 4 rows at a time
+      // ---- join the warps, kJoin rows at a time
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -523,16 +529,18 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
       float* slot = p.part + (size_t)(2 * blockIdx.x + (s.first ? 1 : 0)) * row_part(D, kRows);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::bSegEmpty + k % L::kSlots));  // (nothing of s is read below)
+      constexpr int kJoin = L::kJoin;
 #pragma unroll
-      for (int half = 0; half < 2 * NT; ++half) {
-        const int t = half >> 1;
-        if (4 * half >= rows) break;
-        if (half > 0) meet();  // the rows that stood here have been read
-        // Rows 2 c and 2 c + 1 of this lane, dims from g * D / 8 on; 16-byte chunk x of row r at x ^ 2 r.
-        if (c >> 1 == (half & 1)) {
+      for (int first_row = 0; first_row < 8 * NT; first_row += kJoin) {
+        if (first_row >= rows) break;
+        if (first_row > 0) meet();  // the rows that stood here have been read
+        // Rows 8 t + 2 c and the next of this lane, dims from g * D / 8 on; 16-byte chunk x of row r at x ^ 2 r (two bits of r).
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int r = 2 * (c & 1) + h, at = warp * 4 + r;
+            const int r = 8 * t + 2 * c + h - first_row, at = warp * kJoin + r;
+            if (r < 0 || r >= kJoin) continue;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {  // dims 4 q .. of the lane's
               float4 v;
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
                 const int dim = 4 * q + i;
                 f[i] = D == 128 ? o[(dim & 7) % kMT][t][2 * (dim >> 3) + h] : o[(dim >> 1) % kMT][t][2 * (dim & 1) + h];
               }
-              *reinterpret_cast<float4*>(merge + at * D + (((g * (D / 32) + q) ^ (2 * r)) << 2)) = v;
+              *reinterpret_cast<float4*>(merge + at * D + (((g * (D / 32) + q) ^ (2 * (r & 3))) << 2)) = v;
             }
             if (g == 0) {
               stat[at * 3] = m[t][h];
@@ -550,23 +558,22 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
               stat[at * 3 + 2] = lr[t][h];
             }
           }
-        }
         meet();
-        for (int x = threadIdx.x; x < 4 * (D / 4); x += 32 * kWarps) {  // four columns of a row
-          const int hr = x / (D / 4), row = hr + 4 * half, ch = x % (D / 4);
-          if (row >= rows) continue;
+        const int here = min(kJoin, rows - first_row);
+        for (int x = threadIdx.x; x < here * (D / 4); x += 32 * kWarps) {  // four columns of a row
+          const int hr = x / (D / 4), row = hr + first_row, ch = x % (D / 4);
           float M = -INFINITY, Ls = 0.f, Lr = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[(w * 4 + hr) * 3]);
+          for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[(w * kJoin + hr) * 3]);
           const float Mu = M == -INFINITY ? 0.f : M;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float* sw = stat + (w * 4 + hr) * 3;
+            const float* sw = stat + (w * kJoin + hr) * 3;
             const float f = ex2(sw[0] - Mu);
             Ls += f * sw[1];
             Lr += f * sw[2];
-            const float4 v = *reinterpret_cast<const float4*>(merge + (w * 4 + hr) * D + ((ch ^ (2 * hr)) << 2));
+            const float4 v = *reinterpret_cast<const float4*>(merge + (w * kJoin + hr) * D + ((ch ^ (2 * (hr & 3))) << 2));
             acc.x = fmaf(f, v.x, acc.x);
             acc.y = fmaf(f, v.y, acc.y);
             acc.z = fmaf(f, v.z, acc.z);
@@ -606,11 +613,12 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     }
   }
   if constexpr (NT == 2) {  // (a batch of tiles of 8 or of 32 rows has no pairs)
-    static_assert(NT != 2 || kWarps + 1 == kRowWarps, "join_pairs is for kRowThreads");
-    if (p.tile_ctas > 0) {
+    static_assert(NT != 2 || kWarps + 1 == kRowWarps || kWarps > kRowWarps, "join_pairs is for kRowThreads");
+    if (p.tile_ctas > 0 && warp < kRowWarps) {
       asm volatile("cp.async.wait_all;" ::: "memory");  // (some are in flight after a wait that gave up)
-      __syncthreads();
-      join_pairs<D>(p, [] { __syncthreads(); });
+      auto meet_four = [] { asm volatile("bar.sync 2, %0;" ::"n"(kRowThreads) : "memory"); };
+      meet_four();
+      join_pairs<D>(p, meet_four);
     }
   }
 }

@@ -57,8 +57,8 @@ cudaError_t launch_append4(const RopeLaunch& p, const Append4& a, int d, int num
 __host__ __device__ constexpr int row4_columns(int row_tile, int max_q, int G) {
   return row_tile == 32 ? 4 : ((long long)max_q * G <= 8 ? 1 : 2);
 }
-__host__ __device__ constexpr int row4_warps(int columns) { return columns == 1 ? 7 : 3; }
-__host__ __device__ constexpr int row4_ctas(int columns) { return columns == 2 ? 3 : 2; }
+__host__ __device__ constexpr int row4_warps(int columns, int d) { return columns * d <= 128 ? 7 : 3; }
+__host__ __device__ constexpr int row4_ctas(int columns, int d) { return columns == 2 && d == 128 ? 3 : 2; }
 constexpr int kMostRow4Ctas = 3;
 size_t paged4_rows_workspace_bytes(int d, int row_tile);
 cudaError_t launch_paged4_rows(PagedFwd& p, const PagedCache4& c, int d, int num_sms, cudaStream_t st);

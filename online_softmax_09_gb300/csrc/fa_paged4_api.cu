@@ -197,7 +197,7 @@ int fa_fwd_paged4(const void* q, const long long* q_strides, const fa_paged_cach
   p.b.sms = num_sms;
   set_fwd(p, q, q_strides, o, lse, scale, workspace, batch);
   const fa::PagedCache4 c = device_cache4(cache);
-  const int d = batch->d, ctas = fa::row4_ctas(fa::row4_columns(p.b.row_tile, p.b.max_q, p.b.G));
+  const int d = batch->d, ctas = fa::row4_ctas(fa::row4_columns(p.b.row_tile, p.b.max_q, p.b.G), d);
   p.row_share = few_tiles(batch, p.b, (long long)ctas * num_sms)
                     ? reinterpret_cast<fa::RowShare*>(
                           static_cast<char*>(workspace) +
