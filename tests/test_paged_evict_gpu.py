@@ -109,6 +109,30 @@ def test_more_weights_than_shared_memory_holds(fa, kind):
     s.run(4, 64)
 
 
+@pytest.mark.parametrize("kind", ["random", "ties", "all kinds"])
+def test_more_weights_than_shared_memory_holds_and_many_sequences(fa, kind):
+    """A CTA per sequence and head, which reads the weights again in each pass."""
+    s = Setup(fa, [50000, 45057, 45056, 0, 3] + [20] * 75, 2, 64, 256, 333, seed=4, kind=kind)
+    s.tensors = s.tensors[3:]
+    s.run(4, 64)
+
+
+@pytest.mark.parametrize("kind", ["ties", "all kinds"])
+def test_more_weights_than_a_cluster_holds(fa, kind):
+    s = Setup(fa, [370000], 1, 64, 256, 777, seed=5, kind=kind)
+    s.tensors = s.tensors[3:]
+    s.run(4, 64)
+
+
+@pytest.mark.parametrize("kind", ["random", "ties", "equal", "all kinds"])
+@pytest.mark.parametrize("sinks,recent", [(0, 0), (4, 33), (1000, 5), (3, 1000)])
+@pytest.mark.parametrize("lens", [[2100, 40, 0, 2047], [17000, 5000, 300], [9000]])  # clusters of 2 to 8
+def test_what_stays_by_clusters(fa, kind, sinks, recent, lens):
+    s = Setup(fa, lens, 2, 64, 64, 300, seed=sinks + len(lens), kind=kind)
+    s.tensors = s.tensors[3:]
+    s.run(sinks, recent)
+
+
 def test_lengths_and_pages_out_of_range(fa):
     s = Setup(fa, [100, 200, 90], 2, 64, 16, [50, 60, 40], seed=3)
     s.keep[1] = 61  # above max_keep: nothing of it stays
