@@ -5,9 +5,17 @@
 // lse is the attention's, so no maximum is carried and no key needs another: each block of 128 keys is one CTA's, and its sum
 // is formed in a fixed order (the same bits at every call).
 //
-// What has to be read is each key once. A warp holds 32 keys as A operands (m16n8k16), straight from global memory: which
-// dims a step of the product takes is free as long as keys and queries agree, so a lane's 16-byte loads are its operands.
-// The queries go by as columns, 8 at a time. CTAs take blocks by their sequences' share of the plan's units.
+// What has to be read is each key once. A warp holds 32 keys as A operands (m16n8k16), 64 at d = 64, straight from global
+// memory: which dims a step of the product takes is free as long as keys and queries agree, so a lane's 16-byte loads are its
+// operands. CTAs take blocks by their sequences' share of the plan's units.
+//
+// The queries go by as columns, 8 rows at a time, from shared memory: 64 rows in the order of the lanes' operands, with their
+// -lse in base 2, so that a tile costs its products, exponentials and sums and few instructions more. Up to 64 rows stay from
+// block to block of a head; more are copied anew for each block, 64 beside the products of the 64 before. (Loaded from global
+// memory by each warp, with their places worked out there, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys, 16
+// heads, d = 64, took 48.7 us; so 37.1. The next keys' codes in registers ahead: 42.5; 32 keys per warp: 39 with four CTAs
+// per SM, 42 with five.) Counted: 713 instructions per 64 keys, 86 per tile.
+// A decode step of 64 sequences of 200 to 8192 bf16 keys (582 MB, d = 128, 8 kv heads): 93 us, 6.26 TB/s.
 #include <math.h>
 #include <type_traits>
 
@@ -17,10 +25,11 @@
 namespace fa {
 
 constexpr int kWeightThreads = 128;
-// Granules of 16 keys that a warp holds (64 registers of operands), and CTAs per SM (with four at d = 128 some of the loop's
-// values stand in local memory: 106 us for the decode step of 64 sequences of 200 to 8192 keys, 95 with three).
+// Granules of 16 keys that a warp holds (64 registers of operands), and CTAs per SM (four take 106 us for that decode step,
+// and 42 for those prompts: some of the loop's values stand in local memory then).
 __host__ __device__ constexpr int weight_grans(int D) { return D == 128 ? 2 : 4; }
-__host__ __device__ constexpr int weight_ctas(int D) { return 3 + 0 * D; }
+constexpr int kWeightCtas = 3;
+constexpr int kRows = 64;  // rows of queries in shared memory at a time
 constexpr long long kPairShare = 16;  // a unit of the plan's pairs (256 rows of 128 keys), in units of its small tiles
 
 // a / b of numbers that are rarely beyond 32 bits (in 64 bits the division takes over a hundred instructions).
@@ -29,10 +38,10 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 template <int D, bool kPacked>
-__global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
-    fa_paged_weights_kernel(const PagedWeights p) {
+__global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_kernel(const PagedWeights p) {
   constexpr int kT = weight_grans(D), kKeys = 16 * kT, kBlk = kWeightThreads / 32 * kKeys;
-  constexpr bool kEarly = D == 64;  // the next queries are loaded beside the products (at d = 128 there is no room for them)
+  __shared__ uint4 q_s[2][kRows / 8][D / 32][32];  // queries of kRows rows as B operands: a tile's i-th 16 bytes of each lane
+  __shared__ float2 l_s[2][kRows / 2];             // -lse in base 2 of two rows
   const PagedBatch& b = p.b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   auto start = [&](long long s) { return b.plan.units[0][s] + kPairShare * b.plan.units[1][s]; };
@@ -52,11 +61,7 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
     hi = min(hi, seq + step);
   }
   const unsigned G = b.G;
-  // 8 rows on: tokens and heads, and what that moves a query's and a sum's place by (one more token: `wrap`).
-  const int q8 = (int)(8 / G), r8 = (int)(8 % G);
-  const int tok0[3] = {(int)(g / G), (int)(2 * c / G), (int)((2 * c + 1) / G)};  // tokens of the first rows
-  const long long q_on = q8 * p.q_tok + r8 * p.q_head, q_wrap = p.q_tok - (long long)G * p.q_head;
-  const int l_on = q8 * b.Hq + r8, l_wrap = b.Hq - (int)G;
+  int buf = 0;  // the queries' buffer in turn
   for (bool begin = true; seq < b.S; ++seq, begin = false) {
     const long long base = start(seq);
     if (base >= u_end) break;
@@ -69,7 +74,7 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
     if (hi <= lo) continue;
     const int blk0 = lo / kBlk, nblk = (hi - 1) / kBlk - blk0 + 1;
     const int first_new = ps.kvl - ps.ql, rows_all = ps.ql * (int)G;
-    const bool few = rows_all <= 8;  // one tile of queries, held from block to block
+    const bool few = rows_all <= kRows;  // the queries stay from block to block
     const int* tab = b.table + (long long)seq * b.table_stride;
     int head = 0;
     int k = 0;
@@ -91,50 +96,23 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
       }
     };
     for (; head < b.Hkv; ++head, k = 0) {
-      // The queries that stand from row r on: row r + g as a column of the product, and rows r + 2 c, r + 2 c + 1 as sums.
-      struct Queries {
-        uint4 q[D / 32];
-        float z[2];
-      } now;
-      const __nv_bfloat16* qp = nullptr;
-      const float* zp[2];
-      int tok[3], hd[3];
-      auto set_rows = [&](unsigned r) {
+      // kRows rows from r0 on, into the other buffer than that being read. (One barrier between two calls is enough.)
+      auto stage = [&](int r0) {
+        buf ^= 1;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const unsigned rr = r + (i == 0 ? g : 2 * c + i - 1);
-          tok[i] = r == 0 ? tok0[i] : (int)(rr / G);
-          hd[i] = (int)(rr - tok[i] * G);
-        }
-        qp = p.q + (long long)(ps.q0 + tok[0]) * p.q_tok + ((long long)head * G + hd[0]) * p.q_head +
-             c * (kPacked ? D / 4 : 8);
+        for (int j = warp; j < kRows / 8; j += kWeightThreads / 32) {
+          if (r0 + 8 * j >= rows_all) break;
+          const int r = r0 + 8 * j + g;
+          const bool in = r < rows_all;
+          const unsigned tok = (in ? r : 0) / G, hd = (in ? r : 0) - tok * G;
+          const __nv_bfloat16* src = p.q + (long long)(ps.q0 + (int)tok) * p.q_tok + (long long)(head * G + hd) * p.q_head +
+                                     c * (kPacked ? D / 4 : 8);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          zp[e] = p.lse + (long long)(ps.q0 + tok[1 + e]) * b.Hq + head * (int)G + hd[1 + e];
-      };
-      auto load_rows = [&](Queries& x, bool every) {  // every: no row is past the last
-        const bool q_in = every || tok[0] < ps.ql;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          x.q[i] = q_in ? *reinterpret_cast<const uint4*>(qp + (kPacked ? 8 * i : 32 * i)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) x.z[e] = every || tok[1 + e] < ps.ql ? *zp[e] : -INFINITY;
-      };
-      auto next_rows = [&]() {
-        qp += q_on;
-        zp[0] += l_on;
-        zp[1] += l_on;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) tok[i] += q8;
-        if (r8 == 0) return;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          hd[i] += r8;
-          if (hd[i] >= (int)G) {
-            hd[i] -= (int)G;
-            ++tok[i];
-            if (i == 0) qp += q_wrap;
-            else zp[i - 1] += l_wrap;
+          for (int i = 0; i < D / 32; ++i)
+            cp_async16_or_zero(smem_u32(&q_s[buf][j][i][lane]), src + (kPacked ? 8 * i : 32 * i), in);
+          if (c == 0) {
+            const float z = in ? p.lse[(long long)(ps.q0 + (int)tok) * b.Hq + head * (int)G + hd] : -INFINITY;
+            reinterpret_cast<float*>(l_s[buf])[8 * j + g] = z == -INFINITY ? -INFINITY : z * -1.4426950408889634f;
           }
         }
       };
@@ -153,15 +131,35 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
         entries(key0, page);
         entries(key0 + kBlk, page_next);
       }
-      if (few) {
-        set_rows(0);
-        load_rows(now, false);
-      }
       const long long left = u_end - base - head * per_head;  // units of the head that are this CTA's
       if (left <= 0) return;
+      if (few) {
+        stage(0);
+        cp_async_wait_all();
+        __syncthreads();
+      }
       const int k_end = left >= per_head ? nblk : (int)quotient(left * nblk + per_head - 1, per_head);
       for (; k < k_end; ++k) {
         const int key0 = (blk0 + k) * kBlk + warp * kKeys;
+        // Rows that see a key of the block: [r_lo, r_hi), one of this warp's unit: [r, r_end), every key of it: [full, full_end).
+        int r_lo = 0, r_hi = rows_all, r = 0, r_end = rows_all, full = key0 + kKeys <= ps.kvl ? 0 : rows_all, full_end = rows_all;
+        if (b.causal) {
+          const int blk_key = key0 - warp * kKeys;
+          auto rows_to = [&](int tok) { return min(max(tok, 0), ps.ql) * (int)G; };
+          r_lo = rows_to(blk_key - first_new) & ~7;
+          r = rows_to(key0 - first_new) & ~7;
+          full = rows_to(key0 + kKeys - 1 - first_new);
+          if (b.window > 0) {
+            auto before = [&](int key) {  // rows whose windows begin at or before the key
+              return (int)min(max((long long)key + b.window - first_new, 0LL), (long long)ps.ql) * (int)G;
+            };
+            r_hi = before(blk_key + kBlk - 1);
+            r_end = before(key0 + kKeys - 1);
+            full_end = before(key0);
+          }
+        }
+        if (key0 >= hi || key0 + kKeys <= lo) r_end = 0;
+        if (!few && r_lo < r_hi) stage(r_lo);
         bool whole = key0 >= lo && key0 + kKeys <= hi;  // every key of the unit is seen
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
@@ -238,12 +236,12 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
         if (!kPacked && k + 1 < nblk) {
 #pragma unroll
           for (int y = 0; y < kT / 2; ++y) {
-          const int key = key0 + kBlk + 32 * y + lane, pg = lane < 16 ? page[2 * y] : page[2 * y + 1];
-          if (pg >= 0 && pg < b.num_pages && key < hi) {
-            const uint8_t* at = k_head + (long long)pg * k_page + (long long)(key & (b.page_size - 1)) * k_tok;
+            const int key = key0 + kBlk + 32 * y + lane, pg = lane < 16 ? page[2 * y] : page[2 * y + 1];
+            if (pg >= 0 && pg < b.num_pages && key < hi) {
+              const uint8_t* at = k_head + (long long)pg * k_page + (long long)(key & (b.page_size - 1)) * k_tok;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
-          }
+              for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
+            }
           }
         }
         entries(key0 + 2 * kBlk, page_next);
@@ -251,73 +249,54 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
         float sum[kT][2];
 #pragma unroll
         for (int t = 0; t < kT; ++t) sum[t][0] = sum[t][1] = 0.f;
-        if (key0 < hi && key0 + kKeys > lo) {
-          long long r = 0, r_end = rows_all;
-          if (b.causal && !few) {
-            r = max(0, key0 - first_new) * (long long)G & ~7LL;
-            if (b.window > 0) {
-              const long long past = (long long)key0 + kKeys - 1 + b.window - first_new;  // tokens from here on do not
-              r_end = min(r_end, max(past, 0LL) * G);
-            }
-          }
-          // Rows from `full` to `full_end` see every key of the unit.
-          const long long full = b.causal ? (long long)max(0, key0 + kKeys - 1 - first_new) * G
-                                          : (key0 + kKeys <= ps.kvl ? 0 : rows_all);
-          const long long full_end = b.window > 0 ? max(0LL, ((long long)key0 + b.window - first_new) * G) : rows_all;
-          if (!few && r < r_end) {
-            set_rows((unsigned)r);
-            if (kEarly) load_rows(now, false);
-          }
-          for (; r < r_end; r += 8) {
-            if (!few && !kEarly) load_rows(now, r + 8 <= rows_all);
-            const int at0 = tok[1], at1 = tok[2];
-            const bool masked = r < full || min(r + 8, (long long)rows_all) > full_end;
-            float l2[2];
+        auto add = [&](int buf, int r, int at, auto some) {  // rows r .. r + 7, which stand from row `at` of a buffer on
+          const float2 l2 = l_s[buf][(at >> 1) + c];
+          float x[kT][4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)  // nothing seen: nothing given
-              l2[e] = now.z[e] == -INFINITY ? INFINITY : now.z[e] * 1.4426950408889634f;
-            Queries next;
-            if (!few) next_rows();
-            if (kEarly) {
-              next = now;
-              if (!few && r + 8 < r_end) load_rows(next, r + 16 <= rows_all);
+          for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {  // (the granules' products take turns, not each its own sum's steps)
+            const uint4 q = q_s[buf][at >> 3][i][lane];
+#pragma unroll
+            for (int t = 0; t < kT; ++t) mma16816(x[t], a[t][2 * i], q.x, q.y);
+#pragma unroll
+            for (int t = 0; t < kT; ++t) mma16816(x[t], a[t][2 * i + 1], q.z, q.w);
+          }
+          int klim[2], klo[2];
+          if (decltype(some)::value) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int pos = first_new + (int)((unsigned)(r + 2 * c + e) / G);
+              klim[e] = b.causal ? min(pos, ps.kvl - 1) : ps.kvl - 1;
+              klo[e] = mask_from(pos, b.window);
             }
-            auto add = [&](auto some) {
-              int klim[2], klo[2];
+          }
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float l = e & 1 ? l2.y : l2.x;
+              float w = ex2(fmaf(x[t][e], p.scale_log2, l));
               if (decltype(some)::value) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int pos = first_new + (e == 0 ? at0 : at1);
-                  klim[e] = b.causal ? min(pos, ps.kvl - 1) : ps.kvl - 1;
-                  klo[e] = mask_from(pos, b.window);
-                }
+                const int key = key0 + 16 * t + 8 * (e >> 1) + g;
+                w = key <= klim[e & 1] && key >= klo[e & 1] && l != -INFINITY ? w : 0.f;
               }
-              float x[kT][4];
-#pragma unroll
-              for (int t = 0; t < kT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i)  // (the granules' products take turns, not each its own sum's steps)
-#pragma unroll
-                for (int t = 0; t < kT; ++t)
-                  mma16816(x[t], a[t][i], (i & 1) ? now.q[i >> 1].z : now.q[i >> 1].x,
-                           (i & 1) ? now.q[i >> 1].w : now.q[i >> 1].y);
-#pragma unroll
-              for (int t = 0; t < kT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float w = ex2(fmaf(x[t][e], p.scale_log2, -l2[e & 1]));
-                  if (decltype(some)::value) {
-                    const int key = key0 + 16 * t + 8 * (e >> 1) + g;
-                    w = key <= klim[e & 1] && key >= klo[e & 1] && l2[e & 1] != INFINITY ? w : 0.f;
-                  }
-                  sum[t][e >> 1] += w;
-                }
-            };
-            if (masked) add(std::true_type());
-            else add(std::false_type());
-            if (kEarly) now = next;
+              sum[t][e >> 1] += w;
+            }
+        };
+        for (int first = few ? 0 : r_lo; first < r_hi; first += kRows) {
+          const int here = buf;
+          if (!few) {
+            cp_async_wait_all();
+            __syncthreads();  // these rows are there, and nobody reads the other buffer any more
+            if (first + kRows < r_hi) stage(first + kRows);
+          }
+          const int to = min(first + kRows, r_end);
+          for (int r8 = max(first, r); r8 < to; r8 += 8) {
+            if (r8 < full || min(r8 + 8, rows_all) > full_end) add(here, r8, r8 - first, std::true_type());
+            else add(here, r8, r8 - first, std::false_type());
           }
         }
         float total[kT / 2];
@@ -340,7 +319,7 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D))
 }
 
 cudaError_t launch_paged_weights(const PagedWeights& p, int d, bool packed, int num_sms, cudaStream_t st) {
-  const int grid = weight_ctas(d) * num_sms;
+  const int grid = kWeightCtas * num_sms;
   if (d == 128) {
     if (packed) fa_paged_weights_kernel<128, true><<<grid, kWeightThreads, 0, st>>>(p);
     else fa_paged_weights_kernel<128, false><<<grid, kWeightThreads, 0, st>>>(p);
