@@ -613,7 +613,10 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     }
   }
   if constexpr (NT == 2) {  // (a batch of tiles of 8 or of 32 rows has no pairs)
-    static_assert(NT != 2 || kWarps + 1 == kRowWarps || kWarps > kRowWarps, "join_pairs is for kRowThreads");
+    static_assert(kWarps + 1 == kRowWarps || kWarps >= kRowWarps, "join_pairs is for kRowThreads");
+    // Its list stands in the first warps' rings: the others' copies, of which some may be in flight, do not reach it.
+    static_assert(2 * kPagedSms * (sizeof(TileShare) + 8) + 64 <= (kWarps < kRowWarps ? kWarps : kRowWarps) * L::kWarp,
+                  "room for the list");
     if (p.tile_ctas > 0 && warp < kRowWarps) {
       asm volatile("cp.async.wait_all;" ::: "memory");  // (some are in flight after a wait that gave up)
       auto meet_four = [] { asm volatile("bar.sync 2, %0;" ::"n"(kRowThreads) : "memory"); };

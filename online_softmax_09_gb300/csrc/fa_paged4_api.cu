@@ -1,5 +1,5 @@
-// fa_paged4_api.cu -- the C ABI of the 4-bit paged cache and of eviction (include/fa.h): argument checks and launches. Every check comes
-// before any CUDA call.
+// fa_paged4_api.cu -- the C ABI of the 4-bit paged cache and of eviction (include/fa.h): argument checks and launches.
+// Every check comes before any CUDA call.
 #include "fa_paged_checks.cuh"
 #include "fa_paged_evict.cuh"
 
@@ -45,8 +45,10 @@ fa::PagedCache4 device_cache4(const fa_paged_cache4* c) {
   return x;
 }
 
-// Where a batch has both kinds of tiles: a unit of 64 keys is a quarter of a bf16 cache's bytes.
-float row4_cost(int d) { return d == 64 ? 0.18f : 0.15f; }
+// Where a batch has both kinds of tiles: what a unit of the small ones costs beside one of the pairs. (1000 tokens over 9000
+// keys and 23 single ones over 2000 to 14000, 32 heads of 8 kv heads: 268 us with 0.23, 256 with 0.28, 265 with 0.33 at
+// d = 128; 202 with 0.25, 172 with 0.32, 177 with 0.38 at d = 64. Four other batches have their least between 0.26 and 0.38.)
+float row4_cost(int d) { return d == 64 ? 0.32f : 0.28f; }
 
 // Strides (page, head) in elements of fp32 weights, the page's below 2^32; `distinct`: they are written.
 int check_weights(const float* w, const long long* s, int pages, int heads, bool distinct) {
