@@ -5,17 +5,18 @@
 // lse is the attention's, so no maximum is carried and no key needs another: each block of 128 keys is one CTA's, and its sum
 // is formed in a fixed order (the same bits at every call).
 //
-// What has to be read is each key once. A warp holds 32 keys as A operands (m16n8k16), 64 at d = 64, straight from global
-// memory: which dims a step of the product takes is free as long as keys and queries agree, so a lane's 16-byte loads are its
-// operands. CTAs take blocks by their sequences' share of the plan's units.
+// What has to be read is each key once. A warp holds 32 keys as A operands (m16n8k16), straight from global memory: which
+// dims a step of the product takes is free as long as keys and queries agree, so a lane's 16-byte loads are its operands.
+// CTAs take blocks by their sequences' share of the plan's units.
 //
-// The queries go by as columns, 8 rows at a time, from shared memory: 64 rows in the order of the lanes' operands, with their
-// -lse in base 2, so that a tile costs its products, exponentials and sums and few instructions more. Up to 64 rows stay from
-// block to block of a head; more are copied anew for each block, 64 beside the products of the 64 before. (Loaded from global
-// memory by each warp, with their places worked out there, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys, 16
-// heads, d = 64, took 48.7 us; so 37.1. The next keys' codes in registers ahead: 42.5; 32 keys per warp: 39 with four CTAs
-// per SM, 42 with five.) Counted: 713 instructions per 64 keys, 86 per tile.
-// A decode step of 64 sequences of 200 to 8192 bf16 keys (582 MB, d = 128, 8 kv heads): 93 us, 6.26 TB/s.
+// The queries go by as columns, 8 rows at a time, from shared memory: 64 rows in the order of the lanes' operands, with
+// their -lse in base 2, so that a tile costs its products, exponentials and sums and few instructions more. Up to 64 rows
+// stay from block to block of a head; more are copied anew for each block, 64 beside the products of the 64 before.
+//
+// Measured, 16 heads, d = 64, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys: 37.5 us; 48.7 with queries and
+// their places worked out by each warp from global memory. 1000 tokens of 32 heads over 9000 bf16 keys of 8 kv heads: 168 us
+// at d = 64, 323 at d = 128. A decode step of 64 sequences of 200 to 8192 bf16 keys, d = 128, 8 kv heads (582 MB): 93 us,
+// 6.26 TB/s. So a single token is bound by memory, and many rows by latencies at 12 to 16 warps per SM.
 #include <math.h>
 #include <type_traits>
 
@@ -25,12 +26,16 @@
 namespace fa {
 
 constexpr int kWeightThreads = 128;
-// Granules of 16 keys that a warp holds (64 registers of operands), and CTAs per SM (four take 106 us for that decode step,
-// and 42 for those prompts: some of the loop's values stand in local memory then).
-__host__ __device__ constexpr int weight_grans(int D) { return D == 128 ? 2 : 4; }
-constexpr int kWeightCtas = 3;
+// Granules of 16 keys that a warp holds: 64 or 32 registers of operands. (64 keys at d = 64: the 1000 tokens 239 us, the last
+// 32 tokens of prompts 37.0.)
+constexpr int kGrans = 2;
+// CTAs per SM: what registers leave room for. (One more at d = 128: 106 us for the decode step; at d = 64 42 for the prompts.)
+__host__ __device__ constexpr int weight_ctas(int D) { return D == 64 ? 4 : 3; }
 constexpr int kRows = 64;  // rows of queries in shared memory at a time
-constexpr long long kPairShare = 16;  // a unit of the plan's pairs (256 rows of 128 keys), in units of its small tiles
+// A unit of the plan's pairs (256 rows of 128 keys) in units of its small tiles. (Five batches of chunks beside single tokens,
+// each over bf16 and 4-bit keys, geometric mean at d = 64: 146 us with 5, 132 with 7, 140 with 11, 156 with 16; at d = 128
+// 234, 226, 214 and 215.)
+__host__ __device__ constexpr long long pair_share(int D) { return D == 64 ? 7 : 11; }
 
 // a / b of numbers that are rarely beyond 32 bits (in 64 bits the division takes over a hundred instructions).
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -38,13 +43,13 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 template <int D, bool kPacked>
-__global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_kernel(const PagedWeights p) {
-  constexpr int kT = weight_grans(D), kKeys = 16 * kT, kBlk = kWeightThreads / 32 * kKeys;
+__global__ void __launch_bounds__(kWeightThreads, weight_ctas(D)) fa_paged_weights_kernel(const PagedWeights p) {
+  constexpr int kT = kGrans, kKeys = 16 * kT, kBlk = kWeightThreads / 32 * kKeys;
   __shared__ uint4 q_s[2][kRows / 8][D / 32][32];  // queries of kRows rows as B operands: a tile's i-th 16 bytes of each lane
   __shared__ float2 l_s[2][kRows / 2];             // -lse in base 2 of two rows
   const PagedBatch& b = p.b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  auto start = [&](long long s) { return b.plan.units[0][s] + kPairShare * b.plan.units[1][s]; };
+  auto start = [&](long long s) { return b.plan.units[0][s] + pair_share(D) * b.plan.units[1][s]; };
   const long long W = start(b.S), per = quotient(W + gridDim.x - 1, gridDim.x);
   if (!plan_matches(b, D)) {
     if (threadIdx.x == 0) record_index_error(b.status);
@@ -61,6 +66,7 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
     hi = min(hi, seq + step);
   }
   const unsigned G = b.G;
+  const uint32_t by_G = 0xffffffffu / G + 1;  // a product's high half is the quotient of up to 2^16 rows
   int buf = 0;  // the queries' buffer in turn
   for (bool begin = true; seq < b.S; ++seq, begin = false) {
     const long long base = start(seq);
@@ -97,24 +103,31 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
     };
     for (; head < b.Hkv; ++head, k = 0) {
       // kRows rows from r0 on, into the other buffer than that being read. (One barrier between two calls is enough.)
+      float z[kRows * 4 / kWeightThreads] = {};  // lse of the rows whose copies are under way
       auto stage = [&](int r0) {
         buf ^= 1;
 #pragma unroll
-        for (int j = warp; j < kRows / 8; j += kWeightThreads / 32) {
+        for (int y = 0; y < kRows * 4 / kWeightThreads; ++y) {
+          const int j = warp + y * (kWeightThreads / 32);
           if (r0 + 8 * j >= rows_all) break;
           const int r = r0 + 8 * j + g;
           const bool in = r < rows_all;
-          const unsigned tok = (in ? r : 0) / G, hd = (in ? r : 0) - tok * G;
+          const unsigned rr = in ? r : 0, tok = rr < 65536 && G > 1 ? __umulhi(rr, by_G) : rr / G, hd = rr - tok * G;
           const __nv_bfloat16* src = p.q + (long long)(ps.q0 + (int)tok) * p.q_tok + (long long)(head * G + hd) * p.q_head +
                                      c * (kPacked ? D / 4 : 8);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
             cp_async16_or_zero(smem_u32(&q_s[buf][j][i][lane]), src + (kPacked ? 8 * i : 32 * i), in);
-          if (c == 0) {
-            const float z = in ? p.lse[(long long)(ps.q0 + (int)tok) * b.Hq + head * (int)G + hd] : -INFINITY;
-            reinterpret_cast<float*>(l_s[buf])[8 * j + g] = z == -INFINITY ? -INFINITY : z * -1.4426950408889634f;
-          }
+          if (c == 0) z[y] = in ? p.lse[(long long)(ps.q0 + (int)tok) * b.Hq + head * (int)G + hd] : -INFINITY;
         }
+      };
+      // Their -lse, once it is here: later than the copies go out, so that no warp waits for it before its products.
+      auto stage_lse = [&]() {
+#pragma unroll
+        for (int y = 0; y < kRows * 4 / kWeightThreads; ++y)
+          if (c == 0)
+            reinterpret_cast<float*>(l_s[buf])[8 * (warp + y * (kWeightThreads / 32)) + g] =
+                z[y] == -INFINITY ? -INFINITY : z[y] * -1.4426950408889634f;
       };
       // This lane's place in a key (and its scale's), and of keys g of each granule.
       const long long k_tok = kPacked ? code_bytes(D) : p.c.k_tok * 2, k_page = kPacked ? p.c4.k_page : p.c.k_page * 2;
@@ -135,14 +148,17 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
       if (left <= 0) return;
       if (few) {
         stage(0);
+        stage_lse();
         cp_async_wait_all();
         __syncthreads();
       }
       const int k_end = left >= per_head ? nblk : (int)quotient(left * nblk + per_head - 1, per_head);
       for (; k < k_end; ++k) {
         const int key0 = (blk0 + k) * kBlk + warp * kKeys;
-        // Rows that see a key of the block: [r_lo, r_hi), one of this warp's unit: [r, r_end), every key of it: [full, full_end).
-        int r_lo = 0, r_hi = rows_all, r = 0, r_end = rows_all, full = key0 + kKeys <= ps.kvl ? 0 : rows_all, full_end = rows_all;
+        // Rows that see a key of the block: [r_lo, r_hi), one of this warp's unit: [r, r_end), every key of it: [full,
+        // full_end).
+        int r_lo = 0, r_hi = rows_all, r = 0, r_end = rows_all, full_end = rows_all;
+        int full = key0 + kKeys <= ps.kvl ? 0 : rows_all;
         if (b.causal) {
           const int blk_key = key0 - warp * kKeys;
           auto rows_to = [&](int tok) { return min(max(tok, 0), ps.ql) * (int)G; };
@@ -159,7 +175,10 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
           }
         }
         if (key0 >= hi || key0 + kKeys <= lo) r_end = 0;
-        if (!few && r_lo < r_hi) stage(r_lo);
+        if (!few && r_lo < r_hi) {
+          stage(r_lo);
+          stage_lse();
+        }
         bool whole = key0 >= lo && key0 + kKeys <= hi;  // every key of the unit is seen
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
@@ -294,10 +313,16 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
             if (first + kRows < r_hi) stage(first + kRows);
           }
           const int to = min(first + kRows, r_end);
-          for (int r8 = max(first, r); r8 < to; r8 += 8) {
-            if (r8 < full || min(r8 + 8, rows_all) > full_end) add(here, r8, r8 - first, std::true_type());
-            else add(here, r8, r8 - first, std::false_type());
-          }
+          int r8 = max(first, r);
+          const int from = min(max(r8, (full + 7) & ~7), to);  // [from, until): tiles whose rows see all
+          const int until = full_end == rows_all ? to : max(from, min(to, full_end & ~7));
+#pragma unroll 1
+          for (; r8 < from; r8 += 8) add(here, r8, r8 - first, std::true_type());
+#pragma unroll 1
+          for (; r8 < until; r8 += 8) add(here, r8, r8 - first, std::false_type());
+#pragma unroll 1
+          for (; r8 < to; r8 += 8) add(here, r8, r8 - first, std::true_type());
+          if (!few && first + kRows < r_hi) stage_lse();
         }
         float total[kT / 2];
 #pragma unroll
@@ -319,7 +344,7 @@ __global__ void __launch_bounds__(kWeightThreads, kWeightCtas) fa_paged_weights_
 }
 
 cudaError_t launch_paged_weights(const PagedWeights& p, int d, bool packed, int num_sms, cudaStream_t st) {
-  const int grid = kWeightCtas * num_sms;
+  const int grid = weight_ctas(d) * num_sms;
   if (d == 128) {
     if (packed) fa_paged_weights_kernel<128, true><<<grid, kWeightThreads, 0, st>>>(p);
     else fa_paged_weights_kernel<128, false><<<grid, kWeightThreads, 0, st>>>(p);
