@@ -14,8 +14,8 @@
 // stay from block to block of a head; more are copied anew for each block, 64 beside the products of the 64 before.
 //
 // Measured, 16 heads, d = 64, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys: 37.5 us; 48.7 with queries and
-// their places worked out by each warp from global memory. 1000 tokens of 32 heads over 9000 bf16 keys of 8 kv heads: 168 us
-// at d = 64, 323 at d = 128. A decode step of 64 sequences of 200 to 8192 bf16 keys, d = 128, 8 kv heads (582 MB): 93 us,
+// their places worked out by each warp from global memory. 1000 tokens of 32 heads over 9000 bf16 keys of 8 kv heads: 167 us
+// at d = 64, 345 at d = 128. A decode step of 64 sequences of 200 to 8192 bf16 keys, d = 128, 8 kv heads (582 MB): 93 us,
 // 6.26 TB/s. So a single token is bound by memory, and many rows by latencies at 12 to 16 warps per SM.
 #include <math.h>
 #include <type_traits>
@@ -55,7 +55,11 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D)) fa_paged_weigh
     if (threadIdx.x == 0) record_index_error(b.status);
     return;
   }
-  const long long u = per * blockIdx.x, u_end = min(W, u + per);
+  // CTAs that are likely to stand on one SM (every gridDim / weight_ctas-th) have shares side by side, so that each SM's sum is
+  // even where a share is a block or two: else those with two may all meet on the same SMs (399 us for the 1000 tokens at
+  // d = 128).
+  const unsigned sms = gridDim.x / weight_ctas(D), share = blockIdx.x % sms * weight_ctas(D) + blockIdx.x / sms;
+  const long long u = per * share, u_end = min(W, u + per);
   if (u >= u_end) return;
   int seq = 0;  // the last sequence that starts at or before u
   for (int hi = b.S; hi - seq > 1;) {
