@@ -6,9 +6,11 @@
 // the rotation, as a bf16 cache would have them, and quantised from that. From bf16 numbers both quotients are nearer to
 // a tie than fp32 resolves only where they are at it: the codes are those of exact arithmetic.
 //
-// One CTA per token. A thread takes eight dims, its four neighbours' lanes a group. Memory-bound for prompts: 2 bytes in per
-// element, 0.56 out, and 2 more where the caller wants the values. A few tokens are bound by the chain of plan, table and
-// stores.
+// One CTA per token or four. A thread takes eight dims, four neighbouring lanes a group. Read are 2 bytes per element, written
+// 0.56, and 2 more where the caller wants the values. 8500 tokens of 8 kv heads, d = 128, values wanted (77 MB): 17.7 us,
+// 4.4 TB/s, 65 % of the copy rate, at which they would take 11.6; the chain of look-ups before a CTA's stores is the rest. (28 with
+// divisions and one token per CTA, 25.5 with reciprocals and four loads per thread.) 1 token 2.5 us, 64 tokens 3.3: that chain
+// alone.
 #include "fa_paged4.cuh"
 #include "fa_rope.cuh"
 
@@ -18,11 +20,12 @@ constexpr int kAppendHeads = 32;  // key heads that are rotated at a time
 
 // Eight values' codes as a word, given with their group's scale and the values that they stand for. By whole groups of lanes.
 //
-// Both quotients are products with reciprocals, off by a few units of 2^-23, and their ties are made out by what numbers they can
-// be. max|x| / 7 is T 2^f / 7 with T of 8 bits: a tie of four significant bits is a number of five, and any other value is off
-// every tie by 2^-12 of itself or more, so the quotient's last four bits may be rounded away first. x / s, where it is 1/4 or more, is 2^p X / m
-// with integers X < 256, 8 <= m < 16, p >= -6: off every odd multiple of 1/2 by 2^-7 / 15 or more, or at it. So 1 / s a
-// little too small and a little too large give the same integer, or the two about a tie, of which the even one is taken.
+// Both quotients are products with reciprocals, off by a few units of 2^-23, and their ties are made out by what numbers they
+// can be. max|x| / 7 is T 2^f / 7 with T of 8 bits: a tie of four significant bits is a number of five, and any other value is
+// off every tie by 2^-12 of itself or more, so the quotient's last four bits may be rounded away first. x / s, where it is 1/4
+// or more, is 2^p X / m with integers X < 256, 8 <= m < 16, p >= -6: off every odd multiple of 1/2 by 2^-7 / 15 or more, or
+// at it. So 1 / s a little too small and a little too large give the same integer, or the two about a tie, of which the
+// even one is taken.
 __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t& scale, uint4& stored) {
   const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
   uint32_t top = 0;  // the bits of a magnitude order like it, NaN above all
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(256) fa_paged_append4_rope_kernel(const RopeLa
 }
 
 // Threads and tokens per CTA as in launch_rope: one token each, with all threads, while they fit one wave. Beyond that
-// several, so that a thread has four loads on their way while the places are looked up (8500 tokens: 28 us with one token
+// several, so that a thread has four loads on their way while the places are looked up (8500 tokens: 18 us, 28 with divisions and one token
 // of 128 threads).
 cudaError_t launch_append4(const RopeLaunch& p, const Append4& a, int d, int num_sms, cudaStream_t st) {
   const bool one_wave = p.tokens <= 6LL * num_sms;

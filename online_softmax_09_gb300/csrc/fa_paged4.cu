@@ -1,14 +1,22 @@
 // fa_paged4.cu -- attention of the newest tokens of a ragged batch over a 4-bit paged cache, sequences of few rows (the
 // mathematics, the plan and the division among CTAs are fa_paged.cu's; fa_paged4.cuh has the cache).
 //
-// fa_paged4_rows_kernel: four warps per CTA, each with every fourth granule of 16 keys and a ring of its own, filled by bulk
-// copies (a granule's codes and scales are four dense pieces: 2304 bytes at d = 128). The keys are the rows of the products'
-// tiles, the queries their columns, so that up to 8 queries cost half of what 16 cost:
+// fa_paged4_rows_kernel: per CTA one warp that walks through its stretches and hands them out, and three or seven that
+// compute, each with every third or seventh unit of 32 keys (two granules of 16, each within a page) and a ring of its own.
+// The keys are the rows of the products' tiles, the queries their columns, so that up to 8 queries cost half of what 16 cost:
 //     S^T = K Q^T (m16n8k16, A from codes),  O^T += V^T P^T (A from codes, P^T by a transposition of S^T's registers).
 // Which dims an MMA sums in which step is free as long as both operands agree, and which dims are its rows, as long as the
 // output knows: lane (g, c) of a warp (g = lane / 4, c = lane % 4) takes the quarter c of key g's dims in one piece, and of
 // values 2 c, 2 c + 1, 2 c + 8 and 2 c + 9 the g-th eighth, so codes go from shared memory to operands in registers, in 16
 // and 8 bytes per load, with one scale each, and a lane ends with 16 neighbouring dims of a query's output.
+// At the end of a stretch the warps' sums are joined in shared memory, and parts of tiles that CTAs share in the workspace.
+//
+// Bound by instructions, not by memory: one token of each of 64 sequences of 200 to 8192 keys (32 heads, 8 kv heads, d = 128,
+// 314 MB) takes 89.5 us, 3.5 TB/s or 52 % of the copy rate, at half the issue slots. Counted per 16 keys and warp: 105 for the
+// keys' operands and scores, 128 for the values' and sums, 29 for the weights, 115 for copies, loop, joins. Two sequences
+// of 131072 keys 80 us (292 MB); one of 1000 9.5, and 48 of 4 drafted tokens in a window of 1024 at d = 64 21.5: latencies of
+// plan, table, keys, joins. (A share of the work for each warp, and no joins in CTAs: 87 us for the 64 sequences, but 16 and 30
+// for those two.)
 #include <math.h>
 
 #include "fa_paged4.cuh"
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
     // kernel: 111 us for 64 sequences of 200 to 8192 keys.) A granule that no row sees, or whose page does not exist, is
     // left out.
     constexpr int kPieces = L::kScales / 16, kRounds = L::kCodes / 512;
-    uint32_t fetched = 0, in = 0, none = 0;  // stretches taken; the stage that is filled next; bits 2 i, 2 i + 1: left out in stage i
+    uint32_t fetched = 0, in = 0, none = 0;  // stretches taken; the stage that is filled next; bits 2 i: left out in stage i
     int key_in = 0, end_in = 0, lo_in = 0, hi_in = 0;
     const int* tab = nullptr;
     const uint8_t *kp = nullptr, *vp = nullptr, *sp = nullptr;

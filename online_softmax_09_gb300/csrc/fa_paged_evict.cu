@@ -4,11 +4,17 @@
 // room, the first before the last), and of those between, the heaviest; among equal weights those at lower places. They keep
 // their order. A NaN counts as the heaviest.
 //
-// fa_paged_select_kernel, one to eight CTAs per sequence and head: the m-th largest weight by its digits (11, 11 and 10 bits, or
-// four times 8, of an unsigned number in the weights' order, a histogram each), then two passes in order of place, one that counts and one that
-// writes the places kept, each warp over a stretch of its own. Weights that fit stay in shared memory between the passes.
+// fa_paged_select_kernel, one to eight CTAs per sequence and head: the m-th largest weight by its digits (11, 11 and 10 bits,
+// or four times 8, of an unsigned number in the weights' order, a histogram each), then two passes in order of place, one
+// that counts and one that writes the places kept, each warp over a stretch of its own. Weights that fit stay in shared memory
+// between the passes.
 // fa_paged_move_kernel: a CTA moves 32 slots of one head, all tensors. The pages written are others than those read, so
 // the slots move independently, and pages that sequences share stay as they are.
+//
+// Bound by latencies: plan, table, weights, a meeting of the cluster per digit, then table, slots. 8 kv heads of 32768 tokens
+// cut to 4096 (d = 128, 35 MB): 23.5 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
+// where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 18 us. (With digits of 11 bits in
+// clusters too, and keys and values moved one after the other, 33 and 29 us call by call; now 30 and 25.)
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -55,11 +61,11 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
   extern __shared__ __align__(16) uint32_t cache[];
   // Digits of 11 bits; of 8 in a cluster, whose CTAs all read all histograms (five thousand cycles each with 2048 numbers).
   constexpr int kBits = kCluster ? 8 : 11, kBins = 1 << kBits, kPasses = (32 + kBits - 1) / kBits;
-  __shared__ __align__(16) uint32_t bins[kPasses][kBins];  // of each pass, so that no pass waits for the others' reading of the one before
+  __shared__ __align__(16) uint32_t bins[kPasses][kBins];  // of each pass: none waits for the others' reading of the one before
   __shared__ uint32_t warp_sum[kSelectWarps];
   __shared__ uint32_t above_w[kSelectWarps], level_w[kSelectWarps];
   __shared__ __align__(8) uint32_t counts[2];  // of this CTA: numbers above the bound, and at it
-  __shared__ uint32_t found[2];   // the digit, and how many of its numbers stay
+  __shared__ uint32_t found[2];                // the digit, and how many of its numbers stay
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = kCluster ? (int)cluster.num_blocks() : 1, rank = kCluster ? (int)cluster.block_rank() : 0;
   auto meet = [&]() {

@@ -849,7 +849,8 @@ def paged_evict(weights, caches, plan, keep, out_table, max_keep: int, sinks: in
     ts = out_table.shape
     if out_table.dtype != torch.int32 or out_table.get_device() != i or len(ts) != 2 or ts[0] != S \
             or (out_table.stride(1) != 1 and ts[1] > 1):
-        raise ValueError(f"out_table must be an int32 CUDA tensor [{S}, out_pages] with contiguous last dim, on the plan's device")
+        raise ValueError(f"out_table must be an int32 CUDA tensor [{S}, out_pages] with contiguous last dim, on the plan's "
+                         "device")
     max_keep, sinks, recent = int(max_keep), int(sinks), int(recent)
     if not (0 <= max_keep < 2 ** 31 and 0 <= sinks < 2 ** 31 and 0 <= recent < 2 ** 31):
         raise ValueError("max_keep, sinks and recent must be at least 0 and fit 32 bits")
@@ -863,9 +864,9 @@ def paged_evict(weights, caches, plan, keep, out_table, max_keep: int, sinks: in
         kv_lens = _empty((S,), torch.int32, weights.device, stream)
     elif kv_lens.dtype != torch.int32 or kv_lens.get_device() != i or kv_lens.shape != (S,) or not kv_lens.is_contiguous():
         raise ValueError(f"kv_lens must be a contiguous int32 CUDA tensor {[S]}")
-    r = (_lib or lib()).fa_paged_evict(weights.data_ptr(), _ll2(*ws), rows, len(caches) + 1, pages, plan._ref, keep.data_ptr(), max_keep,
-                                       sinks, recent, out_table.data_ptr(), out_table.stride(0), ts[1],
-                                       kept.data_ptr(), kv_lens.data_ptr(), raw)
+    r = (_lib or lib()).fa_paged_evict(weights.data_ptr(), _ll2(*ws), rows, len(caches) + 1, pages, plan._ref,
+                                       keep.data_ptr(), max_keep, sinks, recent, out_table.data_ptr(), out_table.stride(0),
+                                       ts[1], kept.data_ptr(), kv_lens.data_ptr(), raw)
     if r != FA_OK:
         raise FAError(r, "fa_paged_evict")
     return kept, kv_lens
