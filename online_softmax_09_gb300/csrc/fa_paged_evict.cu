@@ -12,8 +12,8 @@
 // the slots move independently, and pages that sequences share stay as they are.
 //
 // Bound by latencies: plan, table, weights, a meeting of the cluster per digit, then table, slots. 8 kv heads of 32768 tokens
-// cut to 4096 (d = 128, 35 MB): 23.5 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
-// where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 18 us. (With digits of 11 bits in
+// cut to 4096 (d = 128, 35 MB): 22.3 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
+// where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 14.2 us. (With digits of 11 bits in
 // clusters too, and keys and values moved one after the other, 33 and 29 us call by call; now 30 and 25.)
 #include <cooperative_groups.h>
 #include <math.h>
@@ -26,7 +26,9 @@ namespace fa {
 
 constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectMost = 44 * 1024;  // weights held in shared memory
-constexpr int kMoveSlots = 32, kMoveThreads = 256;
+// A chain of look-ups stands before each CTA's copies, so many small ones: 32 sequences cut to 500 tokens 14.2 us, 17.6 with
+// 256 threads for 32 slots (14.0 with 64, but 23.5 for the long sequence), 14.8 with 64 for 16.
+constexpr int kMoveSlots = 32, kMoveThreads = 128;
 
 // What of a sequence's n tokens stays: places [0, a), [b, n), and m of those between.
 struct Split {
