@@ -15,8 +15,8 @@
 //
 // Measured, 16 heads, d = 64, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys: 37.5 us; 48.7 with queries and
 // their places worked out by each warp from global memory. 1000 tokens of 32 heads over 9000 bf16 keys of 8 kv heads: 167 us
-// at d = 64, 345 at d = 128. A decode step of 64 sequences of 200 to 8192 bf16 keys, d = 128, 8 kv heads (582 MB): 93 us,
-// 6.26 TB/s. So a single token is bound by memory, and many rows by latencies at 12 to 16 warps per SM.
+// at d = 64, 345 at d = 128. A decode step of 64 sequences of 200 to 8192 bf16 keys, d = 128, 8 kv heads (582 MB): 94 us,
+// 6.2 TB/s. So a single token is bound by memory, and many rows by latencies at 12 to 16 warps per SM.
 #include <math.h>
 #include <type_traits>
 
