@@ -110,6 +110,14 @@ def test_many_heads_per_kv_head_and_many_sequences(fa, d):
     run(fa, Batch4(fa, lens, 2, 1, d, 16, seed=2))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 500])
+def test_chunks_beside_single_tokens(fa, d, window):
+    """Both kinds of tiles at once, the pairs shared by several CTAs and joined behind the small tiles."""
+    lens = [(1, 700), (90, 3000), (1, 2000)] + [(1, 40 + 13 * i) for i in range(30)] + [(150, 150), (2, 1500)]
+    run(fa, Batch4(fa, lens, 4, 2, d, 64, seed=d + window, lead=1, pad=2), True, window)
+
+
 @pytest.mark.parametrize("ql", [4, 40])
 def test_more_new_tokens_than_cached_ones(fa, ql):
     """The first of them stand before the sequence and see nothing."""

@@ -100,6 +100,21 @@ def test_several_tokens(fa, four, d, page, causal, window):
 
 
 @pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(64, 1), (65, 1), (130, 2), (200, 1)])
+def test_many_heads_per_kv_head(fa, four, d, Hq, Hkv):
+    """Rows that fill the queries' buffer, and more: they are copied anew for each block."""
+    run(fa, make(fa, four, [(1, 300), (0, 5), (1, 1), (2, 140)], Hq, Hkv, d, 32, seed=Hq), four)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 30), (True, 300)])
+def test_chunks_beside_single_tokens(fa, four, causal, window):
+    lens = [(1, 900), (70, 400), (1, 1), (1, 33), (130, 130), (3, 257), (20, 1000)]
+    run(fa, make(fa, four, lens, 4, 2, 128, 16, seed=9, lead=1), four, causal, window)
+
+
+@pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("inplace", [False, True])
 def test_many_sequences_in_place_or_not(fa, four, inplace):
     r = np.random.RandomState(3)
