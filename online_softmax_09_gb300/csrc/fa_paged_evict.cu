@@ -12,7 +12,7 @@
 // the slots move independently, and pages that sequences share stay as they are.
 //
 // Bound by latencies: plan, table, weights, a meeting of the cluster per digit, then table, slots. 8 kv heads of 32768 tokens
-// cut to 4096 (d = 128, 35 MB): 22.3 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
+// cut to 4096 (d = 128, 35 MB): 21.4 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
 // where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 14.2 us. (With digits of 11 bits in
 // clusters too, and keys and values moved one after the other, 33 and 29 us call by call; now 30 and 25.)
 #include <cooperative_groups.h>
@@ -56,24 +56,24 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return x & 0x80000000u ? ~x : x | 0x80000000u;
 }
 
-// A cluster of CTAs per sequence and head, each with a stretch of the places of its own: the histograms and counts of all are
-// added up through distributed shared memory.
+// A cluster of CTAs per sequence and head, each with a stretch of the places of its own: every CTA puts its histograms and
+// counts into the shared memory of all, and adds up what it has there: nothing waits for a write. (Read from the others
+// behind the barrier, the long sequence took 22.3 us; so 21.4. Equal digits of a warp counted together first: 22.3 again.)
 template <bool kCluster>  // (else one CTA has all places)
 __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const PagedEvict p, int held) {
   extern __shared__ __align__(16) uint32_t cache[];
-  // Digits of 11 bits; of 8 in a cluster, whose CTAs all read all histograms (five thousand cycles each with 2048 numbers).
+  // Digits of 11 bits; of 8 in a cluster, whose CTAs all get all histograms.
   constexpr int kBits = kCluster ? 8 : 11, kBins = 1 << kBits, kPasses = (32 + kBits - 1) / kBits;
   __shared__ __align__(16) uint32_t bins[kPasses][kBins];  // of each pass: none waits for the others' reading of the one before
+  constexpr int kMost = kCluster ? 8 : 1, kQuads = kBins / 4;
+  // Of all CTAs, for passes in turn: who writes a pass's again two passes later has met all that read it.
+  __shared__ uint4 all_bins[kCluster ? 2 : 1][kMost][kCluster ? kQuads : 1];
+  __shared__ uint2 all_counts[kMost];  // of each CTA: numbers above the bound, and at it
   __shared__ uint32_t warp_sum[kSelectWarps];
   __shared__ uint32_t above_w[kSelectWarps], level_w[kSelectWarps];
-  __shared__ __align__(8) uint32_t counts[2];  // of this CTA: numbers above the bound, and at it
-  __shared__ uint32_t found[2];                // the digit, and how many of its numbers stay
+  __shared__ uint32_t found[2];  // the digit, and how many of its numbers stay
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = kCluster ? (int)cluster.num_blocks() : 1, rank = kCluster ? (int)cluster.block_rank() : 0;
-  auto meet = [&]() {
-    if constexpr (kCluster) cluster.sync();
-    else __syncthreads();
-  };
   const PagedBatch& b = p.b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
   for (int i = at; i < s.a; i += all) kept[i] = i;
   for (int i = at; i < s.n - s.b; i += all) kept[s.a + s.m + i] = s.b + i;
   if (s.m == 0) return;
+  if constexpr (kCluster) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // this CTA's memory is there
   const int* tab = b.table + (long long)seq * b.table_stride;
   const float* w = p.weights + (long long)head * p.w_head;
   const int each = ((s.b - s.a + C - 1) / C + 31) & ~31;  // places of a CTA: those from s.a + rank * each on
@@ -135,16 +136,22 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
         }
       }
     }
-    meet();
+    __syncthreads();
+    if constexpr (kCluster) {
+      if (pass == 0) asm volatile("barrier.cluster.wait;" ::: "memory");  // the others' too
+      for (int i = tid; i < C * kQuads; i += kSelectThreads)
+        *cluster.map_shared_rank(&all_bins[pass & 1][rank][i % kQuads], i / kQuads) =
+            reinterpret_cast<const uint4*>(bins[pass])[i % kQuads];
+      cluster.sync();
+    }
     // Numbers with a larger digit, for each: thread t has digits kBins - 1 - 4 t and the three below, if there are so many.
     uint32_t v[4] = {0, 0, 0, 0}, sum = 0;
-    constexpr int kMost = kCluster ? 8 : 1;
-    uint4 h[kMost];  // all CTAs' at once: a read from another SM takes about a microsecond
+    uint4 h[kMost];
 #pragma unroll
     for (int c = 0; c < kMost; ++c) {
-      const uint32_t* own = &bins[pass][kBins - 4 - 4 * tid];
       h[c] = make_uint4(0, 0, 0, 0);
-      if (c < C && 4 * tid < kBins) h[c] = *reinterpret_cast<const uint4*>(kCluster ? cluster.map_shared_rank(own, c) : own);
+      if (c < C && tid < kQuads)
+        h[c] = kCluster ? all_bins[pass & 1][c][kQuads - 1 - tid] : reinterpret_cast<const uint4*>(bins[pass])[kQuads - 1 - tid];
     }
 #pragma unroll
     for (int c = 0; c < kMost; ++c) {
@@ -194,19 +201,22 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     level_w[warp] = level;
   }
   __syncthreads();
-  if (tid < 2) {
-    uint32_t x = 0;
-    for (int i = 0; i < kSelectWarps; ++i) x += tid == 0 ? above_w[i] : level_w[i];
-    counts[tid] = x;
-  }
-  if constexpr (kCluster) cluster.sync();
   uint32_t at_above = 0, at_level = 0;  // before this lane's place
-#pragma unroll
-  for (int c = 0; c < (kCluster ? 7 : 0); ++c) {
-    if (c >= rank) continue;
-    const uint2 x = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(counts, c));
-    at_above += x.x;
-    at_level += x.y;
+  if constexpr (kCluster) {
+    if (tid < C) {
+      uint2 x = make_uint2(0, 0);
+      for (int i = 0; i < kSelectWarps; ++i) {
+        x.x += above_w[i];
+        x.y += level_w[i];
+      }
+      *cluster.map_shared_rank(&all_counts[rank], tid) = x;
+    }
+    __syncwarp();
+    cluster.sync();  // (the last that one CTA needs of another)
+    for (int c = 0; c < rank; ++c) {
+      at_above += all_counts[c].x;
+      at_level += all_counts[c].y;
+    }
   }
   for (int i = 0; i < warp; ++i) {
     at_above += above_w[i];
@@ -223,7 +233,6 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
     at_above += __popc(ma);
     at_level += __popc(ml);
   }
-  if constexpr (kCluster) cluster.sync();  // (until the others have read the counts)
 }
 
 __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const PagedEvict p) {
