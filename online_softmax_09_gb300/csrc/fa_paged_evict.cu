@@ -12,8 +12,8 @@
 // the slots move independently, and pages that sequences share stay as they are.
 //
 // Bound by latencies: plan, table, weights, a meeting of the cluster per digit, then table, slots. 8 kv heads of 32768 tokens
-// cut to 4096 (d = 128, 35 MB): 21.4 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
-// where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 14.2 us. (With digits of 11 bits in
+// cut to 4096 (d = 128, 35 MB): 20.9 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
+// where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 14.0 us. (With digits of 11 bits in
 // clusters too, and keys and values moved one after the other, 33 and 29 us call by call; now 30 and 25.)
 #include <cooperative_groups.h>
 #include <math.h>
@@ -238,23 +238,26 @@ __global__ void __launch_bounds__(kSelectThreads) fa_paged_select_kernel(const P
 __global__ void __launch_bounds__(kMoveThreads) fa_paged_move_kernel(const PagedEvict p) {
   __shared__ int page_s[kMoveSlots], slot_s[kMoveSlots], to_s[kMoveSlots];  // a page below 0: nothing to move
   const PagedBatch& b = p.b;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the places are known
   const unsigned chunks = (p.max_keep + kMoveSlots - 1) / kMoveSlots, row = blockIdx.x / chunks;
   const int seq = (int)(row / b.Hkv), head = (int)(row - seq * b.Hkv), tid = threadIdx.x;
   const int i0 = (int)(blockIdx.x - row * chunks) * kMoveSlots;
   const int n = min(kMoveSlots, split_of(p, seq).fresh - i0);
-  if (n <= 0 || !plan_matches(b, b.d)) return;
+  // What the selection does not write is looked up before its end (21.4 us for the long sequence otherwise, 20.9 so). All CTAs
+  // wait for it, so that this kernel does not end before it.
+  const bool mine = plan_matches(b, b.d);
+  const int out_page = tid < n ? p.out_table[(long long)seq * p.out_stride + ((i0 + tid) >> b.page_shift)] : -1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the places are known
+  if (n <= 0 || !mine) return;
   if (tid < n) {
     const int i = i0 + tid, key = p.kept[((long long)seq * b.Hkv + head) * p.max_keep + i];
     int page = b.table[(long long)seq * b.table_stride + (key >> b.page_shift)];
-    int to = p.out_table[(long long)seq * p.out_stride + (i >> b.page_shift)];
-    if ((unsigned)page >= (unsigned)b.num_pages || (unsigned)to >= (unsigned)b.num_pages) {
+    if ((unsigned)page >= (unsigned)b.num_pages || (unsigned)out_page >= (unsigned)b.num_pages) {
       record_index_error(b.status);
       page = -1;
     }
     page_s[tid] = page;
     slot_s[tid] = key & (b.page_size - 1);
-    to_s[tid] = to;
+    to_s[tid] = out_page;
   }
   __syncthreads();
   // Two tensors whose slots are alike (keys and values, say), or one twice over: their loads go out together.
