@@ -30,7 +30,7 @@
 // Over a 4-bit cache (kPacked) warps 8-11 make the operands in place of the TMA's boxes, and the producer (12), the MMA warp (13)
 // and two idle ones stand behind them: 512 tokens over 32768 keys take 262 us, 1040 TFLOP/s. (With two unpacking warps 330; with
 // loads that lanes share evenly, at more instructions, 271.) It follows the count of instructions: 7450 per block and pair of
-// tiles, 5400 over bf16. Blocks are always taken in their order: codes of 8 heads of 100 000 tokens fit L2 (1152 bytes a token).
+// tiles, 5400 over bf16.
 #include <cudaTypedefs.h>
 #include <math.h>
 
@@ -942,11 +942,17 @@ cudaError_t launch_paged_tiles(const TileMaps& m, const PagedFwd& p, int d, int 
               : launch_tiles<64, false, false>(m, p, none, num_sms, st);
 }
 
-// Over a 4-bit cache (m.k and m.v are not read) the keys of fewer than a quarter of the bytes stay in L2.
+// Over a 4-bit cache (m.k and m.v are not read) from 96 MB on, by the table's width as above: 512 tokens of 32 heads over
+// 100 000 keys of 8 kv heads (115 MB) take 762 us with the turned order, 840 without, over 131 072 1033 and 1109 (d = 64, 250 000
+// keys, 144 MB: 1423, 1511); where the codes stay in L2 it costs up to 1 % (60 000 keys, 69 MB: 466, 465; d = 64: 350, 346).
 cudaError_t launch_paged4_tiles(const TileMaps& m, const PagedFwd& p, const PagedCache4& cache, int d, int num_sms,
                                 cudaStream_t st) {
-  return d == 128 ? launch_tiles<128, false, true>(m, p, cache, num_sms, st)
-                  : launch_tiles<64, false, true>(m, p, cache, num_sms, st);
+  const bool turn = (long long)p.b.max_pages * p.b.page_size * p.b.Hkv * 2 * (code_bytes(d) + scale_bytes(d)) > (96LL << 20);
+  if (d == 128)
+    return turn ? launch_tiles<128, true, true>(m, p, cache, num_sms, st)
+                : launch_tiles<128, false, true>(m, p, cache, num_sms, st);
+  return turn ? launch_tiles<64, true, true>(m, p, cache, num_sms, st)
+              : launch_tiles<64, false, true>(m, p, cache, num_sms, st);
 }
 
 }  // namespace fa

@@ -118,6 +118,16 @@ def test_chunks_beside_single_tokens(fa, d, window):
     run(fa, Batch4(fa, lens, 4, 2, d, 64, seed=d + window, lead=1, pad=2), True, window)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 900)])
+def test_chunks_under_a_table_for_long_contexts(fa, d, causal, window):
+    """Blocks in the turned order, as for codes that do not fit L2."""
+    page, Hkv = 256, 2
+    cols = (100 << 20) // (page * Hkv * 2 * (d // 2 + d // 16)) + 1
+    lens = [(70, 5000), (1, 300), (260, 1500), (40, 40)]
+    run(fa, Batch4(fa, lens, 4, Hkv, d, page, seed=d, extra_cols=cols), causal, window)
+
+
 @pytest.mark.parametrize("ql", [4, 40])
 def test_more_new_tokens_than_cached_ones(fa, ql):
     """The first of them stand before the sequence and see nothing."""
