@@ -422,7 +422,7 @@ int fa_fwd_paged4(const void *q, const long long *q_strides, const fa_paged_cach
  *              its kv head,
  * where weights[t] counts as 0 for the step's own tokens, so that a page needs no clearing when it is given to a sequence
  * (call it once for every step). Other slots are not written.
- *   lse      : [T][Hq] fp32, contiguous, as fa_fwd_paged writes it. A query with lse = -inf gives no weight.
+ *   lse      : [T][Hq] fp32, contiguous, as fa_fwd_paged writes it. A query with lse = -inf gives no weight, whatever it holds.
  *   weights, out : fp32, element (page, head, slot) at page * stride + head * stride + slot; weight_strides: HOST,
  *              (page, head) of weights, then of out, in elements, a page's below 2^32. out may be weights (with its strides);
  *              it must not overlap it otherwise. Where sequences of the batch share pages, what they add to a slot is all

@@ -11,12 +11,14 @@
 //
 // The queries go by as columns, 8 rows at a time, from shared memory: 64 rows in the order of the lanes' operands, with
 // their -lse in base 2, so that a tile costs its products, exponentials and sums and few instructions more. Up to 64 rows
-// stay from block to block of a head; more are copied anew for each block, 64 beside the products of the 64 before.
+// stay from block to block of a head; more are copied anew for each block, 64 beside the products of the 64 before. Tiles whose
+// rows see every key of a unit go by without masks, but for 64 rows with an lse of -inf among them, whose scores may be anything.
 //
-// Measured, 16 heads, d = 64, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys: 37.5 us; 48.7 with queries and
+// Measured, 16 heads, d = 64, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys: 36 us; 48.7 with queries and
 // their places worked out by each warp from global memory. 1000 tokens of 32 heads over 9000 bf16 keys of 8 kv heads: 167 us
-// at d = 64, 345 at d = 128. A decode step of 64 sequences of 200 to 8192 bf16 keys, d = 128, 8 kv heads (582 MB): 94 us,
-// 6.2 TB/s. So a single token is bound by memory, and many rows by latencies at 12 to 16 warps per SM.
+// at d = 64, 353 at d = 128 (345 without the look for an lse of -inf). A decode step of 64 sequences of 200 to 8192 bf16 keys,
+// d = 128, 8 kv heads (582 MB): 93 us, 6.2 TB/s. So a single token is bound by memory, and many rows by latencies at 12 to 16
+// warps per SM.
 #include <math.h>
 #include <type_traits>
 
@@ -106,7 +108,8 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D)) fa_paged_weigh
       }
     };
     for (; head < b.Hkv; ++head, k = 0) {
-      // kRows rows from r0 on, into the other buffer than that being read. (One barrier between two calls is enough.)
+      // kRows rows from r0 on, into the other buffer than that being read. (One barrier between two calls is enough.) Behind the
+      // last row its tile is filled up with copies of it at weight 0: of zeros, an infinite key would make NaN.
       float z[kRows * 4 / kWeightThreads] = {};  // lse of the rows whose copies are under way
       auto stage = [&](int r0) {
         buf ^= 1;
@@ -116,22 +119,26 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D)) fa_paged_weigh
           if (r0 + 8 * j >= rows_all) break;
           const int r = r0 + 8 * j + g;
           const bool in = r < rows_all;
-          const unsigned rr = in ? r : 0, tok = rr < 65536 && G > 1 ? __umulhi(rr, by_G) : rr / G, hd = rr - tok * G;
+          const unsigned rr = in ? r : rows_all - 1, tok = rr < 65536 && G > 1 ? __umulhi(rr, by_G) : rr / G, hd = rr - tok * G;
           const __nv_bfloat16* src = p.q + (long long)(ps.q0 + (int)tok) * p.q_tok + (long long)(head * G + hd) * p.q_head +
                                      c * (kPacked ? D / 4 : 8);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
-            cp_async16_or_zero(smem_u32(&q_s[buf][j][i][lane]), src + (kPacked ? 8 * i : 32 * i), in);
-          if (c == 0) z[y] = in ? p.lse[(long long)(ps.q0 + (int)tok) * b.Hq + head * (int)G + hd] : -INFINITY;
+            cp_async16(smem_u32(&q_s[buf][j][i][lane]), src + (kPacked ? 8 * i : 32 * i));
+          if (c == 0) z[y] = in ? p.lse[(long long)(ps.q0 + (int)tok) * b.Hq + head * (int)G + hd] : INFINITY;
         }
       };
+      bool shut = false;  // a row that is staged has lse = -inf: among this thread's, and after a barrier among all
       // Their -lse, once it is here: later than the copies go out, so that no warp waits for it before its products.
       auto stage_lse = [&]() {
+        shut = false;
 #pragma unroll
-        for (int y = 0; y < kRows * 4 / kWeightThreads; ++y)
+        for (int y = 0; y < kRows * 4 / kWeightThreads; ++y) {
+          shut = shut || z[y] == -INFINITY;
           if (c == 0)
             reinterpret_cast<float*>(l_s[buf])[8 * (warp + y * (kWeightThreads / 32)) + g] =
                 z[y] == -INFINITY ? -INFINITY : z[y] * -1.4426950408889634f;
+        }
       };
       // This lane's place in a key (and its scale's), and of keys g of each granule.
       const long long k_tok = kPacked ? code_bytes(D) : p.c.k_tok * 2, k_page = kPacked ? p.c4.k_page : p.c.k_page * 2;
@@ -154,195 +161,202 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D)) fa_paged_weigh
         stage(0);
         stage_lse();
         cp_async_wait_all();
-        __syncthreads();
+        shut = __syncthreads_or(shut);
       }
       const int k_end = left >= per_head ? nblk : (int)quotient(left * nblk + per_head - 1, per_head);
-      for (; k < k_end; ++k) {
-        const int key0 = (blk0 + k) * kBlk + warp * kKeys;
-        // Rows that see a key of the block: [r_lo, r_hi), one of this warp's unit: [r, r_end), every key of it: [full,
-        // full_end).
-        int r_lo = 0, r_hi = rows_all, r = 0, r_end = rows_all, full_end = rows_all;
-        int full = key0 + kKeys <= ps.kvl ? 0 : rows_all;
-        if (b.causal) {
-          const int blk_key = key0 - warp * kKeys;
-          auto rows_to = [&](int tok) { return min(max(tok, 0), ps.ql) * (int)G; };
-          r_lo = rows_to(blk_key - first_new) & ~7;
-          r = rows_to(key0 - first_new) & ~7;
-          full = rows_to(key0 + kKeys - 1 - first_new);
-          if (b.window > 0) {
-            auto before = [&](int key) {  // rows whose windows begin at or before the key
-              return (int)min(max((long long)key + b.window - first_new, 0LL), (long long)ps.ql) * (int)G;
-            };
-            r_hi = before(blk_key + kBlk - 1);
-            r_end = before(key0 + kKeys - 1);
-            full_end = before(key0);
-          }
-        }
-        if (key0 >= hi || key0 + kKeys <= lo) r_end = 0;
-        if (!few && r_lo < r_hi) {
-          stage(r_lo);
-          stage_lse();
-        }
-        bool whole = key0 >= lo && key0 + kKeys <= hi;  // every key of the unit is seen
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          if (page[t] >= b.num_pages || page[t] < -1) {
-            record_index_error(b.status);
-            page[t] = -1;
-          }
-          whole = whole && page[t] >= 0;
-        }
-        // ---- keys g, g + 8 of each granule as A operands
-        uint32_t a[kT][D / 16][4];
-        auto read = [&](int t, auto all) {
-          const int at = key0 + 16 * t, slot = at & (b.page_size - 1);
-          const long long pg = decltype(all)::value || page[t] >= 0 ? page[t] : 0;
-          const uint8_t* row = k_lane + (kPacked ? (uint64_t)(uint32_t)pg * (uint32_t)k_page : (uint64_t)(pg * k_page)) +
-                               slot * k_tok;
-          [[maybe_unused]] const uint8_t* scale =
-              s_lane + (kPacked ? (uint64_t)(uint32_t)pg * (uint32_t)p.c4.ks_page + slot * scale_bytes(D) : 0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h, row += 8 * k_tok) {
-            const int key = at + 8 * h + g;
-            const bool in = decltype(all)::value || (page[t] >= 0 && key >= lo && key < hi);
-            if constexpr (kPacked) {
-              uint32_t w[D / 32];
-              if constexpr (D == 128) {
-                const uint4 v = in ? *reinterpret_cast<const uint4*>(row) : make_uint4(0, 0, 0, 0);
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-              } else {
-                const uint2 v = in ? *reinterpret_cast<const uint2*>(row) : make_uint2(0, 0);
-                w[0] = v.x, w[1] = v.y;
-              }
-              const uint32_t s2 = in ? *reinterpret_cast<const uint16_t*>(scale + 8 * h * scale_bytes(D)) * 0x10001u : 0u;
-              const uint32_t cs = scale_shift(s2);
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  a[t][i][2 * e + h] = fma_bf16x2(code_pair(w[i >> 1], 2 * (i & 1) + e), s2, cs);
-            } else {
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                const uint4 v = in ? *reinterpret_cast<const uint4*>(row + 64 * i) : make_uint4(0, 0, 0, 0);
-                a[t][2 * i][h] = v.x;
-                a[t][2 * i][2 + h] = v.y;
-                a[t][2 * i + 1][h] = v.z;
-                a[t][2 * i + 1][2 + h] = v.w;
-              }
+      // (As code of its own for few rows: with one loop for both, the decode step over 4-bit keys took 159 us in place of 137.)
+      auto blocks = [&](auto small) {
+        constexpr bool kFew = decltype(small)::value;
+        for (; k < k_end; ++k) {
+          const int key0 = (blk0 + k) * kBlk + warp * kKeys;
+          // Rows that see a key of the block: [r_lo, r_hi), one of this warp's unit: [r, r_end), every key of it: [full,
+          // full_end).
+          int r_lo = 0, r_hi = rows_all, r = 0, r_end = rows_all, full_end = rows_all;
+          int full = key0 + kKeys <= ps.kvl ? 0 : rows_all;
+          if (b.causal) {
+            const int blk_key = key0 - warp * kKeys;
+            auto rows_to = [&](int tok) { return min(max(tok, 0), ps.ql) * (int)G; };
+            r_lo = rows_to(blk_key - first_new) & ~7;
+            r = rows_to(key0 - first_new) & ~7;
+            full = rows_to(key0 + kKeys - 1 - first_new);
+            if (b.window > 0) {
+              auto before = [&](int key) {  // rows whose windows begin at or before the key
+                return (int)min(max((long long)key + b.window - first_new, 0LL), (long long)ps.ql) * (int)G;
+              };
+              r_hi = before(blk_key + kBlk - 1);
+              r_end = before(key0 + kKeys - 1);
+              full_end = before(key0);
             }
           }
-        };
-        if (__all_sync(0xffffffffu, whole)) {
+          if (key0 >= hi || key0 + kKeys <= lo) r_end = 0;
+          if (!kFew && r_lo < r_hi) {
+            stage(r_lo);
+            stage_lse();
+          }
+          bool whole = key0 >= lo && key0 + kKeys <= hi;  // every key of the unit is seen
 #pragma unroll
-          for (int t = 0; t < kT; ++t) read(t, std::true_type());
-        } else {
+          for (int t = 0; t < kT; ++t) {
+            if (page[t] >= b.num_pages || page[t] < -1) {
+              record_index_error(b.status);
+              page[t] = -1;
+            }
+            whole = whole && page[t] >= 0;
+          }
+          // ---- keys g, g + 8 of each granule as A operands
+          uint32_t a[kT][D / 16][4];
+          auto read = [&](int t, auto all) {
+            const int at = key0 + 16 * t, slot = at & (b.page_size - 1);
+            const long long pg = decltype(all)::value || page[t] >= 0 ? page[t] : 0;
+            const uint8_t* row = k_lane + (kPacked ? (uint64_t)(uint32_t)pg * (uint32_t)k_page : (uint64_t)(pg * k_page)) +
+                                 slot * k_tok;
+            [[maybe_unused]] const uint8_t* scale =
+                s_lane + (kPacked ? (uint64_t)(uint32_t)pg * (uint32_t)p.c4.ks_page + slot * scale_bytes(D) : 0);
 #pragma unroll
-          for (int t = 0; t < kT; ++t) read(t, std::false_type());
-        }
-        // This lane's keys for the sums: number c + 4 y of (granule, first or second eight), of those the g-th.
-        float old[kT / 2];
-        float* out[kT / 2];
-        bool adds[kT / 2];
+            for (int h = 0; h < 2; ++h, row += 8 * k_tok) {
+              const int key = at + 8 * h + g;
+              const bool in = decltype(all)::value || (page[t] >= 0 && key >= lo && key < hi);
+              if constexpr (kPacked) {
+                uint32_t w[D / 32];
+                if constexpr (D == 128) {
+                  const uint4 v = in ? *reinterpret_cast<const uint4*>(row) : make_uint4(0, 0, 0, 0);
+                  w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                } else {
+                  const uint2 v = in ? *reinterpret_cast<const uint2*>(row) : make_uint2(0, 0);
+                  w[0] = v.x, w[1] = v.y;
+                }
+                const uint32_t s2 = in ? *reinterpret_cast<const uint16_t*>(scale + 8 * h * scale_bytes(D)) * 0x10001u : 0u;
+                const uint32_t cs = scale_shift(s2);
 #pragma unroll
-        for (int y = 0; y < kT / 2; ++y) {
-          const int my = key0 + 32 * y + 8 * c + g, pg = c < 2 ? page[2 * y] : page[2 * y + 1];
-          const unsigned slot = my & (b.page_size - 1);
-          const bool mine = pg >= 0 && my >= lo && my < hi, was = my < first_new;
-          out[y] = mine ? out_lane + (uint64_t)(uint32_t)pg * (uint32_t)p.out_page + slot : nullptr;
-          adds[y] = was && p.old == p.out;  // (pages may be shared by sequences)
-          old[y] = mine && was && !adds[y] ? old_lane[(uint64_t)(uint32_t)pg * (uint32_t)p.old_page + slot] : 0.f;
-        }
+                for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int t = 0; t < kT; ++t) page[t] = page_next[t];
-        // The next block's keys on their way into L2: lane i brings key i.
-        if (!kPacked && k + 1 < nblk) {
+                  for (int e = 0; e < 2; ++e)
+                    a[t][i][2 * e + h] = fma_bf16x2(code_pair(w[i >> 1], 2 * (i & 1) + e), s2, cs);
+              } else {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                  const uint4 v = in ? *reinterpret_cast<const uint4*>(row + 64 * i) : make_uint4(0, 0, 0, 0);
+                  a[t][2 * i][h] = v.x;
+                  a[t][2 * i][2 + h] = v.y;
+                  a[t][2 * i + 1][h] = v.z;
+                  a[t][2 * i + 1][2 + h] = v.w;
+                }
+              }
+            }
+          };
+          if (__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+            for (int t = 0; t < kT; ++t) read(t, std::true_type());
+          } else {
+#pragma unroll
+            for (int t = 0; t < kT; ++t) read(t, std::false_type());
+          }
+          // This lane's keys for the sums: number c + 4 y of (granule, first or second eight), of those the g-th.
+          float old[kT / 2];
+          float* out[kT / 2];
+          bool adds[kT / 2];
 #pragma unroll
           for (int y = 0; y < kT / 2; ++y) {
-            const int key = key0 + kBlk + 32 * y + lane, pg = lane < 16 ? page[2 * y] : page[2 * y + 1];
-            if (pg >= 0 && pg < b.num_pages && key < hi) {
-              const uint8_t* at = k_head + (long long)pg * k_page + (long long)(key & (b.page_size - 1)) * k_tok;
-#pragma unroll
-              for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
-            }
-          }
-        }
-        entries(key0 + 2 * kBlk, page_next);
-        // ---- rows [r, r_end) that may see them
-        float sum[kT][2];
-#pragma unroll
-        for (int t = 0; t < kT; ++t) sum[t][0] = sum[t][1] = 0.f;
-        auto add = [&](int buf, int r, int at, auto some) {  // rows r .. r + 7, which stand from row `at` of a buffer on
-          const float2 l2 = l_s[buf][(at >> 1) + c];
-          float x[kT][4];
-#pragma unroll
-          for (int t = 0; t < kT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {  // (the granules' products take turns, not each its own sum's steps)
-            const uint4 q = q_s[buf][at >> 3][i][lane];
-#pragma unroll
-            for (int t = 0; t < kT; ++t) mma16816(x[t], a[t][2 * i], q.x, q.y);
-#pragma unroll
-            for (int t = 0; t < kT; ++t) mma16816(x[t], a[t][2 * i + 1], q.z, q.w);
-          }
-          int klim[2], klo[2];
-          if (decltype(some)::value) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int pos = first_new + (int)((unsigned)(r + 2 * c + e) / G);
-              klim[e] = b.causal ? min(pos, ps.kvl - 1) : ps.kvl - 1;
-              klo[e] = mask_from(pos, b.window);
-            }
+            const int my = key0 + 32 * y + 8 * c + g, pg = c < 2 ? page[2 * y] : page[2 * y + 1];
+            const unsigned slot = my & (b.page_size - 1);
+            const bool mine = pg >= 0 && my >= lo && my < hi, was = my < first_new;
+            out[y] = mine ? out_lane + (uint64_t)(uint32_t)pg * (uint32_t)p.out_page + slot : nullptr;
+            adds[y] = was && p.old == p.out;  // (pages may be shared by sequences)
+            old[y] = mine && was && !adds[y] ? old_lane[(uint64_t)(uint32_t)pg * (uint32_t)p.old_page + slot] : 0.f;
           }
 #pragma unroll
-          for (int t = 0; t < kT; ++t)
+          for (int t = 0; t < kT; ++t) page[t] = page_next[t];
+          // The next block's keys on their way into L2: lane i brings key i.
+          if (!kPacked && k + 1 < nblk) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float l = e & 1 ? l2.y : l2.x;
-              float w = ex2(fmaf(x[t][e], p.scale_log2, l));
-              if (decltype(some)::value) {
-                const int key = key0 + 16 * t + 8 * (e >> 1) + g;
-                w = key <= klim[e & 1] && key >= klo[e & 1] && l != -INFINITY ? w : 0.f;
+            for (int y = 0; y < kT / 2; ++y) {
+              const int key = key0 + kBlk + 32 * y + lane, pg = lane < 16 ? page[2 * y] : page[2 * y + 1];
+              if (pg >= 0 && pg < b.num_pages && key < hi) {
+                const uint8_t* at = k_head + (long long)pg * k_page + (long long)(key & (b.page_size - 1)) * k_tok;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
               }
-              sum[t][e >> 1] += w;
             }
-        };
-        for (int first = few ? 0 : r_lo; first < r_hi; first += kRows) {
-          const int here = buf;
-          if (!few) {
-            cp_async_wait_all();
-            __syncthreads();  // these rows are there, and nobody reads the other buffer any more
-            if (first + kRows < r_hi) stage(first + kRows);
           }
-          const int to = min(first + kRows, r_end);
-          int r8 = max(first, r);
-          const int from = min(max(r8, (full + 7) & ~7), to);  // [from, until): tiles whose rows see all
-          const int until = full_end == rows_all ? to : max(from, min(to, full_end & ~7));
-#pragma unroll 1
-          for (; r8 < from; r8 += 8) add(here, r8, r8 - first, std::true_type());
-#pragma unroll 1
-          for (; r8 < until; r8 += 8) add(here, r8, r8 - first, std::false_type());
-#pragma unroll 1
-          for (; r8 < to; r8 += 8) add(here, r8, r8 - first, std::true_type());
-          if (!few && first + kRows < r_hi) stage_lse();
-        }
-        float total[kT / 2];
+          entries(key0 + 2 * kBlk, page_next);
+          // ---- rows [r, r_end) that may see them
+          float sum[kT][2];
 #pragma unroll
-        for (int i = 0; i < 2 * kT; ++i) {
-          float v = sum[i >> 1][i & 1];
-          v += __shfl_xor_sync(0xffffffffu, v, 1);
-          v += __shfl_xor_sync(0xffffffffu, v, 2);
-          if ((i & 3) == c) total[i >> 2] = v;
-        }
+          for (int t = 0; t < kT; ++t) sum[t][0] = sum[t][1] = 0.f;
+          auto add = [&](int buf, int r, int at, auto some) {  // rows r .. r + 7, which stand from row `at` of a buffer on
+            const float2 l2 = l_s[buf][(at >> 1) + c];
+            float x[kT][4];
 #pragma unroll
-        for (int y = 0; y < kT / 2; ++y) {
-          if (out[y] == nullptr) continue;
-          if (adds[y]) atomicAdd(out[y], total[y]);
-          else *out[y] = old[y] + total[y];
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {  // (the granules' products take turns, not each its own sum's steps)
+              const uint4 q = q_s[buf][at >> 3][i][lane];
+#pragma unroll
+              for (int t = 0; t < kT; ++t) mma16816(x[t], a[t][2 * i], q.x, q.y);
+#pragma unroll
+              for (int t = 0; t < kT; ++t) mma16816(x[t], a[t][2 * i + 1], q.z, q.w);
+            }
+            int klim[2], klo[2];
+            if (decltype(some)::value) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int pos = first_new + (int)((unsigned)(r + 2 * c + e) / G);
+                klim[e] = b.causal ? min(pos, ps.kvl - 1) : ps.kvl - 1;
+                klo[e] = mask_from(pos, b.window);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float l = e & 1 ? l2.y : l2.x;
+                float w = ex2(fmaf(x[t][e], p.scale_log2, l));
+                if (decltype(some)::value) {
+                  const int key = key0 + 16 * t + 8 * (e >> 1) + g;
+                  w = key <= klim[e & 1] && key >= klo[e & 1] && l != -INFINITY ? w : 0.f;
+                }
+                sum[t][e >> 1] += w;
+              }
+          };
+          for (int first = kFew ? 0 : r_lo; first < r_hi; first += kRows) {
+            const int here = buf;
+            if (!kFew) {
+              cp_async_wait_all();
+              shut = __syncthreads_or(shut);  // these rows are there, and nobody reads the other buffer any more
+              if (first + kRows < r_hi) stage(first + kRows);
+            }
+            const int to = min(first + kRows, r_end);
+            int r8 = max(first, r);
+            const int from = min(max(r8, (full + 7) & ~7), to);  // [from, until): tiles whose rows see all
+            // (With a row of lse = -inf among them none: it gives no weight where its score is NaN or infinite either.)
+            const int until = shut ? from : (full_end == rows_all ? to : max(from, min(to, full_end & ~7)));
+#pragma unroll 1
+            for (; r8 < from; r8 += 8) add(here, r8, r8 - first, std::true_type());
+#pragma unroll 1
+            for (; r8 < until; r8 += 8) add(here, r8, r8 - first, std::false_type());
+#pragma unroll 1
+            for (; r8 < to; r8 += 8) add(here, r8, r8 - first, std::true_type());
+            if (!kFew && first + kRows < r_hi) stage_lse();
+          }
+          float total[kT / 2];
+#pragma unroll
+          for (int i = 0; i < 2 * kT; ++i) {
+            float v = sum[i >> 1][i & 1];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if ((i & 3) == c) total[i >> 2] = v;
+          }
+#pragma unroll
+          for (int y = 0; y < kT / 2; ++y) {
+            if (out[y] == nullptr) continue;
+            if (adds[y]) atomicAdd(out[y], total[y]);
+            else *out[y] = old[y] + total[y];
+          }
         }
-      }
+      };
+      if (few) blocks(std::true_type());
+      else blocks(std::false_type());
     }
   }
 }

@@ -326,9 +326,9 @@ __device__ __forceinline__ void tmem_st_wait() {
 // ------------------------------------------------------------------------------------------
 // Arithmetic helpers
 // ------------------------------------------------------------------------------------------
-// 16 bytes into shared memory beside other work; zeros instead where !in (src is not read).
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// 16 bytes into shared memory beside other work.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {  // hardware 2^x (MUFU), flushes denormals
