@@ -15,8 +15,8 @@
 // rows see every key of a unit go by without masks, but for 64 rows with an lse of -inf among them, whose scores may be anything.
 //
 // Measured, 16 heads, d = 64, the last 32 tokens of 8 prompts of 4001 to 16000 4-bit keys: 36 us; 48.7 with queries and
-// their places worked out by each warp from global memory. 1000 tokens of 32 heads over 9000 bf16 keys of 8 kv heads: 167 us
-// at d = 64, 353 at d = 128 (345 without the look for an lse of -inf). A decode step of 64 sequences of 200 to 8192 bf16 keys,
+// their places worked out by each warp from global memory. 1000 tokens of 32 heads over 9000 bf16 keys of 8 kv heads: 169 us
+// at d = 64, 356 at d = 128 (345 without the look for an lse of -inf). A decode step of 64 sequences of 200 to 8192 bf16 keys,
 // d = 128, 8 kv heads (582 MB): 93 us, 6.2 TB/s. So a single token is bound by memory, and many rows by latencies at 12 to 16
 // warps per SM.
 #include <math.h>
@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(kWeightThreads, weight_ctas(D)) fa_paged_weigh
           bool whole = key0 >= lo && key0 + kKeys <= hi;  // every key of the unit is seen
 #pragma unroll
           for (int t = 0; t < kT; ++t) {
-            if (page[t] >= b.num_pages || page[t] < -1) {
+            const int at = key0 + 16 * t;
+            if (at < hi && at + 16 > lo && (unsigned)page[t] >= (unsigned)b.num_pages) {  // (-1 may stand in the table too)
               record_index_error(b.status);
               page[t] = -1;
             }
