@@ -425,8 +425,9 @@ int fa_fwd_paged4(const void *q, const long long *q_strides, const fa_paged_cach
  *   lse      : [T][Hq] fp32, contiguous, as fa_fwd_paged writes it. A query with lse = -inf gives no weight, whatever it holds.
  *   weights, out : fp32, element (page, head, slot) at page * stride + head * stride + slot; weight_strides: HOST,
  *              (page, head) of weights, then of out, in elements, a page's below 2^32. out may be weights (with its strides);
- *              it must not overlap it otherwise. Where sequences of the batch share pages, what they add to a slot is all
- *              there only if out is weights, in no fixed order; else the same call gives the same bits.
+ *              it must not overlap it otherwise. Where sequences of the batch share pages (a token that is new in one of them
+ *              may stand in the others' too), what they add to a slot is all there only if out is weights, in no fixed
+ *              order; else the same call gives the same bits.
  *   cache    : of fa_paged_weights, only k is looked at (v may be NULL); of fa_paged_weights4, only k and k_scale.
  */
 int fa_paged_weights(const void *q, const long long *q_strides, const float *lse, const fa_paged_cache *cache,

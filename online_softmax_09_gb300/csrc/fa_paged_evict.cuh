@@ -16,8 +16,9 @@ struct PagedWeights {
   float* out;        // the same; may be `old`
   long long old_page, old_head, out_page, out_head;
   float scale_log2;
+  bool cleared;  // the step's own tokens' slots of `out` are 0 before the sums are added
 };
-cudaError_t launch_paged_weights(const PagedWeights& p, int d, bool packed, int num_sms, cudaStream_t st);
+cudaError_t launch_paged_weights(PagedWeights& p, int d, bool packed, int num_sms, cudaStream_t st);
 
 constexpr int kMostRows = 8;  // tensors whose slots are moved in one call
 
