@@ -456,7 +456,8 @@ typedef struct {
  *              16 bytes are copied at a time where base, strides and bytes are multiples of 16 (else 4, 2 or 1).
  *   num_pages: of all these tensors; page numbers of either table outside [0, num_pages) are reported, not followed.
  *   keep     : device int32 [S], 0..max_keep, or the sequence keeps nothing and FA_ERR_INDEX is reported.
- *   out_table: device int32 [S][out_pages], out_stride elements from row to row; max_keep <= out_pages * page_size.
+ *   out_table: device int32 [S][out_pages], out_stride elements from row to row; max_keep <= out_pages * page_size
+ *              and at most 2^31 - 2^16 - 1.
  *   kept     : device int32 [S][Hkv][max_keep]: the places that stay, -1 behind them.
  *   kv_len_out: device int32 [S]: new. Since keys keep their rotation, later tokens need their true positions
  *              (fa_paged_append's `positions`).

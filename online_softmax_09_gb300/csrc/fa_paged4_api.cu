@@ -267,7 +267,7 @@ int fa_paged_evict(const float* weights, const long long* weight_strides, const 
   fa::TraceRange trace("fa_paged_evict");
   FA_TRY(check_batch(batch));
   if (weight_strides == nullptr || n_rows < 0 || n_rows > fa::kMostRows || (n_rows > 0 && rows == nullptr) || num_pages < 1 ||
-      max_keep < 0 || sinks < 0 || recent < 0 || out_pages < 0 || out_stride < 0 ||
+      max_keep < 0 || max_keep > kMaxTokens || sinks < 0 || recent < 0 || out_pages < 0 || out_stride < 0 ||
       (long long)out_pages * batch->page_size < max_keep)
     return FA_ERR_INVALID;
   const long long heads = (long long)batch->S * batch->Hkv;

@@ -816,6 +816,15 @@ def paged_weights(q, lse, keys, weights, plan, scale: float | None = None, out=N
     return out
 
 
+def _check_keep(max_keep, sinks, recent):
+    max_keep, sinks, recent = int(max_keep), int(sinks), int(recent)
+    if not 0 <= max_keep < 2 ** 31 - 2 ** 16:
+        raise ValueError("max_keep must be at least 0 and at most 2^31 - 2^16 - 1, the most tokens of a sequence")
+    if not (0 <= sinks < 2 ** 31 and 0 <= recent < 2 ** 31):
+        raise ValueError("sinks and recent must be at least 0 and fit 32 bits")
+    return max_keep, sinks, recent
+
+
 def paged_evict(weights, caches, plan, keep, out_table, max_keep: int, sinks: int = 4, recent: int = 64, kept=None,
                 kv_lens=None, stream=None):
     """Cut every sequence of the plan down to its keep heaviest tokens per kv head, copied in order into the pages of
@@ -851,9 +860,7 @@ def paged_evict(weights, caches, plan, keep, out_table, max_keep: int, sinks: in
             or (out_table.stride(1) != 1 and ts[1] > 1):
         raise ValueError(f"out_table must be an int32 CUDA tensor [{S}, out_pages] with contiguous last dim, on the plan's "
                          "device")
-    max_keep, sinks, recent = int(max_keep), int(sinks), int(recent)
-    if not (0 <= max_keep < 2 ** 31 and 0 <= sinks < 2 ** 31 and 0 <= recent < 2 ** 31):
-        raise ValueError("max_keep, sinks and recent must be at least 0 and fit 32 bits")
+    max_keep, sinks, recent = _check_keep(max_keep, sinks, recent)
     raw = plan._use(stream, i)
     shape = (S, Hkv, max_keep)
     if kept is None:
