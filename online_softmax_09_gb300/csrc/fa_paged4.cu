@@ -654,9 +654,11 @@ static cudaError_t launch_rows4(PagedFwd& p, const PagedCache4& cache, int num_s
 }
 
 // Tiles of 8 columns: one where no tile of the batch can have more than 8 rows, two for 16, four for 32.
-size_t paged4_rows_workspace_bytes(int d, int row_tile) {
-  const size_t ctas = (size_t)kMostRow4Ctas * kPagedSms;
-  return plan_up(2 * ctas * row_part(d, row_tile) * 4) + plan_up(ctas * sizeof(RowShare));
+size_t paged4_rows_part_bytes(int d, int row_tile, int columns) {
+  return plan_up((size_t)2 * row4_ctas(columns, d) * kPagedSms * row_part(d, row_tile) * 4);
+}
+size_t paged4_rows_workspace_bytes(int d, int row_tile, int columns) {
+  return paged4_rows_part_bytes(d, row_tile, columns) + plan_up((size_t)row4_ctas(columns, d) * kPagedSms * sizeof(RowShare));
 }
 
 cudaError_t launch_paged4_rows(PagedFwd& p, const PagedCache4& cache, int d, int num_sms, cudaStream_t st) {

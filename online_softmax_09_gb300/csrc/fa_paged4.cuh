@@ -59,8 +59,9 @@ __host__ __device__ constexpr int row4_columns(int row_tile, int max_q, int G) {
 }
 __host__ __device__ constexpr int row4_warps(int columns, int d) { return columns * d <= 128 ? 7 : 3; }
 __host__ __device__ constexpr int row4_ctas(int columns, int d) { return columns == 2 && d == 128 ? 3 : 2; }
-constexpr int kMostRow4Ctas = 3;
-size_t paged4_rows_workspace_bytes(int d, int row_tile);
+// Their workspace: two partial results per CTA, then RowShares.
+size_t paged4_rows_part_bytes(int d, int row_tile, int columns);
+size_t paged4_rows_workspace_bytes(int d, int row_tile, int columns);
 cudaError_t launch_paged4_rows(PagedFwd& p, const PagedCache4& c, int d, int num_sms, cudaStream_t st);
 cudaError_t launch_paged4_tiles(const TileMaps& m, const PagedFwd& p, const PagedCache4& c, int d, int num_sms,
                                 cudaStream_t st);

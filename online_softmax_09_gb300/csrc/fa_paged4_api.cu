@@ -103,7 +103,8 @@ int piece_of(const fa_paged_rows& r) {
 }
 
 size_t workspace4_bytes(const fa_paged_batch* b) {
-  return fa::paged4_rows_workspace_bytes(b->d, fa::row_tile_of(b->Hq / b->Hkv, b->max_q)) +
+  const int G = b->Hq / b->Hkv, row_tile = fa::row_tile_of(G, b->max_q);
+  return fa::paged4_rows_workspace_bytes(b->d, row_tile, fa::row4_columns(row_tile, b->max_q, G)) +
          (with_pairs(b) ? fa::paged_tiles_workspace_bytes(b->d) : 0);
 }
 
@@ -199,21 +200,20 @@ int fa_fwd_paged4(const void* q, const long long* q_strides, const fa_paged_cach
   p.b.sms = num_sms;
   set_fwd(p, q, q_strides, o, lse, scale, workspace, batch);
   const fa::PagedCache4 c = device_cache4(cache);
-  const int d = batch->d, ctas = fa::row4_ctas(fa::row4_columns(p.b.row_tile, p.b.max_q, p.b.G), d);
+  const int d = batch->d, columns = fa::row4_columns(p.b.row_tile, p.b.max_q, p.b.G), ctas = fa::row4_ctas(columns, d);
   // The bf16 cache's rule, measured over 4 bits too, without and with the joining kernel (4000 keys, d = 128): 8 tiles of 4 rows
   // 12.4 us and 10.6, of 16 rows 38.3 and 15.7, 32 of 16 rows 30.0 and 23.3; 32 of 4 rows, where it is left out, 15.6 and 16.9.
   // At d = 64 it would bring 1 to 3 us more between 16 and 32 tiles, about what its launch costs the host.
   p.row_share = few_tiles(batch, p.b, (long long)ctas * num_sms)
-                    ? reinterpret_cast<fa::RowShare*>(
-                          static_cast<char*>(workspace) +
-                          fa::plan_up((size_t)2 * fa::kMostRow4Ctas * fa::kPagedSms * fa::row_part(d, p.b.row_tile) * 4))
+                    ? reinterpret_cast<fa::RowShare*>(static_cast<char*>(workspace) +
+                                                      fa::paged4_rows_part_bytes(d, p.b.row_tile, columns))
                     : nullptr;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (with_pairs(batch)) {
     fa::TileMaps m;
     FA_TRY(make_query_maps(m, p, q, q_strides, o, batch));
     m.k = m.v = m.q;  // not used: warps of the kernel write the operands
-    char* ws = static_cast<char*>(workspace) + fa::paged4_rows_workspace_bytes(d, p.b.row_tile);
+    char* ws = static_cast<char*>(workspace) + fa::paged4_rows_workspace_bytes(d, p.b.row_tile, columns);
     p.tile_part = reinterpret_cast<float*>(ws);
     p.share = reinterpret_cast<fa::TileShare*>(ws + fa::plan_up((size_t)2 * fa::kPagedSms * fa::tile_part(d) * 4));
     p.tile_ctas = num_sms;
