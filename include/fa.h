@@ -407,9 +407,9 @@ int fa_paged_append4(const void *q, void *q_out, const void *k, const void *v, v
                      const fa_rotary *rotary, const int *positions, long long pos_axis, fa_stream_t stream);
 
 /*
- * fa_fwd_paged over a 4-bit cache: the same attention over the values that it stands for (the same bits as over a bf16 cache
- * that holds them, where a sequence has more than 32 rows; else sums in another order). Plans are fa_paged_plan's. The
- * workspace is of its own size; calls that overlap on the GPU need a plan and a workspace each.
+ * fa_fwd_paged over a 4-bit cache: the same attention over the values that it stands for, its sums in another order than over a
+ * bf16 cache that holds them (so results agree as far as either is exact, and not always to the bit). Plans are fa_paged_plan's.
+ * The workspace is of its own size; calls that overlap on the GPU need a plan and a workspace each.
  */
 size_t fa_fwd_paged4_workspace_bytes(const fa_paged_batch *batch);
 int fa_fwd_paged4(const void *q, const long long *q_strides, const fa_paged_cache4 *cache, const fa_paged_batch *batch,
