@@ -11,9 +11,11 @@
 // and 8 bytes per load, with one scale each, and a lane ends with 16 neighbouring dims of a query's output.
 // At the end of a stretch the warps' sums are joined in shared memory, and parts of tiles that CTAs share in the workspace.
 //
-// Bound by instructions, not by memory: one token of each of 64 sequences of 200 to 8192 keys (32 heads, 8 kv heads, d = 128,
-// 314 MB) takes 89.5 us, 3.5 TB/s or 52 % of the copy rate, at half the issue slots. Counted per 16 keys and warp: 105 for the
-// keys' operands and scores, 128 for the values' and sums, 29 for the weights, 115 for copies, loop, joins. Two sequences
+// Bound by latencies, with no unit full: one token of each of 64 sequences of 200 to 8192 keys (32 heads, 8 kv heads, d = 128,
+// 314 MB) takes 89.5 us, 3.5 TB/s or 52 % of the copy rate, with 52 % of the issue slots used and the tensor pipe 19 % busy: 14 warps
+// per SM, each in a chain of wait, unpacking, product, maximum over lanes, exponential, transposition and product. Instructions per
+// 16 keys and warp, which fewer of have made it faster: 105 for the keys' operands and scores, 128 for the values' and sums, 29
+// for the weights, 115 for copies, loop, joins. Two sequences
 // of 131072 keys 80 us (292 MB); one of 1000 9.5, and 48 of 4 drafted tokens in a window of 1024 at d = 64 21.5: latencies of
 // plan, table, keys, joins. (A share of the work for each warp, and no joins in CTAs: 87 us for the 64 sequences, but 16 and 30
 // for those two.)
@@ -27,8 +29,7 @@ namespace fa {
 template <int D, int NT>
 struct Row4Smem {
   static constexpr int kRows = NT <= 2 ? 16 : 32;
-  static constexpr int kWarps = row4_warps(NT, D), kThreads = 32 * (kWarps + 1);  // those that compute, and one that copies
-  static constexpr int kShares = kWarps == 7 ? 8 : kWarps;
+  static constexpr int kWarps = row4_warps(NT, D), kThreads = 32 * (kWarps + 1);  // those that compute, and one that walks
   static constexpr int kCtas = row4_ctas(NT, D);
   static constexpr int kCodes = kGran * code_bytes(D), kScales = kGran * scale_bytes(D);
   static constexpr int kPart = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales of a granule
@@ -224,10 +225,8 @@ __global__ void __launch_bounds__(Row4Smem<D, NT>::kThreads, Row4Smem<D, NT>::kC
 
   if (warp < kWarps) {
     const uint32_t ring = sbase + warp * L::kWarp;
-    // Units are dealt to kWarps + 1 shares. The walking warp's is taken by the one in the middle of seven, which is on the
-    // same quarter of the SM and would have half of it to itself.
-    const int step = kWarps * kUnit;
-    // The copying side: units of 32 keys, one of each round of shares, up to kStages ahead of the products,
+    const int step = kWarps * kUnit;  // from one of the warp's units to the next
+    // The copying side: units of 32 keys, one of every kWarps, up to kStages ahead of the products,
     // on into the next stretches. A unit is two granules of 16 keys, each within a page. 16 bytes per lane: two rounds for a
     // granule's codes of keys and of values (one at d = 64), and one for its scales, of keys in the first lanes and of values
     // in the next. (Bulk copies of these four pieces, of 64 bytes to 1 KB, came to one per 60 cycles and SM and bound the

@@ -6,7 +6,7 @@
 //     (128 + u) s + (-136 s):
 // 128 + u is the code beside the bits of 128, 136 s = 17 * 8 s has at most eight significant bits, so both are bf16 numbers,
 // and the sum is rounded once, to a number that bf16 has. (A scale of eight bits would halve the scales' bytes, 6 % of a
-// row, at two more instructions per scale in kernels that are bound by instructions; one of bf16's own eight significant
+// row, at two more instructions per scale in kernels whose time follows theirs; one of bf16's own eight significant
 // bits would round each value.)
 //
 // The 32-bit word i of a group holds dims 8 i .. 8 i + 7, dim 8 i + 2 j + e in the bits from 4 j + 16 e on, so that one shift

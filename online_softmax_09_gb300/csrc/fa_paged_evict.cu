@@ -13,8 +13,9 @@
 //
 // Bound by latencies: plan, table, weights, a meeting of the cluster per digit, then table, slots. 8 kv heads of 32768 tokens
 // cut to 4096 (d = 128, 35 MB): 20.9 us, of which 5.2 at the copy rate; with clusters of 4, 2 and 1 CTAs 28.8, 37.5 and 42.4
-// where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 14.0 us. (With digits of 11 bits in
-// clusters too, and keys and values moved one after the other, 33 and 29 us call by call; now 30 and 25.)
+// where 8 took 28. 32 sequences of 700 to 1500 tokens cut to 500 (4 heads, d = 64, 34 MB): 14.0 us. Call by call from Python, 23
+// to 29 us, both are bound by the host. (With digits of 11 bits in clusters too, and keys and values moved one after the other, 33
+// and 29 us there.)
 #include <cooperative_groups.h>
 #include <math.h>
 
